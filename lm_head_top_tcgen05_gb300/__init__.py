@@ -22,6 +22,10 @@ the shards (``all_reduce_count`` across ranks) and pass it as ``global_count`` t
 shard's forward and backward; the shards' losses then add up to the batch's loss, their dH
 rows are the batch's, and their dW summed (the usual data-parallel gradient all-reduce, or
 ``accumulate=True``) is the batch's dW.
+
+The text of on-policy distillation is drawn with the generation operators of ``generate.py``:
+an LM head in 8-bit integers (``quantize_int8``, ``int8_linear``, ``int8_matmul``) and the
+sampler (``sample``; ``draw_token`` runs both).
 """
 from __future__ import annotations
 
@@ -30,13 +34,15 @@ from typing import Optional, Tuple
 
 import torch
 
+from .generate import draw_token, int8_linear, int8_matmul, quantize_int8, sample
 from ._lib import (DIVERGENCES, FKL_ACCUMULATE_DH, FKL_ACCUMULATE_DW, FKL_NORM_SEQUENCES,  # noqa: F401
                    FKL_NORM_TOKENS, FKL_OK, STATUS, FklError, FklOptions, check, lib)
 
 _DEFAULT_PARAM = {"kl": 0.0, "jsd": 0.5, "skew_kl": 0.1, "skew_rkl": 0.1, "tv": 0.0}
 
 __all__ = ["workspace_size", "Workspace", "forward", "backward", "read_status", "fused_kl",
-           "FusedKL", "FklError", "STATUS", "teacher_topk", "local_count", "all_reduce_count"]
+           "FusedKL", "FklError", "STATUS", "teacher_topk", "local_count", "all_reduce_count",
+           "quantize_int8", "int8_matmul", "int8_linear", "sample", "draw_token"]
 
 
 def workspace_size(T: int, d: int, V: int, K: int, chunk: int, bf16_grads: bool = False) -> int:

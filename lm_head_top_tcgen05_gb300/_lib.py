@@ -1,4 +1,5 @@
-"""ctypes loader of the in-tree CUDA library ``libfkl.so`` (C ABI in include/fkl.h).
+"""ctypes loader of the in-tree CUDA library ``libfkl.so`` (C ABI in include/fkl.h and
+include/fkl_generate.h).
 
 There is no fallback: if the library is missing or cannot be loaded, every call raises.
 """
@@ -7,6 +8,8 @@ from __future__ import annotations
 import ctypes
 import threading
 from pathlib import Path
+
+import torch
 
 LIB_PATH = Path(__file__).resolve().with_name("libfkl.so")
 
@@ -35,10 +38,20 @@ class FklOptions(ctypes.Structure):
                 ("student_topk_logits", ctypes.c_void_p), ("global_count", ctypes.c_void_p)]
 
 
+class FklSampleParams(ctypes.Structure):
+    """fkl_sample_params of include/fkl_generate.h."""
+
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperature_rows", ctypes.c_void_p), ("top_k_rows", ctypes.c_void_p),
+                ("top_p_rows", ctypes.c_void_p), ("min_p_rows", ctypes.c_void_p)]
+
+
 FKL_NORM_TOKENS, FKL_NORM_SEQUENCES = 0, 1
 FKL_ACCUMULATE_DH, FKL_ACCUMULATE_DW = 1, 2
 # fkl_options.divergence, by the names the binding accepts
 DIVERGENCES = {"kl": 0, "jsd": 1, "skew_kl": 2, "skew_rkl": 3, "tv": 4}
+# FKL_TYPE_* of include/fkl_generate.h
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 # Every symbol declared in include/*.h, with (restype, argtypes).
 _P = ctypes.c_void_p
@@ -71,6 +84,15 @@ _SIGNATURES = {
     "fkl_local_count": (ctypes.c_int, [_P, _I64, ctypes.POINTER(FklOptions), _P, _P, ctypes.c_size_t, _P]),
     "fkl_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fkl_last_error": (ctypes.c_char_p, []),
+    "fkl_quantize_int8": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _I64, _I64, _P, _P, _P]),
+    "fkl_int8_matmul_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "fkl_int8_matmul": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int32, _P, _I64, _P,
+                                       ctypes.c_size_t, _P]),
+    "fkl_int8_linear_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "fkl_int8_linear": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _P, _P, _I64, _I64, _I64, ctypes.c_int32, _P, _I64,
+                                       _P, ctypes.c_size_t, _P]),
+    "fkl_sample": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _I64, _I64, _P, ctypes.POINTER(FklSampleParams), _P, _P,
+                                  _P]),
     "fkl_test_gemm": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                      ctypes.c_int, _P, ctypes.c_size_t, _P]),
     "fkl_test_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, _P, ctypes.c_size_t, _P]),

@@ -341,6 +341,13 @@ static fkl_status device_info(DevInfo* out) {
   return FKL_OK;
 }
 
+int require_device(int* sms) {
+  DevInfo di;
+  const fkl_status s = device_info(&di);
+  *sms = di.sms;
+  return s;
+}
+
 // Row blocks per group in the unit order of the dS recompute and the teacher cache's passes
 // (the forward takes fwd_group_rows below): units run split-major within a group, so the 76
 // pairs running together cover 38 row blocks of about 2 vocabulary splits and share each W

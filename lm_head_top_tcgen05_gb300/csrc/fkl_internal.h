@@ -83,6 +83,10 @@ int check_device_memory(const NamedPtr (&ptrs)[N]) {
   return check_device_memory(ptrs, N);
 }
 
+// The current device must be sm_103; writes its SM count (cached per device).  FKL_OK or the
+// error, with the message in fkl_last_error().
+int require_device(int* sms);
+
 // Event pair around one GEMM launch when a trace is active on this thread (fkl_trace.cu).
 // kind: 0 forward, 1 dS recompute, 2 dW, 3 dH.
 void trace_launch_begin(cudaStream_t st);

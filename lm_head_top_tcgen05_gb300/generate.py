@@ -1,0 +1,195 @@
+"""Generation operators: the 8-bit LM head and the sampler (C ABI in include/fkl_generate.h).
+
+On-policy distillation trains on text that the student draws.  One step of drawing it is
+
+    q, scale = quantize_int8(W)                       # once: a head's rows in 8 bits
+    logits = int8_linear(h, q, scale, out_dtype=torch.float32)
+    token, logprob = sample(logits, u, temperature=0.8, top_p=0.95)
+
+with ``h`` the hidden states [M, K] of the rows' last tokens and ``u`` one uniform random
+number per row.  ``int8_matmul`` is the product of operands that are already in 8 bits.
+``draw_token`` is the step as one call.  None of these has a gradient.  Calls run on the
+current stream of their inputs' device and keep one workspace per stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple, Union
+
+import torch
+
+from ._lib import DTYPES, FklError, FklSampleParams, check, lib
+
+__all__ = ["quantize_int8", "int8_matmul", "int8_linear", "sample", "draw_token"]
+
+_Setting = Union[float, int, torch.Tensor]
+_workspaces = {}
+
+
+def _stream(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _workspace(nbytes: int, device, stream: int, given) -> torch.Tensor:
+    """`given` (a Workspace), or this module's buffer of the stream: calls queued on two streams
+    never share one."""
+    if given is not None:
+        return given.get(nbytes, device)
+    key = (device.index, stream)
+    buf = _workspaces.get(key)
+    if buf is None or buf.numel() < nbytes:
+        _workspaces[key] = buf = None
+        _workspaces[key] = buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return buf
+
+
+def _dtype(dtype: torch.dtype, name: str) -> int:
+    if dtype not in DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    return DTYPES[dtype]
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Checks a CUDA matrix whose rows are contiguous; its row stride."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return max(cols, 1)
+    if t.stride(0) < cols:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> None:
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape [{n}] on {device}")
+
+
+def quantize_int8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(q int8 [M, K], scale float32 [M]): each row of x in 8-bit integers, x ~ q * scale.
+
+    scale = largest magnitude / 127, q rounded to nearest even.  A row with a NaN or an infinity
+    has scale NaN."""
+    ld = _rows(x, "x")
+    kind = _dtype(x.dtype, "x")
+    M, K = x.shape
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    st = lib().fkl_quantize_int8(x.data_ptr(), kind, M, K, ld, q.data_ptr(), scale.data_ptr(), _stream(x.device))
+    check(st, "fkl_quantize_int8")
+    return q, scale
+
+
+def _weight(wq: torch.Tensor, w_scale: torch.Tensor, K: int, device) -> int:
+    if wq.dtype != torch.int8 or wq.dim() != 2 or wq.shape[1] != K or wq.device != device or not wq.is_contiguous():
+        raise ValueError(f"wq must be a contiguous int8 tensor [N, {K}] on {device}")
+    _vector(w_scale, "w_scale", torch.float32, wq.shape[0], device)
+    return wq.shape[0]
+
+
+def _output(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty((M, N), dtype=dtype, device=device)
+    if out.dtype != dtype or tuple(out.shape) != (M, N) or out.device != device:
+        raise ValueError(f"out must be {dtype} [{M}, {N}] on {device}")
+    return out
+
+
+def int8_matmul(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
+                out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                workspace=None) -> torch.Tensor:
+    """out [M, N] = (xq wq^T) * x_scale[:, None] * w_scale[None, :] for int8 xq [M, K], wq [N, K].
+
+    K is a multiple of 16.  ``out`` may be given, with rows any stride apart."""
+    if xq.dtype != torch.int8 or xq.dim() != 2 or not xq.is_cuda or not xq.is_contiguous():
+        raise ValueError("xq must be a contiguous int8 CUDA tensor [M, K]")
+    M, K = xq.shape
+    kind = _dtype(out_dtype, "out_dtype")
+    _vector(x_scale, "x_scale", torch.float32, M, xq.device)
+    N = _weight(wq, w_scale, K, xq.device)
+    out = _output(out, M, N, out_dtype, xq.device)
+    n = lib().fkl_int8_matmul_workspace_size(M, N, K)
+    if n == 0:
+        raise FklError(1, "fkl_int8_matmul_workspace_size", f"unsupported shape M={M} N={N} K={K}")
+    stream = _stream(xq.device)
+    ws = _workspace(n, xq.device, stream, workspace)
+    st = lib().fkl_int8_matmul(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), M, N, K, kind,
+                               out.data_ptr(), _rows(out, "out"), ws.data_ptr(), ws.numel(), stream)
+    check(st, "fkl_int8_matmul")
+    return out
+
+
+def int8_linear(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, out_dtype: Optional[torch.dtype] = None,
+                out: Optional[torch.Tensor] = None, workspace=None) -> torch.Tensor:
+    """out [M, N] = x W^T for a weight in 8 bits (``quantize_int8``): x [M, K] is brought to 8 bits
+    with a scale per row, and the product is ``int8_matmul``'s.
+
+    x is float32, bfloat16 or float16 with contiguous rows any stride apart; out_dtype defaults
+    to x's.  K is a multiple of 16."""
+    ldx = _rows(x, "x")
+    M, K = x.shape
+    x_kind = _dtype(x.dtype, "x")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    out_kind = _dtype(out_dtype, "out_dtype")
+    N = _weight(wq, w_scale, K, x.device)
+    out = _output(out, M, N, out_dtype, x.device)
+    n = lib().fkl_int8_linear_workspace_size(M, N, K)
+    if n == 0:
+        raise FklError(1, "fkl_int8_linear_workspace_size", f"unsupported shape M={M} N={N} K={K}")
+    stream = _stream(x.device)
+    ws = _workspace(n, x.device, stream, workspace)
+    st = lib().fkl_int8_linear(x.data_ptr(), x_kind, ldx, wq.data_ptr(), w_scale.data_ptr(), M, N, K, out_kind,
+                               out.data_ptr(), _rows(out, "out"), ws.data_ptr(), ws.numel(), stream)
+    check(st, "fkl_int8_linear")
+    return out
+
+
+def _setting(p: FklSampleParams, name: str, value: _Setting, dtype: torch.dtype, B: int, device) -> None:
+    if isinstance(value, torch.Tensor):
+        _vector(value, name, dtype, B, device)
+        setattr(p, name + "_rows", value.data_ptr())
+    elif dtype == torch.int32:
+        setattr(p, name, max(0, min(int(value), 2**31 - 1)))
+    else:
+        setattr(p, name, float(value))
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: _Setting = 1.0, top_k: _Setting = 0,
+           top_p: _Setting = 1.0, min_p: _Setting = 0.0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token per row of logits [B, V] (float32, bfloat16 or float16; rows any stride apart):
+    (token int32 [B], logprob float32 [B], its log-probability among the ids kept).
+
+    ``u`` (float32 [B], in [0, 1)) are the random numbers: the token is the first id at which the
+    cumulative probability of the kept ids, in the order of ids, exceeds u.  Each setting is one
+    number, or a tensor [B] (float32; int32 for top_k) with one per row: temperature (0 takes the
+    largest logit), top_k (0 keeps all), top_p (1 keeps all) and min_p (0 keeps all), applied in
+    this order; ties keep the lower id.  The same inputs always give the same tokens.  A row
+    whose logits are all -inf (or NaN, which counts as -inf) gives token -1 and logprob NaN."""
+    ld = _rows(logits, "logits")
+    kind = _dtype(logits.dtype, "logits")
+    B, V = logits.shape
+    device = logits.device
+    _vector(u, "u", torch.float32, B, device)
+    p = FklSampleParams()
+    _setting(p, "temperature", temperature, torch.float32, B, device)
+    _setting(p, "top_k", top_k, torch.int32, B, device)
+    _setting(p, "top_p", top_p, torch.float32, B, device)
+    _setting(p, "min_p", min_p, torch.float32, B, device)
+    token = torch.empty(B, dtype=torch.int32, device=device)
+    logprob = torch.empty(B, dtype=torch.float32, device=device)
+    st = lib().fkl_sample(logits.data_ptr(), kind, B, V, ld, u.data_ptr(), ctypes.byref(p), token.data_ptr(),
+                          logprob.data_ptr(), _stream(device))
+    check(st, "fkl_sample")
+    return token, logprob
+
+
+def draw_token(h: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, u: torch.Tensor, temperature: _Setting = 1.0,
+               top_k: _Setting = 0, top_p: _Setting = 1.0, min_p: _Setting = 0.0,
+               logits: Optional[torch.Tensor] = None, workspace=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One generation step: the 8-bit head's float32 logits of h [M, K] (``int8_linear``; written
+    to ``logits`` if given) and a token per row drawn from them (``sample``)."""
+    logits = int8_linear(h, wq, w_scale, out_dtype=torch.float32, out=logits, workspace=workspace)
+    return sample(logits, u, temperature, top_k, top_p, min_p)

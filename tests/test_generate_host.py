@@ -1,0 +1,100 @@
+"""The generation entry points refuse bad arguments on the host, before touching CUDA."""
+import ctypes
+
+import pytest
+import torch
+
+INVALID, ALIGN, WS = 1, 2, 4
+HUGE = 2 ** 31
+
+
+@pytest.fixture(scope="module")
+def L():
+    from lm_head_top_tcgen05_gb300 import build
+    from lm_head_top_tcgen05_gb300._lib import lib
+
+    build.build()
+    return lib()
+
+
+def test_quantize_is_checked(L):
+    def call(x=16, t=0, rows=4, cols=64, ld=64, q=16, s=16):
+        return L.fkl_quantize_int8(x, t, rows, cols, ld, q, s, None)
+
+    assert call(t=3) == INVALID and call(t=-1) == INVALID
+    assert call(rows=-1) == INVALID and call(rows=HUGE) == INVALID
+    assert call(cols=0) == INVALID and call(ld=63) == INVALID
+    assert call(x=None) == INVALID and call(q=None) == INVALID and call(s=None) == INVALID
+    assert call(x=18) == ALIGN and call(s=18) == ALIGN
+    assert call(x=17, t=1) == ALIGN
+
+
+def test_workspace_sizes(L):
+    for f in (L.fkl_int8_matmul_workspace_size, L.fkl_int8_linear_workspace_size):
+        assert f(1, 1, 16) >= 256 and f(0, 5, 64) >= 256
+        assert f(4096, 201088, 2880) >= 256
+        assert f(4, 10, 40) == 0          # K not a multiple of 16
+        assert f(4, 10, 0) == 0 and f(4, 0, 64) == 0 and f(-1, 10, 64) == 0
+        assert f(4, 10, 131072) > 0 and f(4, 10, 131088) == 0
+        assert f(HUGE, 10, 64) == 0 and f(4, HUGE, 64) == 0
+
+
+def test_products_are_checked(L):
+    def call(M=4, N=10, K=64, x=16, xs=16, w=16, ws=16, t=0, out=16, ldo=10, work=256, n=1 << 30):
+        return L.fkl_int8_matmul(x, xs, w, ws, M, N, K, t, out, ldo, work, n, None)
+
+    def linear(M=4, N=10, K=64, x=16, xt=1, ldx=64, w=16, ws=16, t=0, out=16, ldo=10, work=256, n=1 << 30):
+        return L.fkl_int8_linear(x, xt, ldx, w, ws, M, N, K, t, out, ldo, work, n, None)
+
+    for f in (call, linear):
+        assert f(t=9) == INVALID and f(K=72) == INVALID and f(M=-1) == INVALID and f(N=0) == INVALID
+        assert f(ldo=9) == INVALID
+        for name in ("x", "w", "ws", "out"):
+            assert f(**{name: None}) == INVALID, name
+        assert f(w=24) == ALIGN and f(ws=18) == ALIGN and f(out=18) == ALIGN
+        assert f(work=None) == WS and f(n=8) == WS and f(work=128) == ALIGN
+    assert call(x=24) == ALIGN and call(xs=None) == INVALID
+    assert linear(xt=5) == INVALID and linear(ldx=63) == INVALID and linear(x=17) == ALIGN
+
+
+def test_sample_is_checked(L):
+    from lm_head_top_tcgen05_gb300._lib import FklSampleParams
+
+    def call(x=16, t=0, B=4, V=100, ld=100, u=16, p=None, tok=16, lp=16):
+        p = FklSampleParams() if p is None else p
+        return L.fkl_sample(x, t, B, V, ld, u, ctypes.byref(p), tok, lp, None)
+
+    assert call(t=3) == INVALID and call(B=-1) == INVALID and call(B=HUGE) == INVALID
+    assert call(V=0) == INVALID and call(V=2 ** 22 + 1, ld=2 ** 23) == INVALID and call(ld=99) == INVALID
+    assert call(x=None) == INVALID and call(u=None) == INVALID and call(tok=None) == INVALID
+    assert call(x=18) == ALIGN and call(x=17, t=2) == ALIGN and call(u=18) == ALIGN
+    assert call(p=FklSampleParams(top_k_rows=18)) == ALIGN
+    assert L.fkl_sample(16, 0, 4, 100, 100, 16, None, 16, 16, None) == INVALID
+
+
+def test_params_struct_layout_matches_header(tmp_path):
+    import subprocess
+    from pathlib import Path
+
+    from lm_head_top_tcgen05_gb300._lib import FklSampleParams
+
+    root = Path(__file__).resolve().parent.parent
+    fields = [f[0] for f in FklSampleParams._fields_]
+    src = tmp_path / "t.c"
+    src.write_text('#include <stdio.h>\n#include "fkl_generate.h"\nint main(void) {\n'
+                   + "".join(f'printf("%zu\\n", offsetof(fkl_sample_params, {f}));\n' for f in fields)
+                   + 'printf("%zu\\n", sizeof(fkl_sample_params)); return 0; }\n')
+    subprocess.run(["gcc", "-I", str(root / "include"), str(src), "-o", str(tmp_path / "t")], check=True)
+    got = [int(v) for v in subprocess.run([str(tmp_path / "t")], capture_output=True, text=True).stdout.split()]
+    assert got == [getattr(FklSampleParams, f).offset for f in fields] + [ctypes.sizeof(FklSampleParams)]
+
+
+def test_binding_needs_cuda_tensors():
+    import lm_head_top_tcgen05_gb300 as fkl
+
+    with pytest.raises(ValueError):
+        fkl.quantize_int8(torch.zeros(2, 16))
+    with pytest.raises(ValueError):
+        fkl.int8_linear(torch.zeros(2, 16), torch.zeros(3, 16, dtype=torch.int8), torch.zeros(3))
+    with pytest.raises(ValueError):
+        fkl.sample(torch.zeros(2, 16), torch.zeros(2))

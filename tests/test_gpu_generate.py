@@ -1,0 +1,487 @@
+"""The generation operators on the GPU against the float64 oracle (oracle/generate.py).
+
+Tolerances, derived: the quantised integers and scales are IEEE float32 arithmetic and are
+compared exactly.  A product's integer sum is exact while its partial sums stay below 2^24;
+otherwise each of the K / 16 accumulation steps loses at most 2^-23 of the largest partial sum.
+The two scales add a rounding each (2^-24), the output type its own half unit in the last
+place.  Sampled tokens must be among those the oracle allows when exponentials are off by
+2^-22 (CUDA's expf is within 2 units in the last place, 2^-22), the log-probability within
+2^-20 relative plus 1e-6.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import generate as og
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+HALF_ULP = {t: torch.finfo(t).eps / 2 for t in TYPES}
+
+
+@pytest.fixture(scope="module")
+def fkl(cuda_device):
+    from lm_head_top_tcgen05_gb300 import build
+
+    build.build()
+    import lm_head_top_tcgen05_gb300 as m
+
+    return m
+
+
+# ---------------------------------------------------------------- quantisation
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 16), (3, 17), (5, 2880), (2, 4100), (70, 48), (2, 40000)])
+def test_quantize(fkl, dtype, M, K):
+    g = torch.Generator().manual_seed(M * 1000 + K)
+    x = (torch.randn(M, K, generator=g) * 3).to(dtype)
+    q, s = fkl.quantize_int8(x.cuda())
+    rq, rs = og.quantize_int8(x.float().numpy())
+    np.testing.assert_array_equal(s.cpu().numpy(), rs)
+    np.testing.assert_array_equal(q.cpu().numpy(), rq)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_special_rows_and_strides(fkl, dtype):
+    x = torch.randn(8, 100, generator=torch.Generator().manual_seed(1)).to(dtype)
+    x[0] = 0
+    x[1, 3] = float("nan")
+    x[2, 5] = float("-inf")
+    x[3] = torch.finfo(dtype).tiny * 2.0 ** -3      # subnormal values
+    x[4] = torch.finfo(dtype).max
+    x[5, 1:] = 0
+    for view in (x, x[:, 1:], x[:, :64], x[::2, 3:51]):
+        v = x.cuda()[tuple(slice(*i) for i in _slices(x, view))]
+        q, s = fkl.quantize_int8(v)
+        rq, rs = og.quantize_int8(view.float().numpy())
+        np.testing.assert_array_equal(s.cpu().numpy(), rs)
+        np.testing.assert_array_equal(q.cpu().numpy(), rq)
+
+
+def _slices(x, view):
+    off = view.storage_offset()
+    r0, c0 = divmod(off, x.shape[1])
+    step = view.stride(0) // x.shape[1]
+    return (r0, r0 + view.shape[0] * step, step), (c0, c0 + view.shape[1], 1)
+
+
+def test_quantize_empty(fkl):
+    q, s = fkl.quantize_int8(torch.empty(0, 64, device="cuda"))
+    assert q.shape == (0, 64) and s.shape == (0,)
+
+
+# ---------------------------------------------------------------- product
+def operands(M, N, K, seed):
+    rng = np.random.default_rng(seed)
+    xq = rng.integers(-128, 128, (M, K)).astype(np.int8)
+    wq = rng.integers(-128, 128, (N, K)).astype(np.int8)
+    # scales that keep every output a normal float16
+    xs = (rng.uniform(0.5, 2.0, M) / 256).astype(np.float32)
+    ws = (rng.uniform(0.5, 2.0, N) / 256).astype(np.float32)
+    return xq, xs, wq, ws
+
+
+def dev(*arrays):
+    return [torch.from_numpy(a).cuda() for a in arrays]
+
+
+def assert_product(got, ops, dtype):
+    xq, xs, wq, ws = ops
+    ref = og.int8_matmul(xq, xs, wq, ws)
+    K = xq.shape[1]
+    mag = og.int8_matmul(np.abs(xq.astype(np.int16)), xs, np.abs(wq.astype(np.int16)), ws)
+    exact_sum = K <= 1024
+    tol = np.abs(ref) * (3 * 2.0 ** -24 + HALF_ULP[dtype]) + (2.0 ** -24 if dtype == torch.float16 else 0)
+    if not exact_sum:
+        tol = tol + mag * (K / 16) * 2.0 ** -23
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert got.dtype == dtype
+    assert (err <= tol).all(), (float((err - tol).max()), np.argwhere(err > tol)[:4])
+
+
+MATMUL_SHAPES = [(1, 1, 16), (1, 5, 48), (1, 130, 2880), (2, 4099, 64), (3, 128, 144), (4, 1000, 4096), (5, 77, 160),
+                 (7, 129, 272), (8, 1024, 512), (9, 300, 1040), (15, 257, 128), (16, 256, 256), (17, 640, 2880),
+                 (31, 515, 1456), (33, 1001, 96), (64, 384, 1024), (65, 2000, 320), (100, 133, 208), (127, 260, 112),
+                 (128, 512, 640), (129, 383, 784), (192, 1030, 176), (200, 700, 1456), (255, 129, 64), (256, 256, 2880),
+                 (257, 513, 272), (300, 2100, 512), (513, 300, 400), (1000, 1000, 1040), (40, 30000, 128), (1, 60001, 32)]
+
+
+@pytest.mark.parametrize("M,N,K", MATMUL_SHAPES)
+def test_int8_matmul(fkl, M, N, K):
+    ops = operands(M, N, K, M * 7 + N * 3 + K)
+    t = dev(*ops)
+    for dtype in TYPES:
+        assert_product(fkl.int8_matmul(*t, out_dtype=dtype), ops, dtype)
+
+
+@pytest.mark.parametrize("M", [1, 6, 40, 300])
+def test_int8_matmul_largest_values(fkl, M):
+    # every product 128 * 128: the largest sums that K = 4096 can give
+    xq = np.full((M, 4096), -128, dtype=np.int8)
+    wq = np.full((200, 4096), -128, dtype=np.int8)
+    wq[::3] = 127
+    ops = (xq, np.full(M, 0.25, np.float32), wq, np.ones(200, np.float32))
+    assert_product(fkl.int8_matmul(*dev(*ops)), ops, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [1, 5, 20, 270])
+def test_int8_matmul_into_strided_output(fkl, dtype, M):
+    ops = operands(M, 301, 256, 4 + M)
+    big = torch.full((M, 333), 7.0, dtype=dtype, device="cuda")
+    out = big[:, 5:306]
+    got = fkl.int8_matmul(*dev(*ops), out_dtype=dtype, out=out)
+    assert got.data_ptr() == out.data_ptr()
+    assert_product(out, ops, dtype)
+    assert (big[:, :5] == 7).all() and (big[:, 306:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [2, 33])
+def test_int8_matmul_special_scales(fkl, M):
+    ops = list(operands(M, 150, 128, 9))
+    ops[1][0] = np.nan
+    ops[3][3] = 0.0
+    y = fkl.int8_matmul(*dev(*ops)).cpu().numpy()
+    assert np.isnan(y[0]).all()
+    assert (y[1:, 3] == 0).all() and np.isfinite(y[1:]).all()
+
+
+@pytest.mark.parametrize("x_dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 500, 2880), (2, 129, 48), (8, 1000, 256), (9, 300, 1456), (50, 257, 512),
+                                   (300, 400, 1024)])
+def test_int8_linear(fkl, x_dtype, M, N, K):
+    g = torch.Generator().manual_seed(M + N + K)
+    x = torch.randn(M, K, generator=g).to(x_dtype)
+    W = torch.randn(N, K, generator=g) * 0.02
+    wq, ws = og.quantize_int8(W.numpy())
+    xq, xs = og.quantize_int8(x.float().numpy())
+    for dtype in TYPES:
+        y = fkl.int8_linear(x.cuda(), *dev(wq, ws), out_dtype=dtype)
+        ref = og.int8_matmul(xq, xs, wq, ws)
+        tol = np.abs(ref) * (3 * 2.0 ** -24 + HALF_ULP[dtype]) + (2.0 ** -24 if dtype == torch.float16 else 0)
+        if K > 1024:
+            tol = tol + og.int8_matmul(np.abs(xq), xs, np.abs(wq), ws) * (K / 16) * 2.0 ** -23
+        assert (np.abs(y.double().cpu().numpy() - ref) <= tol).all()
+    assert fkl.int8_linear(x.cuda(), *dev(wq, ws)).dtype == x_dtype
+
+
+@pytest.mark.parametrize("M", [1, 7, 40])
+def test_int8_linear_strided_and_special_rows(fkl, M):
+    # the last token of each sequence of a batch; rows that are zero or hold a NaN
+    g = torch.Generator().manual_seed(M)
+    h = torch.randn(M, 5, 320, generator=g).to(torch.bfloat16)
+    h[0, -1] = 0
+    if M > 1:
+        h[1, -1, 7] = float("nan")
+    x = h[:, -1]
+    W = torch.randn(333, 320, generator=g) * 0.02
+    wq, ws = og.quantize_int8(W.numpy())
+    y = fkl.int8_linear(h.cuda()[:, -1], *dev(wq, ws), out_dtype=torch.float32).cpu().numpy()
+    xq, xs = og.quantize_int8(x.float().numpy())
+    ref = og.int8_matmul(xq, xs, wq, ws)
+    assert (y[0] == 0).all()
+    if M > 1:
+        assert np.isnan(y[1]).all()
+    ok = [0] + list(range(2, M))
+    assert (np.abs(y[ok] - ref[ok]) <= np.abs(ref[ok]) * 4 * 2.0 ** -24).all()
+
+
+def test_products_of_no_tokens(fkl):
+    wq, ws = torch.zeros(50, 64, dtype=torch.int8, device="cuda"), torch.ones(50, device="cuda")
+    assert fkl.int8_linear(torch.empty(0, 64, device="cuda"), wq, ws).shape == (0, 50)
+    xq = torch.empty(0, 64, dtype=torch.int8, device="cuda")
+    assert fkl.int8_matmul(xq, torch.empty(0, device="cuda"), wq, ws).shape == (0, 50)
+
+
+@pytest.mark.parametrize("M", [1, 30, 300])
+def test_product_status_and_repeat(fkl, M):
+    ops = dev(*operands(M, 3000, 1456, 2))
+    ws = fkl.Workspace("cuda")
+    a = fkl.int8_matmul(*ops, workspace=ws)
+    b = fkl.int8_matmul(*ops, workspace=ws)
+    assert fkl.read_status(ws) == 0
+    assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- sampler
+def check_sample(fkl, logits, u, **kw):
+    """logits: CPU tensor; settings: numbers or CPU tensors [B]."""
+    B = logits.shape[0]
+    dk = {n: (v.cuda() if isinstance(v, torch.Tensor) else v) for n, v in kw.items()}
+    lg = logits.cuda() if logits.is_contiguous() else _on_gpu_strided(logits)
+    token, logprob = fkl.sample(lg, u.cuda(), **dk)
+    token2, logprob2 = fkl.sample(lg, u.cuda(), **dk)
+    assert token.dtype == torch.int32 and logprob.dtype == torch.float32
+    assert torch.equal(token, token2)
+    assert torch.equal(logprob.nan_to_num(7), logprob2.nan_to_num(7))
+    token, logprob = token.cpu().tolist(), logprob.cpu().tolist()
+    rows = logits.float().numpy()
+    for b in range(B):
+        a = {n: (v[b].item() if isinstance(v, torch.Tensor) else v) for n, v in kw.items()}
+        ok = og.sample_row(rows[b], u[b].item(), **a)
+        assert token[b] in ok, (b, token[b], ok, a)
+        if token[b] < 0:
+            assert np.isnan(logprob[b])
+        else:
+            lo, hi = ok[token[b]]
+            margin = 2.0 ** -20 * abs(lo) + 1e-6
+            assert lo - margin <= logprob[b] <= hi + margin, (b, logprob[b], lo, hi)
+    return token
+
+
+def _on_gpu_strided(t):
+    big = torch.zeros(t.shape[0], t.stride(0), dtype=t.dtype)
+    out = big.cuda()[:, :t.shape[1]]
+    out.copy_(t)
+    return out
+
+
+def lm_logits(B, V, seed, dtype=torch.float32, hot=10):
+    g = torch.Generator().manual_seed(seed)
+    x = 2.0 * torch.randn(B, V, generator=g)
+    if V > 4 * hot:
+        x.scatter_add_(1, torch.randint(0, V, (B, hot), generator=g), 5 + 4 * torch.rand(B, hot, generator=g))
+    return x.to(dtype), torch.rand(B, generator=g)
+
+
+SETTINGS = [dict(), dict(temperature=0.0), dict(temperature=0.7, top_k=50, top_p=0.95), dict(top_k=1), dict(top_k=5),
+            dict(top_p=0.9), dict(top_p=0.999), dict(top_p=0.0), dict(min_p=0.05), dict(min_p=2.0),
+            dict(temperature=1.5, top_k=3000), dict(temperature=1.3, top_k=2000, top_p=0.8, min_p=0.001),
+            dict(temperature=8.0, top_p=0.5), dict(temperature=0.05, top_p=0.9), dict(top_k=10 ** 6),
+            dict(temperature=100.0, top_p=0.99)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kw", SETTINGS, ids=lambda k: ",".join(f"{a}={b}" for a, b in k.items()) or "plain")
+def test_sample_settings(fkl, dtype, kw):
+    logits, u = lm_logits(6, 20011, 3, dtype)
+    check_sample(fkl, logits, u, **kw)
+
+
+@pytest.mark.parametrize("V", [1, 2, 3, 31, 32, 33, 255, 1000, 1024, 1025, 4096, 50261, 201088, 300007])
+def test_sample_sizes(fkl, V):
+    for seed, kw in enumerate((dict(), dict(top_k=7), dict(top_p=0.8), dict(top_k=40, top_p=0.9, min_p=0.01))):
+        logits, u = lm_logits(3, V, V + seed)
+        check_sample(fkl, logits, u, **kw)
+
+
+def test_sample_largest_vocabulary(fkl):
+    V = 2 ** 22
+    logits, u = lm_logits(2, V, 1, torch.bfloat16)
+    check_sample(fkl, logits, u)
+    check_sample(fkl, logits, u, top_p=0.7)
+    check_sample(fkl, torch.zeros(2, V), u)
+    check_sample(fkl, torch.zeros(2, V), u, top_k=V - 3, top_p=0.5)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pad", [1, 3, 8])
+def test_sample_strided_rows(fkl, dtype, pad):
+    logits, u = lm_logits(7, 3001 + pad, 8, dtype)
+    check_sample(fkl, logits[:, :3001], u, top_k=20)
+    check_sample(fkl, logits[:, :3001], u, top_p=0.9)
+    # a view that starts inside a row
+    t, _ = fkl.sample(logits.cuda()[:, pad:], u.cuda(), top_p=0.9)
+    t2, _ = fkl.sample(logits[:, pad:].contiguous().cuda(), u.cuda(), top_p=0.9)
+    assert torch.equal(t, t2)
+
+
+@pytest.mark.parametrize("B", [1, 2, 19, 37, 40, 77, 160, 333])
+def test_sample_batches_with_settings_per_row(fkl, B):
+    logits, u = lm_logits(B, 5003, B, torch.bfloat16)
+    g = torch.Generator().manual_seed(B)
+    t = torch.rand(B, generator=g) * 1.5
+    t[::5] = 0
+    k = torch.randint(0, 60, (B,), generator=g, dtype=torch.int32)
+    p = torch.rand(B, generator=g) * 1.2
+    m = torch.rand(B, generator=g) * 0.2 - 0.05
+    check_sample(fkl, logits, u, temperature=t, top_k=k, top_p=p, min_p=m)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=3), dict(top_p=0.5), dict(top_k=700, top_p=0.5), dict(min_p=0.5),
+                                dict(temperature=0.0)])
+@pytest.mark.parametrize("V", [40, 9001])
+def test_sample_ties(fkl, V, kw):
+    u = torch.tensor([0.0, 0.3, 0.999, 0.5])
+    check_sample(fkl, torch.zeros(4, V), u, **kw)                       # all equal
+    x = torch.zeros(4, V)
+    x[:, 1::2] = -0.0                                                   # -0 and +0 are the same logit
+    check_sample(fkl, x, u, **kw)
+    x = torch.full((4, V), -1.0)
+    x[:, 7::3] = 2.0                                                    # a third tied at the top
+    check_sample(fkl, x, u, **kw)
+    x = (torch.randint(0, 4, (4, V), generator=torch.Generator().manual_seed(V))).float()
+    check_sample(fkl, x, u, **kw)                                       # four values
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=3), dict(top_p=0.5), dict(min_p=0.1), dict(temperature=0.0)])
+def test_sample_special_values(fkl, kw):
+    V = 3000
+    x = torch.randn(12, V, generator=torch.Generator().manual_seed(4))
+    inf, nan = float("inf"), float("nan")
+    x[0] = -inf
+    x[1] = nan
+    x[2, :] = -inf
+    x[2, 1234] = -5.0                              # one id left
+    x[3, 100:] = -inf
+    x[4, ::2] = nan
+    x[5, 17] = inf
+    x[6, [17, 2000]] = inf
+    x[7] = torch.finfo(torch.float32).min          # masked with the type's lowest value
+    x[7, 5] = 1.0
+    x[8] = torch.finfo(torch.float32).min
+    x[9, 0] = torch.finfo(torch.float32).max
+    x[10] = -inf
+    x[10, [V - 1, 0]] = 3.0
+    x[11] *= 1e30
+    u = torch.linspace(0, 0.99, 12)
+    token = check_sample(fkl, x, u, **kw)
+    assert token[0] == -1 and token[1] == -1 and token[2] == 1234 and token[5] == 17 and token[7] == 5
+
+
+def test_sample_random_numbers_out_of_range(fkl):
+    logits, _ = lm_logits(5, 500, 2)
+    u = torch.tensor([-1.0, 1.0, 2.0, float("nan"), float("inf")])
+    token, _ = fkl.sample(logits.cuda(), u.cuda())
+    first, _ = fkl.sample(logits.cuda(), torch.zeros(5, device="cuda"))
+    assert token[0] == first[0] and token[3] == first[3]
+    assert ((token >= 0) & (token < 500)).all()
+
+
+def test_sample_frequencies(fkl):
+    # 40000 draws of one row: every id's share within 5 standard deviations of its probability
+    V, B = 12, 40000
+    x = torch.randn(V, generator=torch.Generator().manual_seed(1))
+    u = torch.rand(B, generator=torch.Generator().manual_seed(2))
+    token, logprob = fkl.sample(x.cuda().expand(B, V).contiguous(), u.cuda(), temperature=0.8)
+    p = torch.softmax(x.double() / 0.8, 0)
+    share = torch.bincount(token.cpu().long(), minlength=V).double() / B
+    assert ((share - p).abs() <= 5 * (p * (1 - p) / B).sqrt()).all()
+    assert (logprob.cpu().double() - p.log()[token.cpu().long()]).abs().max() < 2e-6
+
+
+def test_sample_empty_batch(fkl):
+    t, lp = fkl.sample(torch.empty(0, 100, device="cuda"), torch.empty(0, device="cuda"))
+    assert t.shape == (0,) and lp.shape == (0,)
+
+
+# ---------------------------------------------------------------- the step as a whole
+def test_draw_token_streams_and_graph(fkl):
+    g = torch.Generator().manual_seed(5)
+    W = torch.randn(5000, 256, generator=g) * 0.05
+    wq, ws = fkl.quantize_int8(W.cuda())
+    for M in (1, 12, 40, 300):
+        h = torch.randn(M, 256, generator=g).to(torch.bfloat16).cuda()
+        u = torch.rand(M, generator=g).cuda()
+        ref = fkl.draw_token(h, wq, ws, u, temperature=0.9, top_k=40, top_p=0.95)
+        torch.cuda.synchronize()
+        side = [torch.cuda.Stream() for _ in range(2)]
+        got = []
+        for s in side:
+            with torch.cuda.stream(s):
+                got.append(fkl.draw_token(h, wq, ws, u, temperature=0.9, top_k=40, top_p=0.95))
+        torch.cuda.synchronize()
+        for t, lp in got:
+            assert torch.equal(t, ref[0]) and torch.equal(lp, ref[1])
+        work = fkl.Workspace("cuda")
+        logits = torch.empty(M, 5000, device="cuda")
+        hs, us = h.clone(), u.clone()
+        s = side[0]
+        with torch.cuda.stream(s):
+            fkl.draw_token(hs, wq, ws, us, temperature=0.9, top_k=40, top_p=0.95, logits=logits, workspace=work)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                out = fkl.draw_token(hs, wq, ws, us, temperature=0.9, top_k=40, top_p=0.95, logits=logits,
+                                     workspace=work)
+        torch.cuda.synchronize()
+        for _ in range(2):
+            h2 = torch.randn(M, 256, generator=g).to(torch.bfloat16).cuda()
+            hs.copy_(h2)
+            graph.replay()
+            torch.cuda.synchronize()
+            want = fkl.draw_token(h2, wq, ws, u, temperature=0.9, top_k=40, top_p=0.95)
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+# ---------------------------------------------------------------- refusals
+def test_refusals(fkl):
+    c = dict(device="cuda")
+    x = torch.zeros(4, 64, **c)
+    wq, ws = torch.zeros(10, 64, dtype=torch.int8, **c), torch.zeros(10, **c)
+    xq, xs = torch.zeros(4, 64, dtype=torch.int8, **c), torch.zeros(4, **c)
+    u = torch.zeros(4, **c)
+    with pytest.raises(ValueError):
+        fkl.quantize_int8(x[0])
+    with pytest.raises(ValueError):
+        fkl.quantize_int8(x.t())
+    with pytest.raises(TypeError):
+        fkl.quantize_int8(x.double())
+    with pytest.raises(ValueError):
+        fkl.quantize_int8(x.cpu())
+    with pytest.raises(ValueError):
+        fkl.int8_linear(x, wq[:, :32], ws)
+    with pytest.raises(ValueError):
+        fkl.int8_linear(x, wq.float(), ws)
+    with pytest.raises(ValueError):
+        fkl.int8_linear(x, wq, ws.double())
+    with pytest.raises(ValueError):
+        fkl.int8_linear(x, wq, ws[:5])
+    with pytest.raises(TypeError):
+        fkl.int8_linear(x, wq, ws, out_dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fkl.int8_linear(x, wq, ws, out=torch.zeros(4, 11, **c))
+    with pytest.raises(ValueError):
+        fkl.int8_linear(x, wq, ws, out=torch.zeros(10, 4, **c).t())
+    with pytest.raises(fkl.FklError):  # K not a multiple of 16
+        fkl.int8_linear(torch.zeros(4, 40, **c), torch.zeros(10, 40, dtype=torch.int8, **c), ws)
+    with pytest.raises(fkl.FklError) as e:  # rows of a view that do not start on 16 bytes
+        flat = torch.zeros(10 * 64 + 1, dtype=torch.int8, **c)[1:].view(10, 64)
+        fkl.int8_linear(x, flat, ws)
+    assert e.value.status == 2
+    with pytest.raises(ValueError):
+        fkl.int8_matmul(xq.float(), xs, wq, ws)
+    with pytest.raises(ValueError):
+        fkl.int8_matmul(xq, xs[:3], wq, ws)
+    with pytest.raises(ValueError):
+        fkl.sample(x, u[:3])
+    with pytest.raises(ValueError):
+        fkl.sample(x, u.double())
+    with pytest.raises(ValueError):
+        fkl.sample(x, u.cpu())
+    with pytest.raises(ValueError):
+        fkl.sample(x.t(), u)
+    with pytest.raises(ValueError):
+        fkl.sample(x[:1].expand(4, 64), u)
+    with pytest.raises(TypeError):
+        fkl.sample(x.to(torch.int32), u)
+    with pytest.raises(ValueError):
+        fkl.sample(x, u, top_k=torch.zeros(4, **c))
+    with pytest.raises(ValueError):
+        fkl.sample(x, u, temperature=torch.zeros(3, **c))
+    with pytest.raises(fkl.FklError):
+        fkl.sample(torch.zeros(1, 2 ** 22 + 1, **c), u[:1])
+    with pytest.raises(fkl.FklError):
+        fkl.sample(torch.zeros(4, 0, **c), u)
+
+
+def test_host_memory_is_refused(fkl):
+    import ctypes
+
+    from lm_head_top_tcgen05_gb300._lib import FklSampleParams, lib
+
+    L = lib()
+    x = torch.zeros(4, 64, device="cuda")
+    host = torch.zeros(4, pin_memory=True)
+    tok = torch.zeros(4, dtype=torch.int32, device="cuda")
+    p = FklSampleParams(temperature=1.0, top_p=1.0)
+    st = L.fkl_sample(x.data_ptr(), 0, 4, 64, 64, host.data_ptr(), ctypes.byref(p), tok.data_ptr(), None, None)
+    assert st == 1 and b"u is not" in L.fkl_last_error()
+    q = torch.zeros(4, 64, dtype=torch.int8, device="cuda")
+    st = L.fkl_quantize_int8(x.data_ptr(), 0, 4, 64, 64, q.data_ptr(), host.data_ptr(), None)
+    assert st == 1 and b"scale" in L.fkl_last_error()
+    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(4, device="cuda")
+    st = L.fkl_int8_matmul(q.data_ptr(), s.data_ptr(), q.data_ptr(), host.data_ptr(), 4, 4, 64, 0, x.data_ptr(), 4,
+                           ws.data_ptr(), ws.numel(), None)
+    assert st == 1 and b"w_scale" in L.fkl_last_error()
