@@ -5,7 +5,8 @@
 //     y_mn = (sum_k q_mk w_nk) * s_m * t_n
 #include <climits>
 
-#include "fkl_internal.h"
+#include "fkl_gemm.cuh"
+#include "fkl_int8.h"
 #include "fkl_types.cuh"
 
 namespace fkl {
@@ -27,16 +28,32 @@ __device__ __forceinline__ int quantize(float x, float s) {
   return static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f));
 }
 
+// Four quantised values as bytes, or (for the tensor cores) as fp16.
+__device__ __forceinline__ void put4(int8_t* o, const int (&q)[4]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) w |= (static_cast<uint32_t>(q[b]) & 0xffu) << (8 * b);
+  *reinterpret_cast<uint32_t*>(o) = w;
+}
+__device__ __forceinline__ void put4(__half* o, const int (&q)[4]) {
+  __half2 h[2] = {__floats2half2_rn(static_cast<float>(q[0]), static_cast<float>(q[1])),
+                  __floats2half2_rn(static_cast<float>(q[2]), static_cast<float>(q[3]))};
+  *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(h);
+}
+
 // One block per row, two reads of it (the second from cache).  The IEEE division keeps the
-// integers equal to the definition's.
-template <class T, bool kVec>
+// integers equal to the definition's.  Block 0 zeroes `hdr`, if there is one.
+template <class T, class Q, bool kVec>
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_kernel(const T* __restrict__ x, int64_t cols, int64_t ldx, int8_t* __restrict__ q,
-                    float* __restrict__ scale) {
+    quantize_kernel(const T* __restrict__ x, int64_t cols, int64_t ldx, Q* __restrict__ q, float* __restrict__ scale,
+                    uint4* __restrict__ hdr) {
   constexpr int E = 16 / sizeof(T);
   __shared__ uint32_t warp_max[kQuantThreads / 32];
   const T* row = x + static_cast<int64_t>(blockIdx.x) * ldx;
-  int8_t* out = q + static_cast<int64_t>(blockIdx.x) * cols;
+  Q* out = q + static_cast<int64_t>(blockIdx.x) * cols;
+  if (hdr != nullptr && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(Int8Header) / 16); i += kQuantThreads)
+      hdr[i] = make_uint4(0, 0, 0, 0);
   uint32_t amax = 0;
   if (kVec) {
     for (int64_t i = threadIdx.x; i < cols / E; i += kQuantThreads) {
@@ -61,116 +78,284 @@ __global__ void __launch_bounds__(kQuantThreads)
     for (int64_t i = threadIdx.x; i < cols / E; i += kQuantThreads) {
       float v[E];
       unpack16<T>(reinterpret_cast<const uint4*>(row)[i], v);
-      uint32_t w[E / 4];
 #pragma unroll
       for (int j = 0; j < E / 4; ++j) {
-        w[j] = 0;
+        int w[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) w[j] |= (static_cast<uint32_t>(quantize(v[4 * j + b], s)) & 0xffu) << (8 * b);
+        for (int b = 0; b < 4; ++b) w[b] = quantize(v[4 * j + b], s);
+        put4(out + i * E + 4 * j, w);
       }
-#pragma unroll
-      for (int j = 0; j < E / 4; ++j) reinterpret_cast<uint32_t*>(out)[i * (E / 4) + j] = w[j];
     }
   } else {
     for (int64_t i = threadIdx.x; i < cols; i += kQuantThreads)
-      out[i] = static_cast<int8_t>(quantize(to_float(row[i]), s));
+      out[i] = static_cast<Q>(static_cast<float>(quantize(to_float(row[i]), s)));
   }
 }
 
-static cudaError_t launch_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t ldx, int8_t* q,
-                                   float* scale, cudaStream_t st) {
+template <class Q>
+static cudaError_t launch_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t ldx, Q* q,
+                                   float* scale, Int8Header* hdr, cudaStream_t st) {
   return with_type(type, [&](auto t) {
     using T = decltype(t);
     const T* p = static_cast<const T*>(x);
     const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * sizeof(T) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(q) % 4 == 0 && cols % 16 == 0;
+                     reinterpret_cast<uintptr_t>(q) % (4 * sizeof(Q)) == 0 && cols % 16 == 0;
+    uint4* h = reinterpret_cast<uint4*>(hdr);
     if (vec)
-      quantize_kernel<T, true><<<static_cast<unsigned>(rows), kQuantThreads, 0, st>>>(p, cols, ldx, q, scale);
+      quantize_kernel<T, Q, true><<<static_cast<unsigned>(rows), kQuantThreads, 0, st>>>(p, cols, ldx, q, scale, h);
     else
-      quantize_kernel<T, false><<<static_cast<unsigned>(rows), kQuantThreads, 0, st>>>(p, cols, ldx, q, scale);
+      quantize_kernel<T, Q, false><<<static_cast<unsigned>(rows), kQuantThreads, 0, st>>>(p, cols, ldx, q, scale, h);
     return cudaGetLastError();
   });
 }
 
-// ---------------------------------------------------------------- product
-struct Int8Shape {
-  int64_t M, N, K, ldo;
+// Tokens that are in 8 bits already, as fp16 for the tensor cores; zeroes `hdr`.
+__global__ void __launch_bounds__(256)
+    widen_kernel(const uint32_t* __restrict__ xq, int64_t words, uint2* __restrict__ x16, uint4* __restrict__ hdr) {
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(Int8Header) / 16); i += 256) hdr[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = i0; i < words; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const uint32_t w = xq[i];
+    int q[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) q[b] = static_cast<int8_t>(w >> (8 * b));
+    put4(reinterpret_cast<__half*>(x16 + i), q);
+  }
+}
+
+// ---------------------------------------------------------------- few tokens: dp4a
+// Up to 8 tokens: each warp streams rows of W through registers, 16 bytes a lane, against the
+// tokens' integers in shared memory; the sums are exact int32.  Bound by reading W.  Every block
+// brings the tokens to 8 bits for itself (they come from L2), so a call is one launch; W's first
+// rows are prefetched into L2 meanwhile.
+constexpr int kFewThreads = 512;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int64_t kFewTokens = 8;
+constexpr int64_t kFewSmem = 96 * 1024;  // two blocks to an SM
+
+// V values per lane, summed over the lanes: lane l gets the sum of value l * V / 32 (V < 32: of
+// the value whose 32 / V lanes it is one of).
+template <int V>
+__device__ __forceinline__ int reduce_over_lanes(int (&v)[V], int lane) {
+  static_assert(V <= 32 && (V & (V - 1)) == 0, "a power of two up to 32");
+  int n = V;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if (i < n) {
+          const int give = up ? v[i] : v[i + n];
+          const int keep = up ? v[i + n] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  return v[0];
+}
+
+struct FewParams {
+  const void* x;  // float types of x_type with rows ldx apart, or (x_scale given) int8 [M][K]
+  const float* x_scale;
+  int64_t ldx;
+  int x_type, vec;
+  const int8_t* wq;
+  const float* w_scale;
+  void* out;
+  int64_t ldo;
+  int out_type;
+  int M, N, K;
+  uint4* hdr;
 };
 
-constexpr int kTile = 64;  // outputs per block along M and along N
-constexpr int kTileK = 64;
-
-// 64 x 64 outputs per block of 256 threads, 4 x 4 per thread, by dp4a.
-template <class T>
-__global__ void __launch_bounds__(256)
-    int8_tile_kernel(const int8_t* __restrict__ xq, const float* __restrict__ xs, const int8_t* __restrict__ wq,
-                     const float* __restrict__ ws, const Int8Shape g, T* __restrict__ out) {
-  __shared__ int sx[kTile][kTileK / 4 + 1], sw[kTile][kTileK / 4 + 1];
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTile, m0 = static_cast<int64_t>(blockIdx.y) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  const int lr = threadIdx.x >> 2, lc = threadIdx.x & 3;  // row and 16-byte chunk this thread loads
-  for (int64_t k0 = 0; k0 < g.K; k0 += kTileK) {
-    const int64_t k = k0 + 16 * lc;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 a = m0 + lr < g.M && k < g.K ? *reinterpret_cast<const uint4*>(xq + (m0 + lr) * g.K + k) : zero;
-    const uint4 b = n0 + lr < g.N && k < g.K ? *reinterpret_cast<const uint4*>(wq + (n0 + lr) * g.K + k) : zero;
-    __syncthreads();
-    sx[lr][4 * lc] = a.x; sx[lr][4 * lc + 1] = a.y; sx[lr][4 * lc + 2] = a.z; sx[lr][4 * lc + 3] = a.w;
-    sw[lr][4 * lc] = b.x; sw[lr][4 * lc + 1] = b.y; sw[lr][4 * lc + 2] = b.z; sw[lr][4 * lc + 3] = b.w;
-    __syncthreads();
+// The tokens' integers into shared memory: kFewWarps / MT warps per token.
+template <int MT, class T>
+__device__ void few_quantize(const FewParams& p, int8_t* sq, float* ss, uint32_t* warp_max) {
+  constexpr int W = kFewWarps / MT, E = 16 / sizeof(T);
+  const int warp = threadIdx.x >> 5, m = warp / W;
+  const int at = threadIdx.x - m * W * 32;
+  const T* row = static_cast<const T*>(p.x) + static_cast<int64_t>(m) * p.ldx;
+  const bool live = m < p.M;
+  uint32_t amax = 0;
+  if (live && p.vec) {
+    for (int i = at; i < p.K / E; i += W * 32) {
+      float v[E];
+      unpack16<T>(reinterpret_cast<const uint4*>(row)[i], v);
 #pragma unroll
-    for (int c = 0; c < kTileK / 4; ++c) {
-      int av[4], bv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) av[i] = sx[ty * 4 + i][c];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bv[j] = sw[tx + 16 * j][c];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(av[i], bv[j], acc[i][j]);
+      for (int j = 0; j < E; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
     }
+  } else if (live) {
+    for (int i = at; i < p.K; i += W * 32) amax = max(amax, __float_as_uint(to_float(row[i])) & 0x7fffffffu);
   }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if ((threadIdx.x & 31) == 0) warp_max[warp] = amax;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
-    if (m >= g.M) continue;
-    const float s = xs[m];
+  for (int w = 0; w < W; ++w) amax = max(amax, warp_max[m * W + w]);
+  const float s = live ? row_scale(amax) : 0.f;
+  if (at == 0) ss[m] = s;
+  int8_t* out = sq + static_cast<int64_t>(m) * p.K;
+  if (live && p.vec) {
+    for (int i = at; i < p.K / E; i += W * 32) {
+      float v[E];
+      unpack16<T>(reinterpret_cast<const uint4*>(row)[i], v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + tx + 16 * j;
-      if (n < g.N) out[m * g.ldo + n] = from_float<T>(static_cast<float>(acc[i][j]) * s * ws[n]);
+      for (int j = 0; j < E / 4; ++j) {
+        int q[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) q[b] = quantize(v[4 * j + b], s);
+        put4(out + i * E + 4 * j, q);
+      }
+    }
+  } else {
+    for (int i = at; i < p.K; i += W * 32) out[i] = live ? static_cast<int8_t>(quantize(to_float(row[i]), s)) : 0;
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void few_store(const FewParams& p, int m, int n, float y) {
+  static_cast<T*>(p.out)[static_cast<int64_t>(m) * p.ldo + n] = from_float<T>(y);
+}
+
+// MT tokens (those past M are zero), R rows of W per warp at a time.
+template <int MT, int R>
+__global__ void __launch_bounds__(kFewThreads, MT * R <= 16 ? 2 : 1) few_tokens_kernel(const __grid_constant__ FewParams p) {
+  extern __shared__ __align__(16) int8_t sq[];  // [MT][K]
+  __shared__ float ss[MT];
+  __shared__ uint32_t warp_max[kFewWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = (p.N + R - 1) / R, step = static_cast<int>(gridDim.x) * kFewWarps;
+  const int g0 = static_cast<int>(blockIdx.x) * kFewWarps + warp;
+  if (g0 < groups) {
+    const int8_t* w = p.wq + static_cast<int64_t>(g0) * R * p.K;
+    const int bytes = min(R, p.N - g0 * R) * p.K;
+    for (int i = lane * 128; i < bytes; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + i));
+  }
+  if (blockIdx.x == 0 && threadIdx.x < 16) p.hdr[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  if (p.x_scale != nullptr) {
+    const uint4* src = static_cast<const uint4*>(p.x);
+    for (int i = threadIdx.x; i < MT * (p.K / 16); i += kFewThreads)
+      reinterpret_cast<uint4*>(sq)[i] = i < p.M * (p.K / 16) ? src[i] : make_uint4(0, 0, 0, 0);
+    if (threadIdx.x < MT) ss[threadIdx.x] = static_cast<int>(threadIdx.x) < p.M ? p.x_scale[threadIdx.x] : 0.f;
+  } else if (p.x_type == FKL_TYPE_F32) {
+    few_quantize<MT, float>(p, sq, ss, warp_max);
+  } else if (p.x_type == FKL_TYPE_BF16) {
+    few_quantize<MT, __nv_bfloat16>(p, sq, ss, warp_max);
+  } else {
+    few_quantize<MT, __half>(p, sq, ss, warp_max);
+  }
+  __syncthreads();
+
+  const int chunks = p.K / 16;
+  const uint4* xs = reinterpret_cast<const uint4*>(sq);
+  for (int g = g0; g < groups; g += step) {
+    const uint4* w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)  // rows past N read the last one; their sums are not stored
+      w[r] = reinterpret_cast<const uint4*>(p.wq + static_cast<int64_t>(min(g * R + r, p.N - 1)) * p.K);
+    int acc[MT * R] = {};
+#pragma unroll(R == 1 ? 6 : 2)
+    for (int c = lane; c < chunks; c += 32) {
+      uint4 wv[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) wv[r] = __ldcs(w[r] + c);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint4 xv = xs[m * chunks + c];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          int a = acc[m * R + r];
+          a = __dp4a(static_cast<int>(wv[r].x), static_cast<int>(xv.x), a);
+          a = __dp4a(static_cast<int>(wv[r].y), static_cast<int>(xv.y), a);
+          a = __dp4a(static_cast<int>(wv[r].z), static_cast<int>(xv.z), a);
+          acc[m * R + r] = __dp4a(static_cast<int>(wv[r].w), static_cast<int>(xv.w), a);
+        }
+      }
+    }
+    const int sum = reduce_over_lanes<MT * R>(acc, lane);
+    constexpr int kLanes = 32 / (MT * R);  // lanes that hold the same sum
+    const int i = lane / kLanes, m = i / R, n = g * R + i % R;
+    if (lane % kLanes == 0 && m < p.M && n < p.N) {
+      const float y = static_cast<float>(sum) * ss[m] * p.w_scale[n];
+      if (p.out_type == FKL_TYPE_F32)
+        few_store<float>(p, m, n, y);
+      else if (p.out_type == FKL_TYPE_BF16)
+        few_store<__nv_bfloat16>(p, m, n, y);
+      else
+        few_store<__half>(p, m, n, y);
     }
   }
 }
 
-static cudaError_t launch_product(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
-                                  const Int8Shape& g, int32_t type, void* out, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((g.N + kTile - 1) / kTile), static_cast<unsigned>((g.M + kTile - 1) / kTile));
-  return with_type(type, [&](auto t) {
-    using T = decltype(t);
-    int8_tile_kernel<T><<<grid, 256, 0, st>>>(xq, xs, wq, ws, g, static_cast<T*>(out));
-    return cudaGetLastError();
-  });
+template <int MT, int R>
+static cudaError_t launch_few_t(const FewParams& p, int sms, cudaStream_t st) {
+  static bool done[128];
+  const size_t smem = static_cast<size_t>(MT) * p.K;
+  const cudaError_t e = smem_limit_once(few_tokens_kernel<MT, R>, kFewSmem, done);
+  if (e != cudaSuccess) return e;
+  const int per_sm = MT * R <= 16 ? 2 : 1;
+  const int blocks = ((p.N + R - 1) / R + kFewWarps - 1) / kFewWarps;
+  few_tokens_kernel<MT, R><<<blocks < per_sm * sms ? blocks : per_sm * sms, kFewThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+// One row of W per warp at a time until the device is full, then 4: the loads of four rows share
+// each read of the tokens and keep four times as many bytes in flight per lane.
+template <int MT>
+static cudaError_t launch_few_m(const FewParams& p, int sms, cudaStream_t st) {
+  return p.N < 4 * kFewWarps * sms ? launch_few_t<MT, 1>(p, sms, st) : launch_few_t<MT, 4>(p, sms, st);
+}
+
+static int few_rounded(int64_t M) { return M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8; }
+
+static bool few_tokens(int64_t M, int64_t K) { return M <= kFewTokens && few_rounded(M) * K <= kFewSmem; }
+
+static cudaError_t launch_few(const FewParams& p, int sms, cudaStream_t st) {
+  switch (few_rounded(p.M)) {
+    case 1: return launch_few_m<1>(p, sms, st);
+    case 2: return launch_few_m<2>(p, sms, st);
+    case 4: return launch_few_m<4>(p, sms, st);
+    default: return launch_few_m<8>(p, sms, st);
+  }
 }
 
 // ---------------------------------------------------------------- host side
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Int8Plan {
-  size_t off_q, off_scale, total;
+  bool few;
+  Int8GemmPlan gemm;
+  size_t off_x16, off_scale, off_part, total;
 };
 
-static bool make_int8_plan(int64_t M, int64_t N, int64_t K, bool quantize, Int8Plan* p) {
+// The workspace for a device of `sms` SMs.
+static bool make_int8_plan(int64_t M, int64_t N, int64_t K, int sms, Int8Plan* p) {
   if (M < 0 || M > INT32_MAX || N < 1 || N > INT32_MAX || K < 16 || K % 16 != 0 || K > kMaxInt8K) return false;
-  size_t off = 256;  // status header
-  p->off_q = off;
-  if (quantize) off = up256(off + static_cast<size_t>(M) * K);
-  p->off_scale = off;
-  if (quantize) off = up256(off + static_cast<size_t>(M) * 4);
+  p->few = few_tokens(M, K);
+  size_t off = p->few ? 256 : up256(sizeof(Int8Header));  // few tokens: the status word's 256 bytes
+  p->off_x16 = p->off_scale = p->off_part = off;
+  if (!p->few) {
+    p->gemm = plan_int8_gemm(M, N, K, sms);
+    off = up256(off + static_cast<size_t>(M) * K * 2);
+    p->off_scale = off;
+    off = up256(off + static_cast<size_t>(M) * 4);
+    p->off_part = off;
+    off = up256(off + p->gemm.part_bytes);
+  }
   p->total = off;
   return true;
+}
+
+// Bytes for any device: the partial sums grow with the number of SMs.
+static size_t int8_workspace(int64_t M, int64_t N, int64_t K) {
+  Int8Plan p;
+  return make_int8_plan(M, N, K, 2 * kMaxPairs, &p) ? p.total : 0;
 }
 
 static fkl_status bad(fkl_status s, const char* msg) {
@@ -199,43 +384,81 @@ extern "C" fkl_status fkl_quantize_int8(const void* x, int32_t x_type, int64_t r
   if (rows == 0) return FKL_OK;
   const NamedPtr ptrs[] = {{x, "x"}, {q, "q"}, {scale, "scale"}};
   if (const int s = check_device_memory(ptrs); s != FKL_OK) return static_cast<fkl_status>(s);
-  if (launch_quantize(x, x_type, rows, cols, ldx, q, scale, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  if (launch_quantize(x, x_type, rows, cols, ldx, q, scale, nullptr, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return bad(FKL_ERR_CUDA, "quantisation launch failed");
   return FKL_OK;
 }
 
-extern "C" size_t fkl_int8_matmul_workspace_size(int64_t M, int64_t N, int64_t K) {
-  Int8Plan p;
-  return make_int8_plan(M, N, K, false, &p) ? p.total : 0;
-}
+extern "C" size_t fkl_int8_matmul_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_workspace(M, N, K); }
 
-extern "C" size_t fkl_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
-  Int8Plan p;
-  return make_int8_plan(M, N, K, true, &p) ? p.total : 0;
-}
+extern "C" size_t fkl_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K) { return int8_workspace(M, N, K); }
 
 namespace fkl {
 
-// Checks shared by the two products; `x` is the tokens (of x_align-byte alignment).
-static fkl_status check_product(bool quantize, const void* x, size_t x_align, const float* x_scale, const int8_t* wq,
-                                const float* w_scale, const Int8Shape& g, int32_t out_type, const void* out,
-                                const void* workspace, size_t ws_bytes, Int8Plan* pl, int* sms) {
+// Both products; x_type < 0: x is int8 [M][K] with the scales x_scale.
+static fkl_status int8_product(const char* x_name, const void* x, int32_t x_type, int64_t ldx, const float* x_scale,
+                               const int8_t* wq, const float* w_scale, const Int8Shape& g, int32_t out_type, void* out,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  const bool given = x_type < 0;
   if (!type_ok(out_type)) return bad(FKL_ERR_INVALID_ARG, "out_type must be one of FKL_TYPE_*");
-  if (!make_int8_plan(g.M, g.N, g.K, quantize, pl))
+  const size_t need = int8_workspace(g.M, g.N, g.K);
+  if (need == 0)
     return bad(FKL_ERR_INVALID_ARG, "unsupported shape (need K % 16 == 0, 16 <= K <= 131072, 0 <= M < 2^31, 1 <= N < 2^31)");
   if (g.ldo < g.N) return bad(FKL_ERR_INVALID_ARG, "ldo must be at least N");
   if (wq == nullptr || w_scale == nullptr ||
-      (g.M > 0 && (x == nullptr || out == nullptr || (!quantize && x_scale == nullptr))))
+      (g.M > 0 && (x == nullptr || out == nullptr || (given && x_scale == nullptr))))
     return bad(FKL_ERR_INVALID_ARG, "a required pointer is NULL");
-  if (misaligned(wq, 16) || misaligned(x, x_align) || misaligned(x_scale, 4) || misaligned(w_scale, 4) ||
-      misaligned(out, type_bytes(out_type)))
+  if (misaligned(wq, 16) || misaligned(x, given ? 16 : type_bytes(x_type)) || misaligned(x_scale, 4) ||
+      misaligned(w_scale, 4) || misaligned(out, type_bytes(out_type)))
     return bad(FKL_ERR_ALIGNMENT, "8-bit operands need 16-byte alignment, everything else its element's");
-  if (workspace == nullptr || ws_bytes < pl->total) return bad(FKL_ERR_WORKSPACE, "workspace missing or too small");
+  if (workspace == nullptr || ws_bytes < need) return bad(FKL_ERR_WORKSPACE, "workspace missing or too small");
   if (misaligned(workspace, 256)) return bad(FKL_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
-  if (const int s = require_device(sms); s != FKL_OK) return static_cast<fkl_status>(s);
-  const NamedPtr ptrs[] = {{x, quantize ? "x" : "xq"}, {x_scale, "x_scale"}, {wq, "wq"}, {w_scale, "w_scale"},
-                           {out, "out"}, {workspace, "workspace"}};
-  return static_cast<fkl_status>(check_device_memory(ptrs));
+  int sms = 0;
+  if (const int s = require_device(&sms); s != FKL_OK) return static_cast<fkl_status>(s);
+  const NamedPtr ptrs[] = {{x, x_name}, {x_scale, "x_scale"}, {wq, "wq"}, {w_scale, "w_scale"}, {out, "out"},
+                           {workspace, "workspace"}};
+  if (const int s = check_device_memory(ptrs); s != FKL_OK) return static_cast<fkl_status>(s);
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Int8Header* hdr = reinterpret_cast<Int8Header*>(ws);
+  if (g.M == 0)
+    return cudaMemsetAsync(ws, 0, 256, st) == cudaSuccess ? FKL_OK : bad(FKL_ERR_CUDA, "cudaMemsetAsync failed");
+  Int8Plan pl;
+  make_int8_plan(g.M, g.N, g.K, sms, &pl);
+  if (pl.few) {
+    FewParams p;
+    p.x = x;
+    p.x_scale = given ? x_scale : nullptr;
+    p.ldx = ldx;
+    p.x_type = x_type;
+    p.vec = !given && !misaligned(x, 16) && ldx * type_bytes(x_type) % 16 == 0;
+    p.wq = wq;
+    p.w_scale = w_scale;
+    p.out = out;
+    p.ldo = g.ldo;
+    p.out_type = out_type;
+    p.M = static_cast<int>(g.M);
+    p.N = static_cast<int>(g.N);
+    p.K = static_cast<int>(g.K);
+    p.hdr = reinterpret_cast<uint4*>(hdr);
+    return launch_few(p, sms, st) == cudaSuccess ? FKL_OK : bad(FKL_ERR_CUDA, "8-bit product launch failed");
+  }
+  __half* x16 = reinterpret_cast<__half*>(ws + pl.off_x16);
+  float* scale = reinterpret_cast<float*>(ws + pl.off_scale);
+  cudaError_t e;
+  if (given) {
+    const int64_t words = g.M * g.K / 4, blocks = (words + 255) / 256;
+    widen_kernel<<<static_cast<unsigned>(blocks < 16 * sms ? blocks : 16 * sms), 256, 0, st>>>(
+        static_cast<const uint32_t*>(x), words, reinterpret_cast<uint2*>(x16), reinterpret_cast<uint4*>(hdr));
+    e = cudaGetLastError();
+  } else {
+    e = launch_quantize(x, x_type, g.M, g.K, ldx, x16, scale, hdr, st);
+  }
+  if (e != cudaSuccess) return bad(FKL_ERR_CUDA, "launch of the tokens' kernel failed");
+  e = launch_int8_gemm(reinterpret_cast<const uint16_t*>(x16), given ? x_scale : scale, wq, w_scale, g, out_type, out,
+                       pl.gemm, reinterpret_cast<float*>(ws + pl.off_part), hdr, st);
+  return e == cudaSuccess ? FKL_OK : bad(FKL_ERR_CUDA, "8-bit product launch failed");
 }
 
 }  // namespace fkl
@@ -244,18 +467,8 @@ extern "C" fkl_status fkl_int8_matmul(const int8_t* xq, const float* x_scale, co
                                       int64_t M, int64_t N, int64_t K, int32_t out_type, void* out, int64_t ldo,
                                       void* workspace, size_t ws_bytes, void* stream) {
   set_last_error_message("");
-  const Int8Shape g{M, N, K, ldo};
-  Int8Plan pl;
-  int sms = 0;
-  const fkl_status s =
-      check_product(false, xq, 16, x_scale, wq, w_scale, g, out_type, out, workspace, ws_bytes, &pl, &sms);
-  if (s != FKL_OK) return s;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 256, st) != cudaSuccess) return bad(FKL_ERR_CUDA, "cudaMemsetAsync failed");
-  if (M == 0) return FKL_OK;
-  if (launch_product(xq, x_scale, wq, w_scale, g, out_type, out, st) != cudaSuccess)
-    return bad(FKL_ERR_CUDA, "8-bit product launch failed");
-  return FKL_OK;
+  return int8_product("xq", xq, -1, K, x_scale, wq, w_scale, Int8Shape{M, N, K, ldo}, out_type, out, workspace, ws_bytes,
+                      stream);
 }
 
 extern "C" fkl_status fkl_int8_linear(const void* x, int32_t x_type, int64_t ldx, const int8_t* wq,
@@ -264,21 +477,6 @@ extern "C" fkl_status fkl_int8_linear(const void* x, int32_t x_type, int64_t ldx
   set_last_error_message("");
   if (!type_ok(x_type)) return bad(FKL_ERR_INVALID_ARG, "x_type must be one of FKL_TYPE_*");
   if (ldx < K) return bad(FKL_ERR_INVALID_ARG, "ldx must be at least K");
-  const Int8Shape g{M, N, K, ldo};
-  Int8Plan pl;
-  int sms = 0;
-  const fkl_status s = check_product(true, x, type_bytes(x_type), nullptr, wq, w_scale, g, out_type, out, workspace,
-                                     ws_bytes, &pl, &sms);
-  if (s != FKL_OK) return s;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 256, st) != cudaSuccess) return bad(FKL_ERR_CUDA, "cudaMemsetAsync failed");
-  if (M == 0) return FKL_OK;
-  uint8_t* w8 = static_cast<uint8_t*>(workspace);
-  int8_t* xq = reinterpret_cast<int8_t*>(w8 + pl.off_q);
-  float* xs = reinterpret_cast<float*>(w8 + pl.off_scale);
-  if (launch_quantize(x, x_type, M, K, ldx, xq, xs, st) != cudaSuccess)
-    return bad(FKL_ERR_CUDA, "quantisation launch failed");
-  if (launch_product(xq, xs, wq, w_scale, g, out_type, out, st) != cudaSuccess)
-    return bad(FKL_ERR_CUDA, "8-bit product launch failed");
-  return FKL_OK;
+  return int8_product("x", x, x_type, ldx, nullptr, wq, w_scale, Int8Shape{M, N, K, ldo}, out_type, out, workspace,
+                      ws_bytes, stream);
 }

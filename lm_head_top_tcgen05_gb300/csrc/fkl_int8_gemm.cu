@@ -1,0 +1,466 @@
+// The 8-bit product on the tensor cores, for more tokens than the dp4a kernel takes.
+//
+//     y[m][n] = (sum_k q_mk w_nk) * s_m * t_n
+//
+// sm_103a's fast tensor formats do not include 8-bit integers, but fp16 holds every int8 value
+// exactly and the products of two (at most 2^14) add up exactly in fp32 up to 2^24.  So the
+// weights stay in 8 bits in HBM, where reading them is what a generation step costs, and are
+// turned into fp16 on the way to the tensor cores:
+//
+//   HBM --TMA--> shared memory (int8) --8 warps--> TMEM (fp16 A operand) --tcgen05.mma--> TMEM
+//
+// The weights are the A operand (256 rows of W per CTA pair, 128 per CTA), read from TMEM, so
+// their fp16 form costs no shared-memory traffic; the tokens, quantised to fp16 integers by a
+// kernel before, are the B operand in shared memory (up to 256 per tile, half per CTA).
+//
+// Roles per CTA (16 warps):
+//   warps 0..7   convert: 128 rows x 128 k of int8 to fp16 in a TMEM slot; warps 0..3 take the
+//                lower 64 k, warps 4..7 the upper (a warp reaches the 32 TMEM lanes of its
+//                number modulo 4);
+//   warps 8..11  epilogue: accumulator * s_m * t_n, rounded and stored; lane = row of W = n;
+//   warp 12      TMA producer of W, warp 13 of the tokens;
+//   warp 14      (even CTA) issues the MMAs.
+// The work, tiles of 256 rows x one tile of tokens in blocks of 128 k, is a line cut into equal
+// parts, one per pair, so that every SM reads the same share of W.  A tile that is cut has its
+// fp32 partial sums in the workspace; the last of its parts to finish (per 32 rows) adds them
+// in the order of the parts, so the result does not depend on which one that is.
+#include <algorithm>
+
+#include "fkl_gemm.cuh"
+#include "fkl_int8.h"
+#include "fkl_types.cuh"
+
+namespace fkl {
+
+constexpr int kI8Threads = 512;
+constexpr int kI8BK = 128;           // k per block
+constexpr int kI8Slots = 4;          // fp16 blocks of W in TMEM and of the tokens in shared memory
+constexpr int kI8WStages = 6;        // int8 blocks of W in shared memory
+constexpr uint32_t kI8WBytes = 128 * kI8BK;
+constexpr uint32_t kI8XBytes = 128 * kI8BK * 2;  // room of a token slot (half of 256 tokens)
+constexpr uint32_t kI8TmemA = 256;   // first TMEM column of the A slots; accumulators are below
+constexpr size_t kI8Smem = kI8WStages * kI8WBytes + kI8Slots * kI8XBytes + 1024 + 512;
+constexpr uint32_t kI8ConvertWarps = 8;
+
+struct I8Params {
+  int M, N, K;
+  int nt;        // tokens per tile, a multiple of 16 up to 256
+  int m_tiles, k_blocks;
+  int accs;      // accumulators: 2 for tiles of up to 128 tokens
+  long long total;  // blocks of the whole line
+  const float* x_scale;
+  const float* w_scale;
+  void* out;
+  int64_t ldo;
+  int out_type, paired;  // paired: two adjacent 16-bit outputs share an aligned word
+  float* part;   // [2 * pairs][nt][256]
+  int* arrived;  // [pairs][8]
+  uint32_t* status;
+  uint64_t limit_ns;
+};
+
+// This pair's part of the line, walked tile by tile.
+struct I8Seq {
+  long long at, end;
+  int tile, kb0, kb1;
+  __device__ I8Seq(const I8Params& p, int pair, int pairs) {
+    at = p.total * pair / pairs;
+    end = p.total * (pair + 1) / pairs;
+    set(p);
+  }
+  __device__ __forceinline__ void set(const I8Params& p) {
+    tile = static_cast<int>(at / p.k_blocks);
+    kb0 = static_cast<int>(at - static_cast<long long>(tile) * p.k_blocks);
+    kb1 = static_cast<int>(min(static_cast<long long>(p.k_blocks), kb0 + (end - at)));
+  }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ void next(const I8Params& p) {
+    at += kb1 - kb0;
+    if (at < end) set(p);
+  }
+};
+
+struct I8Ctx {
+  uint32_t rank;
+  bool even;
+  int pair, pairs;
+  uint32_t w0, x0;                          // shared-memory rings
+  uint32_t wfull0, wempty0, xfull0, afull0, empty0, tfull0, tempty0, drain;
+  uint32_t tmem;
+  WaitCtl ctl;
+};
+
+// Four int8 values as two pairs of fp16: with the sign bit flipped a byte u = v + 128 is the
+// low byte of the fp16 number 1024 + u.
+__device__ __forceinline__ void int8x4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ void i8_w_producer(const CUtensorMap* tm, const I8Params& p, const I8Ctx& c) {
+  int stage = 0;
+  uint32_t phase = 0, issued = 0, issued_par = 0;
+  bool ok = true;
+  for (I8Seq q(p, c.pair, c.pairs); ok && q.more(); q.next(p)) {
+    const int row = (q.tile / p.m_tiles) * 256 + static_cast<int>(c.rank) * 128;
+    for (int kb = q.kb0; kb < q.kb1; ++kb) {
+      if (!mbar_wait(c.wempty0 + 8 * stage, phase ^ 1u, c.ctl)) { ok = false; break; }
+      mbar_arrive_expect_tx(c.wfull0 + 8 * stage, kI8WBytes);
+      tma_load_2d(c.w0 + stage * kI8WBytes, tm, c.wfull0 + 8 * stage, kb * kI8BK, row);
+      issued |= 1u << stage;
+      issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+      if (++stage == kI8WStages) { stage = 0; phase ^= 1u; }
+    }
+  }
+  for (int s = 0; s < kI8WStages; ++s)
+    if ((issued >> s) & 1u) mbar_wait_drain(c.wfull0 + 8 * s, (issued_par >> s) & 1u, p.limit_ns);
+}
+
+__device__ void i8_x_producer(const CUtensorMap* tm, const I8Params& p, const I8Ctx& c) {
+  int slot = 0;
+  uint32_t phase = 0, issued = 0, issued_par = 0;
+  bool ok = true;
+  const uint32_t even_full = map_to_rank(c.xfull0, 0);
+  const uint32_t half_bytes = static_cast<uint32_t>(p.nt / 2) * 128;  // 64 k of this CTA's tokens
+  for (I8Seq q(p, c.pair, c.pairs); ok && q.more(); q.next(p)) {
+    const int row = (q.tile % p.m_tiles) * p.nt + static_cast<int>(c.rank) * (p.nt / 2);
+    for (int kb = q.kb0; kb < q.kb1; ++kb) {
+      if (!mbar_wait_cluster(c.empty0 + 8 * slot, phase ^ 1u, c.ctl)) { ok = false; break; }
+      if (c.even) mbar_arrive_expect_tx(c.xfull0 + 8 * slot, 4 * half_bytes);
+      const uint32_t to = c.x0 + slot * kI8XBytes;
+      tma_load_2d_pair(to, tm, even_full + 8 * slot, kb * kI8BK, row);
+      tma_load_2d_pair(to + half_bytes, tm, even_full + 8 * slot, kb * kI8BK + 64, row);
+      issued |= 1u << slot;
+      issued_par = (issued_par & ~(1u << slot)) | (phase << slot);
+      if (++slot == kI8Slots) { slot = 0; phase ^= 1u; }
+    }
+  }
+  if (c.even)  // the even CTA's phases count the copies of both
+    for (int s = 0; s < kI8Slots; ++s)
+      if ((issued >> s) & 1u) mbar_wait_drain(c.xfull0 + 8 * s, (issued_par >> s) & 1u, p.limit_ns);
+}
+
+// Convert warps: lane = row of W.  A row's 128 bytes lie in 16-byte pieces permuted by the
+// TMA's swizzle (piece j of row r at j ^ (r & 7)), which spreads a warp's reads over all banks.
+__device__ void i8_convert(const I8Params& p, const I8Ctx& c, int warp, int lane) {
+  const int row = (warp & 3) * 32 + lane;
+  const int upper = warp >> 2;  // which 64 of the block's 128 k
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t even_afull = map_to_rank(c.afull0, 0);
+  int stage = 0, slot = 0;
+  uint32_t wphase = 0, phase = 0;
+  for (I8Seq q(p, c.pair, c.pairs); q.more(); q.next(p)) {
+    for (int kb = q.kb0; kb < q.kb1; ++kb) {
+      if (!__all_sync(0xffffffffu, mbar_wait(c.wfull0 + 8 * stage, wphase, c.ctl))) return;
+      const uint32_t base = c.w0 + stage * kI8WBytes + static_cast<uint32_t>(row) * 128;
+      uint32_t h[32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 v = ld_shared_v4(base + static_cast<uint32_t>(((upper * 4 + j) ^ (row & 7)) * 16));
+        int8x4_to_half(v.x, h[8 * j + 0], h[8 * j + 1]);
+        int8x4_to_half(v.y, h[8 * j + 2], h[8 * j + 3]);
+        int8x4_to_half(v.z, h[8 * j + 4], h[8 * j + 5]);
+        int8x4_to_half(v.w, h[8 * j + 6], h[8 * j + 7]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.wempty0 + 8 * stage);
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(c.empty0 + 8 * slot, phase ^ 1u, c.ctl))) return;
+      tc_fence_after();
+      tmem_st32(c.tmem + lanes + kI8TmemA + static_cast<uint32_t>(slot * 64 + upper * 32), h);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_release_cluster(even_afull + 8 * slot);
+      if (++stage == kI8WStages) { stage = 0; wphase ^= 1u; }
+      if (++slot == kI8Slots) { slot = 0; phase ^= 1u; }
+    }
+  }
+}
+
+__device__ void i8_mma(const I8Params& p, const I8Ctx& c) {
+  const uint32_t idesc = instr_desc_f16(256, p.nt);
+  const uint64_t half_step = (static_cast<uint64_t>(p.nt / 2) * 128) >> 4;
+  int slot = 0, acc = 0;
+  uint32_t phase = 0, acc_phase = 0;
+  bool ok = true;
+  for (I8Seq q(p, c.pair, c.pairs); ok && q.more(); q.next(p)) {
+    if (!mbar_wait_cluster(c.tempty0 + 8 * acc, acc_phase ^ 1u, c.ctl)) { ok = false; break; }
+    tc_fence_after();
+    const uint32_t d = c.tmem + static_cast<uint32_t>(acc * 128);
+    for (int kb = q.kb0; kb < q.kb1; ++kb) {
+      if (!mbar_wait_cluster(c.xfull0 + 8 * slot, phase, c.ctl) ||
+          !mbar_wait_acquire_cluster(c.afull0 + 8 * slot, phase, c.ctl)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t b0 = smem_desc_sw128(c.x0 + slot * kI8XBytes, 16, 1024);
+      const uint32_t a0 = c.tmem + kI8TmemA + static_cast<uint32_t>(slot * 64);
+      const int slices = min(kI8BK, p.K - kb * kI8BK) / 16;
+      for (int k = 0; k < slices; ++k)
+        tc_mma_f16_pair_ta(d, a0 + static_cast<uint32_t>(8 * k), b0 + (k >> 2) * half_step + (k & 3) * 2, idesc,
+                           (kb != q.kb0 || k != 0) ? 1u : 0u);
+      tc_commit_pair_mc(c.empty0 + 8 * slot, 0x3);
+      if (++slot == kI8Slots) { slot = 0; phase ^= 1u; }
+    }
+    if (!ok) break;
+    tc_commit_pair_mc(c.tfull0 + 8 * acc, 0x3);
+    if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
+  }
+  tc_commit_pair(c.drain);
+  mbar_wait_drain(c.drain, 0u, p.limit_ns);
+}
+
+// 32 tokens from m0 on of this lane's column n: scaled, rounded and stored.
+template <class T>
+__device__ __forceinline__ void i8_store(const I8Params& p, const float (&v)[32], int m0, int m_end, int n, float ws,
+                                         int lane) {
+  T* out = static_cast<T*>(p.out);
+  if constexpr (sizeof(T) == 2) {
+    if (p.paired) {
+      // lanes 2i and 2i + 1 hold two adjacent columns: the even lane stores both of one token,
+      // the odd lane both of the next
+      const bool odd = lane & 1;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const int m = m0 + j;
+        if (m >= m_end) break;
+        const float s0 = p.x_scale[m], s1 = m + 1 < m_end ? p.x_scale[m + 1] : 0.f;
+        const float a = v[j] * s0 * ws, b = v[j + 1] * s1 * ws;
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+        const T lo = from_float<T>(odd ? other : a), hi = from_float<T>(odd ? b : other);
+        const int mm = m + (odd ? 1 : 0), nn = n & ~1;
+        if (mm >= m_end || nn >= p.N) continue;
+        T* o = out + static_cast<int64_t>(mm) * p.ldo + nn;
+        if (nn + 1 < p.N) {
+          uint32_t w;
+          reinterpret_cast<T*>(&w)[0] = lo;
+          reinterpret_cast<T*>(&w)[1] = hi;
+          *reinterpret_cast<uint32_t*>(o) = w;
+        } else {
+          o[0] = lo;
+        }
+      }
+      return;
+    }
+  }
+  if (n >= p.N) return;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (m0 + j >= m_end) break;
+    out[static_cast<int64_t>(m0 + j) * p.ldo + n] = from_float<T>(v[j] * p.x_scale[m0 + j] * ws);
+  }
+}
+
+__device__ __forceinline__ void i8_store_any(const I8Params& p, const float (&v)[32], int m0, int m_end, int n, float ws,
+                                             int lane) {
+  if (p.out_type == FKL_TYPE_F32)
+    i8_store<float>(p, v, m0, m_end, n, ws, lane);
+  else if (p.out_type == FKL_TYPE_BF16)
+    i8_store<__nv_bfloat16>(p, v, m0, m_end, n, ws, lane);
+  else
+    i8_store<__half>(p, v, m0, m_end, n, ws, lane);
+}
+
+// The pair whose part of the line holds block x.
+__device__ __forceinline__ int i8_owner(const I8Params& p, long long x, int pairs) {
+  return static_cast<int>(((x + 1) * pairs - 1) / p.total);
+}
+
+__device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lane) {
+  const int strip = warp & 3;
+  const int row = static_cast<int>(c.rank) * 128 + strip * 32 + lane;  // of the pair's 256
+  const uint32_t lanes = static_cast<uint32_t>(strip * 32) << 16;
+  const uint32_t even_tempty = map_to_rank(c.tempty0, 0);
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  for (I8Seq q(p, c.pair, c.pairs); q.more(); q.next(p)) {
+    const int n = (q.tile / p.m_tiles) * 256 + row;
+    const int m0 = (q.tile % p.m_tiles) * p.nt;
+    const int m_end = min(p.M, m0 + p.nt);
+    const float ws = n < p.N ? p.w_scale[n] : 0.f;
+    const bool whole = q.kb0 == 0 && q.kb1 == p.k_blocks;
+    float* part = p.part + static_cast<size_t>(2 * c.pair + (q.kb0 == 0 ? 1 : 0)) * p.nt * 256 + row;
+    if (!__all_sync(0xffffffffu, mbar_wait_cluster(c.tfull0 + 8 * acc, acc_phase, c.ctl))) return;
+    tc_fence_after();
+    const uint32_t t = c.tmem + lanes + static_cast<uint32_t>(acc * 128);
+#pragma unroll 1
+    for (int col = 0; m0 + col < m_end; col += 32) {
+      float v[32];
+      tmem_ld32(t + col, v);
+      tmem_ld_wait(v);
+      if (whole) {
+        i8_store_any(p, v, m0 + col, m_end, n, ws, lane);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (m0 + col + j < m_end) part[static_cast<size_t>(col + j) * 256] = v[j];
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_release_cluster(even_tempty + 8 * acc);
+    if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
+    if (whole) continue;
+    // a cut tile: the last part to arrive adds them all up, in their order
+    const long long first = static_cast<long long>(q.tile) * p.k_blocks;
+    const int p0 = i8_owner(p, first, c.pairs), p1 = i8_owner(p, first + p.k_blocks - 1, c.pairs);
+    __threadfence();
+    __syncwarp();
+    int before = 0;
+    if (lane == 0) before = atomicAdd(p.arrived + p0 * 8 + static_cast<int>(c.rank) * 4 + strip, 1);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (before != p1 - p0) continue;
+    __threadfence();
+#pragma unroll 1
+    for (int col = 0; m0 + col < m_end; col += 32) {
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      for (int r = p0; r <= p1; ++r) {
+        // the tile's first part is the last of its pair, the others the first of theirs
+        const float* src = p.part + static_cast<size_t>(2 * r + (r == p0 ? 1 : 0)) * p.nt * 256 + row;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (m0 + col + j < m_end) v[j] += __ldcg(src + static_cast<size_t>(col + j) * 256);
+      }
+      i8_store_any(p, v, m0 + col, m_end, n, ws, lane);
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                     const __grid_constant__ I8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kI8WStages * kI8WBytes + kI8Slots * kI8XBytes);
+  constexpr int kBars = 2 * kI8WStages + 3 * kI8Slots + 5;
+  static_assert(kBars * 8 + 8 <= 512, "barriers and words fit in their 512 bytes");
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // [0] TMEM base, [1] abort
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  I8Ctx c;
+  c.rank = cluster_ctarank();
+  c.even = c.rank == 0;
+  c.pair = static_cast<int>(blockIdx.x >> 1);
+  c.pairs = static_cast<int>(gridDim.x >> 1);
+  c.w0 = smem_addr(smem);
+  c.x0 = c.w0 + kI8WStages * kI8WBytes;
+  c.wfull0 = smem_addr(bars);
+  c.wempty0 = c.wfull0 + 8 * kI8WStages;
+  c.xfull0 = c.wempty0 + 8 * kI8WStages;
+  c.afull0 = c.xfull0 + 8 * kI8Slots;
+  c.empty0 = c.afull0 + 8 * kI8Slots;
+  c.tfull0 = c.empty0 + 8 * kI8Slots;
+  c.tempty0 = c.tfull0 + 16;
+  c.drain = c.tempty0 + 16;
+  c.ctl = WaitCtl{reinterpret_cast<volatile uint32_t*>(&misc[1]), p.status, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kI8WStages; ++s) {
+      mbar_init(c.wfull0 + 8 * s, 1);
+      mbar_init(c.wempty0 + 8 * s, kI8ConvertWarps);
+    }
+    for (int s = 0; s < kI8Slots; ++s) {
+      mbar_init(c.xfull0 + 8 * s, 1);
+      mbar_init(c.afull0 + 8 * s, 2 * kI8ConvertWarps);
+      mbar_init(c.empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(c.tfull0 + 8 * b, 1);
+      mbar_init(c.tempty0 + 8 * b, 2 * 4);
+    }
+    mbar_init(c.drain, 1);
+    misc[1] = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 12 && lane == 0) tma_prefetch_desc(&tmW);
+  if (warp == 13 && lane == 0) tma_prefetch_desc(&tmX);
+  if (warp == 14) {
+    tmem_alloc_pair(smem_addr(&misc[0]), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  c.tmem = misc[0];
+
+  if (warp < 8) {
+    i8_convert(p, c, warp, lane);
+  } else if (warp < 12) {
+    i8_epilogue(p, c, warp, lane);
+  } else if (lane == 0) {
+    if (warp == 12) i8_w_producer(&tmW, p, c);
+    if (warp == 13) i8_x_producer(&tmX, p, c);
+    if (warp == 14 && c.even) i8_mma(p, c);
+  }
+
+  __syncwarp();
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 14) tmem_dealloc_pair(c.tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- host side
+Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
+  Int8GemmPlan g;
+  g.m_tiles = static_cast<int>((M + 255) / 256);
+  const int64_t even = (M + g.m_tiles - 1) / g.m_tiles;
+  g.nt = static_cast<int>((even + 15) / 16 * 16);
+  g.k_blocks = static_cast<int>((K + kI8BK - 1) / kI8BK);
+  g.total = (N + 255) / 256 * g.m_tiles * g.k_blocks;
+  g.pairs = static_cast<int>(std::min<int64_t>(std::min(sms / 2, kMaxPairs), g.total));
+  g.part_bytes = static_cast<size_t>(2 * g.pairs) * g.nt * 256 * 4;
+  return g;
+}
+
+cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const int8_t* wq, const float* w_scale,
+                             const Int8Shape& s, int32_t out_type, void* out, const Int8GemmPlan& g, float* part,
+                             Int8Header* hdr, cudaStream_t st) {
+  CUtensorMap mw, mx;
+  if (!encode_map_bytes(&mw, wq, s.K, s.N, s.K, kI8BK, 128) ||
+      !encode_map_f16(&mx, x16, s.K, s.M, s.K * 2, 64, static_cast<uint32_t>(g.nt / 2)))
+    return cudaErrorInvalidValue;
+  I8Params p;
+  p.M = static_cast<int>(s.M);
+  p.N = static_cast<int>(s.N);
+  p.K = static_cast<int>(s.K);
+  p.nt = g.nt;
+  p.m_tiles = g.m_tiles;
+  p.k_blocks = g.k_blocks;
+  p.accs = g.nt <= 128 ? 2 : 1;
+  p.total = g.total;
+  p.x_scale = x_scale;
+  p.w_scale = w_scale;
+  p.out = out;
+  p.ldo = s.ldo;
+  p.out_type = out_type;
+  p.paired = reinterpret_cast<uintptr_t>(out) % 4 == 0 && s.ldo % 2 == 0;
+  p.part = part;
+  p.arrived = hdr->arrived;
+  p.status = &hdr->status;
+  p.limit_ns = kWaitLimitNs;
+  static bool done[128];
+  const cudaError_t e = smem_limit_once(int8_gemm_kernel, kI8Smem, done);
+  if (e != cudaSuccess) return e;
+  int8_gemm_kernel<<<2 * g.pairs, kI8Threads, kI8Smem, st>>>(mw, mx, p);
+  return cudaGetLastError();
+}
+
+}  // namespace fkl
