@@ -109,10 +109,13 @@ static cudaError_t launch_quantize(const void* x, int32_t type, int64_t rows, in
   });
 }
 
-// Tokens that are in 8 bits already, as fp16 for the tensor cores; zeroes `hdr`.
+// Tokens that are in 8 bits already, as fp16 for the tensor cores, and an aligned copy of their
+// scales; zeroes `hdr`.
 __global__ void __launch_bounds__(256)
-    widen_kernel(const uint32_t* __restrict__ xq, int64_t words, uint2* __restrict__ x16, uint4* __restrict__ hdr) {
+    widen_kernel(const uint32_t* __restrict__ xq, int64_t words, uint2* __restrict__ x16,
+                 const float* __restrict__ x_scale, int M, float* __restrict__ scale, uint4* __restrict__ hdr) {
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t i = i0; i < M; i += static_cast<int64_t>(gridDim.x) * 256) scale[i] = x_scale[i];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < static_cast<int>(sizeof(Int8Header) / 16); i += 256) hdr[i] = make_uint4(0, 0, 0, 0);
   for (int64_t i = i0; i < words; i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -450,13 +453,14 @@ static fkl_status int8_product(const char* x_name, const void* x, int32_t x_type
   if (given) {
     const int64_t words = g.M * g.K / 4, blocks = (words + 255) / 256;
     widen_kernel<<<static_cast<unsigned>(blocks < 16 * sms ? blocks : 16 * sms), 256, 0, st>>>(
-        static_cast<const uint32_t*>(x), words, reinterpret_cast<uint2*>(x16), reinterpret_cast<uint4*>(hdr));
+        static_cast<const uint32_t*>(x), words, reinterpret_cast<uint2*>(x16), x_scale, static_cast<int>(g.M), scale,
+        reinterpret_cast<uint4*>(hdr));
     e = cudaGetLastError();
   } else {
     e = launch_quantize(x, x_type, g.M, g.K, ldx, x16, scale, hdr, st);
   }
   if (e != cudaSuccess) return bad(FKL_ERR_CUDA, "launch of the tokens' kernel failed");
-  e = launch_int8_gemm(reinterpret_cast<const uint16_t*>(x16), given ? x_scale : scale, wq, w_scale, g, out_type, out,
+  e = launch_int8_gemm(reinterpret_cast<const uint16_t*>(x16), scale, wq, w_scale, g, out_type, out,
                        pl.gemm, reinterpret_cast<float*>(ws + pl.off_part), hdr, st);
   return e == cudaSuccess ? FKL_OK : bad(FKL_ERR_CUDA, "8-bit product launch failed");
 }

@@ -15,7 +15,7 @@ constexpr int kMaxPairs = 128;  // most CTA pairs of a launch
 struct Int8Header {
   uint32_t status;
   uint32_t pad[63];
-  int arrived[kMaxPairs * 8];  // parts of a cut tile that are done, per 32 of its rows
+  int arrived[kMaxPairs * 16];  // parts of a cut tile that are done, per epilogue warp
 };
 
 // How the tensor-core product is cut: tiles of 256 channels x nt tokens, blocks of 128 k.
@@ -25,7 +25,8 @@ struct Int8GemmPlan {
   size_t part_bytes;  // partial sums of the tiles that are cut
 };
 Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms);
-// x16: the tokens' integers as fp16 [M][K]; hdr zeroed before on the stream.
+// x16: the tokens' integers as fp16 [M][K]; x_scale: 16-byte aligned; hdr zeroed before on the
+// stream.
 cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const int8_t* wq, const float* w_scale,
                              const Int8Shape& s, int32_t out_type, void* out, const Int8GemmPlan& g, float* part,
                              Int8Header* hdr, cudaStream_t st);

@@ -13,16 +13,18 @@
 // their fp16 form costs no shared-memory traffic; the tokens, quantised to fp16 integers by a
 // kernel before, are the B operand in shared memory (up to 256 per tile, half per CTA).
 //
-// Roles per CTA (16 warps):
+// Roles per CTA (20 warps):
 //   warps 0..7   convert: 128 rows x 128 k of int8 to fp16 in a TMEM slot; warps 0..3 take the
 //                lower 64 k, warps 4..7 the upper (a warp reaches the 32 TMEM lanes of its
 //                number modulo 4);
-//   warps 8..11  epilogue: accumulator * s_m * t_n, rounded and stored; lane = row of W = n;
-//   warp 12      TMA producer of W, warp 13 of the tokens;
-//   warp 14      (even CTA) issues the MMAs.
+//   warps 8..15  epilogue: accumulator * s_m * t_n, rounded and stored; lane = row of W = n,
+//                warps 8..11 and 12..15 take alternate groups of 32 tokens;
+//   warp 16      TMA producer of W, warp 17 of the tokens;
+//   warp 18      (even CTA) issues the MMAs.
 // The work, tiles of 256 rows x one tile of tokens in blocks of 128 k, is a line cut into equal
 // parts, one per pair, so that every SM reads the same share of W.  A tile that is cut has its
-// fp32 partial sums in the workspace; the last of its parts to finish (per 32 rows) adds them
+// fp32 partial sums in the workspace; the last of its parts to finish (per warp of the
+// epilogue) adds them
 // in the order of the parts, so the result does not depend on which one that is.
 #include <algorithm>
 
@@ -32,21 +34,22 @@
 
 namespace fkl {
 
-constexpr int kI8Threads = 512;
-constexpr int kI8BK = 128;           // k per block
-constexpr int kI8Slots = 4;          // fp16 blocks of W in TMEM and of the tokens in shared memory
-constexpr int kI8WStages = 6;        // int8 blocks of W in shared memory
+constexpr int kI8Threads = 640;
+constexpr int kI8BK = 128;  // k per block
 constexpr uint32_t kI8WBytes = 128 * kI8BK;
-constexpr uint32_t kI8XBytes = 128 * kI8BK * 2;  // room of a token slot (half of 256 tokens)
-constexpr uint32_t kI8TmemA = 256;   // first TMEM column of the A slots; accumulators are below
-constexpr size_t kI8Smem = kI8WStages * kI8WBytes + kI8Slots * kI8XBytes + 1024 + 512;
-constexpr uint32_t kI8ConvertWarps = 8;
+constexpr int kI8MaxSlots = 7, kI8MaxStages = 10;
+constexpr uint32_t kI8Ring = 224 * 1024;  // shared memory of both rings
+constexpr size_t kI8Smem = kI8Ring + 1024 + 512;
+constexpr uint32_t kI8ConvertWarps = 8, kI8EpiWarps = 8;
 
 struct I8Params {
   int M, N, K;
   int nt;        // tokens per tile, a multiple of 16 up to 256
   int m_tiles, k_blocks;
-  int accs;      // accumulators: 2 for tiles of up to 128 tokens
+  // TMEM: accs accumulators acc_cols columns apart (2 for tiles of up to 128 tokens, so that a
+  // tile's epilogue runs beside the next tile's MMAs), then slots of 64 columns for W's fp16
+  // blocks, with as many token blocks in shared memory; the rest of that holds int8 blocks of W.
+  int accs, acc_cols, slots, w_stages;
   long long total;  // blocks of the whole line
   const float* x_scale;
   const float* w_scale;
@@ -54,7 +57,7 @@ struct I8Params {
   int64_t ldo;
   int out_type, paired;  // paired: two adjacent 16-bit outputs share an aligned word
   float* part;   // [2 * pairs][nt][256]
-  int* arrived;  // [pairs][8]
+  int* arrived;  // [pairs][16]
   uint32_t* status;
   uint64_t limit_ns;
 };
@@ -84,7 +87,8 @@ struct I8Ctx {
   uint32_t rank;
   bool even;
   int pair, pairs;
-  uint32_t w0, x0;                          // shared-memory rings
+  uint32_t w0, x0, x_bytes;  // shared-memory rings; bytes of a token block (this CTA's half)
+  uint32_t tmem_a;           // first column of the A slots
   uint32_t wfull0, wempty0, xfull0, afull0, empty0, tfull0, tempty0, drain;
   uint32_t tmem;
   WaitCtl ctl;
@@ -120,10 +124,10 @@ __device__ void i8_w_producer(const CUtensorMap* tm, const I8Params& p, const I8
       tma_load_2d(c.w0 + stage * kI8WBytes, tm, c.wfull0 + 8 * stage, kb * kI8BK, row);
       issued |= 1u << stage;
       issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-      if (++stage == kI8WStages) { stage = 0; phase ^= 1u; }
+      if (++stage == p.w_stages) { stage = 0; phase ^= 1u; }
     }
   }
-  for (int s = 0; s < kI8WStages; ++s)
+  for (int s = 0; s < p.w_stages; ++s)
     if ((issued >> s) & 1u) mbar_wait_drain(c.wfull0 + 8 * s, (issued_par >> s) & 1u, p.limit_ns);
 }
 
@@ -138,16 +142,16 @@ __device__ void i8_x_producer(const CUtensorMap* tm, const I8Params& p, const I8
     for (int kb = q.kb0; kb < q.kb1; ++kb) {
       if (!mbar_wait_cluster(c.empty0 + 8 * slot, phase ^ 1u, c.ctl)) { ok = false; break; }
       if (c.even) mbar_arrive_expect_tx(c.xfull0 + 8 * slot, 4 * half_bytes);
-      const uint32_t to = c.x0 + slot * kI8XBytes;
+      const uint32_t to = c.x0 + slot * c.x_bytes;
       tma_load_2d_pair(to, tm, even_full + 8 * slot, kb * kI8BK, row);
       tma_load_2d_pair(to + half_bytes, tm, even_full + 8 * slot, kb * kI8BK + 64, row);
       issued |= 1u << slot;
       issued_par = (issued_par & ~(1u << slot)) | (phase << slot);
-      if (++slot == kI8Slots) { slot = 0; phase ^= 1u; }
+      if (++slot == p.slots) { slot = 0; phase ^= 1u; }
     }
   }
   if (c.even)  // the even CTA's phases count the copies of both
-    for (int s = 0; s < kI8Slots; ++s)
+    for (int s = 0; s < p.slots; ++s)
       if ((issued >> s) & 1u) mbar_wait_drain(c.xfull0 + 8 * s, (issued_par >> s) & 1u, p.limit_ns);
 }
 
@@ -177,90 +181,112 @@ __device__ void i8_convert(const I8Params& p, const I8Ctx& c, int warp, int lane
       if (lane == 0) mbar_arrive(c.wempty0 + 8 * stage);
       if (!__all_sync(0xffffffffu, mbar_wait_cluster(c.empty0 + 8 * slot, phase ^ 1u, c.ctl))) return;
       tc_fence_after();
-      tmem_st32(c.tmem + lanes + kI8TmemA + static_cast<uint32_t>(slot * 64 + upper * 32), h);
+      tmem_st32(c.tmem_a + lanes + static_cast<uint32_t>(slot * 64 + upper * 32), h);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_release_cluster(even_afull + 8 * slot);
-      if (++stage == kI8WStages) { stage = 0; wphase ^= 1u; }
-      if (++slot == kI8Slots) { slot = 0; phase ^= 1u; }
+      if (lane == 0) mbar_arrive_cluster(even_afull + 8 * slot);
+      if (++stage == p.w_stages) { stage = 0; wphase ^= 1u; }
+      if (++slot == p.slots) { slot = 0; phase ^= 1u; }
     }
   }
 }
 
+// One thread issues, but the whole warp walks the loop: its operands are then the same for the
+// warp as the compiler sees it and stay in uniform registers.  (With the loop inside the one
+// thread's branch each MMA took about 50 cycles to issue, more than a tile of few tokens takes
+// to execute.)
 __device__ void i8_mma(const I8Params& p, const I8Ctx& c) {
   const uint32_t idesc = instr_desc_f16(256, p.nt);
-  const uint64_t half_step = (static_cast<uint64_t>(p.nt / 2) * 128) >> 4;
+  const uint32_t half_step = (static_cast<uint32_t>(p.nt / 2) * 128) >> 4;
+  const uint64_t b_desc0 = smem_desc_sw128(c.x0, 16, 1024);
+  const bool issuer = elect_one();
   int slot = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
   bool ok = true;
   for (I8Seq q(p, c.pair, c.pairs); ok && q.more(); q.next(p)) {
     if (!mbar_wait_cluster(c.tempty0 + 8 * acc, acc_phase ^ 1u, c.ctl)) { ok = false; break; }
     tc_fence_after();
-    const uint32_t d = c.tmem + static_cast<uint32_t>(acc * 128);
+    const uint32_t d = c.tmem + static_cast<uint32_t>(acc * p.acc_cols);
     for (int kb = q.kb0; kb < q.kb1; ++kb) {
       if (!mbar_wait_cluster(c.xfull0 + 8 * slot, phase, c.ctl) ||
-          !mbar_wait_acquire_cluster(c.afull0 + 8 * slot, phase, c.ctl)) {
+          !mbar_wait_cluster(c.afull0 + 8 * slot, phase, c.ctl)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint64_t b0 = smem_desc_sw128(c.x0 + slot * kI8XBytes, 16, 1024);
-      const uint32_t a0 = c.tmem + kI8TmemA + static_cast<uint32_t>(slot * 64);
+      const uint64_t b0 = b_desc0 + ((static_cast<uint32_t>(slot) * c.x_bytes) >> 4);
+      const uint32_t a0 = c.tmem_a + static_cast<uint32_t>(slot * 64);
       const int slices = min(kI8BK, p.K - kb * kI8BK) / 16;
-      for (int k = 0; k < slices; ++k)
-        tc_mma_f16_pair_ta(d, a0 + static_cast<uint32_t>(8 * k), b0 + (k >> 2) * half_step + (k & 3) * 2, idesc,
-                           (kb != q.kb0 || k != 0) ? 1u : 0u);
-      tc_commit_pair_mc(c.empty0 + 8 * slot, 0x3);
-      if (++slot == kI8Slots) { slot = 0; phase ^= 1u; }
+      if (issuer) {
+        if (slices == 8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_f16_pair_ta(d, a0 + static_cast<uint32_t>(8 * k), b0 + ((k >> 2) * half_step + (k & 3) * 2), idesc,
+                               (kb != q.kb0 || k != 0) ? 1u : 0u);
+        } else {
+          for (int k = 0; k < slices; ++k)
+            tc_mma_f16_pair_ta(d, a0 + static_cast<uint32_t>(8 * k), b0 + ((k >> 2) * half_step + (k & 3) * 2), idesc,
+                               (kb != q.kb0 || k != 0) ? 1u : 0u);
+        }
+        tc_commit_pair_mc(c.empty0 + 8 * slot, 0x3);
+      }
+      __syncwarp();
+      if (++slot == p.slots) { slot = 0; phase ^= 1u; }
     }
     if (!ok) break;
-    tc_commit_pair_mc(c.tfull0 + 8 * acc, 0x3);
+    if (issuer) tc_commit_pair_mc(c.tfull0 + 8 * acc, 0x3);
+    __syncwarp();
     if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
   }
-  tc_commit_pair(c.drain);
-  mbar_wait_drain(c.drain, 0u, p.limit_ns);
+  if (issuer) {
+    tc_commit_pair(c.drain);
+    mbar_wait_drain(c.drain, 0u, p.limit_ns);
+  }
+  __syncwarp();
 }
 
-// 32 tokens from m0 on of this lane's column n: scaled, rounded and stored.
+// 32 tokens from m0 on of this lane's column n: scaled, rounded and stored.  A warp has one
+// instruction stream, so this is counted in instructions: a whole group takes about 4 per
+// value.  16-bit outputs: lanes 2i and 2i + 1 hold two adjacent columns; the even lane stores
+// both of one token, the odd lane both of the next (p.paired).
 template <class T>
 __device__ __forceinline__ void i8_store(const I8Params& p, const float (&v)[32], int m0, int m_end, int n, float ws,
                                          int lane) {
   T* out = static_cast<T*>(p.out);
-  if constexpr (sizeof(T) == 2) {
-    if (p.paired) {
-      // lanes 2i and 2i + 1 hold two adjacent columns: the even lane stores both of one token,
-      // the odd lane both of the next
-      const bool odd = lane & 1;
+  const int64_t ldo = p.ldo;
+  const float2 ws2 = make_float2(ws, ws);
+  const bool odd = lane & 1;
+  const bool whole = m0 + 32 <= m_end && (n | 31) < p.N;  // the same for the whole warp
+  if (whole && (sizeof(T) == 4 || p.paired)) {
+    const float4* xs = reinterpret_cast<const float4*>(p.x_scale + m0);  // m0 is a multiple of 16
+    T* o = sizeof(T) == 4 ? out + static_cast<int64_t>(m0) * ldo + n
+                          : out + static_cast<int64_t>(m0 + (odd ? 1 : 0)) * ldo + (n & ~1);
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const int m = m0 + j;
-        if (m >= m_end) break;
-        const float s0 = p.x_scale[m], s1 = m + 1 < m_end ? p.x_scale[m + 1] : 0.f;
-        const float a = v[j] * s0 * ws, b = v[j + 1] * s1 * ws;
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-        const T lo = from_float<T>(odd ? other : a), hi = from_float<T>(odd ? b : other);
-        const int mm = m + (odd ? 1 : 0), nn = n & ~1;
-        if (mm >= m_end || nn >= p.N) continue;
-        T* o = out + static_cast<int64_t>(mm) * p.ldo + nn;
-        if (nn + 1 < p.N) {
-          uint32_t w;
-          reinterpret_cast<T*>(&w)[0] = lo;
-          reinterpret_cast<T*>(&w)[1] = hi;
-          *reinterpret_cast<uint32_t*>(o) = w;
-        } else {
-          o[0] = lo;
-        }
+    for (int j = 0; j < 32; j += 4) {
+      const float4 s = __ldg(xs + j / 4);
+      const float2 a = fmul2(fmul2(make_float2(v[j], v[j + 1]), make_float2(s.x, s.y)), ws2);
+      const float2 b = fmul2(fmul2(make_float2(v[j + 2], v[j + 3]), make_float2(s.z, s.w)), ws2);
+      if constexpr (sizeof(T) == 4) {
+        o[0] = a.x;
+        o[ldo] = a.y;
+        o[2 * ldo] = b.x;
+        o[3 * ldo] = b.y;
+      } else {
+        const float oa = __shfl_xor_sync(0xffffffffu, odd ? a.x : a.y, 1);
+        const float ob = __shfl_xor_sync(0xffffffffu, odd ? b.x : b.y, 1);
+        *reinterpret_cast<uint32_t*>(o) = pack2<T>(odd ? oa : a.x, odd ? a.y : oa);
+        *reinterpret_cast<uint32_t*>(o + 2 * ldo) = pack2<T>(odd ? ob : b.x, odd ? b.y : ob);
       }
-      return;
+      o += 4 * ldo;
     }
+    return;
   }
   if (n >= p.N) return;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (m0 + j >= m_end) break;
-    out[static_cast<int64_t>(m0 + j) * p.ldo + n] = from_float<T>(v[j] * p.x_scale[m0 + j] * ws);
-  }
+  for (int j = 0; j < 32; ++j)
+    if (m0 + j < m_end)
+      out[static_cast<int64_t>(m0 + j) * ldo + n] = from_float<T>(v[j] * __ldg(p.x_scale + m0 + j) * ws);
 }
 
 __device__ __forceinline__ void i8_store_any(const I8Params& p, const float (&v)[32], int m0, int m_end, int n, float ws,
@@ -279,7 +305,7 @@ __device__ __forceinline__ int i8_owner(const I8Params& p, long long x, int pair
 }
 
 __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lane) {
-  const int strip = warp & 3;
+  const int strip = warp & 3, half = (warp >> 2) & 1;
   const int row = static_cast<int>(c.rank) * 128 + strip * 32 + lane;  // of the pair's 256
   const uint32_t lanes = static_cast<uint32_t>(strip * 32) << 16;
   const uint32_t even_tempty = map_to_rank(c.tempty0, 0);
@@ -294,9 +320,9 @@ __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lan
     float* part = p.part + static_cast<size_t>(2 * c.pair + (q.kb0 == 0 ? 1 : 0)) * p.nt * 256 + row;
     if (!__all_sync(0xffffffffu, mbar_wait_cluster(c.tfull0 + 8 * acc, acc_phase, c.ctl))) return;
     tc_fence_after();
-    const uint32_t t = c.tmem + lanes + static_cast<uint32_t>(acc * 128);
+    const uint32_t t = c.tmem + lanes + static_cast<uint32_t>(acc * p.acc_cols);
 #pragma unroll 1
-    for (int col = 0; m0 + col < m_end; col += 32) {
+    for (int col = 32 * half; m0 + col < m_end; col += 64) {
       float v[32];
       tmem_ld32(t + col, v);
       tmem_ld_wait(v);
@@ -310,7 +336,7 @@ __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lan
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_release_cluster(even_tempty + 8 * acc);
+    if (lane == 0) mbar_arrive_cluster(even_tempty + 8 * acc);
     if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
     if (whole) continue;
     // a cut tile: the last part to arrive adds them all up, in their order
@@ -319,12 +345,12 @@ __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lan
     __threadfence();
     __syncwarp();
     int before = 0;
-    if (lane == 0) before = atomicAdd(p.arrived + p0 * 8 + static_cast<int>(c.rank) * 4 + strip, 1);
+    if (lane == 0) before = atomicAdd(p.arrived + p0 * 16 + static_cast<int>(c.rank) * 8 + half * 4 + strip, 1);
     before = __shfl_sync(0xffffffffu, before, 0);
     if (before != p1 - p0) continue;
     __threadfence();
 #pragma unroll 1
-    for (int col = 0; m0 + col < m_end; col += 32) {
+    for (int col = 32 * half; m0 + col < m_end; col += 64) {
       float v[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = 0.f;
@@ -346,8 +372,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kI8WStages * kI8WBytes + kI8Slots * kI8XBytes);
-  constexpr int kBars = 2 * kI8WStages + 3 * kI8Slots + 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kI8Ring);
+  constexpr int kBars = 2 * kI8MaxStages + 3 * kI8MaxSlots + 5;
   static_assert(kBars * 8 + 8 <= 512, "barriers and words fit in their 512 bytes");
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // [0] TMEM base, [1] abort
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -358,38 +384,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   c.pair = static_cast<int>(blockIdx.x >> 1);
   c.pairs = static_cast<int>(gridDim.x >> 1);
   c.w0 = smem_addr(smem);
-  c.x0 = c.w0 + kI8WStages * kI8WBytes;
+  c.x0 = c.w0 + static_cast<uint32_t>(p.w_stages) * kI8WBytes;
+  c.x_bytes = static_cast<uint32_t>(p.nt / 2) * kI8BK * 2;
   c.wfull0 = smem_addr(bars);
-  c.wempty0 = c.wfull0 + 8 * kI8WStages;
-  c.xfull0 = c.wempty0 + 8 * kI8WStages;
-  c.afull0 = c.xfull0 + 8 * kI8Slots;
-  c.empty0 = c.afull0 + 8 * kI8Slots;
-  c.tfull0 = c.empty0 + 8 * kI8Slots;
+  c.wempty0 = c.wfull0 + 8 * kI8MaxStages;
+  c.xfull0 = c.wempty0 + 8 * kI8MaxStages;
+  c.afull0 = c.xfull0 + 8 * kI8MaxSlots;
+  c.empty0 = c.afull0 + 8 * kI8MaxSlots;
+  c.tfull0 = c.empty0 + 8 * kI8MaxSlots;
   c.tempty0 = c.tfull0 + 16;
   c.drain = c.tempty0 + 16;
   c.ctl = WaitCtl{reinterpret_cast<volatile uint32_t*>(&misc[1]), p.status, p.limit_ns};
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kI8WStages; ++s) {
+    for (int s = 0; s < p.w_stages; ++s) {
       mbar_init(c.wfull0 + 8 * s, 1);
       mbar_init(c.wempty0 + 8 * s, kI8ConvertWarps);
     }
-    for (int s = 0; s < kI8Slots; ++s) {
+    for (int s = 0; s < p.slots; ++s) {
       mbar_init(c.xfull0 + 8 * s, 1);
       mbar_init(c.afull0 + 8 * s, 2 * kI8ConvertWarps);
       mbar_init(c.empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(c.tfull0 + 8 * b, 1);
-      mbar_init(c.tempty0 + 8 * b, 2 * 4);
+      mbar_init(c.tempty0 + 8 * b, 2 * kI8EpiWarps);
     }
     mbar_init(c.drain, 1);
     misc[1] = 0u;
     fence_barrier_init();
   }
-  if (warp == 12 && lane == 0) tma_prefetch_desc(&tmW);
-  if (warp == 13 && lane == 0) tma_prefetch_desc(&tmX);
-  if (warp == 14) {
+  if (warp == 16 && lane == 0) tma_prefetch_desc(&tmW);
+  if (warp == 17 && lane == 0) tma_prefetch_desc(&tmX);
+  if (warp == 18) {
     tmem_alloc_pair(smem_addr(&misc[0]), kTmemCols);
     tmem_relinquish_pair();
   }
@@ -398,15 +425,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   cluster_sync();
   tc_fence_after();
   c.tmem = misc[0];
+  c.tmem_a = c.tmem + static_cast<uint32_t>(p.accs * p.acc_cols);
 
   if (warp < 8) {
     i8_convert(p, c, warp, lane);
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     i8_epilogue(p, c, warp, lane);
+  } else if (warp == 18) {
+    if (c.even) i8_mma(p, c);
   } else if (lane == 0) {
-    if (warp == 12) i8_w_producer(&tmW, p, c);
-    if (warp == 13) i8_x_producer(&tmX, p, c);
-    if (warp == 14 && c.even) i8_mma(p, c);
+    if (warp == 16) i8_w_producer(&tmW, p, c);
+    if (warp == 17) i8_x_producer(&tmX, p, c);
   }
 
   __syncwarp();
@@ -414,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  if (warp == 14) tmem_dealloc_pair(c.tmem, kTmemCols);
+  if (warp == 18) tmem_dealloc_pair(c.tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------- host side
@@ -445,6 +474,9 @@ cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const in
   p.m_tiles = g.m_tiles;
   p.k_blocks = g.k_blocks;
   p.accs = g.nt <= 128 ? 2 : 1;
+  p.acc_cols = (g.nt + 31) / 32 * 32;
+  p.slots = std::min(kI8MaxSlots, (static_cast<int>(kTmemCols) - p.accs * p.acc_cols) / 64);
+  p.w_stages = std::min<int>(kI8MaxStages, (kI8Ring - p.slots * g.nt * kI8BK) / kI8WBytes);
   p.total = g.total;
   p.x_scale = x_scale;
   p.w_scale = w_scale;
