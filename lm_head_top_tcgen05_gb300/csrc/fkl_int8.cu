@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kQuantThreads)
                     uint4* __restrict__ hdr) {
   constexpr int E = 16 / sizeof(T);
   __shared__ uint32_t warp_max[kQuantThreads / 32];
+  if (hdr != nullptr) launch_dependents();  // the product follows
   const T* row = x + static_cast<int64_t>(blockIdx.x) * ldx;
   Q* out = q + static_cast<int64_t>(blockIdx.x) * cols;
   if (hdr != nullptr && blockIdx.x == 0)
@@ -114,6 +115,7 @@ static cudaError_t launch_quantize(const void* x, int32_t type, int64_t rows, in
 __global__ void __launch_bounds__(256)
     widen_kernel(const uint32_t* __restrict__ xq, int64_t words, uint2* __restrict__ x16,
                  const float* __restrict__ x_scale, int M, float* __restrict__ scale, uint4* __restrict__ hdr) {
+  launch_dependents();
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   for (int64_t i = i0; i < M; i += static_cast<int64_t>(gridDim.x) * 256) scale[i] = x_scale[i];
   if (blockIdx.x == 0)
@@ -355,10 +357,16 @@ static bool make_int8_plan(int64_t M, int64_t N, int64_t K, int sms, Int8Plan* p
   return true;
 }
 
-// Bytes for any device: the partial sums grow with the number of SMs.
+// Bytes on the current device (the partial sums grow with the number of its SMs; a GB300's 152
+// are assumed when no device is visible).
 static size_t int8_workspace(int64_t M, int64_t N, int64_t K) {
+  int sms = 0;
+  if (require_device(&sms) != FKL_OK) {
+    sms = 152;
+    set_last_error_message("");
+  }
   Int8Plan p;
-  return make_int8_plan(M, N, K, 2 * kMaxPairs, &p) ? p.total : 0;
+  return make_int8_plan(M, N, K, sms, &p) ? p.total : 0;
 }
 
 static fkl_status bad(fkl_status s, const char* msg) {

@@ -18,11 +18,14 @@ struct Int8Header {
   int arrived[kMaxPairs * 16];  // parts of a cut tile that are done, per epilogue warp
 };
 
-// How the tensor-core product is cut: tiles of 256 channels x nt tokens, blocks of 128 k.
+// How the tensor-core product is cut (fkl_int8_gemm.cu): tiles of 256 channels x nt tokens,
+// blocks of 128 * sub k.
 struct Int8GemmPlan {
-  int m_tiles, nt, k_blocks, pairs;
-  int64_t total;      // blocks in all
-  size_t part_bytes;  // partial sums of the tiles that are cut
+  int m_tiles, nt, sub, k_blocks, pairs;
+  int accs, acc_cols, slots, w_stages;  // TMEM and shared memory
+  int rounds;                           // whole tiles per pair
+  int64_t cut_blocks;                   // blocks of the tiles that are cut
+  size_t part_bytes;                    // their partial sums
 };
 Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms);
 // x16: the tokens' integers as fp16 [M][K]; x_scale: 16-byte aligned; hdr zeroed before on the
