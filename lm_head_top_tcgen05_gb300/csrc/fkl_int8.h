@@ -23,7 +23,7 @@ struct Int8Header {
 struct Int8GemmPlan {
   int m_tiles, nt, sub, k_blocks, pairs;
   int accs, acc_cols, slots, w_stages;  // TMEM and shared memory
-  int rounds;                           // whole tiles per pair
+  int tiles, rounds;                    // tiles in all; whole tiles of a pair, at most
   int64_t cut_blocks;                   // blocks of the tiles that are cut
   size_t part_bytes;                    // their partial sums
 };

@@ -21,10 +21,9 @@
 //                warps 8..11 and 12..15 take alternate groups of 32 tokens;
 //   warp 16      TMA producer of W, warp 17 of the tokens;
 //   warp 18      (even CTA) issues the MMAs.
-// The work is tiles of 256 rows of W x one tile of tokens, walked in blocks of 128 or 256 k.  With
-// several tiles of tokens, the tiles that fill whole waves of pairs are dealt round-robin; the
-// remaining ones (with one tile of tokens, all) are a line of blocks cut into equal parts, one
-// per pair, so that every SM reads the same share of W.  A tile that is cut has its fp32 partial sums in the workspace;
+// The work is tiles of 256 rows of W x one tile of tokens, walked in blocks of 128 or 256 k.  Tiles
+// are dealt round-robin to the pairs.  Those that would leave many pairs idle in the last wave
+// (or the only one) are a line of blocks cut into equal parts, one per pair.  A tile that is cut has its fp32 partial sums in the workspace;
 // the last of its parts to finish (per warp of the epilogue) adds them in the order of the
 // parts, so the result does not depend on which one that is.  The cut tiles come first, so
 // that adding them up overlaps the whole ones.
@@ -56,7 +55,7 @@ struct I8Params {
   // tile's epilogue runs beside the next tile's MMAs), then slots of 64 columns for W's fp16
   // blocks, with as many token blocks in shared memory; the rest of that holds int8 blocks of W.
   int accs, acc_cols, slots, w_stages;
-  int rounds;            // whole tiles per pair
+  int tiles, rounds;     // tiles in all; whole tiles of a pair, at most
   long long cut_blocks;  // blocks of the cut tiles
   const float* x_scale;
   const float* w_scale;
@@ -92,7 +91,9 @@ struct I8Seq {
       kb1 = p.k_blocks;
     }
   }
-  __device__ __forceinline__ bool more(const I8Params& p) const { return at < end || round < p.rounds; }
+  __device__ __forceinline__ bool more(const I8Params& p) const {
+    return at < end || (round < p.rounds && tile < p.tiles);
+  }
   __device__ __forceinline__ void next(const I8Params& p) {
     if (at < end)
       at += kb1 - kb0;
@@ -283,24 +284,24 @@ __device__ void i8_mma(const I8Params& p, const I8Ctx& c) {
   __syncwarp();
 }
 
-// 32 tokens from m0 on of this lane's column n: scaled, rounded and stored.  A warp has one
+// C tokens from m0 on of this lane's column n: scaled, rounded and stored.  A warp has one
 // instruction stream, so this is counted in instructions: a whole group takes about 4 per
 // value.  16-bit outputs: lanes 2i and 2i + 1 hold two adjacent columns; the even lane stores
 // both of one token, the odd lane both of the next (p.paired).
-template <class T>
-__device__ __forceinline__ void i8_store(const I8Params& p, const float (&v)[32], int m0, int m_end, int n, float ws,
+template <class T, int C>
+__device__ __forceinline__ void i8_store(const I8Params& p, const float (&v)[C], int m0, int m_end, int n, float ws,
                                          int lane) {
   T* out = static_cast<T*>(p.out);
   const int64_t ldo = p.ldo;
   const float2 ws2 = make_float2(ws, ws);
   const bool odd = lane & 1;
-  const bool whole = m0 + 32 <= m_end && (n | 31) < p.N;  // the same for the whole warp
+  const bool whole = m0 + C <= m_end && (n | 31) < p.N;  // the same for the whole warp
   if (whole && (sizeof(T) == 4 || p.paired)) {
     const float4* xs = reinterpret_cast<const float4*>(p.x_scale + m0);  // m0 is a multiple of 16
     T* o = sizeof(T) == 4 ? out + static_cast<int64_t>(m0) * ldo + n
                           : out + static_cast<int64_t>(m0 + (odd ? 1 : 0)) * ldo + (n & ~1);
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
+    for (int j = 0; j < C; j += 4) {
       const float4 s = __ldg(xs + j / 4);
       const float2 a = fmul2(fmul2(make_float2(v[j], v[j + 1]), make_float2(s.x, s.y)), ws2);
       const float2 b = fmul2(fmul2(make_float2(v[j + 2], v[j + 3]), make_float2(s.z, s.w)), ws2);
@@ -321,19 +322,20 @@ __device__ __forceinline__ void i8_store(const I8Params& p, const float (&v)[32]
   }
   if (n >= p.N) return;
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
+  for (int j = 0; j < C; ++j)
     if (m0 + j < m_end)
       out[static_cast<int64_t>(m0 + j) * ldo + n] = from_float<T>(v[j] * __ldg(p.x_scale + m0 + j) * ws);
 }
 
-__device__ __forceinline__ void i8_store_any(const I8Params& p, const float (&v)[32], int m0, int m_end, int n, float ws,
+template <int C>
+__device__ __forceinline__ void i8_store_any(const I8Params& p, const float (&v)[C], int m0, int m_end, int n, float ws,
                                              int lane) {
   if (p.out_type == FKL_TYPE_F32)
-    i8_store<float>(p, v, m0, m_end, n, ws, lane);
+    i8_store<float, C>(p, v, m0, m_end, n, ws, lane);
   else if (p.out_type == FKL_TYPE_BF16)
-    i8_store<__nv_bfloat16>(p, v, m0, m_end, n, ws, lane);
+    i8_store<__nv_bfloat16, C>(p, v, m0, m_end, n, ws, lane);
   else
-    i8_store<__half>(p, v, m0, m_end, n, ws, lane);
+    i8_store<__half, C>(p, v, m0, m_end, n, ws, lane);
 }
 
 // The pair whose part of the line of cut tiles holds block x.
@@ -388,16 +390,28 @@ __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lan
     if (before != p1 - p0) continue;
     __threadfence();
 #pragma unroll 1
-    for (int col = 32 * half; m0 + col < m_end; col += 64) {
-      float v[32];
+    for (int col = 32 * half; m0 + col < m_end; col += col % 32 ? 48 : 16) {
+      // Two parts' loads are in flight at once.  Columns past m_end are read, not stored.
+      float v[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = 0.f;
-      for (int r = p0; r <= p1; ++r) {
-        // the tile's first part is the last of its pair, the others the first of theirs
-        const float* src = p.part + static_cast<size_t>(2 * r + (r == p0 ? 1 : 0)) * p.nt * 256 + row;
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
+      // the tile's first part is the last of its pair, the others the first of theirs
+      const size_t part_step = static_cast<size_t>(p.nt) * 256;
+      const float* src = p.part + (2 * p0 + 1) * part_step + static_cast<size_t>(col) * 256 + row;
+      for (int r = p0; r <= p1; r += 2) {
+        float u[2][16];
+        const float* from = r == p0 ? src : src + (2 * (r - p0) - 1) * part_step;
+        const float* then = r < p1 ? src + (2 * (r + 1 - p0) - 1) * part_step : from;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (m0 + col + j < m_end) v[j] += __ldcg(src + static_cast<size_t>(col + j) * 256);
+        for (int j = 0; j < 16; ++j) u[0][j] = __ldcg(from + j * 256);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) u[1][j] = __ldcg(then + j * 256);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += u[0][j];
+        if (r < p1) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] += u[1][j];
+        }
       }
       i8_store_any(p, v, m0 + col, m_end, n, ws, lane);
     }
@@ -504,12 +518,18 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   g.k_blocks = static_cast<int>((K + kI8K * g.sub - 1) / (kI8K * g.sub));
   const int64_t tiles = (N + 255) / 256 * g.m_tiles;
   g.pairs = static_cast<int>(std::min<int64_t>(std::min(sms / 2, kMaxPairs), tiles * g.k_blocks));
-  // One tile of tokens: bound by reading W, all of it is cut.  The pairs then start and end
-  // their tiles at different times, and their output mixes better with the reads than in waves
-  // (201088 x 2880, 128 tokens: 149 us against 190).  Several: pairs that run together share tiles
-  // of W and of the tokens in L2 (4096 tokens: 2.70 ms against 2.86).
-  g.rounds = g.m_tiles == 1 ? 0 : static_cast<int>(tiles / g.pairs);
-  g.cut_blocks = (tiles - static_cast<int64_t>(g.rounds) * g.pairs) * g.k_blocks;
+  // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are
+  // cut, which costs the sums of their parts at the end.  Measured per pair: a block of 128 k takes
+  // 0.36 us (W from HBM) or nt / 256 * 0.55 us (MMAs), adding up about 3 us + nt * 0.06 us
+  // (203 x 50261 x 1456, 45 tiles beyond 2 waves: whole 48 us, cut 64 us; 9 x 4096 x 2880, 16 tiles
+  // in all: cut 9 us, whole 15 us).
+  g.rounds = static_cast<int>(tiles / g.pairs);
+  const int64_t rest = tiles - static_cast<int64_t>(g.rounds) * g.pairs;
+  const double tile_us = static_cast<double>(K) / kI8K * std::max(0.36, g.nt / 256.0 * 0.55);
+  const bool cut = rest * tile_us / g.pairs + 3.0 + 0.06 * g.nt < tile_us;
+  if (rest > 0 && !cut) ++g.rounds;
+  g.tiles = static_cast<int>(tiles);
+  g.cut_blocks = cut ? rest * g.k_blocks : 0;
   g.part_bytes = static_cast<size_t>(2 * g.pairs) * g.nt * 256 * 4;
   return g;
 }
@@ -551,6 +571,7 @@ cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const in
   p.acc_cols = g.acc_cols;
   p.slots = g.slots;
   p.w_stages = g.w_stages;
+  p.tiles = g.tiles;
   p.rounds = g.rounds;
   p.cut_blocks = g.cut_blocks;
   p.x_scale = x_scale;
