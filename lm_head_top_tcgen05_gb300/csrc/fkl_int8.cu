@@ -41,32 +41,42 @@ __device__ __forceinline__ void put4(__half* o, const int (&q)[4]) {
   *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(h);
 }
 
-// One block per row, two reads of it (the second from cache).  The IEEE division keeps the
-// integers equal to the definition's.  Block 0 zeroes `hdr`, if there is one.
+// One block per row.  A thread's first kHeld vectors (16 bytes) stay in registers between the
+// two passes; the rest of a longer row is read twice, the second time from cache.  The IEEE
+// division keeps the integers equal to the definition's.  Block 0 zeroes `hdr`, if there is one.
 template <class T, class Q, bool kVec>
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_kernel(const T* __restrict__ x, int64_t cols, int64_t ldx, Q* __restrict__ q, float* __restrict__ scale,
                     uint4* __restrict__ hdr) {
-  constexpr int E = 16 / sizeof(T);
+  constexpr int E = 16 / sizeof(T), kHeld = 4;
   __shared__ uint32_t warp_max[kQuantThreads / 32];
   if (hdr != nullptr) launch_dependents();  // the product follows
   const T* row = x + static_cast<int64_t>(blockIdx.x) * ldx;
+  const uint4* rowv = reinterpret_cast<const uint4*>(row);
   Q* out = q + static_cast<int64_t>(blockIdx.x) * cols;
+  const int64_t vecs = kVec ? cols / E : 0;
+  uint32_t amax = 0;
+  uint4 held[kHeld];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int64_t i = threadIdx.x + h * kQuantThreads;
+    held[h] = i < vecs ? rowv[i] : make_uint4(0, 0, 0, 0);
+  }
   if (hdr != nullptr && blockIdx.x == 0)
     for (int i = threadIdx.x; i < static_cast<int>(sizeof(Int8Header) / 16); i += kQuantThreads)
       hdr[i] = make_uint4(0, 0, 0, 0);
-  uint32_t amax = 0;
-  if (kVec) {
-    for (int64_t i = threadIdx.x; i < cols / E; i += kQuantThreads) {
-      float v[E];
-      unpack16<T>(reinterpret_cast<const uint4*>(row)[i], v);
+  auto largest = [&](const uint4& raw) {
+    float v[E];
+    unpack16<T>(raw, v);
 #pragma unroll
-      for (int j = 0; j < E; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
-    }
-  } else {
+    for (int j = 0; j < E; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) largest(held[h]);
+  for (int64_t i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) largest(rowv[i]);
+  if (!kVec)
     for (int64_t i = threadIdx.x; i < cols; i += kQuantThreads)
       amax = max(amax, __float_as_uint(to_float(row[i])) & 0x7fffffffu);
-  }
   amax = __reduce_max_sync(0xffffffffu, amax);
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
   __syncthreads();
@@ -75,22 +85,26 @@ __global__ void __launch_bounds__(kQuantThreads)
   for (int w = 0; w < kQuantThreads / 32; ++w) amax = max(amax, warp_max[w]);
   const float s = row_scale(amax);
   if (threadIdx.x == 0) scale[blockIdx.x] = s;
-  if (kVec) {
-    for (int64_t i = threadIdx.x; i < cols / E; i += kQuantThreads) {
-      float v[E];
-      unpack16<T>(reinterpret_cast<const uint4*>(row)[i], v);
+  auto put = [&](const uint4& raw, int64_t i) {
+    float v[E];
+    unpack16<T>(raw, v);
 #pragma unroll
-      for (int j = 0; j < E / 4; ++j) {
-        int w[4];
+    for (int j = 0; j < E / 4; ++j) {
+      int w[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) w[b] = quantize(v[4 * j + b], s);
-        put4(out + i * E + 4 * j, w);
-      }
+      for (int b = 0; b < 4; ++b) w[b] = quantize(v[4 * j + b], s);
+      put4(out + i * E + 4 * j, w);
     }
-  } else {
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int64_t i = threadIdx.x + h * kQuantThreads;
+    if (i < vecs) put(held[h], i);
+  }
+  for (int64_t i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) put(rowv[i], i);
+  if (!kVec)
     for (int64_t i = threadIdx.x; i < cols; i += kQuantThreads)
       out[i] = static_cast<Q>(static_cast<float>(quantize(to_float(row[i]), s)));
-  }
 }
 
 template <class Q>
@@ -136,7 +150,7 @@ __global__ void __launch_bounds__(256)
 // rows are prefetched into L2 meanwhile.
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
-constexpr int64_t kFewTokens = 8;
+constexpr int64_t kFewTokens = 4;
 constexpr int64_t kFewSmem = 96 * 1024;  // two blocks to an SM
 
 // V values per lane, summed over the lanes: lane l gets the sum of value l * V / 32 (V < 32: of
@@ -179,25 +193,32 @@ struct FewParams {
   uint4* hdr;
 };
 
-// The tokens' integers into shared memory: kFewWarps / MT warps per token.
+// The tokens' integers into shared memory: kFewWarps / MT warps per token.  A thread's first
+// kHeld vectors stay in registers between the two passes.
 template <int MT, class T>
 __device__ void few_quantize(const FewParams& p, int8_t* sq, float* ss, uint32_t* warp_max) {
-  constexpr int W = kFewWarps / MT, E = 16 / sizeof(T);
+  constexpr int W = kFewWarps / MT, E = 16 / sizeof(T), kHeld = 2;
   const int warp = threadIdx.x >> 5, m = warp / W;
   const int at = threadIdx.x - m * W * 32;
   const T* row = static_cast<const T*>(p.x) + static_cast<int64_t>(m) * p.ldx;
   const bool live = m < p.M;
+  const int vecs = live && p.vec ? p.K / E : 0;
   uint32_t amax = 0;
-  if (live && p.vec) {
-    for (int i = at; i < p.K / E; i += W * 32) {
-      float v[E];
-      unpack16<T>(reinterpret_cast<const uint4*>(row)[i], v);
+  uint4 held[kHeld];
 #pragma unroll
-      for (int j = 0; j < E; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
-    }
-  } else if (live) {
+  for (int h = 0; h < kHeld; ++h)
+    held[h] = at + h * W * 32 < vecs ? reinterpret_cast<const uint4*>(row)[at + h * W * 32] : make_uint4(0, 0, 0, 0);
+  auto largest = [&](const uint4& raw) {
+    float v[E];
+    unpack16<T>(raw, v);
+#pragma unroll
+    for (int j = 0; j < E; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) largest(held[h]);
+  for (int i = at + kHeld * W * 32; i < vecs; i += W * 32) largest(reinterpret_cast<const uint4*>(row)[i]);
+  if (live && !p.vec)
     for (int i = at; i < p.K; i += W * 32) amax = max(amax, __float_as_uint(to_float(row[i])) & 0x7fffffffu);
-  }
   amax = __reduce_max_sync(0xffffffffu, amax);
   if ((threadIdx.x & 31) == 0) warp_max[warp] = amax;
   __syncthreads();
@@ -206,21 +227,23 @@ __device__ void few_quantize(const FewParams& p, int8_t* sq, float* ss, uint32_t
   const float s = live ? row_scale(amax) : 0.f;
   if (at == 0) ss[m] = s;
   int8_t* out = sq + static_cast<int64_t>(m) * p.K;
-  if (live && p.vec) {
-    for (int i = at; i < p.K / E; i += W * 32) {
-      float v[E];
-      unpack16<T>(reinterpret_cast<const uint4*>(row)[i], v);
+  auto put = [&](const uint4& raw, int i) {
+    float v[E];
+    unpack16<T>(raw, v);
 #pragma unroll
-      for (int j = 0; j < E / 4; ++j) {
-        int q[4];
+    for (int j = 0; j < E / 4; ++j) {
+      int q[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) q[b] = quantize(v[4 * j + b], s);
-        put4(out + i * E + 4 * j, q);
-      }
+      for (int b = 0; b < 4; ++b) q[b] = quantize(v[4 * j + b], s);
+      put4(out + i * E + 4 * j, q);
     }
-  } else {
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (at + h * W * 32 < vecs) put(held[h], at + h * W * 32);
+  for (int i = at + kHeld * W * 32; i < vecs; i += W * 32) put(reinterpret_cast<const uint4*>(row)[i], i);
+  if (!live || !p.vec)
     for (int i = at; i < p.K; i += W * 32) out[i] = live ? static_cast<int8_t>(quantize(to_float(row[i]), s)) : 0;
-  }
 }
 
 template <class T>
@@ -228,25 +251,51 @@ __device__ __forceinline__ void few_store(const FewParams& p, int m, int n, floa
   static_cast<T*>(p.out)[static_cast<int64_t>(m) * p.ldo + n] = from_float<T>(y);
 }
 
-// MT tokens (those past M are zero), R rows of W per warp at a time.
 template <int MT, int R>
-__global__ void __launch_bounds__(kFewThreads, MT * R <= 16 ? 2 : 1) few_tokens_kernel(const __grid_constant__ FewParams p) {
+__device__ __forceinline__ void few_dot(int (&acc)[MT * R], const uint4 (&wv)[R], const uint4* xs, int chunks, int c) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const uint4 xv = xs[m * chunks + c];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      int a = acc[m * R + r];
+      a = __dp4a(static_cast<int>(wv[r].x), static_cast<int>(xv.x), a);
+      a = __dp4a(static_cast<int>(wv[r].y), static_cast<int>(xv.y), a);
+      a = __dp4a(static_cast<int>(wv[r].z), static_cast<int>(xv.z), a);
+      acc[m * R + r] = __dp4a(static_cast<int>(wv[r].w), static_cast<int>(xv.w), a);
+    }
+  }
+}
+
+// MT tokens (those past M are zero), R rows of W per warp at a time, H 16-byte pieces of each row
+// in flight per lane.  The first rows' pieces are loaded before the tokens are brought to 8 bits.
+template <int MT, int R, int H>
+__global__ void __launch_bounds__(kFewThreads, 2) few_tokens_kernel(const __grid_constant__ FewParams p) {
   extern __shared__ __align__(16) int8_t sq[];  // [MT][K]
   __shared__ float ss[MT];
   __shared__ uint32_t warp_max[kFewWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (p.N + R - 1) / R, step = static_cast<int>(gridDim.x) * kFewWarps;
-  const int g0 = static_cast<int>(blockIdx.x) * kFewWarps + warp;
-  if (g0 < groups) {
-    const int8_t* w = p.wq + static_cast<int64_t>(g0) * R * p.K;
-    const int bytes = min(R, p.N - g0 * R) * p.K;
-    for (int i = lane * 128; i < bytes; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + i));
-  }
+  const int chunks = p.K / 16;
+  int g = static_cast<int>(blockIdx.x) * kFewWarps + warp;
+  uint4 held[H][R];
+  auto load = [&](int c0) {  // rows past N read the last one; their sums are not stored
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int c = c0 + 32 * h;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        held[h][r] = c < chunks
+                         ? __ldcs(reinterpret_cast<const uint4*>(p.wq + static_cast<int64_t>(min(g * R + r, p.N - 1)) * p.K) + c)
+                         : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (g < groups) load(lane);
   if (blockIdx.x == 0 && threadIdx.x < 16) p.hdr[threadIdx.x] = make_uint4(0, 0, 0, 0);
   if (p.x_scale != nullptr) {
     const uint4* src = static_cast<const uint4*>(p.x);
-    for (int i = threadIdx.x; i < MT * (p.K / 16); i += kFewThreads)
-      reinterpret_cast<uint4*>(sq)[i] = i < p.M * (p.K / 16) ? src[i] : make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < MT * chunks; i += kFewThreads)
+      reinterpret_cast<uint4*>(sq)[i] = i < p.M * chunks ? src[i] : make_uint4(0, 0, 0, 0);
     if (threadIdx.x < MT) ss[threadIdx.x] = static_cast<int>(threadIdx.x) < p.M ? p.x_scale[threadIdx.x] : 0.f;
   } else if (p.x_type == FKL_TYPE_F32) {
     few_quantize<MT, float>(p, sq, ss, warp_max);
@@ -257,35 +306,22 @@ __global__ void __launch_bounds__(kFewThreads, MT * R <= 16 ? 2 : 1) few_tokens_
   }
   __syncthreads();
 
-  const int chunks = p.K / 16;
   const uint4* xs = reinterpret_cast<const uint4*>(sq);
-  for (int g = g0; g < groups; g += step) {
-    const uint4* w[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r)  // rows past N read the last one; their sums are not stored
-      w[r] = reinterpret_cast<const uint4*>(p.wq + static_cast<int64_t>(min(g * R + r, p.N - 1)) * p.K);
+  while (g < groups) {
     int acc[MT * R] = {};
-#pragma unroll(R == 1 ? 6 : 2)
-    for (int c = lane; c < chunks; c += 32) {
-      uint4 wv[R];
+    const int row0 = g * R;
+    for (int c0 = lane;;) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) wv[r] = __ldcs(w[r] + c);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint4 xv = xs[m * chunks + c];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          int a = acc[m * R + r];
-          a = __dp4a(static_cast<int>(wv[r].x), static_cast<int>(xv.x), a);
-          a = __dp4a(static_cast<int>(wv[r].y), static_cast<int>(xv.y), a);
-          a = __dp4a(static_cast<int>(wv[r].z), static_cast<int>(xv.z), a);
-          acc[m * R + r] = __dp4a(static_cast<int>(wv[r].w), static_cast<int>(xv.w), a);
-        }
-      }
+      for (int h = 0; h < H; ++h) few_dot<MT, R>(acc, held[h], xs, chunks, min(c0 + 32 * h, chunks - 1));
+      c0 += 32 * H;
+      if (c0 - lane >= chunks) break;
+      load(c0);
     }
+    g += step;
+    if (g < groups) load(lane);  // the next rows' pieces, while this group's sums are finished
     const int sum = reduce_over_lanes<MT * R>(acc, lane);
     constexpr int kLanes = 32 / (MT * R);  // lanes that hold the same sum
-    const int i = lane / kLanes, m = i / R, n = g * R + i % R;
+    const int i = lane / kLanes, m = i / R, n = row0 + i % R;
     if (lane % kLanes == 0 && m < p.M && n < p.N) {
       const float y = static_cast<float>(sum) * ss[m] * p.w_scale[n];
       if (p.out_type == FKL_TYPE_F32)
@@ -298,26 +334,26 @@ __global__ void __launch_bounds__(kFewThreads, MT * R <= 16 ? 2 : 1) few_tokens_
   }
 }
 
-template <int MT, int R>
+template <int MT, int R, int H>
 static cudaError_t launch_few_t(const FewParams& p, int sms, cudaStream_t st) {
   static bool done[128];
   const size_t smem = static_cast<size_t>(MT) * p.K;
-  const cudaError_t e = smem_limit_once(few_tokens_kernel<MT, R>, kFewSmem, done);
+  const cudaError_t e = smem_limit_once(few_tokens_kernel<MT, R, H>, kFewSmem, done);
   if (e != cudaSuccess) return e;
-  const int per_sm = MT * R <= 16 ? 2 : 1;
   const int blocks = ((p.N + R - 1) / R + kFewWarps - 1) / kFewWarps;
-  few_tokens_kernel<MT, R><<<blocks < per_sm * sms ? blocks : per_sm * sms, kFewThreads, smem, st>>>(p);
+  few_tokens_kernel<MT, R, H><<<blocks < 2 * sms ? blocks : 2 * sms, kFewThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-// One row of W per warp at a time until the device is full, then 4: the loads of four rows share
-// each read of the tokens and keep four times as many bytes in flight per lane.
+// One row of W per warp, with several of its pieces in flight, until every warp has rows enough;
+// then several rows, which share each read of the tokens.
 template <int MT>
 static cudaError_t launch_few_m(const FewParams& p, int sms, cudaStream_t st) {
-  return p.N < 4 * kFewWarps * sms ? launch_few_t<MT, 1>(p, sms, st) : launch_few_t<MT, 4>(p, sms, st);
+  return p.N < 4 * 2 * kFewWarps * sms ? launch_few_t<MT, 1, MT == 4 ? 4 : 6>(p, sms, st)
+                                       : launch_few_t<MT, 2, 3>(p, sms, st);
 }
 
-static int few_rounded(int64_t M) { return M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8; }
+static int few_rounded(int64_t M) { return M <= 1 ? 1 : M <= 2 ? 2 : 4; }
 
 static bool few_tokens(int64_t M, int64_t K) { return M <= kFewTokens && few_rounded(M) * K <= kFewSmem; }
 
@@ -325,8 +361,7 @@ static cudaError_t launch_few(const FewParams& p, int sms, cudaStream_t st) {
   switch (few_rounded(p.M)) {
     case 1: return launch_few_m<1>(p, sms, st);
     case 2: return launch_few_m<2>(p, sms, st);
-    case 4: return launch_few_m<4>(p, sms, st);
-    default: return launch_few_m<8>(p, sms, st);
+    default: return launch_few_m<4>(p, sms, st);
   }
 }
 

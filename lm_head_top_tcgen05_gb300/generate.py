@@ -14,6 +14,7 @@ current stream of their inputs' device and keep one workspace per stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple, Union
 
 import torch
@@ -25,9 +26,23 @@ __all__ = ["quantize_int8", "int8_matmul", "int8_linear", "sample", "draw_token"
 _Setting = Union[float, int, torch.Tensor]
 _workspaces = {}
 
+# A generation step is a handful of microseconds on the device, so the calls below keep the
+# host's part short: the raw stream without a Stream object, workspace sizes looked up by shape.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
 
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(fn: str, M: int, N: int, K: int, device_index: int) -> int:
+    n = getattr(lib(), fn)(M, N, K)
+    if n == 0:
+        raise FklError(1, fn, f"unsupported shape M={M} N={N} K={K}")
+    return n
 
 
 def _workspace(nbytes: int, device, stream: int, given) -> torch.Tensor:
@@ -44,28 +59,31 @@ def _workspace(nbytes: int, device, stream: int, given) -> torch.Tensor:
 
 
 def _dtype(dtype: torch.dtype, name: str) -> int:
-    if dtype not in DTYPES:
+    kind = DTYPES.get(dtype)
+    if kind is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16")
-    return DTYPES[dtype]
+    return kind
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
-    """Checks a CUDA matrix whose rows are contiguous; its row stride."""
+def _rows(t: torch.Tensor, name: str):
+    """Checks a CUDA matrix whose rows are contiguous: (rows, cols, row stride)."""
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if rows <= 1:
-        return max(cols, 1)
-    if t.stride(0) < cols:
+        ld = max(cols, 1)
+    elif ld < cols:
         raise ValueError(f"the rows of {name} must not overlap")
-    return t.stride(0)
+    return rows, cols, ld
 
 
-def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> None:
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> int:
+    if t.dtype != dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape [{n}] on {device}")
+    return t.data_ptr()
 
 
 def quantize_int8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -73,9 +91,8 @@ def quantize_int8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
 
     scale = largest magnitude / 127, q rounded to nearest even.  A row with a NaN or an infinity
     has scale NaN."""
-    ld = _rows(x, "x")
+    M, K, ld = _rows(x, "x")
     kind = _dtype(x.dtype, "x")
-    M, K = x.shape
     q = torch.empty((M, K), dtype=torch.int8, device=x.device)
     scale = torch.empty(M, dtype=torch.float32, device=x.device)
     st = lib().fkl_quantize_int8(x.data_ptr(), kind, M, K, ld, q.data_ptr(), scale.data_ptr(), _stream(x.device))
@@ -83,19 +100,19 @@ def quantize_int8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     return q, scale
 
 
-def _weight(wq: torch.Tensor, w_scale: torch.Tensor, K: int, device) -> int:
+def _weight(wq: torch.Tensor, K: int, device) -> int:
     if wq.dtype != torch.int8 or wq.dim() != 2 or wq.shape[1] != K or wq.device != device or not wq.is_contiguous():
         raise ValueError(f"wq must be a contiguous int8 tensor [N, {K}] on {device}")
-    _vector(w_scale, "w_scale", torch.float32, wq.shape[0], device)
     return wq.shape[0]
 
 
-def _output(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, device) -> torch.Tensor:
+def _output(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, device):
+    """The output and its row stride."""
     if out is None:
-        return torch.empty((M, N), dtype=dtype, device=device)
-    if out.dtype != dtype or tuple(out.shape) != (M, N) or out.device != device:
+        return torch.empty((M, N), dtype=dtype, device=device), N
+    if out.dtype != dtype or out.shape != (M, N) or out.device != device:
         raise ValueError(f"out must be {dtype} [{M}, {N}] on {device}")
-    return out
+    return out, _rows(out, "out")[2]
 
 
 def int8_matmul(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
@@ -107,17 +124,15 @@ def int8_matmul(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_sca
     if xq.dtype != torch.int8 or xq.dim() != 2 or not xq.is_cuda or not xq.is_contiguous():
         raise ValueError("xq must be a contiguous int8 CUDA tensor [M, K]")
     M, K = xq.shape
+    device = xq.device
     kind = _dtype(out_dtype, "out_dtype")
-    _vector(x_scale, "x_scale", torch.float32, M, xq.device)
-    N = _weight(wq, w_scale, K, xq.device)
-    out = _output(out, M, N, out_dtype, xq.device)
-    n = lib().fkl_int8_matmul_workspace_size(M, N, K)
-    if n == 0:
-        raise FklError(1, "fkl_int8_matmul_workspace_size", f"unsupported shape M={M} N={N} K={K}")
-    stream = _stream(xq.device)
-    ws = _workspace(n, xq.device, stream, workspace)
-    st = lib().fkl_int8_matmul(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), M, N, K, kind,
-                               out.data_ptr(), _rows(out, "out"), ws.data_ptr(), ws.numel(), stream)
+    N = _weight(wq, K, device)
+    xs, ws = _vector(x_scale, "x_scale", torch.float32, M, device), _vector(w_scale, "w_scale", torch.float32, N, device)
+    out, ldo = _output(out, M, N, out_dtype, device)
+    stream = _stream(device)
+    work = _workspace(_workspace_bytes("fkl_int8_matmul_workspace_size", M, N, K, device.index), device, stream, workspace)
+    st = lib().fkl_int8_matmul(xq.data_ptr(), xs, wq.data_ptr(), ws, M, N, K, kind, out.data_ptr(), ldo,
+                               work.data_ptr(), work.numel(), stream)
     check(st, "fkl_int8_matmul")
     return out
 
@@ -129,32 +144,20 @@ def int8_linear(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, out_dt
 
     x is float32, bfloat16 or float16 with contiguous rows any stride apart; out_dtype defaults
     to x's.  K is a multiple of 16."""
-    ldx = _rows(x, "x")
-    M, K = x.shape
+    M, K, ldx = _rows(x, "x")
+    device = x.device
     x_kind = _dtype(x.dtype, "x")
     out_dtype = x.dtype if out_dtype is None else out_dtype
     out_kind = _dtype(out_dtype, "out_dtype")
-    N = _weight(wq, w_scale, K, x.device)
-    out = _output(out, M, N, out_dtype, x.device)
-    n = lib().fkl_int8_linear_workspace_size(M, N, K)
-    if n == 0:
-        raise FklError(1, "fkl_int8_linear_workspace_size", f"unsupported shape M={M} N={N} K={K}")
-    stream = _stream(x.device)
-    ws = _workspace(n, x.device, stream, workspace)
-    st = lib().fkl_int8_linear(x.data_ptr(), x_kind, ldx, wq.data_ptr(), w_scale.data_ptr(), M, N, K, out_kind,
-                               out.data_ptr(), _rows(out, "out"), ws.data_ptr(), ws.numel(), stream)
+    N = _weight(wq, K, device)
+    ws = _vector(w_scale, "w_scale", torch.float32, N, device)
+    out, ldo = _output(out, M, N, out_dtype, device)
+    stream = _stream(device)
+    work = _workspace(_workspace_bytes("fkl_int8_linear_workspace_size", M, N, K, device.index), device, stream, workspace)
+    st = lib().fkl_int8_linear(x.data_ptr(), x_kind, ldx, wq.data_ptr(), ws, M, N, K, out_kind, out.data_ptr(), ldo,
+                               work.data_ptr(), work.numel(), stream)
     check(st, "fkl_int8_linear")
     return out
-
-
-def _setting(p: FklSampleParams, name: str, value: _Setting, dtype: torch.dtype, B: int, device) -> None:
-    if isinstance(value, torch.Tensor):
-        _vector(value, name, dtype, B, device)
-        setattr(p, name + "_rows", value.data_ptr())
-    elif dtype == torch.int32:
-        setattr(p, name, max(0, min(int(value), 2**31 - 1)))
-    else:
-        setattr(p, name, float(value))
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature: _Setting = 1.0, top_k: _Setting = 0,
@@ -168,20 +171,24 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: _Setting = 1.0, t
     largest logit), top_k (0 keeps all), top_p (1 keeps all) and min_p (0 keeps all), applied in
     this order; ties keep the lower id.  The same inputs always give the same tokens.  A row
     whose logits are all -inf (or NaN, which counts as -inf) gives token -1 and logprob NaN."""
-    ld = _rows(logits, "logits")
+    B, V, ld = _rows(logits, "logits")
     kind = _dtype(logits.dtype, "logits")
-    B, V = logits.shape
     device = logits.device
-    _vector(u, "u", torch.float32, B, device)
-    p = FklSampleParams()
-    _setting(p, "temperature", temperature, torch.float32, B, device)
-    _setting(p, "top_k", top_k, torch.int32, B, device)
-    _setting(p, "top_p", top_p, torch.float32, B, device)
-    _setting(p, "min_p", min_p, torch.float32, B, device)
+    up = _vector(u, "u", torch.float32, B, device)
+    rows = [None, None, None, None]
+    if isinstance(temperature, torch.Tensor):
+        rows[0], temperature = _vector(temperature, "temperature", torch.float32, B, device), 1.0
+    if isinstance(top_k, torch.Tensor):
+        rows[1], top_k = _vector(top_k, "top_k", torch.int32, B, device), 0
+    if isinstance(top_p, torch.Tensor):
+        rows[2], top_p = _vector(top_p, "top_p", torch.float32, B, device), 1.0
+    if isinstance(min_p, torch.Tensor):
+        rows[3], min_p = _vector(min_p, "min_p", torch.float32, B, device), 0.0
+    p = FklSampleParams(temperature, max(0, min(int(top_k), 2**31 - 1)), top_p, min_p, *rows)
     token = torch.empty(B, dtype=torch.int32, device=device)
     logprob = torch.empty(B, dtype=torch.float32, device=device)
-    st = lib().fkl_sample(logits.data_ptr(), kind, B, V, ld, u.data_ptr(), ctypes.byref(p), token.data_ptr(),
-                          logprob.data_ptr(), _stream(device))
+    st = lib().fkl_sample(logits.data_ptr(), kind, B, V, ld, up, ctypes.byref(p), token.data_ptr(), logprob.data_ptr(),
+                          _stream(device))
     check(st, "fkl_sample")
     return token, logprob
 
