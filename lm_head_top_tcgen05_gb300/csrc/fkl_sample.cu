@@ -8,21 +8,26 @@
 //
 // One cluster of 1 to 8 CTAs per row.  Each CTA reads its slice of the row once into shared
 // memory, where all further passes run; the CTAs exchange a few sums through distributed
-// shared memory.  The steps:
+// shared memory.  After the load every CTA knows the row's largest logit m.  Then
 //
-//   1. load      the slice, each thread's largest logit, the row's largest m, and tau, a lower
-//                bound of the target-th largest logit: the least, over the CTAs, of the
-//                ceil(target / C)-th largest of their threads' maxima;
-//   2. gather    the logits >= tau into a list (and, for top-p alone, the total weight).  The
-//                list holds the top k by construction, or is checked to hold the top-p weight;
-//   3. finish    the first CTA sorts the list (some hundreds of entries), cuts it, sorts what
-//                stays by id and draws.
+//   no top-k, no top-p   one pass sums the weights (of what min-p keeps) per warp, and the draw
+//                        looks up the id in the one warp's stretch that holds it;
+//   top-k up to 512      a list: tau is a lower bound of the k-th largest logit (the least, over the
+//                        CTAs, of the k / C-th largest of their threads' maxima), the logits
+//                        >= tau (about k log-many) are gathered and the first CTA finishes;
+//   otherwise            a histogram over 2048 bins of equal width in z (of counts for top-k, of
+//                        weights rounded to 2^-17 for top-p, beside their exact sum) gives the bin of
+//                        the boundary; a second pass sums the exact weights above that bin per
+//                        warp and lists the bin's logits, from which the first CTA takes the
+//                        boundary.  The rounded histogram only proposes the bin: the exact sums
+//                        confirm it.
 //
-// When the list cannot hold the answer (a flat row whose top-p set has thousands of ids, a
-// large k, many ties) the boundary is found from histograms instead: 1024 bins of equal width
-// in z, then of the logits' bits within the bin that holds the boundary, until its logits fit
-// the list or are all equal; then the draw makes two more passes over the slices.  Without
-// top-k and top-p only the draw remains.
+// When the list or the bin holds too many logits (many ties, a temperature so high that a bin is
+// most of the row), or the bin is not confirmed, the boundary is found from exact histograms,
+// first in z and then of the logits' bits, until what is left fits a list or is all equal.
+//
+// The passes are bound by their instructions (about 15 per logit with the exponential), not by
+// memory: that is why the exact sums are kept in two 32-bit words, see WeightSum.
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -38,7 +43,10 @@ constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxSampleV = int64_t{1} << 22;  // 2^22 weights of 2^40 stay below 2^63
 constexpr int kBins = 1024;
 constexpr int kListCap = 1024;
-constexpr int kTopPTarget = 192;  // list entries aimed at for top-p alone
+constexpr int kZBins = 2304;           // of the first histogram, over z in [-kZRange, 0]
+constexpr float kZRange = 24.f;        // lower logits (weights below 2^-34) share the last bin
+constexpr int kFineBins = 2048;        // of the second one, over one bin of the first
+constexpr int kCountingMax = 160;      // longest list that is ranked by counting, not sorted
 
 using u64 = unsigned long long;
 
@@ -51,40 +59,81 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// floor(2^40 e) for 0 <= e <= 1, from e's bits.
+// floor(2^40 e) for 0 <= e <= 1 in two words: hi = floor(2^17 e) and the rest's lo = floor(2^40 rest)
+// < 2^23.  Adding 64, whose last place is 2^-17, with rounding down leaves hi in the low bits of
+// the sum; the rest e - hi 2^-17 is exact, and adding 2^-17, whose last place is 2^-40, to it
+// leaves lo in the same way.
+constexpr uint32_t kHiBias = 0x42800000u, kLoBias = 0x37000000u;  // bits of 64 and of 2^-17
+__device__ __forceinline__ void split_weight(float e, uint32_t& hi, uint32_t& lo) {  // biased
+  const float t = __fadd_rd(e, 64.f);
+  const float rest = __fsub_rn(e, __fsub_rn(t, 64.f));
+  hi = __float_as_uint(t);
+  lo = __float_as_uint(__fadd_rd(rest, 7.62939453125e-6f));
+}
 __device__ __forceinline__ u64 fixed_point(float e) {
-  const uint32_t b = __float_as_uint(e);
-  const int s = static_cast<int>(b >> 23) - 110;  // 2^40 e = mantissa * 2^s
-  const uint32_t mant = (b & 0x7fffffu) | 0x800000u;
-  return static_cast<u64>(mant >> min(max(-s, 0), 31)) * (1u << max(s, 0));
+  uint32_t hi, lo;
+  split_weight(e, hi, lo);
+  return (static_cast<u64>(hi - kHiBias) << 23) + (lo - kLoBias);
 }
 
-// The row's largest logit and its scale.
+// Exact sum of up to kMaxAdds weights in two words (the biases are taken off at the end).
+struct WeightSum {
+  static constexpr int kMaxAdds = 512;
+  uint32_t hi = 0, lo = 0, n = 0;
+  __device__ __forceinline__ void add(float e) {
+    uint32_t h, l;
+    split_weight(e, h, l);
+    hi += h;
+    lo += l;
+    ++n;
+  }
+  __device__ __forceinline__ u64 total() const {
+    return (static_cast<u64>(hi - n * kHiBias) << 23) + (lo - n * kLoBias);
+  }
+};
+
+// The row's largest logit and its scale.  kPlain: m and 1/T are ordinary numbers, so (x - m) / T
+// needs no special cases.
+template <bool kPlain>
 struct RowScale {
   float m, inv_t;
-  bool plain;  // m and 1/T are ordinary numbers: (x - m) / T needs no special cases
   __device__ __forceinline__ float z(float x) const {
-    if (plain) return (x - m) * inv_t;
+    if (kPlain) return (x - m) * inv_t;
     return x == m ? 0.f : (x - m) * inv_t;
   }
   // exp(z); 0 for -inf (and where infinities leave no number)
   __device__ __forceinline__ float e(float x) const {
     const float v = expf(z(x));
-    if (plain) return v;
+    if (kPlain) return v;
     return x > -INFINITY && v > 0.f ? v : 0.f;
   }
   __device__ __forceinline__ u64 weight(float x) const { return fixed_point(e(x)); }
+  // Bin of the first histogram as a float 2^23 + bin (rounded to nearest); falls as x rises.
+  __device__ __forceinline__ float z_bin_of(float z) const {
+    const float u = fmaf(z, -static_cast<float>(kZBins) / kZRange, 8388608.f);
+    return fminf(u, 8388608.f + static_cast<float>(kZBins - 1));
+  }
+  __device__ __forceinline__ float z_bin(float x) const { return z_bin_of(z(x)); }
+  // Bin of the second histogram, within `bin` of the first: rises and falls with z alone too.
+  __device__ __forceinline__ int fine_bin(float x, int bin) const {
+    constexpr float kScale = static_cast<float>(kZBins) / kZRange * static_cast<float>(kFineBins);
+    const float mid = static_cast<float>(bin) * (kZRange / static_cast<float>(kZBins));
+    const float u = (z(x) + mid) * -kScale + static_cast<float>(kFineBins / 2);
+    return static_cast<int>(fminf(fmaxf(u, 0.f), static_cast<float>(kFineBins - 1)));
+  }
 };
 
-// A boundary in the order (logit descending, id ascending).
+// A boundary in the order (logit descending, id ascending): the last logit that is kept, with its
+// id.  -0 and +0 compare equal, as in the order.
 struct Boundary {
-  uint32_t key;
+  float x;
   int id;
-  __device__ __forceinline__ bool keeps(uint32_t k, int v) const { return k > key || (k == key && v <= id); }
+  __device__ __forceinline__ bool keeps(float v, int i) const { return v > x || (v == x && i <= id); }
 };
+__device__ __forceinline__ Boundary no_boundary() { return Boundary{-INFINITY, INT_MAX}; }
 
-// Weights (41 bits) are added to the histograms in pieces, each into 32 bits: 3 of 14 bits for
-// a slice in shared memory (at most 2^17 logits), 4 of 12 bits for longer ones (at most 2^19).
+// Weights (41 bits) are added to the exact histograms in pieces, each into 32 bits: 3 of 14 bits
+// for a slice in shared memory (at most 2^17 logits), 4 of 12 bits for longer ones (at most 2^19).
 template <bool kResident>
 struct Pieces {
   static constexpr int kCount = kResident ? 3 : 4, kBits = kResident ? 14 : 12;
@@ -94,22 +143,31 @@ static_assert(Pieces<false>::kMaxSlice * kMaxCluster >= kMaxSampleV, "a piece su
 
 template <bool kResident>
 struct SampleShared {
-  // a histogram, then the list of gathered logits, in the same place
   union {
-    uint32_t hist[Pieces<kResident>::kCount][kBins];
-    u64 list[kListCap];
+    struct {
+      union {
+        uint32_t fine[kFineBins];
+        u64 list[kListCap];  // the first CTA's list of the whole row: (key, ~id)
+      };
+      uint32_t near_ids[kListCap];  // this CTA's gathered ids
+    };
+    uint32_t zhist[kZBins];
+    uint32_t hist[Pieces<kResident>::kCount][kBins];  // exact histograms
   } work;
   u64 warp_sum[kSampleWarps];
+  u64 kept_sum[kSampleWarps];  // weight that the draw can reach, per warp's stretch of the row
   // exchanged between the CTAs of the cluster (written before a cluster barrier, read after)
-  u64 part[2];
+  u64 part[4];
   uint32_t count, key_lo, key_hi;
   float cta_max, tau;
   Boundary bound;
+  int found;
   // this CTA only
   float warp_max[kSampleWarps];
+  uint32_t warp_lo[kSampleWarps], warp_hi[kSampleWarps];
   uint32_t list_count, lo, hi;
   int bin;
-  u64 before;
+  u64 before, want, draw;
 };
 
 // Barrier of the cluster's threads: shared memory written before it is seen by every CTA after.
@@ -187,6 +245,32 @@ __device__ void sort_descending(u64* keys, int n) {
   __syncthreads();
 }
 
+// The largest of a vector's logits, or NaN if one is NaN.
+template <class T>
+__device__ __forceinline__ float vector_max(const uint4& raw);
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <>
+__device__ __forceinline__ float vector_max<float>(const uint4& raw) {
+  const float w = __uint_as_float(raw.w);
+  return max3_nan(max3_nan(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z)), w, w);
+}
+template <>
+__device__ __forceinline__ float vector_max<__nv_bfloat16>(const uint4& raw) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+  return __bfloat162float(__hmax_nan(m.x, m.y));
+}
+template <>
+__device__ __forceinline__ float vector_max<__half>(const uint4& raw) {
+  const __half2* h = reinterpret_cast<const __half2*>(&raw);
+  const __half2 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+  return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+}
+
 // One CTA's slice of a row: ids [first, first + n), as 16-byte vectors of E logits.  Vectors are
 // aligned in global memory, so the first and the last may be partial; the rest of them reads
 // -inf, and so does NaN.  kResident: the vectors are held in shared memory.
@@ -200,30 +284,70 @@ struct Slice {
 
   __device__ __forceinline__ int id(int i, int j) const { return first + i * E + j - shift; }
 
-  __device__ __forceinline__ void read_global(int i, float (&v)[E]) const {
-    const int at = i * E - shift;
-    if (at >= 0 && at + E <= n) {
-      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(g + at));
-      unpack16<T>(raw, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j) v[j] = at + j >= 0 && at + j < n ? to_float(g[at + j]) : -INFINITY;
-    }
-#pragma unroll
-    for (int j = 0; j < E; ++j) v[j] = v[j] == v[j] ? v[j] : -INFINITY;
-  }
-  __device__ __forceinline__ void put(int i, const float (&v)[E]) const {
+  __device__ __forceinline__ bool inside(int i) const { return i * E >= shift && i * E - shift + E <= n; }
+  // A vector at the slice's end, with -inf outside.
+  __device__ __forceinline__ uint4 edge(int i) const {
     uint4 raw;
     T* e = reinterpret_cast<T*>(&raw);
+    const int at = i * E - shift;
 #pragma unroll
-    for (int j = 0; j < E; ++j) e[j] = from_float<T>(v[j]);  // exact: the values came from T
-    s[i] = raw;
+    for (int j = 0; j < E; ++j) e[j] = at + j >= 0 && at + j < n ? g[at + j] : from_float<T>(-INFINITY);
+    return raw;
+  }
+  // The largest logit of a vector, in which NaN becomes -inf.  NaN is rare, so it is looked for in
+  // the maximum, which it passes through.
+  static __device__ __forceinline__ float settle(uint4& raw, bool& changed) {
+    float most = vector_max<T>(raw);
+    changed = most != most;
+    if (changed) {
+      float v[E];
+      unpack16<T>(raw, v);
+      T* e = reinterpret_cast<T*>(&raw);
+      most = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        v[j] = v[j] == v[j] ? v[j] : -INFINITY;
+        most = fmaxf(most, v[j]);
+        e[j] = from_float<T>(v[j]);
+      }
+    }
+    return most;
+  }
+  // This thread's vectors (v0 + lane, every 32nd) into shared memory, and their largest logit.  All
+  // of the copies are in flight at once: an SM then has 200 KB under way, which HBM's latency needs.
+  __device__ __forceinline__ float load(int lane) const {
+    float most = -INFINITY;
+    bool changed;
+    if constexpr (kResident) {
+      for (int i = v0 + lane; i < v1; i += 32) {
+        if (inside(i))
+          copy16_async(s + i, g + (i * E - shift));
+        else
+          s[i] = edge(i);
+      }
+      copy_async_wait();
+      for (int i = v0 + lane; i < v1; i += 32) {
+        uint4 raw = s[i];
+        most = fmaxf(most, settle(raw, changed));
+        if (changed) s[i] = raw;
+      }
+    } else {
+      for (int i = v0 + lane; i < v1; i += 32) {
+        uint4 raw = inside(i) ? __ldg(reinterpret_cast<const uint4*>(g + (i * E - shift))) : edge(i);
+        most = fmaxf(most, settle(raw, changed));
+      }
+    }
+    return most;
   }
   __device__ __forceinline__ void get(int i, float (&v)[E]) const {
-    if (kResident)
-      unpack16<T>(s[i], v);
-    else
-      read_global(i, v);
+    unpack16<T>(raw(i), v);
+  }
+  __device__ __forceinline__ uint4 raw(int i) const {
+    if (kResident) return s[i];
+    uint4 v = inside(i) ? __ldg(reinterpret_cast<const uint4*>(g + (i * E - shift))) : edge(i);
+    bool changed;
+    settle(v, changed);
+    return v;
   }
   // f(logit, id) for every element of this warp's vectors.
   template <class F>
@@ -234,280 +358,6 @@ struct Slice {
 #pragma unroll
       for (int j = 0; j < E; ++j) f(v[j], id(i, j));
     }
-  }
-};
-
-// State of one row, shared by the steps.
-template <class T, bool kResident>
-struct RowCtx {
-  Slice<T, kResident> slice;
-  SampleShared<kResident>& s;
-  u64* merged;  // this CTA's share of the merged histogram: kBins / ranks sums
-  RowScale rs;
-  int rank, ranks, warp, lane;
-
-  // Sum of v over the block's threads, into s.part[slot] (visible to the cluster after its
-  // next barrier).
-  __device__ __forceinline__ void sum_to_part(u64 v, int slot) {
-    v = warp_add(v);
-    __syncthreads();
-    if (lane == 0) s.warp_sum[warp] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      u64 t = 0;
-      for (int w = 0; w < kSampleWarps; ++w) t += s.warp_sum[w];
-      s.part[slot] = t;
-    }
-  }
-  // Sum of part[slot] over the cluster, and over the CTAs before this one.
-  __device__ __forceinline__ u64 total_of(int slot, u64* before = nullptr) {
-    u64 t = 0;
-    for (int r = 0; r < ranks; ++r) {
-      if (r == rank && before != nullptr) *before = t;
-      t += peer(&s, r)->part[slot];
-    }
-    return t;
-  }
-  __device__ __forceinline__ uint32_t total_count() {
-    uint32_t t = 0;
-    for (int r = 0; r < ranks; ++r) t += peer(&s, r)->count;
-    return t;
-  }
-
-  // Appends the logits for which f holds to this CTA's list; their number (which may exceed
-  // the list) and the range of their keys go to s.count, s.key_lo and s.key_hi.
-  template <class F>
-  __device__ void gather(F f) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s.list_count = 0;
-      s.lo = 0xffffffffu;
-      s.hi = 0u;
-    }
-    __syncthreads();
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    slice.each(lane, [&](float x, int v) {
-      if (f(x, v)) {
-        const uint32_t k = logit_key(x);
-        lo = min(lo, k);
-        hi = max(hi, k);
-        const uint32_t at = atomicAdd(&s.list_count, 1u);
-        if (at < kListCap) s.work.list[at] = (static_cast<u64>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(v));
-      }
-    });
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0 && lo <= hi) {
-      atomicMin(&s.lo, lo);
-      atomicMax(&s.hi, hi);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s.count = s.list_count;
-      s.key_lo = s.lo;
-      s.key_hi = s.hi;
-    }
-  }
-  // Moves this CTA's list behind those of the CTAs before it, in the first CTA.  Between two
-  // cluster barriers.
-  __device__ __forceinline__ void push_list() {
-    if (rank == 0) return;
-    uint32_t at = 0;
-    for (int r = 0; r < rank; ++r) at += peer(&s, r)->count;
-    u64* to = peer(&s.work.list[0], 0);
-    for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) to[at + i] = s.work.list[i];
-  }
-  // First CTA: pads the list's n entries to a power of two and sorts them.
-  __device__ __forceinline__ void sort_list(u64* keys, int n) {
-    int n2 = 1;
-    while (n2 < n) n2 <<= 1;
-    for (int i = n + threadIdx.x; i < n2; i += kSampleThreads) keys[i] = 0;
-    sort_descending(keys, n2);
-  }
-
-  // Histogram over the cluster of f's amounts (f(x, v, bin, amount) gives whether the logit
-  // counts, its bin and its amount): the bin at which the running sum reaches `want`, and the
-  // sum before it.
-  template <class F>
-  __device__ int find_bin(u64 want, u64& before, F f) {
-    using P = Pieces<kResident>;
-    __syncthreads();
-    for (int i = threadIdx.x; i < P::kCount * kBins; i += kSampleThreads) s.work.hist[0][i] = 0;
-    __syncthreads();
-    slice.each(lane, [&](float x, int v) {
-      uint32_t bin;
-      u64 amount;
-      if (f(x, v, bin, amount)) {
-#pragma unroll
-        for (int q = 0; q < P::kCount; ++q) {
-          const uint32_t part = static_cast<uint32_t>(amount >> (q * P::kBits)) & ((1u << P::kBits) - 1);
-          if (part) atomicAdd(&s.work.hist[q][bin], part);
-        }
-      }
-    });
-    sync_cluster();
-    // this CTA merges its share of the bins
-    const int per = kBins / ranks;
-    u64 sum = 0;
-    for (int i = threadIdx.x; i < per; i += kSampleThreads) {
-      u64 t = 0;
-      for (int r = 0; r < ranks; ++r) {
-        const SampleShared<kResident>* o = peer(&s, r);
-#pragma unroll
-        for (int q = 0; q < P::kCount; ++q) t += static_cast<u64>(o->work.hist[q][rank * per + i]) << (q * P::kBits);
-      }
-      merged[i] = t;
-      sum += t;
-    }
-    sum_to_part(sum, 0);
-    sync_cluster();
-    // the share that holds the boundary, then the bin within it
-    u64 run = 0;
-    int owner = ranks - 1;
-    for (int r = 0; r < ranks; ++r) {
-      const u64 t = peer(&s, r)->part[0];
-      if (run + t >= want) {
-        owner = r;
-        break;
-      }
-      if (r + 1 < ranks) run += t;
-    }
-    const u64* m = peer(merged, owner);
-    const int i0 = 2 * static_cast<int>(threadIdx.x);
-    const u64 a = i0 < per ? m[i0] : 0, b = i0 + 1 < per ? m[i0 + 1] : 0;
-    u64 total;
-    const u64 upto = run + block_prefix(a + b, s.warp_sum, total);
-    if (threadIdx.x == 0) s.bin = -1;
-    __syncthreads();
-    const u64 start = upto - a - b;
-    if (start < want && want <= upto) {
-      const bool second = start + a < want;
-      s.bin = owner * per + i0 + (second ? 1 : 0);
-      s.before = start + (second ? a : 0);
-    }
-    __syncthreads();
-    before = s.before;
-    return s.bin;
-  }
-
-  // Sum of f over the ids before, and the id at which the running sum exceeds r, when it lies in
-  // this CTA: each warp's sum must be in s.warp_sum and `before` be the sum of the CTAs before.
-  // Returns the id in every lane of the warp that holds it, -1 elsewhere.
-  template <class F>
-  __device__ __forceinline__ int locate(u64 before, u64 r, F f) {
-    constexpr int E = Slice<T, kResident>::E;
-    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-    if (!(before <= r && r < before + s.warp_sum[warp])) return -1;
-    for (int i0 = slice.v0; i0 < slice.v1; i0 += 32) {
-      const int i = i0 + lane;
-      u64 a[E], sum = 0;
-#pragma unroll
-      for (int j = 0; j < E; ++j) a[j] = 0;
-      if (i < slice.v1) {
-        float v[E];
-        slice.get(i, v);
-#pragma unroll
-        for (int j = 0; j < E; ++j) sum += a[j] = f(v[j], slice.id(i, j));
-      }
-      const u64 run = before + warp_prefix(sum, lane);
-      const uint32_t hit = __ballot_sync(0xffffffffu, run > r);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        u64 c = run - sum;
-        int id = -1;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          c += a[j];
-          if (id < 0 && c > r) id = slice.id(i, j);
-        }
-        return __shfl_sync(0xffffffffu, id, src);
-      }
-      before = __shfl_sync(0xffffffffu, run, 31);
-    }
-    return -1;
-  }
-
-  // The boundary at which `want` logits (by_mass false) or a weight of `want` (by_mass true)
-  // have been kept, among those that `keeps`; want is at least 1 and at most what there is.
-  // The whole cluster.
-  __device__ Boundary find_boundary(const Boundary& keeps, bool by_mass, u64 want) {
-    // z of weight 1 (2^-40) is -27.7; logits further down share the last bin
-    const float scale = static_cast<float>(kBins) / 27.8f;
-    auto z_bin = [&](float x) -> uint32_t {  // falls as x rises; rounds to the nearest bin
-      const float t = fminf(rs.z(x) * -scale, static_cast<float>(kBins - 1));
-      return __float_as_uint(t + 8388608.f) & (kBins - 1);
-    };
-    auto amount_of = [&](float x) -> u64 { return by_mass ? rs.weight(x) : 1ull; };
-    u64 before = 0;
-    int bin = find_bin(want, before, [&](float x, int v, uint32_t& b, u64& amount) -> bool {
-      if (!(x > -INFINITY) || !keeps.keeps(logit_key(x), v)) return false;
-      b = z_bin(x);
-      amount = amount_of(x);
-      return true;
-    });
-    want -= before;
-    gather([&](float x, int v) {
-      return x > -INFINITY && static_cast<int>(z_bin(x)) == bin && keeps.keeps(logit_key(x), v);
-    });
-    for (;;) {
-      sync_cluster();
-      const uint32_t n = total_count();
-      uint32_t lo = 0xffffffffu, hi = 0u;
-      for (int r = 0; r < ranks; ++r) {
-        lo = min(lo, peer(&s, r)->key_lo);
-        hi = max(hi, peer(&s, r)->key_hi);
-      }
-      if (n <= kListCap) {
-        push_list();
-        sync_cluster();
-        if (rank == 0) {
-          sort_list(s.work.list, static_cast<int>(n));
-          const int i0 = 2 * static_cast<int>(threadIdx.x);
-          u64 w[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[j] = i0 + j < static_cast<int>(n) ? amount_of(key_logit(static_cast<uint32_t>(s.work.list[i0 + j] >> 32))) : 0;
-          u64 total;
-          const u64 upto = block_prefix(w[0] + w[1], s.warp_sum, total);
-          const u64 start = upto - w[0] - w[1];
-          if (start < want && want <= upto) {
-            const u64 c = s.work.list[i0 + (start + w[0] < want ? 1 : 0)];
-            s.bound = Boundary{static_cast<uint32_t>(c >> 32), static_cast<int>(0xffffffffu - static_cast<uint32_t>(c))};
-          }
-        }
-        break;
-      }
-      if (lo == hi) {  // more equal logits than the list holds: the ids decide
-        const u64 each = by_mass ? rs.weight(key_logit(lo)) : 1ull;
-        const u64 skip = (want - 1) / each;  // equal logits kept before the last one
-        auto tie = [&](float x, int v) -> u64 { return logit_key(x) == lo && keeps.keeps(lo, v) ? 1ull : 0ull; };
-        u64 sum = 0, ahead = 0;
-        slice.each(lane, [&](float x, int v) { sum += tie(x, v); });
-        sum_to_part(sum, 0);
-        sync_cluster();
-        total_of(0, &ahead);
-        const int id = locate(ahead, skip, tie);
-        if (id >= 0 && lane == 0) peer(&s, 0)->bound = Boundary{lo, id};
-        break;
-      }
-      const int bits = 32 - __clz(hi - lo);
-      const int shift = bits > 10 ? bits - 10 : 0;
-      static_assert(kBins == 1 << 10, "bins of the logits' bits");
-      bin = find_bin(want, before, [&](float x, int v, uint32_t& b, u64& amount) -> bool {
-        const uint32_t k = logit_key(x);
-        if (k < lo || k > hi || !keeps.keeps(k, v)) return false;
-        b = (hi - k) >> shift;
-        amount = amount_of(x);
-        return true;
-      });
-      want -= before;
-      gather([&](float x, int v) {
-        const uint32_t k = logit_key(x);
-        return k >= lo && k <= hi && static_cast<int>((hi - k) >> shift) == bin && keeps.keeps(k, v);
-      });
-    }
-    sync_cluster();
-    return peer(&s, 0)->bound;
   }
 };
 
@@ -526,6 +376,809 @@ __device__ __forceinline__ float log_probability(float z, u64 total) {
   return z - logf(static_cast<float>(total) * 9.094947017729282e-13f);  // 2^-40
 }
 
+// State of one row, shared by the steps.
+template <class T, bool kResident, bool kPlain>
+struct RowCtx {
+  static constexpr int E = Slice<T, kResident>::E;
+  const Slice<T, kResident>& slice;
+  SampleShared<kResident>& s;
+  u64* merged;  // this CTA's share of the merged histogram
+  RowScale<kPlain> rs;
+  int rank, ranks, warp, lane;
+
+  // Sum of v over the block's threads, into s.part[slot] (visible to the cluster after its
+  // next barrier); the warps' sums stay in `warps`.
+  __device__ __forceinline__ void sum_to_part(u64 v, int slot, u64* warps) {
+    v = warp_add(v);
+    __syncthreads();
+    if (lane == 0) warps[warp] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      u64 t = 0;
+      for (int w = 0; w < kSampleWarps; ++w) t += warps[w];
+      s.part[slot] = t;
+    }
+  }
+  // Sum of part[slot] over the cluster, and over the CTAs before this one.  Lane r of each warp
+  // reads CTA r's, so that it takes one trip to their shared memory.
+  __device__ __forceinline__ u64 total_of(int slot, u64* before = nullptr) {
+    const u64 v = lane < ranks ? peer(&s, lane)->part[slot] : 0ull;
+    const u64 run = warp_prefix(v, lane);
+    if (before != nullptr) *before = __shfl_sync(0xffffffffu, run - v, rank);
+    return __shfl_sync(0xffffffffu, run, 31);
+  }
+  __device__ __forceinline__ uint32_t total_count(uint32_t* before = nullptr) {
+    const uint32_t v = lane < ranks ? peer(&s, lane)->count : 0u;
+    if (before != nullptr) *before = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0u);
+    return __reduce_add_sync(0xffffffffu, v);
+  }
+  // A value that one thread computes in double (those units are few), for the block.
+  template <class F>
+  __device__ __forceinline__ u64 by_one_thread(u64& slot, F f) {
+    if (threadIdx.x == 0) slot = f();
+    __syncthreads();
+    return slot;
+  }
+
+  // Exact sum of the weights f adds (f(x, id, sum)) over this thread's logits.
+  template <class F>
+  __device__ __forceinline__ u64 sum_weights(F f) {
+    WeightSum sum;
+    u64 total = 0;
+    for (int i = slice.v0 + lane; i < slice.v1; i += 32) {
+      float v[E];
+      slice.get(i, v);
+#pragma unroll
+      for (int j = 0; j < E; ++j) f(v[j], slice.id(i, j), sum);
+      if (!kResident && sum.n > WeightSum::kMaxAdds - E) {  // a resident slice has at most 256 a thread
+        total += sum.total();
+        sum = WeightSum();
+      }
+    }
+    return total + sum.total();
+  }
+
+  // The same of every weight, two logits at a time where that is one instruction.
+  __device__ __forceinline__ u64 sum_all() {
+    if constexpr (!kPlain || !kResident) {
+      return sum_weights([&](float x, int, WeightSum& w) { w.add(rs.e(x)); });
+    } else {
+      WeightSum sum;
+      const float2 om = make_float2(-rs.m, -rs.m), it = make_float2(rs.inv_t, rs.inv_t);
+      for (int i = slice.v0 + lane; i < slice.v1; i += 32) {
+        float v[E];
+        slice.get(i, v);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+          const float2 z = fmul2(fadd2(make_float2(v[j], v[j + 1]), om), it);
+          sum.add(expf(z.x));
+          sum.add(expf(z.y));
+        }
+      }
+      return sum.total();
+    }
+  }
+
+  // Resets this CTA's list.
+  __device__ __forceinline__ void clear_list() {
+    __syncthreads();
+    if (threadIdx.x == 0) s.list_count = 0;
+    __syncthreads();
+  }
+  __device__ __forceinline__ void append(int id) {
+    const uint32_t at = atomicAdd(&s.list_count, 1u);
+    if (at < kListCap) s.work.near_ids[at] = static_cast<uint32_t>(id);
+  }
+  __device__ __forceinline__ float logit(int id) const {
+    if (kResident) {
+      const int at = id - slice.first + slice.shift;
+      return to_float(reinterpret_cast<const T*>(slice.s)[at]);
+    }
+    const float x = to_float(slice.g[id - slice.first]);
+    return x == x ? x : -INFINITY;
+  }
+  __device__ __forceinline__ u64 entry(int id, float x) const {
+    return (static_cast<u64>(logit_key(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+  }
+  static __device__ __forceinline__ float entry_logit(u64 e) { return key_logit(static_cast<uint32_t>(e >> 32)); }
+  static __device__ __forceinline__ int entry_id(u64 e) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)); }
+  // Brings the CTAs' lists together in the first CTA, in the order of the CTAs.  Between two
+  // cluster barriers; s.count is this CTA's number.
+  __device__ __forceinline__ void push_list() {
+    uint32_t at;
+    total_count(&at);
+    u64* to = rank == 0 ? &s.work.list[0] : peer(&s.work.list[0], 0);
+    for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) {
+      const int id = static_cast<int>(s.work.near_ids[i]);
+      to[at + i] = entry(id, logit(id));
+    }
+  }
+  // First CTA: pads the list's n entries to a power of two and sorts them.
+  __device__ __forceinline__ void sort_list(u64* keys, int n) {
+    int n2 = 1;
+    while (n2 < n) n2 <<= 1;
+    for (int i = n + threadIdx.x; i < n2; i += kSampleThreads) keys[i] = 0;
+    sort_descending(keys, n2);
+  }
+  // First CTA: in the sorted list of n entries, the one at which the running sum of amounts (1,
+  // or the weights) reaches want, into s.bound; s.found tells whether there is one.
+  __device__ __forceinline__ void bound_in_list(int n, bool by_mass, u64 want) {
+    if (threadIdx.x == 0) s.found = 0;
+    const int i0 = 2 * static_cast<int>(threadIdx.x);
+    u64 w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) w[j] = i0 + j < n ? (by_mass ? rs.weight(entry_logit(s.work.list[i0 + j])) : 1ull) : 0ull;
+    u64 total;
+    const u64 upto = block_prefix(w[0] + w[1], s.warp_sum, total);
+    const u64 start = upto - w[0] - w[1];
+    if (start < want && want <= upto) {
+      const u64 c = s.work.list[i0 + (start + w[0] < want ? 1 : 0)];
+      s.bound = Boundary{entry_logit(c), entry_id(c)};
+      s.found = 1;
+    }
+  }
+
+  // Merges the CTAs' histograms (read(other, bin) gives a bin's sum) and finds the bin at which the
+  // running sum reaches `want`, and the sum before it.  Called after a cluster barrier; ends
+  // with the histograms free.  -1: the sum stays below want.
+  template <class F>
+  __device__ int merge_bins(int bins, u64 want, u64& before, F read) {
+    const int per = bins / ranks;
+    u64 sum = 0;
+    for (int i = threadIdx.x; i < per; i += kSampleThreads) {
+      u64 t = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < ranks) t += read(peer(&s, r), rank * per + i);
+      merged[i] = t;
+      sum += t;
+    }
+    sum_to_part(sum, 0, s.warp_sum);
+    sync_cluster();
+    // the share that holds the boundary, then the bin within it
+    const u64 share = lane < ranks ? peer(&s, lane)->part[0] : 0ull;
+    const u64 upto = warp_prefix(share, lane);
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
+    if (owner < 0) return -1;
+    const u64 run = __shfl_sync(0xffffffffu, upto - share, owner);
+    const u64* m = peer(merged, owner);
+    constexpr int kPer = (kZBins + kSampleThreads - 1) / kSampleThreads;
+    static_assert(kZBins >= kBins && kZBins >= kFineBins && kZBins % (2 * kMaxCluster) == 0, "a thread's bins; 16-byte shares");
+    u64 a[kPer], mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = kPer * static_cast<int>(threadIdx.x) + j;
+      a[j] = i < per ? m[i] : 0;
+      mine += a[j];
+    }
+    u64 total;
+    u64 c = run + block_prefix(mine, s.warp_sum, total) - mine;
+    if (c < want && want <= c + mine) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (c < want && want <= c + a[j]) {
+          s.bin = owner * per + kPer * static_cast<int>(threadIdx.x) + j;
+          s.before = c;
+        }
+        c += a[j];
+      }
+    }
+    __syncthreads();
+    before = s.before;
+    return s.bin;
+  }
+
+  // Exact histogram over the cluster of f's amounts (f(x, v, bin, amount) gives whether the logit
+  // counts, its bin and its amount).
+  template <class F>
+  __device__ int find_bin(u64 want, u64& before, F f) {
+    using P = Pieces<kResident>;
+    __syncthreads();
+    for (int i = threadIdx.x; i < P::kCount * kBins; i += kSampleThreads) s.work.hist[0][i] = 0;
+    __syncthreads();
+    slice.each(lane, [&](float x, int v) {
+      uint32_t bin;
+      u64 amount;
+      if (f(x, v, bin, amount)) {
+#pragma unroll
+        for (int q = 0; q < P::kCount; ++q) {
+          const uint32_t part = static_cast<uint32_t>(amount >> (q * P::kBits)) & ((1u << P::kBits) - 1);
+          if (part) atomicAdd(&s.work.hist[q][bin], part);
+        }
+      }
+    });
+    sync_cluster();
+    return merge_bins(kBins, want, before, [](const SampleShared<kResident>* o, int i) {
+      u64 t = 0;
+#pragma unroll
+      for (int q = 0; q < P::kCount; ++q) t += static_cast<u64>(o->work.hist[q][i]) << (q * P::kBits);
+      return t;
+    });
+  }
+
+  // The id at which the running sum of f (over the ids, after `before` in the CTAs before) exceeds r,
+  // when it lies in this CTA, in every lane of one warp; -1 elsewhere.  kept_sum holds f's sums per
+  // warp's stretch.  The block's warps share the stretch that holds the id.
+  template <class F>
+  __device__ int locate(u64 before, u64 r, F f) {
+    int owner = -1;
+    for (int w = 0; w < kSampleWarps; ++w) {
+      const u64 t = s.kept_sum[w];
+      if (before <= r && r < before + t) {
+        owner = w;
+        break;
+      }
+      before += t;
+    }
+    if (owner < 0) return -1;  // the same in the whole block
+    const int per = (slice.nvec + kSampleWarps - 1) / kSampleWarps;
+    const int w0 = min(slice.nvec, owner * per), w1 = min(slice.nvec, w0 + per);
+    const int sub = (w1 - w0 + kSampleWarps - 1) / kSampleWarps;
+    const int b = min(w1, w0 + warp * sub), e = min(w1, b + sub);
+    u64 sum = 0;
+    for (int i = b + lane; i < e; i += 32) {
+      float v[E];
+      slice.get(i, v);
+#pragma unroll
+      for (int j = 0; j < E; ++j) sum += f(v[j], slice.id(i, j));
+    }
+    sum = warp_add(sum);
+    if (lane == 0) s.warp_sum[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+    if (!(before <= r && r < before + sum)) return -1;
+    for (int i0 = b; i0 < e; i0 += 32) {
+      const int i = i0 + lane;
+      u64 a[E], mine = 0;
+#pragma unroll
+      for (int j = 0; j < E; ++j) a[j] = 0;
+      if (i < e) {
+        float v[E];
+        slice.get(i, v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) mine += a[j] = f(v[j], slice.id(i, j));
+      }
+      const u64 run = before + warp_prefix(mine, lane);
+      const uint32_t hit = __ballot_sync(0xffffffffu, run > r);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        u64 c = run - mine;
+        int id = -1;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          c += a[j];
+          if (id < 0 && c > r) id = slice.id(i, j);
+        }
+        return __shfl_sync(0xffffffffu, id, src);
+      }
+      before = __shfl_sync(0xffffffffu, run, 31);
+    }
+    return -1;
+  }
+
+  // Bits that the second histogram leaves off the weights of the bin at `edge`: its largest weight
+  // is then below 2^19, so that 2^13 of them add up in 32 bits.
+  static __device__ __forceinline__ int fine_shift(float edge) {
+    const float z = (edge - 8388608.f - 0.5f) * (kZRange / static_cast<float>(kZBins));  // nearest to 0 in the bin
+    return max(0, 41 - static_cast<int>(z * 1.442695f) - 19);
+  }
+
+  // What min-p keeps of a logit above the boundaries.
+  __device__ __forceinline__ bool min_p_keeps(float x, float e, float min_p) const { return x == rs.m || e >= min_p; }
+
+  // The boundary of top-k (want logits) or top-p (a weight of want(total), by_mass), from the
+  // histogram in z and the exact sums above its bin.  Leaves the weights that the draw can reach in
+  // kept_sum, and their total without min-p in `kept`.  False, for the whole cluster: the bin
+  // holds too many logits or is not the right one.
+  __device__ bool z_boundary(const Boundary& keeps, bool by_mass, u64 count, float top_p, float min_p, Boundary& bound,
+                             u64& kept) {
+    const bool cut = keeps.x > -INFINITY;
+    for (int i = threadIdx.x; i < kZBins; i += kSampleThreads) s.work.zhist[i] = 0;
+    __syncthreads();
+    u64 total = 0, want = count;
+    if (by_mass) {
+      const u64 sum = sum_weights([&](float x, int v, WeightSum& w) {
+        if (cut && !keeps.keeps(x, v)) return;
+        const float z = rs.z(x), e = kPlain ? expf(z) : rs.e(x);
+        w.add(e);
+        // rounded to 2^-17, so that 2^15 of them add up in 32 bits; a longer slice's bins wrap at
+        // worst, and the exact sums then refuse the bin
+        const uint32_t rounded = __float_as_uint(__fadd_rn(e, 64.f)) - kHiBias;
+        if (rounded) atomicAdd(&s.work.zhist[__float_as_uint(rs.z_bin_of(z)) - 0x4b000000u], rounded);
+      });
+      sum_to_part(sum, 1, s.warp_sum);
+    } else {
+      slice.each(lane, [&](float x, int) {
+        if (x > -INFINITY) atomicAdd(&s.work.zhist[__float_as_uint(rs.z_bin(x)) - 0x4b000000u], 1u);
+      });
+    }
+    sync_cluster();
+    if (by_mass) {
+      total = total_of(1);
+      want = by_one_thread(s.want, [&] { return top_p_weight(top_p, total); });
+    }
+    u64 before = 0;
+    // rounded weights may add up to a little less than the exact ones
+    const int bin = merge_bins(kZBins, by_mass ? max(want >> 23, 1ull) : want, before,
+                               [](const SampleShared<kResident>* o, int i) { return static_cast<u64>(o->work.zhist[i]); });
+    if (bin < 0) return false;
+    // the weights above the bin, and the bin's logits
+    clear_list();
+    const float edge = 8388608.f + static_cast<float>(bin);
+    const bool filter = !(min_p <= 0.f);
+    WeightSum open;
+    u64 all = 0;
+    const u64 reach = sum_weights([&](float x, int v, WeightSum& w) {
+      const float z = rs.z(x), u = rs.z_bin_of(z);
+      if (!(u <= edge)) return;
+      if (cut && !keeps.keeps(x, v)) return;
+      if (u == edge) {
+        if (x > -INFINITY) append(v);
+        return;
+      }
+      const float e = kPlain ? expf(z) : rs.e(x);
+      if (filter) {
+        open.add(e);
+        if (!kResident && open.n >= WeightSum::kMaxAdds) {
+          all += open.total();
+          open = WeightSum();
+        }
+        if (!min_p_keeps(x, e, min_p)) return;
+      }
+      w.add(e);
+    });
+    all = filter ? all + open.total() : reach;
+    // part[0] may still be read by the others' merges
+    sum_to_part(reach, 3, s.kept_sum);
+    sum_to_part(all, 2, s.warp_sum);
+    if (threadIdx.x == 0) s.count = s.list_count;
+    sync_cluster();
+    const uint32_t n = total_count();
+    const u64 above = total_of(2);
+    const bool overfull = __ballot_sync(0xffffffffu, lane < ranks && peer(&s, lane)->count > kListCap) != 0;
+    if (overfull || (by_mass && above >= want)) return false;
+    u64 rest = want - (by_mass ? above : before);  // what is wanted of the bin
+    int fine = -1;                                 // the second histogram's bin, if one was needed
+    if (n > kListCap) {
+      // the bin's logits do not fit the first CTA's list: a second histogram of them alone
+      sync_cluster();
+      for (int i = threadIdx.x; i < kFineBins; i += kSampleThreads) s.work.fine[i] = 0;
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) {
+        const float x = logit(static_cast<int>(s.work.near_ids[i]));
+        const uint32_t amount = by_mass ? static_cast<uint32_t>(rs.weight(x) >> fine_shift(edge)) : 1u;
+        atomicAdd(&s.work.fine[rs.fine_bin(x, bin)], amount);
+      }
+      sync_cluster();
+      u64 ahead = 0;
+      fine = merge_bins(kFineBins, by_mass ? max(rest >> fine_shift(edge), 1ull) : rest, ahead,
+                        [](const SampleShared<kResident>* o, int i) { return static_cast<u64>(o->work.fine[i]); });
+      if (fine < 0) return false;
+      u64 sum = 0, number = 0;
+      for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) {
+        const float x = logit(static_cast<int>(s.work.near_ids[i]));
+        const int f = rs.fine_bin(x, bin);
+        if (f < fine) sum += by_mass ? rs.weight(x) : 1ull;
+        number += f == fine;
+      }
+      sum_to_part(sum, 2, s.warp_sum);
+      sum_to_part(number, 3, s.warp_sum);
+      sync_cluster();
+      const u64 in_front = total_of(2);
+      if (total_of(3) > kListCap || in_front >= rest) return false;
+      rest -= in_front;
+      u64 at = 0;
+      total_of(3, &at);
+      clear_list();
+      u64* to = rank == 0 ? &s.work.list[0] : peer(&s.work.list[0], 0);
+      for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) {
+        const int id = static_cast<int>(s.work.near_ids[i]);
+        const float x = logit(id);
+        if (rs.fine_bin(x, bin) == fine) to[at + atomicAdd(&s.list_count, 1u)] = entry(id, x);
+      }
+    } else {
+      push_list();
+    }
+    const int listed = fine < 0 ? static_cast<int>(n) : static_cast<int>(total_of(3));
+    sync_cluster();
+    if (rank == 0) {
+      sort_list(s.work.list, listed);
+      bound_in_list(listed, by_mass, rest);
+    }
+    sync_cluster();
+    if (!peer(&s, 0)->found) return false;
+    bound = peer(&s, 0)->bound;
+    // the bin's logits that stay join the sums of their stretches
+    const int per = (slice.nvec + kSampleWarps - 1) / kSampleWarps;
+    u64 more = 0;
+    for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) {
+      const int id = static_cast<int>(s.work.near_ids[i]);
+      const float x = logit(id);
+      if (!bound.keeps(x, id)) continue;
+      const float e = rs.e(x);
+      const u64 w = fixed_point(e);
+      more += w;
+      if (!filter || min_p_keeps(x, e, min_p))
+        atomicAdd(&s.kept_sum[((id - slice.first + slice.shift) / E) / per], w);
+    }
+    if (!by_mass) {  // the weight that top-p takes its share of
+      sum_to_part(more, 1, s.warp_sum);
+      sync_cluster();
+      kept = above + total_of(1);
+    }
+    return true;
+  }
+
+  // The boundary at which `want` logits (by_mass false) or a weight of `want` (by_mass true)
+  // have been kept, among those that `keeps`, from exact histograms; want is at least 1 and at
+  // most what there is.  The whole cluster.
+  __device__ Boundary find_boundary(const Boundary& keeps, bool by_mass, u64 want) {
+    auto amount_of = [&](float x) -> u64 { return by_mass ? rs.weight(x) : 1ull; };
+    auto coarse = [&](float x) -> int { return static_cast<int>(__float_as_uint(rs.z_bin(x)) - 0x4b000000u) * kBins / kZBins; };
+    u64 before = 0;
+    int bin = find_bin(want, before, [&](float x, int v, uint32_t& b, u64& amount) -> bool {
+      if (!(x > -INFINITY) || !keeps.keeps(x, v)) return false;
+      b = static_cast<uint32_t>(coarse(x));
+      amount = amount_of(x);
+      return true;
+    });
+    want -= before;
+    gather_exact([&](float x, int v) { return x > -INFINITY && coarse(x) == bin && keeps.keeps(x, v); });
+    for (;;) {
+      sync_cluster();
+      const uint32_t n = total_count();
+      const uint32_t lo = __reduce_min_sync(0xffffffffu, lane < ranks ? peer(&s, lane)->key_lo : 0xffffffffu);
+      const uint32_t hi = __reduce_max_sync(0xffffffffu, lane < ranks ? peer(&s, lane)->key_hi : 0u);
+      if (n <= kListCap) {
+        push_list();
+        sync_cluster();
+        if (rank == 0) {
+          sort_list(s.work.list, static_cast<int>(n));
+          bound_in_list(static_cast<int>(n), by_mass, want);
+        }
+        break;
+      }
+      if (lo == hi) {  // more equal logits than the list holds: the ids decide
+        const float x0 = key_logit(lo);
+        const u64 each = by_mass ? rs.weight(x0) : 1ull;
+        const u64 skip = (want - 1) / each;  // equal logits kept before the last one
+        auto tie = [&](float x, int v) -> u64 { return x == x0 && keeps.keeps(x, v) ? 1ull : 0ull; };
+        u64 sum = 0, ahead = 0;
+        slice.each(lane, [&](float x, int v) { sum += tie(x, v); });
+        sum_to_part(sum, 0, s.kept_sum);
+        sync_cluster();
+        total_of(0, &ahead);
+        const int id = locate(ahead, skip, tie);
+        if (id >= 0 && lane == 0) peer(&s, 0)->bound = Boundary{x0, id};
+        break;
+      }
+      const int bits = 32 - __clz(hi - lo);
+      const int shift = bits > 10 ? bits - 10 : 0;
+      static_assert(kBins == 1 << 10, "bins of the logits' bits");
+      bin = find_bin(want, before, [&](float x, int v, uint32_t& b, u64& amount) -> bool {
+        const uint32_t k = logit_key(x);
+        if (k < lo || k > hi || !keeps.keeps(x, v)) return false;
+        b = (hi - k) >> shift;
+        amount = amount_of(x);
+        return true;
+      });
+      want -= before;
+      gather_exact([&](float x, int v) {
+        const uint32_t k = logit_key(x);
+        return k >= lo && k <= hi && static_cast<int>((hi - k) >> shift) == bin && keeps.keeps(x, v);
+      });
+    }
+    sync_cluster();
+    return peer(&s, 0)->bound;
+  }
+
+  // Lists the logits for which f holds; their number and the range of their keys go to s.count,
+  // s.key_lo and s.key_hi.
+  template <class F>
+  __device__ void gather_exact(F f) {
+    clear_list();
+    if (threadIdx.x == 0) {
+      s.lo = 0xffffffffu;
+      s.hi = 0u;
+    }
+    __syncthreads();
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    slice.each(lane, [&](float x, int v) {
+      if (f(x, v)) {
+        const uint32_t k = logit_key(x);
+        lo = min(lo, k);
+        hi = max(hi, k);
+        append(v);
+      }
+    });
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0 && lo <= hi) {
+      atomicMin(&s.lo, lo);
+      atomicMax(&s.hi, hi);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s.count = s.list_count;
+      s.key_lo = s.lo;
+      s.key_hi = s.hi;
+    }
+  }
+
+  // The first CTA's finish when the list holds everything that can be drawn: the top k, then
+  // top-p and min-p among them, then the draw.  weights and by_id: room for kListCap each.
+  __device__ void finish_list(int n, int k, bool need_p, float top_p, float min_p, float u, u64* weights, u64* by_id,
+                              int32_t* token, float* logprob) {
+    u64* list = s.work.list;
+    if (n <= kCountingMax) {
+      // Short: a thread per pair of an entry and a share of the list counts the entries ranked
+      // before it and adds up their weights, then, of those kept, the weights of lower ids.
+      for (int i = threadIdx.x; i < n; i += kSampleThreads) weights[i] = rs.weight(entry_logit(list[i]));
+      __syncthreads();
+      constexpr int kShare = 4;  // threads per entry
+      static_assert(kCountingMax * kShare <= 2 * kSampleThreads, "two rounds of entries");
+      const int part = threadIdx.x % kShare;
+      u64 kept_w[2], top = 0;
+      bool in_top[2];
+      u64 ahead[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = q * (kSampleThreads / kShare) + static_cast<int>(threadIdx.x) / kShare;
+        const u64 e = i < n ? list[i] : ~0ull;
+        int rank_of = 0;
+        u64 mass = 0;
+        for (int j = part; j < n; j += kShare) {
+          if (list[j] > e) {
+            ++rank_of;
+            mass += weights[j];
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < kShare; o <<= 1) {
+          rank_of += __shfl_xor_sync(0xffffffffu, rank_of, o);
+          mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        }
+        in_top[q] = i < n && rank_of < k;
+        ahead[q] = mass;
+        kept_w[q] = in_top[q] ? weights[i] : 0;
+        if (part == 0) top += kept_w[q];
+      }
+      u64 total;
+      block_prefix(top, s.warp_sum, total);
+      const u64 want = need_p ? by_one_thread(s.want, [&] { return top_p_weight(top_p, total); }) : 0ull;
+      u64 left = 0;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = q * (kSampleThreads / kShare) + static_cast<int>(threadIdx.x) / kShare;
+        bool keep = in_top[q] && (!need_p || ahead[q] < want);
+        if (keep) {
+          const float x = entry_logit(list[i]);
+          keep = min_p_keeps(x, rs.e(x), min_p);
+        }
+        if (!keep) kept_w[q] = 0;
+        if (i < n && part == 0) by_id[i] = kept_w[q];
+        if (part == 0) left += kept_w[q];
+      }
+      block_prefix(left, s.warp_sum, total);  // by_id is complete after its barriers
+      const u64 r = by_one_thread(s.draw, [&] { return draw_at(u, total); });
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = q * (kSampleThreads / kShare) + static_cast<int>(threadIdx.x) / kShare;
+        const int id = i < n ? entry_id(list[i]) : 0;
+        u64 mass = 0;
+        for (int j = part; j < n; j += kShare)
+          if (entry_id(list[j]) < id) mass += by_id[j];
+#pragma unroll
+        for (int o = 1; o < kShare; o <<= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        if (part == 0 && mass <= r && r < mass + kept_w[q]) {
+          *token = id;
+          if (logprob != nullptr) *logprob = log_probability(rs.z(entry_logit(list[i])), total);
+        }
+      }
+      return;
+    }
+    sort_list(list, n);
+    const int kk = min(k, n);
+    const int i0 = 2 * static_cast<int>(threadIdx.x);
+    u64 w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) w[j] = i0 + j < kk ? rs.weight(entry_logit(list[i0 + j])) : 0;
+    u64 total;
+    u64 upto = block_prefix(w[0] + w[1], s.warp_sum, total);
+    if (threadIdx.x == 0) s.bin = kk;
+    __syncthreads();
+    if (need_p) {
+      const u64 want = by_one_thread(s.want, [&] { return top_p_weight(top_p, total); });
+      const u64 start = upto - w[0] - w[1];
+      if (start < want && want <= upto) s.bin = i0 + (start + w[0] < want ? 2 : 1);
+      __syncthreads();
+    }
+    const int keep = s.bin;
+    u64 left = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = i0 + j;
+      if (i < keep) {
+        const float x = entry_logit(list[i]);
+        if (!min_p_keeps(x, rs.e(x), min_p)) w[j] = 0;
+        weights[i] = w[j];
+        left += w[j];
+        by_id[i] = ~((static_cast<u64>(entry_id(list[i])) << 32) | static_cast<uint32_t>(i));
+      }
+    }
+    block_prefix(left, s.warp_sum, total);
+    sort_list(by_id, keep);  // complements in descending order: ids in ascending order
+    const u64 r = by_one_thread(s.draw, [&] { return draw_at(u, total); });
+    u64 y[2] = {0, 0}, all;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (i0 + j < keep) y[j] = weights[static_cast<uint32_t>(~by_id[i0 + j])];
+    upto = block_prefix(y[0] + y[1], s.warp_sum, all);
+    const u64 start = upto - y[0] - y[1];
+    if (start <= r && r < upto) {
+      const u64 e = ~by_id[i0 + (start + y[0] <= r ? 1 : 0)];
+      *token = static_cast<int32_t>(e >> 32);
+      if (logprob != nullptr) *logprob = log_probability(rs.z(entry_logit(list[static_cast<uint32_t>(e)])), total);
+    }
+  }
+
+  // Everything after the load.
+  __device__ void run(int V, int k, bool list_first, float tau, float top_p, float min_p, float u, u64* scratch,
+                      int32_t* token, float* logprob) {
+    const bool need_k = k < V, need_p = !(top_p >= 1.f);
+    if (list_first) {
+      clear_list();
+      for (int i = slice.v0 + lane; i < slice.v1; i += 32) {
+        float v[E];
+        slice.get(i, v);
+        float most = v[0];
+#pragma unroll
+        for (int j = 1; j < E; ++j) most = fmaxf(most, v[j]);
+        if (most >= tau) {
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (v[j] >= tau && v[j] > -INFINITY) append(slice.id(i, j));
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) s.count = s.list_count;
+      sync_cluster();
+      const uint32_t n = total_count();
+      if (n <= kListCap) {
+        push_list();
+        sync_cluster();
+        if (rank == 0)  // the slice is no longer needed
+          finish_list(static_cast<int>(n), k, need_p, top_p, min_p, u, scratch, scratch + kListCap, token, logprob);
+        return;
+      }
+    }
+    Boundary bound = no_boundary();
+    u64 kept = 0;
+    bool sums = false, have_kept = false;  // kept_sum is up to date; kept is top-p's total
+    if (need_k) {
+      u64 valid = 0;
+      slice.each(lane, [&](float x, int) { valid += x > -INFINITY; });
+      sum_to_part(valid, 1, s.warp_sum);
+      sync_cluster();
+      const u64 n = total_of(1);
+      if (static_cast<u64>(k) < n) {
+        sync_cluster();
+        sums = have_kept = z_boundary(bound, false, static_cast<u64>(k), top_p, min_p, bound, kept);
+        if (!sums) {
+          sync_cluster();
+          bound = find_boundary(no_boundary(), false, static_cast<u64>(k));
+        }
+      }
+    }
+    if (need_p) {
+      sync_cluster();
+      sums = z_boundary(bound, true, 0, top_p, min_p, bound, kept);
+      if (!sums) {
+        sync_cluster();
+        if (!have_kept) {
+          const u64 sum = sum_weights([&](float x, int v, WeightSum& w) {
+            if (bound.keeps(x, v)) w.add(rs.e(x));
+          });
+          sum_to_part(sum, 1, s.warp_sum);
+          sync_cluster();
+          kept = total_of(1);
+        }
+        bound = find_boundary(bound, true, by_one_thread(s.want, [&] { return top_p_weight(top_p, kept); }));
+      }
+    }
+    // ---- draw
+    const bool cut = bound.x > -INFINITY, filter = !(min_p <= 0.f);
+    if (!sums) {
+      sync_cluster();
+      u64 sum;
+      if (!cut && !filter)
+        sum = sum_all();
+      else
+        sum = sum_weights([&](float x, int v, WeightSum& w) {
+          if (cut && !bound.keeps(x, v)) return;
+          const float e = rs.e(x);
+          if (!filter || min_p_keeps(x, e, min_p)) w.add(e);
+        });
+      sum_to_part(sum, 1, s.kept_sum);
+    } else {
+      sync_cluster();
+      if (threadIdx.x == 0) {
+        u64 t = 0;
+        for (int w = 0; w < kSampleWarps; ++w) t += s.kept_sum[w];
+        s.part[1] = t;
+      }
+    }
+    sync_cluster();
+    u64 before = 0;
+    const u64 total = total_of(1, &before);
+    const u64 r = by_one_thread(s.draw, [&] { return draw_at(u, total); });
+    const int id = locate(before, r, [&](float x, int v) -> u64 {
+      if (cut && !bound.keeps(x, v)) return 0;
+      const float e = rs.e(x);
+      return !filter || min_p_keeps(x, e, min_p) ? fixed_point(e) : 0;
+    });
+    if (id >= 0 && lane == 0) {
+      *token = id;
+      if (logprob != nullptr) *logprob = log_probability(rs.z(logit(id)), total);
+    }
+    sync_cluster();  // no CTA leaves while another reads its shared memory
+  }
+};
+
+// A lower bound of the want-th largest of the block's thread maxima (-inf if fewer have a logit).
+// 256 bins of equal width between the least and the largest; then the least maximum of the bins
+// that hold the first `want`.
+template <bool kResident>
+__device__ float block_tau(float tmax, int want, SampleShared<kResident>& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool valid = tmax > -INFINITY;
+  const uint32_t key = logit_key(tmax);
+  const uint32_t whi = __reduce_max_sync(0xffffffffu, valid ? key : 0u);
+  const uint32_t wlo = __reduce_min_sync(0xffffffffu, valid ? key : 0xffffffffu);
+  if (lane == 0) {
+    s.warp_hi[warp] = whi;
+    s.warp_lo[warp] = wlo;
+  }
+  if (threadIdx.x < 256) s.work.zhist[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    s.bin = -1;
+    s.lo = 0xffffffffu;
+  }
+  __syncthreads();
+  uint32_t hi = 0, lo = 0xffffffffu;
+#pragma unroll
+  for (int w = 0; w < kSampleWarps; ++w) {
+    hi = max(hi, s.warp_hi[w]);
+    lo = min(lo, s.warp_lo[w]);
+  }
+  const float x_hi = key_logit(hi), width = x_hi - key_logit(lo);
+  const bool spread = lo < hi && width > 0.f && width < INFINITY;  // the same for the block
+  const int bin = !valid || !spread ? 0 : static_cast<int>(fminf((x_hi - tmax) * (256.f / width), 255.f));
+  if (valid) atomicAdd(&s.work.zhist[bin], 1u);
+  __syncthreads();
+  if (warp == 0) {
+    u64 mine = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine += s.work.zhist[8 * lane + j];
+    u64 c = warp_prefix(mine, lane) - mine;
+    if (c < static_cast<u64>(want) && static_cast<u64>(want) <= c + mine) {
+      for (int j = 0; j < 8; ++j) {
+        c += s.work.zhist[8 * lane + j];
+        if (c >= static_cast<u64>(want)) {
+          s.bin = 8 * lane + j;
+          break;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  const int last = s.bin;
+  const uint32_t least = __reduce_min_sync(0xffffffffu, valid && bin <= last ? key : 0xffffffffu);
+  if (lane == 0) atomicMin(&s.lo, least);
+  __syncthreads();
+  return last < 0 ? -INFINITY : key_logit(s.lo);
+}
+
 template <class T, bool kResident>
 __global__ void __launch_bounds__(kSampleThreads, 2)
     sample_kernel(const T* __restrict__ logits, int V, int64_t ld, int per, const float* __restrict__ u,
@@ -542,7 +1195,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   sl.first = min(V, rank * per);
   sl.n = min(V, sl.first + per) - sl.first;
   sl.g = logits + b * ld + sl.first;
-  sl.s = dyn + kBins / ranks * sizeof(u64) / sizeof(uint4);
+  sl.s = dyn + kZBins / ranks * sizeof(u64) / sizeof(uint4);
   sl.shift = static_cast<int>((reinterpret_cast<uintptr_t>(sl.g) % 16) / sizeof(T));
   sl.nvec = sl.n > 0 ? (sl.n + sl.shift + E - 1) / E : 0;
   const int per_warp = (sl.nvec + kSampleWarps - 1) / kSampleWarps;
@@ -553,28 +1206,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   const float t = p.temperature_rows != nullptr ? p.temperature_rows[b] : p.temperature;
   const float top_p = p.top_p_rows != nullptr ? p.top_p_rows[b] : p.top_p;
   const float min_p = p.min_p_rows != nullptr ? p.min_p_rows[b] : p.min_p;
-  const float draw = u[b];
   const bool greedy = !(t > 0.f);
   if (greedy) k = 1;
   if (k <= 0 || k > V) k = V;
-  const bool need_k = k < V, need_p = !(top_p >= 1.f);
 
-  // ---- 1. load
-  float tmax = -INFINITY;
-  constexpr int U = 4;  // vectors in flight per thread
-  for (int i0 = sl.v0; i0 < sl.v1; i0 += 32 * U) {
-    float v[U][E];
-#pragma unroll
-    for (int q = 0; q < U; ++q)
-      if (i0 + 32 * q + lane < sl.v1) sl.read_global(i0 + 32 * q + lane, v[q]);
-#pragma unroll
-    for (int q = 0; q < U; ++q)
-      if (i0 + 32 * q + lane < sl.v1) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) tmax = fmaxf(tmax, v[q][j]);
-        if (kResident) sl.put(i0 + 32 * q + lane, v[q]);
-      }
-  }
+  // ---- load
+  const float tmax = sl.load(lane);
   {
     float m = tmax;
 #pragma unroll
@@ -582,199 +1219,67 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     if (lane == 0) s.warp_max[warp] = m;
   }
   // With w of n threads wanted the list holds about n log(n / (n - w)) logits.
-  const bool list_first = k > 1 && (need_k ? k <= min(kListCap / 2, kSampleThreads * 3 / 4 * ranks) : need_p);
-  float tau = -INFINITY;
-  if (list_first) {
-    // the upper 16 bits of the want-th largest thread maximum, bit by bit
-    const int want = ((need_k ? k : kTopPTarget) + ranks - 1) / ranks;
-    const uint32_t key = logit_key(tmax);
-    uint32_t th = 0;
-    for (int bit = 31; bit >= 16; --bit) {
-      const uint32_t c = th | (1u << bit);
-      if (__syncthreads_count(key >= c) >= want) th = c;
-    }
-    // below -inf's key when fewer threads than wanted have a logit: every logit is gathered
-    tau = th > logit_key(-INFINITY) ? key_logit(th) : -INFINITY;
-  }
+  const bool list_first = k > 1 && k < V && k <= min(kListCap / 2, kSampleThreads * 3 / 4 * ranks);
+  const float own_tau = list_first ? block_tau(tmax, (k + ranks - 1) / ranks, s) : -INFINITY;
   __syncthreads();
   if (threadIdx.x == 0) {
     float m = s.warp_max[0];
     for (int w = 1; w < kSampleWarps; ++w) m = fmaxf(m, s.warp_max[w]);
     s.cta_max = m;
-    s.tau = tau;
+    s.tau = own_tau;
   }
   sync_cluster();
-  float m = -INFINITY;
-  for (int r = 0; r < ranks; ++r) {
-    m = fmaxf(m, peer(&s, r)->cta_max);
-    tau = fminf(tau, peer(&s, r)->tau);
+  float m = lane < ranks ? peer(&s, lane)->cta_max : -INFINITY;
+  float tau = lane < ranks ? peer(&s, lane)->tau : INFINITY;
+#pragma unroll
+  for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    tau = fminf(tau, __shfl_xor_sync(0xffffffffu, tau, o));
   }
+  m = __shfl_sync(0xffffffffu, m, 0);
+  tau = __shfl_sync(0xffffffffu, tau, 0);
+  float* const lp = logprob != nullptr ? logprob + b : nullptr;
   if (!(m > -INFINITY)) {  // nothing to draw
     if (rank == 0 && threadIdx.x == 0) {
       token[b] = -1;
-      if (logprob != nullptr) logprob[b] = NAN;
+      if (lp != nullptr) *lp = NAN;
     }
     sync_cluster();
     return;
   }
-  const float inv_t = greedy ? 1.f : 1.f / t;
-  const RowScale rs{m, inv_t, m < INFINITY && inv_t > 0.f && inv_t < INFINITY};
-  RowCtx<T, kResident> c{sl, s, merged, rs, rank, ranks, warp, lane};
-
   if (k == 1) {  // the largest logit's first id
     int first = INT_MAX;
-    sl.each(lane, [&](float x, int v) {
-      if (x == m) first = min(first, v);
-    });
+    if (s.cta_max == m)
+      sl.each(lane, [&](float x, int v) {
+        if (x == m) first = min(first, v);
+      });
     first = __reduce_min_sync(0xffffffffu, first);
-    if (lane == 0) s.warp_sum[warp] = static_cast<u64>(first);
+    if (lane == 0) s.warp_hi[warp] = static_cast<uint32_t>(first);
     __syncthreads();
     if (threadIdx.x == 0) {
-      u64 f = s.warp_sum[0];
-      for (int w = 1; w < kSampleWarps; ++w) f = min(f, s.warp_sum[w]);
-      s.part[0] = f;
+      uint32_t f = s.warp_hi[0];
+      for (int w = 1; w < kSampleWarps; ++w) f = min(f, s.warp_hi[w]);
+      s.count = f;
     }
     sync_cluster();
     if (rank == 0 && threadIdx.x == 0) {
-      u64 f = s.part[0];
-      for (int r = 1; r < ranks; ++r) f = min(f, peer(&s, r)->part[0]);
+      uint32_t f = s.count;
+      for (int r = 1; r < ranks; ++r) f = min(f, peer(&s, r)->count);
       token[b] = static_cast<int32_t>(f);
-      if (logprob != nullptr) logprob[b] = 0.f;
+      if (lp != nullptr) *lp = 0.f;
     }
     sync_cluster();
     return;
   }
-
-  // ---- 2. gather
-  u64 total = 0;      // weight that top-p takes its share of
-  bool have_total = false;
-  if (list_first) {
-    u64 all = 0, listed = 0;
-    const bool sum_all = !need_k;
-    c.gather([&](float x, int) {
-      const bool in = x >= tau && x > -INFINITY;
-      if (sum_all) {
-        const u64 w = rs.weight(x);
-        all += w;
-        if (in) listed += w;
-      }
-      return in;
-    });
-    if (sum_all) {
-      c.sum_to_part(all, 0);
-      c.sum_to_part(listed, 1);
-    }
-    sync_cluster();
-    const uint32_t n = c.total_count();
-    bool finish = n <= kListCap;
-    if (sum_all) {
-      total = c.total_of(0);
-      have_total = true;
-      finish = finish && c.total_of(1) >= top_p_weight(top_p, total);
-    }
-    if (finish) {
-      // ---- 3. the first CTA finishes
-      c.push_list();
-      sync_cluster();
-      if (rank != 0) return;
-      u64* list = s.work.list;
-      c.sort_list(list, static_cast<int>(n));
-      u64* weights = reinterpret_cast<u64*>(dyn);  // the row's slice is no longer needed
-      u64* by_id = weights + kListCap;
-      const int kk = need_k ? min(k, static_cast<int>(n)) : static_cast<int>(n);
-      const int i0 = 2 * static_cast<int>(threadIdx.x);
-      u64 w[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) w[j] = i0 + j < kk ? rs.weight(key_logit(static_cast<uint32_t>(list[i0 + j] >> 32))) : 0;
-      u64 sum;
-      u64 upto = block_prefix(w[0] + w[1], s.warp_sum, sum);
-      if (need_k) total = sum;
-      if (threadIdx.x == 0) s.bin = kk;
-      __syncthreads();
-      if (need_p) {
-        const u64 want = top_p_weight(top_p, total);
-        const u64 start = upto - w[0] - w[1];
-        if (start < want && want <= upto) s.bin = i0 + (start + w[0] < want ? 2 : 1);
-        __syncthreads();
-      }
-      const int keep = s.bin;
-      u64 left = 0;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = i0 + j;
-        if (i < keep) {
-          const uint32_t key = static_cast<uint32_t>(list[i] >> 32);
-          const uint32_t id = 0xffffffffu - static_cast<uint32_t>(list[i]);
-          const float x = key_logit(key);
-          if (!(x == m) && !(rs.e(x) >= min_p)) w[j] = 0;
-          weights[i] = w[j];
-          left += w[j];
-          by_id[i] = ~((static_cast<u64>(id) << 32) | static_cast<uint32_t>(i));
-        }
-      }
-      block_prefix(left, s.warp_sum, sum);
-      c.sort_list(by_id, keep);  // complements in descending order: ids in ascending order
-      const u64 r = draw_at(draw, sum);
-      u64 x2[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (i0 + j < keep) x2[j] = weights[static_cast<uint32_t>(~by_id[i0 + j])];
-      u64 all2;
-      upto = block_prefix(x2[0] + x2[1], s.warp_sum, all2);
-      const u64 start = upto - x2[0] - x2[1];
-      if (start <= r && r < upto) {
-        const u64 e = ~by_id[i0 + (start + x2[0] <= r ? 1 : 0)];
-        token[b] = static_cast<int32_t>(e >> 32);
-        if (logprob != nullptr)
-          logprob[b] = log_probability(rs.z(key_logit(static_cast<uint32_t>(list[static_cast<uint32_t>(e)] >> 32))), sum);
-      }
-      return;
-    }
+  const float inv_t = 1.f / t;
+  u64* const scratch = reinterpret_cast<u64*>(dyn);
+  if (m < INFINITY && inv_t > 0.f && inv_t < INFINITY) {
+    RowCtx<T, kResident, true> c{sl, s, merged, RowScale<true>{m, inv_t}, rank, ranks, warp, lane};
+    c.run(V, k, list_first, tau, top_p, min_p, u[b], scratch, token + b, lp);
+  } else {
+    RowCtx<T, kResident, false> c{sl, s, merged, RowScale<false>{m, inv_t}, rank, ranks, warp, lane};
+    c.run(V, k, list_first, tau, top_p, min_p, u[b], scratch, token + b, lp);
   }
-
-  // ---- boundaries from histograms
-  Boundary bound{0u, INT_MAX};
-  if (need_k) {
-    u64 valid = 0;
-    sl.each(lane, [&](float x, int) { valid += x > -INFINITY; });
-    c.sum_to_part(valid, 0);
-    sync_cluster();
-    const u64 n = c.total_of(0);
-    if (static_cast<u64>(k) < n) bound = c.find_boundary(bound, false, static_cast<u64>(k));
-  }
-  if (need_p) {
-    if (!have_total) {
-      u64 sum = 0;
-      sl.each(lane, [&](float x, int v) {
-        if (bound.keeps(logit_key(x), v)) sum += rs.weight(x);
-      });
-      c.sum_to_part(sum, 1);  // part[0] may still be read
-      sync_cluster();
-      total = c.total_of(1);
-    }
-    bound = c.find_boundary(bound, true, top_p_weight(top_p, total));
-  }
-
-  // ---- draw
-  const bool cut = need_k || need_p, filter = min_p > 0.f;
-  auto kept = [&](float x, int v) -> u64 {
-    if (cut && !bound.keeps(logit_key(x), v)) return 0;
-    const float e = rs.e(x);
-    if (filter && !(x == m) && !(e >= min_p)) return 0;
-    return fixed_point(e);
-  };
-  u64 sum = 0, before = 0;
-  sl.each(lane, [&](float x, int v) { sum += kept(x, v); });
-  c.sum_to_part(sum, 1);
-  sync_cluster();
-  total = c.total_of(1, &before);
-  const int id = c.locate(before, draw_at(draw, total), kept);
-  if (id >= 0 && lane == 0) {
-    const float x = to_float(logits[b * ld + id]);
-    token[b] = id;
-    if (logprob != nullptr) logprob[b] = log_probability(rs.z(x), total);
-  }
-  sync_cluster();  // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------- launch
@@ -791,7 +1296,7 @@ struct SamplePlan {
 // several), beside the static part.
 template <bool kResident>
 constexpr size_t max_dynamic(int n) {
-  return (n == 1 ? 227 * 1024 : 228 * 1024 / n - 1024) / 128 * 128 - (sizeof(SampleShared<kResident>) + 255) / 128 * 128;
+  return ((n == 1 ? 227 * 1024 : 228 * 1024 / n - 1024) - sizeof(SampleShared<kResident>)) / 16 * 16;
 }
 
 // Fewest logits that a CTA gets a slice of.
@@ -806,7 +1311,7 @@ static SamplePlan plan_sample(int64_t B, int64_t V, size_t elem, int sms) {
     const int64_t per = ((V + p.ranks - 1) / p.ranks + vec - 1) / vec * vec;
     p.per = static_cast<int>(per);
     // the merged histogram and the slice, which may start inside a vector
-    const size_t need = kBins / p.ranks * sizeof(u64) + static_cast<size_t>(per) * elem + 16;
+    const size_t need = kZBins / p.ranks * sizeof(u64) + static_cast<size_t>(per) * elem + 16;
     p.resident = need <= kOne && per <= Pieces<true>::kMaxSlice;
     p.smem = p.resident && need > kScratch ? need : kScratch;
     const bool wide = need <= kTwo && per <= Pieces<true>::kMaxSlice;
