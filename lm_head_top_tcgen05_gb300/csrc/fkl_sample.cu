@@ -43,9 +43,13 @@ constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxSampleV = int64_t{1} << 22;  // 2^22 weights of 2^40 stay below 2^63
 constexpr int kBins = 1024;
 constexpr int kListCap = 1024;
-constexpr int kZBins = 2304;           // of the first histogram, over z in [-kZRange, 0]
-constexpr float kZRange = 24.f;        // lower logits (weights below 2^-34) share the last bin
-constexpr int kFineBins = 2048;        // of the second one, over one bin of the first
+// The first histogram, over z: 64 bins to each halving of the weight, 36 halvings; smaller weights
+// share the last bin.
+constexpr int kOctaveBits = 6, kOctaves = 36;
+constexpr int kZBins = kOctaves << kOctaveBits;
+constexpr float kZBinWidth = 0.6931471806f / 64.f;
+constexpr int kFineBins = 2048;        // of the second histogram, over one bin of the first
+constexpr int kGroups = 32;            // groups of bins that are added up before they are exchanged
 constexpr int kCountingMax = 160;      // longest list that is ranked by counting, not sorted
 
 using u64 = unsigned long long;
@@ -108,20 +112,19 @@ struct RowScale {
     return x > -INFINITY && v > 0.f ? v : 0.f;
   }
   __device__ __forceinline__ u64 weight(float x) const { return fixed_point(e(x)); }
-  // Bin of the first histogram as a float 2^23 + bin (rounded to nearest); falls as x rises.
+  // Bin of the first histogram as a float 2^23 + bin; falls as x rises.
   __device__ __forceinline__ float z_bin_of(float z) const {
-    const float u = fmaf(z, -static_cast<float>(kZBins) / kZRange, 8388608.f);
+    const float u = __fmaf_rd(z, -1.f / kZBinWidth, 8388608.f);  // rounded down to a whole number
     return fminf(u, 8388608.f + static_cast<float>(kZBins - 1));
   }
   __device__ __forceinline__ float z_bin(float x) const { return z_bin_of(z(x)); }
-  // Bin of the second histogram, within `bin` of the first: rises and falls with z alone too.
+  // Bin of the second histogram, within `bin` of the first; depends on z alone too.
   __device__ __forceinline__ int fine_bin(float x, int bin) const {
-    constexpr float kScale = static_cast<float>(kZBins) / kZRange * static_cast<float>(kFineBins);
-    const float mid = static_cast<float>(bin) * (kZRange / static_cast<float>(kZBins));
-    const float u = (z(x) + mid) * -kScale + static_cast<float>(kFineBins / 2);
+    const float u = (z(x) + static_cast<float>(bin) * kZBinWidth) * (-static_cast<float>(kFineBins) / kZBinWidth);
     return static_cast<int>(fminf(fmaxf(u, 0.f), static_cast<float>(kFineBins - 1)));
   }
 };
+__device__ __forceinline__ int bin_number(float z_bin) { return static_cast<int>(__float_as_uint(z_bin) - 0x4b000000u); }
 
 // A boundary in the order (logit descending, id ascending): the last logit that is kept, with its
 // id.  -0 and +0 compare equal, as in the order.
@@ -155,6 +158,7 @@ struct SampleShared {
     uint32_t hist[Pieces<kResident>::kCount][kBins];  // exact histograms
   } work;
   u64 warp_sum[kSampleWarps];
+  u64 groups[kGroups];  // exchanged: this CTA's sums of each group of bins
   u64 kept_sum[kSampleWarps];  // weight that the draw can reach, per warp's stretch of the row
   // exchanged between the CTAs of the cluster (written before a cluster barrier, read after)
   u64 part[4];
@@ -168,6 +172,7 @@ struct SampleShared {
   uint32_t list_count, lo, hi;
   int bin;
   u64 before, want, draw;
+  u64 group_sum[kGroups];
 };
 
 // Barrier of the cluster's threads: shared memory written before it is seen by every CTA after.
@@ -382,7 +387,7 @@ struct RowCtx {
   static constexpr int E = Slice<T, kResident>::E;
   const Slice<T, kResident>& slice;
   SampleShared<kResident>& s;
-  u64* merged;  // this CTA's share of the merged histogram
+  u64* counting;  // room for kCountingMax weights
   RowScale<kPlain> rs;
   int rank, ranks, warp, lane;
 
@@ -500,68 +505,110 @@ struct RowCtx {
     for (int i = n + threadIdx.x; i < n2; i += kSampleThreads) keys[i] = 0;
     sort_descending(keys, n2);
   }
-  // First CTA: in the sorted list of n entries, the one at which the running sum of amounts (1,
-  // or the weights) reaches want, into s.bound; s.found tells whether there is one.
-  __device__ __forceinline__ void bound_in_list(int n, bool by_mass, u64 want) {
+  // First CTA: in the list of n entries, the one at which the running sum of amounts (1, or the
+  // weights), in their order, reaches want, into s.bound; s.found tells whether there is one.
+  __device__ __forceinline__ void bound_in_list(int n, bool by_mass, u64 want, u64* weights) {
     if (threadIdx.x == 0) s.found = 0;
+    u64* list = s.work.list;
+    auto found = [&](u64 c) {
+      s.bound = Boundary{entry_logit(c), entry_id(c)};
+      s.found = 1;
+    };
+    if (n <= kCountingMax) {
+      for (int i = threadIdx.x; i < n; i += kSampleThreads) weights[i] = by_mass ? rs.weight(entry_logit(list[i])) : 1ull;
+      __syncthreads();
+      const int part = threadIdx.x % kShare;
+      for (int i0 = 0; i0 < n; i0 += kSampleThreads / kShare) {
+        const int i = i0 + static_cast<int>(threadIdx.x) / kShare;
+        const u64 e = i < n ? list[i] : ~0ull;
+        int rank_of;
+        const u64 start = ahead_of(e, n, part, weights, rank_of);
+        if (part == 0 && i < n && start < want && want <= start + weights[i]) found(e);
+      }
+      return;
+    }
+    sort_list(list, n);
     const int i0 = 2 * static_cast<int>(threadIdx.x);
     u64 w[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) w[j] = i0 + j < n ? (by_mass ? rs.weight(entry_logit(s.work.list[i0 + j])) : 1ull) : 0ull;
+    for (int j = 0; j < 2; ++j) w[j] = i0 + j < n ? (by_mass ? rs.weight(entry_logit(list[i0 + j])) : 1ull) : 0ull;
     u64 total;
     const u64 upto = block_prefix(w[0] + w[1], s.warp_sum, total);
     const u64 start = upto - w[0] - w[1];
-    if (start < want && want <= upto) {
-      const u64 c = s.work.list[i0 + (start + w[0] < want ? 1 : 0)];
-      s.bound = Boundary{entry_logit(c), entry_id(c)};
-      s.found = 1;
+    if (start < want && want <= upto) found(list[i0 + (start + w[0] < want ? 1 : 0)]);
+  }
+  // Entries of the list (of n) ranked before e: their number and their weights' sum, counted by a
+  // team of kShare lanes, each its share.
+  static constexpr int kShare = 4;
+  __device__ __forceinline__ u64 ahead_of(u64 e, int n, int part, const u64* weights, int& rank_of) {
+    u64 mass = 0;
+    rank_of = 0;
+#pragma unroll 4
+    for (int j = part; j < n; j += kShare) {
+      const u64 c = s.work.list[j], w = weights[j];
+      if (c > e) {
+        ++rank_of;
+        mass += w;
+      }
     }
+#pragma unroll
+    for (int o = 1; o < kShare; o <<= 1) {
+      rank_of += __shfl_xor_sync(0xffffffffu, rank_of, o);
+      mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    }
+    return mass;
   }
 
-  // Merges the CTAs' histograms (read(other, bin) gives a bin's sum) and finds the bin at which the
-  // running sum reaches `want`, and the sum before it.  Called after a cluster barrier; ends
-  // with the histograms free.  -1: the sum stays below want.
-  template <class F>
-  __device__ int merge_bins(int bins, u64 want, u64& before, F read) {
-    const int per = bins / ranks;
-    u64 sum = 0;
-    for (int i = threadIdx.x; i < per; i += kSampleThreads) {
+  // The bin of the CTAs' histograms together (read(other, bin) gives a bin's amount in one) at which
+  // the running sum reaches `want`, and the sum before it; -1 if the sum stays below want.  want_of
+  // gives want; one warp calls it, after the cluster barrier in here.  Called
+  // when the block's histogram is complete; the histograms may be overwritten after the next
+  // cluster barrier.  Each CTA adds its bins up in 32 groups; the group is found from
+  // everyone's sums, and only its bins are read from the other CTAs.
+  template <class W, class F>
+  __device__ int find_in_bins(int bins, W want_of, u64& want, u64& before, F read) {
+    const int per = bins / kGroups;
+    __syncthreads();
+    {
+      constexpr int kTeam = kSampleThreads / kGroups;  // 16 threads per group
+      const int g = static_cast<int>(threadIdx.x) / kTeam, at = static_cast<int>(threadIdx.x) % kTeam;
       u64 t = 0;
+      for (int i = at; i < per; i += kTeam) t += read(&s, g * per + i);
+#pragma unroll
+      for (int o = kTeam / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (at == 0) s.groups[g] = t;
+    }
+    sync_cluster();
+    if (threadIdx.x < kGroups * kMaxCluster) {
+      const int g = static_cast<int>(threadIdx.x) / kMaxCluster, r = static_cast<int>(threadIdx.x) % kMaxCluster;
+      u64 t = r < ranks ? peer(&s, r)->groups[g] : 0ull;
+#pragma unroll
+      for (int o = kMaxCluster / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (r == 0) s.group_sum[g] = t;
+    }
+    if (warp == kSampleWarps - 1) {
+      const u64 w = want_of();
+      if (lane == 0) s.want = w;
+    }
+    __syncthreads();
+    want = s.want;
+    const u64 mine = s.group_sum[lane];
+    const u64 upto = warp_prefix(mine, lane);
+    const int group = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
+    if (group < 0) return -1;
+    const u64 run = __shfl_sync(0xffffffffu, upto - mine, group);
+    static_assert(kZBins / kGroups <= kSampleThreads && kFineBins <= kZBins && kBins <= kZBins, "a thread per bin of a group");
+    u64 v = 0;
+    if (static_cast<int>(threadIdx.x) < per) {
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r)
-        if (r < ranks) t += read(peer(&s, r), rank * per + i);
-      merged[i] = t;
-      sum += t;
-    }
-    sum_to_part(sum, 0, s.warp_sum);
-    sync_cluster();
-    // the share that holds the boundary, then the bin within it
-    const u64 share = lane < ranks ? peer(&s, lane)->part[0] : 0ull;
-    const u64 upto = warp_prefix(share, lane);
-    const int owner = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
-    if (owner < 0) return -1;
-    const u64 run = __shfl_sync(0xffffffffu, upto - share, owner);
-    const u64* m = peer(merged, owner);
-    constexpr int kPer = (kZBins + kSampleThreads - 1) / kSampleThreads;
-    static_assert(kZBins >= kBins && kZBins >= kFineBins && kZBins % (2 * kMaxCluster) == 0, "a thread's bins; 16-byte shares");
-    u64 a[kPer], mine = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = kPer * static_cast<int>(threadIdx.x) + j;
-      a[j] = i < per ? m[i] : 0;
-      mine += a[j];
+        if (r < ranks) v += read(peer(&s, r), group * per + static_cast<int>(threadIdx.x));
     }
     u64 total;
-    u64 c = run + block_prefix(mine, s.warp_sum, total) - mine;
-    if (c < want && want <= c + mine) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (c < want && want <= c + a[j]) {
-          s.bin = owner * per + kPer * static_cast<int>(threadIdx.x) + j;
-          s.before = c;
-        }
-        c += a[j];
-      }
+    const u64 c = run + block_prefix(v, s.warp_sum, total);
+    if (c - v < want && want <= c) {
+      s.bin = group * per + static_cast<int>(threadIdx.x);
+      s.before = c - v;
     }
     __syncthreads();
     before = s.before;
@@ -587,13 +634,14 @@ struct RowCtx {
         }
       }
     });
-    sync_cluster();
-    return merge_bins(kBins, want, before, [](const SampleShared<kResident>* o, int i) {
+    const int bin = find_in_bins(kBins, [want] { return want; }, want, before, [](const SampleShared<kResident>* o, int i) {
       u64 t = 0;
 #pragma unroll
       for (int q = 0; q < P::kCount; ++q) t += static_cast<u64>(o->work.hist[q][i]) << (q * P::kBits);
       return t;
     });
+    sync_cluster();
+    return bin;
   }
 
   // The id at which the running sum of f (over the ids, after `before` in the CTAs before) exceeds r,
@@ -656,13 +704,6 @@ struct RowCtx {
     return -1;
   }
 
-  // Bits that the second histogram leaves off the weights of the bin at `edge`: its largest weight
-  // is then below 2^19, so that 2^13 of them add up in 32 bits.
-  static __device__ __forceinline__ int fine_shift(float edge) {
-    const float z = (edge - 8388608.f - 0.5f) * (kZRange / static_cast<float>(kZBins));  // nearest to 0 in the bin
-    return max(0, 41 - static_cast<int>(z * 1.442695f) - 19);
-  }
-
   // What min-p keeps of a logit above the boundaries.
   __device__ __forceinline__ bool min_p_keeps(float x, float e, float min_p) const { return x == rs.m || e >= min_p; }
 
@@ -675,32 +716,31 @@ struct RowCtx {
     const bool cut = keeps.x > -INFINITY;
     for (int i = threadIdx.x; i < kZBins; i += kSampleThreads) s.work.zhist[i] = 0;
     __syncthreads();
-    u64 total = 0, want = count;
     if (by_mass) {
       const u64 sum = sum_weights([&](float x, int v, WeightSum& w) {
         if (cut && !keeps.keeps(x, v)) return;
         const float z = rs.z(x), e = kPlain ? expf(z) : rs.e(x);
         w.add(e);
-        // rounded to 2^-17, so that 2^15 of them add up in 32 bits; a longer slice's bins wrap at
-        // worst, and the exact sums then refuse the bin
-        const uint32_t rounded = __float_as_uint(__fadd_rn(e, 64.f)) - kHiBias;
-        if (rounded) atomicAdd(&s.work.zhist[__float_as_uint(rs.z_bin_of(z)) - 0x4b000000u], rounded);
+        // The weight relative to its octave's 1, in 17 bits, so that 2^15 add up in 32 bits; a longer
+        // slice's bins wrap at worst, and the exact sums then refuse the bin.
+        const int b = bin_number(rs.z_bin_of(z));
+        const float one = __uint_as_float(static_cast<uint32_t>(127 + (b >> kOctaveBits)) << 23);
+        atomicAdd(&s.work.zhist[b], __float_as_uint(__fadd_rn(e * one, 64.f)) - kHiBias);
       });
       sum_to_part(sum, 1, s.warp_sum);
     } else {
       slice.each(lane, [&](float x, int) {
-        if (x > -INFINITY) atomicAdd(&s.work.zhist[__float_as_uint(rs.z_bin(x)) - 0x4b000000u], 1u);
+        if (x > -INFINITY) atomicAdd(&s.work.zhist[bin_number(rs.z_bin(x))], 1u);
       });
     }
-    sync_cluster();
-    if (by_mass) {
-      total = total_of(1);
-      want = by_one_thread(s.want, [&] { return top_p_weight(top_p, total); });
-    }
-    u64 before = 0;
-    // rounded weights may add up to a little less than the exact ones
-    const int bin = merge_bins(kZBins, by_mass ? max(want >> 23, 1ull) : want, before,
-                               [](const SampleShared<kResident>* o, int i) { return static_cast<u64>(o->work.zhist[i]); });
+    u64 want, before = 0;
+    auto want_of = [&] { return by_mass ? top_p_weight(top_p, total_of(1)) : count; };
+    const int bin = find_in_bins(kZBins, want_of, want, before, [by_mass](const SampleShared<kResident>* o, int i) -> u64 {
+      const u64 v = o->work.zhist[i];
+      const int shift = 23 - (i >> kOctaveBits);
+      return !by_mass ? v : shift >= 0 ? v << shift : v >> -shift;
+    });
+    sync_cluster();  // the lists overwrite the histograms
     if (bin < 0) return false;
     // the weights above the bin, and the bin's logits
     clear_list();
@@ -728,7 +768,6 @@ struct RowCtx {
       w.add(e);
     });
     all = filter ? all + open.total() : reach;
-    // part[0] may still be read by the others' merges
     sum_to_part(reach, 3, s.kept_sum);
     sum_to_part(all, 2, s.warp_sum);
     if (threadIdx.x == 0) s.count = s.list_count;
@@ -739,21 +778,24 @@ struct RowCtx {
     if (overfull || (by_mass && above >= want)) return false;
     u64 rest = want - (by_mass ? above : before);  // what is wanted of the bin
     int fine = -1;                                 // the second histogram's bin, if one was needed
-    if (n > kListCap) {
-      // the bin's logits do not fit the first CTA's list: a second histogram of them alone
-      sync_cluster();
+    if (n > kCountingMax) {
+      // too many to rank by counting: a second histogram of them alone
+      // weights lose the bits that bring the bin's largest below 2^19: 2^13 of them add up in 32 bits
+      const int shift = max(0, 41 - (bin >> kOctaveBits) - 19);
       for (int i = threadIdx.x; i < kFineBins; i += kSampleThreads) s.work.fine[i] = 0;
       __syncthreads();
       for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) {
         const float x = logit(static_cast<int>(s.work.near_ids[i]));
-        const uint32_t amount = by_mass ? static_cast<uint32_t>(rs.weight(x) >> fine_shift(edge)) : 1u;
+        const uint32_t amount = by_mass ? static_cast<uint32_t>(rs.weight(x) >> shift) : 1u;
         atomicAdd(&s.work.fine[rs.fine_bin(x, bin)], amount);
       }
-      sync_cluster();
-      u64 ahead = 0;
-      fine = merge_bins(kFineBins, by_mass ? max(rest >> fine_shift(edge), 1ull) : rest, ahead,
-                        [](const SampleShared<kResident>* o, int i) { return static_cast<u64>(o->work.fine[i]); });
-      if (fine < 0) return false;
+      u64 part_want = 0, ahead = 0;
+      fine = find_in_bins(kFineBins, [&] { return by_mass ? max(rest >> shift, 1ull) : rest; }, part_want, ahead,
+                          [](const SampleShared<kResident>* o, int i) { return static_cast<u64>(o->work.fine[i]); });
+      if (fine < 0) {
+        sync_cluster();
+        return false;
+      }
       u64 sum = 0, number = 0;
       for (uint32_t i = threadIdx.x; i < s.count; i += kSampleThreads) {
         const float x = logit(static_cast<int>(s.work.near_ids[i]));
@@ -781,10 +823,7 @@ struct RowCtx {
     }
     const int listed = fine < 0 ? static_cast<int>(n) : static_cast<int>(total_of(3));
     sync_cluster();
-    if (rank == 0) {
-      sort_list(s.work.list, listed);
-      bound_in_list(listed, by_mass, rest);
-    }
+    if (rank == 0) bound_in_list(listed, by_mass, rest, counting);
     sync_cluster();
     if (!peer(&s, 0)->found) return false;
     bound = peer(&s, 0)->bound;
@@ -814,7 +853,7 @@ struct RowCtx {
   // most what there is.  The whole cluster.
   __device__ Boundary find_boundary(const Boundary& keeps, bool by_mass, u64 want) {
     auto amount_of = [&](float x) -> u64 { return by_mass ? rs.weight(x) : 1ull; };
-    auto coarse = [&](float x) -> int { return static_cast<int>(__float_as_uint(rs.z_bin(x)) - 0x4b000000u) * kBins / kZBins; };
+    auto coarse = [&](float x) -> int { return bin_number(rs.z_bin(x)) * kBins / kZBins; };
     u64 before = 0;
     int bin = find_bin(want, before, [&](float x, int v, uint32_t& b, u64& amount) -> bool {
       if (!(x > -INFINITY) || !keeps.keeps(x, v)) return false;
@@ -832,10 +871,7 @@ struct RowCtx {
       if (n <= kListCap) {
         push_list();
         sync_cluster();
-        if (rank == 0) {
-          sort_list(s.work.list, static_cast<int>(n));
-          bound_in_list(static_cast<int>(n), by_mass, want);
-        }
+        if (rank == 0) bound_in_list(static_cast<int>(n), by_mass, want, counting);
         break;
       }
       if (lo == hi) {  // more equal logits than the list holds: the ids decide
@@ -915,31 +951,18 @@ struct RowCtx {
       // before it and adds up their weights, then, of those kept, the weights of lower ids.
       for (int i = threadIdx.x; i < n; i += kSampleThreads) weights[i] = rs.weight(entry_logit(list[i]));
       __syncthreads();
-      constexpr int kShare = 4;  // threads per entry
-      static_assert(kCountingMax * kShare <= 2 * kSampleThreads, "two rounds of entries");
+      constexpr int kRound = kSampleThreads / kShare;  // entries per round
+      static_assert(kCountingMax <= 2 * kRound, "two rounds of entries");
       const int part = threadIdx.x % kShare;
-      u64 kept_w[2], top = 0;
-      bool in_top[2];
-      u64 ahead[2];
+      u64 kept_w[2] = {0, 0}, ahead[2] = {0, 0}, top = 0;
+      bool in_top[2] = {false, false};
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int i = q * (kSampleThreads / kShare) + static_cast<int>(threadIdx.x) / kShare;
-        const u64 e = i < n ? list[i] : ~0ull;
-        int rank_of = 0;
-        u64 mass = 0;
-        for (int j = part; j < n; j += kShare) {
-          if (list[j] > e) {
-            ++rank_of;
-            mass += weights[j];
-          }
-        }
-#pragma unroll
-        for (int o = 1; o < kShare; o <<= 1) {
-          rank_of += __shfl_xor_sync(0xffffffffu, rank_of, o);
-          mass += __shfl_xor_sync(0xffffffffu, mass, o);
-        }
+        if (q * kRound >= n) break;
+        const int i = q * kRound + static_cast<int>(threadIdx.x) / kShare;
+        int rank_of;
+        ahead[q] = ahead_of(i < n ? list[i] : ~0ull, n, part, weights, rank_of);
         in_top[q] = i < n && rank_of < k;
-        ahead[q] = mass;
         kept_w[q] = in_top[q] ? weights[i] : 0;
         if (part == 0) top += kept_w[q];
       }
@@ -949,7 +972,7 @@ struct RowCtx {
       u64 left = 0;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int i = q * (kSampleThreads / kShare) + static_cast<int>(threadIdx.x) / kShare;
+        const int i = q * kRound + static_cast<int>(threadIdx.x) / kShare;
         bool keep = in_top[q] && (!need_p || ahead[q] < want);
         if (keep) {
           const float x = entry_logit(list[i]);
@@ -963,11 +986,15 @@ struct RowCtx {
       const u64 r = by_one_thread(s.draw, [&] { return draw_at(u, total); });
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const int i = q * (kSampleThreads / kShare) + static_cast<int>(threadIdx.x) / kShare;
+        if (q * kRound >= n) break;
+        const int i = q * kRound + static_cast<int>(threadIdx.x) / kShare;
         const int id = i < n ? entry_id(list[i]) : 0;
         u64 mass = 0;
-        for (int j = part; j < n; j += kShare)
-          if (entry_id(list[j]) < id) mass += by_id[j];
+#pragma unroll 4
+        for (int j = part; j < n; j += kShare) {
+          const u64 w = by_id[j];
+          if (entry_id(list[j]) < id) mass += w;
+        }
 #pragma unroll
         for (int o = 1; o < kShare; o <<= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
         if (part == 0 && mass <= r && r < mass + kept_w[q]) {
@@ -1190,12 +1217,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   const int64_t b = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  u64* const merged = reinterpret_cast<u64*>(dyn);
+  u64* const counting = reinterpret_cast<u64*>(dyn);
   Slice<T, kResident> sl;
   sl.first = min(V, rank * per);
   sl.n = min(V, sl.first + per) - sl.first;
   sl.g = logits + b * ld + sl.first;
-  sl.s = dyn + kZBins / ranks * sizeof(u64) / sizeof(uint4);
+  sl.s = dyn + kCountingMax * sizeof(u64) / sizeof(uint4);
   sl.shift = static_cast<int>((reinterpret_cast<uintptr_t>(sl.g) % 16) / sizeof(T));
   sl.nvec = sl.n > 0 ? (sl.n + sl.shift + E - 1) / E : 0;
   const int per_warp = (sl.nvec + kSampleWarps - 1) / kSampleWarps;
@@ -1274,10 +1301,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   const float inv_t = 1.f / t;
   u64* const scratch = reinterpret_cast<u64*>(dyn);
   if (m < INFINITY && inv_t > 0.f && inv_t < INFINITY) {
-    RowCtx<T, kResident, true> c{sl, s, merged, RowScale<true>{m, inv_t}, rank, ranks, warp, lane};
+    RowCtx<T, kResident, true> c{sl, s, counting, RowScale<true>{m, inv_t}, rank, ranks, warp, lane};
     c.run(V, k, list_first, tau, top_p, min_p, u[b], scratch, token + b, lp);
   } else {
-    RowCtx<T, kResident, false> c{sl, s, merged, RowScale<false>{m, inv_t}, rank, ranks, warp, lane};
+    RowCtx<T, kResident, false> c{sl, s, counting, RowScale<false>{m, inv_t}, rank, ranks, warp, lane};
     c.run(V, k, list_first, tau, top_p, min_p, u[b], scratch, token + b, lp);
   }
 }
@@ -1310,8 +1337,8 @@ static SamplePlan plan_sample(int64_t B, int64_t V, size_t elem, int sms) {
   for (p.ranks = 1;; p.ranks *= 2) {
     const int64_t per = ((V + p.ranks - 1) / p.ranks + vec - 1) / vec * vec;
     p.per = static_cast<int>(per);
-    // the merged histogram and the slice, which may start inside a vector
-    const size_t need = kZBins / p.ranks * sizeof(u64) + static_cast<size_t>(per) * elem + 16;
+    // the counted entries' weights and the slice, which may start inside a vector
+    const size_t need = kCountingMax * sizeof(u64) + static_cast<size_t>(per) * elem + 16;
     p.resident = need <= kOne && per <= Pieces<true>::kMaxSlice;
     p.smem = p.resident && need > kScratch ? need : kScratch;
     const bool wide = need <= kTwo && per <= Pieces<true>::kMaxSlice;
