@@ -50,6 +50,7 @@ constexpr int kZBins = kOctaves << kOctaveBits;
 constexpr float kZBinWidth = 0.6931471806f / 64.f;
 constexpr int kFineBins = 2048;        // of the second histogram, over one bin of the first
 constexpr int kGroups = 32;            // groups of bins that are added up before they are exchanged
+constexpr int kFew = 32;
 constexpr int kCountingMax = 160;      // longest list that is ranked by counting, not sorted
 
 using u64 = unsigned long long;
@@ -101,9 +102,9 @@ struct WeightSum {
 template <bool kPlain>
 struct RowScale {
   float m, inv_t;
-  __device__ __forceinline__ float z(float x) const {
-    if (kPlain) return (x - m) * inv_t;
-    return x == m ? 0.f : (x - m) * inv_t;
+  __device__ __forceinline__ float z(float x) const {  // the product is rounded by itself
+    if (kPlain) return __fmul_rn(x - m, inv_t);
+    return x == m ? 0.f : __fmul_rn(x - m, inv_t);
   }
   // exp(z); 0 for -inf (and where infinities leave no number)
   __device__ __forceinline__ float e(float x) const {
@@ -173,6 +174,7 @@ struct SampleShared {
   int bin;
   u64 before, want, draw;
   u64 group_sum[kGroups];
+  u64 few[kFew], few_weights[kFew];
 };
 
 // Barrier of the cluster's threads: shared memory written before it is seen by every CTA after.
@@ -527,6 +529,80 @@ struct RowCtx {
       }
       return;
     }
+    // Longer: exact sums of 128 bins of the keys' range, then the bin's few entries by counting.
+    constexpr int kKeyBins = 128;
+    static_assert(kKeyBins <= kCountingMax && kListCap <= 2 * kSampleThreads, "the bins fit, two entries a thread");
+    u64 mine[2] = {0, 0}, amount[2] = {0, 0};
+    uint32_t klo = 0xffffffffu, khi = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = static_cast<int>(threadIdx.x) + j * kSampleThreads;
+      if (i >= n) break;
+      mine[j] = list[i];
+      amount[j] = by_mass ? rs.weight(entry_logit(mine[j])) : 1ull;
+      klo = min(klo, static_cast<uint32_t>(mine[j] >> 32));
+      khi = max(khi, static_cast<uint32_t>(mine[j] >> 32));
+    }
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    if (lane == 0) {
+      s.warp_lo[warp] = klo;
+      s.warp_hi[warp] = khi;
+    }
+    if (threadIdx.x < kKeyBins) weights[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+      s.bin = -1;
+      s.list_count = 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSampleWarps; ++w) {
+      klo = min(klo, s.warp_lo[w]);
+      khi = max(khi, s.warp_hi[w]);
+    }
+    const int bits = 32 - __clz(khi - klo), shift = bits > 7 ? bits - 7 : 0;
+    auto key_bin = [&](u64 e) { return static_cast<int>((khi - static_cast<uint32_t>(e >> 32)) >> shift); };
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (amount[j] != 0) atomicAdd(&weights[key_bin(mine[j])], amount[j]);
+    __syncthreads();
+    if (warp == 0) {
+      u64 a[kKeyBins / 32], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kKeyBins / 32; ++j) sum += a[j] = weights[kKeyBins / 32 * lane + j];
+      u64 c = warp_prefix(sum, lane) - sum;
+#pragma unroll
+      for (int j = 0; j < kKeyBins / 32; ++j) {
+        if (c < want && want <= c + a[j]) {
+          s.bin = kKeyBins / 32 * lane + j;
+          s.before = c;
+        }
+        c += a[j];
+      }
+    }
+    __syncthreads();
+    if (s.bin < 0) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (amount[j] != 0 && key_bin(mine[j]) == s.bin) {
+        const uint32_t at = atomicAdd(&s.list_count, 1u);
+        if (at < kFew) {
+          s.few[at] = mine[j];
+          s.few_weights[at] = amount[j];
+        }
+      }
+    __syncthreads();
+    const int m = static_cast<int>(s.list_count);
+    if (m <= kFew) {
+      if (static_cast<int>(threadIdx.x) < m) {
+        const u64 e = s.few[threadIdx.x];
+        u64 start = s.before;
+        for (int j = 0; j < m; ++j)
+          if (s.few[j] > e) start += s.few_weights[j];
+        if (start < want && want <= start + s.few_weights[threadIdx.x]) found(e);
+      }
+      return;
+    }
     sort_list(list, n);
     const int i0 = 2 * static_cast<int>(threadIdx.x);
     u64 w[2];
@@ -717,16 +793,35 @@ struct RowCtx {
     for (int i = threadIdx.x; i < kZBins; i += kSampleThreads) s.work.zhist[i] = 0;
     __syncthreads();
     if (by_mass) {
-      const u64 sum = sum_weights([&](float x, int v, WeightSum& w) {
-        if (cut && !keeps.keeps(x, v)) return;
-        const float z = rs.z(x), e = kPlain ? expf(z) : rs.e(x);
+      auto count_in = [&](float z, float e, WeightSum& w) {
         w.add(e);
-        // The weight relative to its octave's 1, in 17 bits, so that 2^15 add up in 32 bits; a longer
-        // slice's bins wrap at worst, and the exact sums then refuse the bin.
-        const int b = bin_number(rs.z_bin_of(z));
-        const float one = __uint_as_float(static_cast<uint32_t>(127 + (b >> kOctaveBits)) << 23);
-        atomicAdd(&s.work.zhist[b], __float_as_uint(__fadd_rn(e * one, 64.f)) - kHiBias);
-      });
+        // The weight relative to its octave, in 17 bits (its mantissa's; 1 counts as the number below
+        // it, which has the octave's exponent), so that 2^15 add up in 32 bits; a longer slice's
+        // bins wrap at worst, and the exact sums then refuse the bin.
+        const uint32_t amount = ((((__float_as_uint(e) - 1u) & 0x7fffffu) | 0x800000u) + 64u) >> 7;
+        atomicAdd(&s.work.zhist[bin_number(rs.z_bin_of(z))], amount);
+      };
+      u64 sum;
+      if (kPlain && kResident && !cut) {  // two logits at a time where that is one instruction
+        WeightSum w;
+        const float2 om = make_float2(-rs.m, -rs.m), it = make_float2(rs.inv_t, rs.inv_t);
+        for (int i = slice.v0 + lane; i < slice.v1; i += 32) {
+          float v[E];
+          slice.get(i, v);
+#pragma unroll
+          for (int j = 0; j < E; j += 2) {
+            const float2 z = fmul2(fadd2(make_float2(v[j], v[j + 1]), om), it);
+            count_in(z.x, expf(z.x), w);
+            count_in(z.y, expf(z.y), w);
+          }
+        }
+        sum = w.total();
+      } else {
+        sum = sum_weights([&](float x, int v, WeightSum& w) {
+          if (cut && !keeps.keeps(x, v)) return;
+          count_in(rs.z(x), rs.e(x), w);
+        });
+      }
       sum_to_part(sum, 1, s.warp_sum);
     } else {
       slice.each(lane, [&](float x, int) {
@@ -737,7 +832,7 @@ struct RowCtx {
     auto want_of = [&] { return by_mass ? top_p_weight(top_p, total_of(1)) : count; };
     const int bin = find_in_bins(kZBins, want_of, want, before, [by_mass](const SampleShared<kResident>* o, int i) -> u64 {
       const u64 v = o->work.zhist[i];
-      const int shift = 23 - (i >> kOctaveBits);
+      const int shift = 23 - (i >> kOctaveBits);  // to units of 2^-40
       return !by_mass ? v : shift >= 0 ? v << shift : v >> -shift;
     });
     sync_cluster();  // the lists overwrite the histograms
@@ -748,25 +843,45 @@ struct RowCtx {
     const bool filter = !(min_p <= 0.f);
     WeightSum open;
     u64 all = 0;
-    const u64 reach = sum_weights([&](float x, int v, WeightSum& w) {
-      const float z = rs.z(x), u = rs.z_bin_of(z);
-      if (!(u <= edge)) return;
-      if (cut && !keeps.keeps(x, v)) return;
-      if (u == edge) {
-        if (x > -INFINITY) append(v);
-        return;
-      }
-      const float e = kPlain ? expf(z) : rs.e(x);
-      if (filter) {
-        open.add(e);
-        if (!kResident && open.n >= WeightSum::kMaxAdds) {
-          all += open.total();
-          open = WeightSum();
+    u64 reach;
+    if (kPlain && kResident && !cut && !filter) {  // two logits at a time where that is one instruction
+      WeightSum w;
+      const float2 om = make_float2(-rs.m, -rs.m), it = make_float2(rs.inv_t, rs.inv_t);
+      for (int i = slice.v0 + lane; i < slice.v1; i += 32) {
+        float v[E];
+        slice.get(i, v);
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+          const float2 z = fmul2(fadd2(make_float2(v[j], v[j + 1]), om), it);
+          const float u0 = rs.z_bin_of(z.x), u1 = rs.z_bin_of(z.y);
+          if (u0 < edge) w.add(expf(z.x));
+          if (u1 < edge) w.add(expf(z.y));
+          if (u0 == edge && v[j] > -INFINITY) append(slice.id(i, j));
+          if (u1 == edge && v[j + 1] > -INFINITY) append(slice.id(i, j + 1));
         }
-        if (!min_p_keeps(x, e, min_p)) return;
       }
-      w.add(e);
-    });
+      reach = w.total();
+    } else {
+      reach = sum_weights([&](float x, int v, WeightSum& w) {
+        const float u = rs.z_bin(x);
+        if (!(u <= edge)) return;
+        if (cut && !keeps.keeps(x, v)) return;
+        if (u == edge) {
+          if (x > -INFINITY) append(v);
+          return;
+        }
+        const float e = rs.e(x);
+        if (filter) {
+          open.add(e);
+          if (!kResident && open.n >= WeightSum::kMaxAdds) {
+            all += open.total();
+            open = WeightSum();
+          }
+          if (!min_p_keeps(x, e, min_p)) return;
+        }
+        w.add(e);
+      });
+    }
     all = filter ? all + open.total() : reach;
     sum_to_part(reach, 3, s.kept_sum);
     sum_to_part(all, 2, s.warp_sum);
@@ -778,8 +893,8 @@ struct RowCtx {
     if (overfull || (by_mass && above >= want)) return false;
     u64 rest = want - (by_mass ? above : before);  // what is wanted of the bin
     int fine = -1;                                 // the second histogram's bin, if one was needed
-    if (n > kCountingMax) {
-      // too many to rank by counting: a second histogram of them alone
+    if (n > kListCap) {
+      // too many for the first CTA's list: a second histogram of them alone
       // weights lose the bits that bring the bin's largest below 2^19: 2^13 of them add up in 32 bits
       const int shift = max(0, 41 - (bin >> kOctaveBits) - 19);
       for (int i = threadIdx.x; i < kFineBins; i += kSampleThreads) s.work.fine[i] = 0;
