@@ -485,3 +485,78 @@ def test_host_memory_is_refused(fkl):
     st = L.fkl_int8_matmul(q.data_ptr(), s.data_ptr(), q.data_ptr(), host.data_ptr(), 4, 4, 64, 0, x.data_ptr(), 4,
                            ws.data_ptr(), ws.numel(), None)
     assert st == 1 and b"w_scale" in L.fkl_last_error()
+
+
+# ---------------------------------------------------------------- paths that sizes and values choose
+@pytest.mark.parametrize("kw", [dict(temperature=1000.0, top_p=0.5), dict(temperature=1000.0, top_k=9000),
+                                dict(temperature=1e-3, top_p=0.9), dict(top_k=600, top_p=0.7, min_p=1e-4),
+                                dict(top_k=513), dict(top_k=512, top_p=0.3), dict(top_p=1e-6), dict(min_p=1e-6, top_p=0.9),
+                                dict(temperature=1e30, top_p=0.4), dict(temperature=float("inf"), top_p=0.4),
+                                dict(temperature=1e-30)])
+@pytest.mark.parametrize("V,dtype", [(20011, torch.float32), (151936, torch.bfloat16), (700001, torch.float16),
+                                     (700001, torch.float32)])
+def test_sample_paths(fkl, V, dtype, kw):
+    # lists, histograms in z, exact histograms, rows too long for shared memory
+    logits, u = lm_logits(2, V, V % 1000, dtype)
+    if kw.get("temperature", 1.0) > 1e20 and dtype == torch.float32:
+        logits[0, 5] = 3e38                      # z underflows to 0 for all others
+    check_sample(fkl, logits, u, **kw)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-6, 0.01, 1.0, 30.0])
+@pytest.mark.parametrize("p", [0.05, 0.5, 0.9, 0.999])
+def test_sample_top_p_of_flat_and_sharp_rows(fkl, scale, p):
+    g = torch.Generator().manual_seed(int(p * 1000))
+    logits = torch.randn(4, 30011, generator=g) * scale
+    check_sample(fkl, logits, torch.rand(4, generator=g), top_p=p)
+
+
+def test_sample_rows_do_not_disturb_each_other(fkl):
+    # the same row alone and inside a batch with rows of other kinds
+    logits, u = lm_logits(12, 9001, 3)
+    logits[3] = float("-inf")
+    logits[5] = 0
+    kw = dict(temperature=torch.linspace(0, 2, 12), top_k=torch.arange(12, dtype=torch.int32) * 100,
+              top_p=torch.linspace(0.5, 1.1, 12), min_p=torch.linspace(0, 0.1, 12))
+    dk = {n: v.cuda() for n, v in kw.items()}
+    t, lp = fkl.sample(logits.cuda(), u.cuda(), **dk)
+    for b in range(12):
+        t1, lp1 = fkl.sample(logits[b:b + 1].cuda(), u[b:b + 1].cuda(), **{n: v[b:b + 1] for n, v in dk.items()})
+        assert t1[0] == t[b] and (lp1[0] == lp[b] or (t[b] == -1 and torch.isnan(lp[b])))
+
+
+@pytest.mark.parametrize("N", [1, 255, 256, 257, 19456, 19457, 20000, 40000])
+@pytest.mark.parametrize("M", [1, 4, 5, 16])
+def test_int8_matmul_waves(fkl, M, N):
+    # around whole waves of CTA pairs (76 x 256 channels) and of the streaming kernel's warps
+    ops = operands(M, N, 144, N + M)
+    assert_product(fkl.int8_matmul(*dev(*ops)), ops, torch.float32)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 98304), (2, 70, 49168), (3, 40, 131072), (20, 300, 131072), (4, 17, 24592)])
+def test_int8_matmul_deep(fkl, M, N, K):
+    # the streaming kernel's tokens no longer fit shared memory beyond M * K = 96 K
+    rng = np.random.default_rng(K)
+    xq = rng.integers(-3, 4, (M, K)).astype(np.int8)   # sums stay below 2^24: exact
+    wq = rng.integers(-3, 4, (N, K)).astype(np.int8)
+    one, w1 = np.full(M, 0.5, np.float32), np.full(N, 0.25, np.float32)
+    y = fkl.int8_matmul(*dev(xq, one, wq, w1)).double().cpu().numpy()
+    np.testing.assert_array_equal(y, og.int8_matmul(xq, one, wq, w1))
+
+
+def test_int8_linear_default_workspaces_of_two_streams(fkl):
+    # calls queued on two streams do not share the module's workspace
+    g = torch.Generator().manual_seed(9)
+    wq, ws = fkl.quantize_int8((torch.randn(6000, 512, generator=g) * 0.02).cuda())
+    xs = [torch.randn(64, 512, generator=g).cuda() for _ in range(2)]
+    ref = [fkl.int8_linear(x, wq, ws) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(fkl.int8_linear(xs[i], wq, ws))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, ref[i]) for y in got[i])
