@@ -183,6 +183,16 @@ __device__ __forceinline__ void sync_cluster() {
   cluster_sync();
 }
 
+// The barrier's two halves.
+__device__ __forceinline__ void arrive_cluster() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void wait_cluster() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // The same shared-memory object in CTA `rank` of the cluster.
 template <class P>
 __device__ __forceinline__ P* peer(P* p, int rank) {
@@ -217,14 +227,10 @@ __device__ u64 block_prefix(u64 v, u64* warp_sum, u64& total) {
   __syncthreads();
   if (lane == 31) warp_sum[warp] = v;
   __syncthreads();
-  u64 before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kSampleWarps; ++w) {
-    if (w == warp) before = total;
-    total += warp_sum[w];
-  }
-  return before + v;
+  const u64 sums = warp_prefix(lane < kSampleWarps ? warp_sum[lane] : 0ull, lane);
+  total = __shfl_sync(0xffffffffu, sums, 31);
+  const u64 before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0ull) + v;
 }
 
 // Sorts the first n (a power of two, at most 2 * kSampleThreads) keys in descending order with
@@ -400,11 +406,12 @@ struct RowCtx {
     __syncthreads();
     if (lane == 0) warps[warp] = v;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      u64 t = 0;
-      for (int w = 0; w < kSampleWarps; ++w) t += warps[w];
-      s.part[slot] = t;
-    }
+    if (warp == 0) add_warps(warps, slot);
+  }
+  // One warp: the sum of the warps' sums into s.part[slot].
+  __device__ __forceinline__ void add_warps(const u64* warps, int slot) {
+    const u64 t = warp_add(lane < kSampleWarps ? warps[lane] : 0ull);
+    if (lane == 0) s.part[slot] = t;
   }
   // Sum of part[slot] over the cluster, and over the CTAs before this one.  Lane r of each warp
   // reads CTA r's, so that it takes one trip to their shared memory.
@@ -555,11 +562,8 @@ struct RowCtx {
       s.list_count = 0;
     }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSampleWarps; ++w) {
-      klo = min(klo, s.warp_lo[w]);
-      khi = max(khi, s.warp_hi[w]);
-    }
+    klo = __reduce_min_sync(0xffffffffu, s.warp_lo[lane % kSampleWarps]);
+    khi = __reduce_max_sync(0xffffffffu, s.warp_hi[lane % kSampleWarps]);
     const int bits = 32 - __clz(khi - klo), shift = bits > 7 ? bits - 7 : 0;
     auto key_bin = [&](u64 e) { return static_cast<int>((khi - static_cast<uint32_t>(e >> 32)) >> shift); };
 #pragma unroll
@@ -725,16 +729,11 @@ struct RowCtx {
   // warp's stretch.  The block's warps share the stretch that holds the id.
   template <class F>
   __device__ int locate(u64 before, u64 r, F f) {
-    int owner = -1;
-    for (int w = 0; w < kSampleWarps; ++w) {
-      const u64 t = s.kept_sum[w];
-      if (before <= r && r < before + t) {
-        owner = w;
-        break;
-      }
-      before += t;
-    }
+    const u64 stretch = lane < kSampleWarps ? s.kept_sum[lane] : 0ull;
+    const u64 upto = before + warp_prefix(stretch, lane);
+    const int owner = before <= r ? __ffs(__ballot_sync(0xffffffffu, upto > r)) - 1 : -1;
     if (owner < 0) return -1;  // the same in the whole block
+    before = __shfl_sync(0xffffffffu, upto - stretch, owner);
     const int per = (slice.nvec + kSampleWarps - 1) / kSampleWarps;
     const int w0 = min(slice.nvec, owner * per), w1 = min(slice.nvec, w0 + per);
     const int sub = (w1 - w0 + kSampleWarps - 1) / kSampleWarps;
@@ -749,7 +748,7 @@ struct RowCtx {
     sum = warp_add(sum);
     if (lane == 0) s.warp_sum[warp] = sum;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+    before += warp_add(lane < warp ? s.warp_sum[lane] : 0ull);
     if (!(before <= r && r < before + sum)) return -1;
     for (int i0 = b; i0 < e; i0 += 32) {
       const int i = i0 + lane;
@@ -1244,15 +1243,12 @@ struct RowCtx {
       sum_to_part(sum, 1, s.kept_sum);
     } else {
       sync_cluster();
-      if (threadIdx.x == 0) {
-        u64 t = 0;
-        for (int w = 0; w < kSampleWarps; ++w) t += s.kept_sum[w];
-        s.part[1] = t;
-      }
+      if (warp == 0) add_warps(s.kept_sum, 1);
     }
     sync_cluster();
     u64 before = 0;
     const u64 total = total_of(1, &before);
+    arrive_cluster();  // nothing of another CTA is read from here on
     const u64 r = by_one_thread(s.draw, [&] { return draw_at(u, total); });
     const int id = locate(before, r, [&](float x, int v) -> u64 {
       if (cut && !bound.keeps(x, v)) return 0;
@@ -1263,7 +1259,7 @@ struct RowCtx {
       *token = id;
       if (logprob != nullptr) *logprob = log_probability(rs.z(logit(id)), total);
     }
-    sync_cluster();  // no CTA leaves while another reads its shared memory
+    wait_cluster();  // no CTA leaves while another reads its shared memory
   }
 };
 
@@ -1287,12 +1283,8 @@ __device__ float block_tau(float tmax, int want, SampleShared<kResident>& s) {
     s.lo = 0xffffffffu;
   }
   __syncthreads();
-  uint32_t hi = 0, lo = 0xffffffffu;
-#pragma unroll
-  for (int w = 0; w < kSampleWarps; ++w) {
-    hi = max(hi, s.warp_hi[w]);
-    lo = min(lo, s.warp_lo[w]);
-  }
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, s.warp_hi[lane % kSampleWarps]);
+  const uint32_t lo = __reduce_min_sync(0xffffffffu, s.warp_lo[lane % kSampleWarps]);
   const float x_hi = key_logit(hi), width = x_hi - key_logit(lo);
   const bool spread = lo < hi && width > 0.f && width < INFINITY;  // the same for the block
   const int bin = !valid || !spread ? 0 : static_cast<int>(fminf((x_hi - tmax) * (256.f / width), 255.f));
@@ -1364,11 +1356,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
   const bool list_first = k > 1 && k < V && k <= min(kListCap / 2, kSampleThreads * 3 / 4 * ranks);
   const float own_tau = list_first ? block_tau(tmax, (k + ranks - 1) / ranks, s) : -INFINITY;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float m = s.warp_max[0];
-    for (int w = 1; w < kSampleWarps; ++w) m = fmaxf(m, s.warp_max[w]);
-    s.cta_max = m;
-    s.tau = own_tau;
+  if (warp == 0) {
+    float m = lane < kSampleWarps ? s.warp_max[lane] : -INFINITY;
+#pragma unroll
+    for (int o = kSampleWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) {
+      s.cta_max = m;
+      s.tau = own_tau;
+    }
   }
   sync_cluster();
   float m = lane < ranks ? peer(&s, lane)->cta_max : -INFINITY;
@@ -1398,17 +1393,15 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) s.warp_hi[warp] = static_cast<uint32_t>(first);
     __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t f = s.warp_hi[0];
-      for (int w = 1; w < kSampleWarps; ++w) f = min(f, s.warp_hi[w]);
-      s.count = f;
-    }
+    const uint32_t own = __reduce_min_sync(0xffffffffu, s.warp_hi[lane % kSampleWarps]);
+    if (threadIdx.x == 0) s.count = own;
     sync_cluster();
-    if (rank == 0 && threadIdx.x == 0) {
-      uint32_t f = s.count;
-      for (int r = 1; r < ranks; ++r) f = min(f, peer(&s, r)->count);
-      token[b] = static_cast<int32_t>(f);
-      if (lp != nullptr) *lp = 0.f;
+    if (rank == 0 && warp == 0) {
+      const uint32_t f = __reduce_min_sync(0xffffffffu, lane < ranks ? peer(&s, lane)->count : 0xffffffffu);
+      if (lane == 0) {
+        token[b] = static_cast<int32_t>(f);
+        if (lp != nullptr) *lp = 0.f;
+      }
     }
     sync_cluster();
     return;
@@ -1426,7 +1419,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2)
 
 // ---------------------------------------------------------------- launch
 // CTAs per row: the fewest whose slices fit two to an SM, or one to an SM, in shared memory;
-// more (up to 8) while the rows do not fill the device.  Rows beyond what 8 CTAs hold are read
+// more (up to 8) as long as all rows still run at once.  Rows beyond what 8 CTAs hold are read
 // again by each pass instead.
 struct SamplePlan {
   int ranks, per;
@@ -1444,21 +1437,70 @@ constexpr size_t max_dynamic(int n) {
 // Fewest logits that a CTA gets a slice of.
 constexpr int64_t kMinSlice = 4096;
 
-static SamplePlan plan_sample(int64_t B, int64_t V, size_t elem, int sms) {
+// Clusters of `ranks` CTAs (1, 2, 4 or 8) of one kernel that run at once, two CTAs to an SM, on the
+// current device; asked of the driver once.
+template <class Kern>
+static int clusters_at_once(Kern kern, int ranks, int sms) {
+  static std::atomic<int> known[64][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 2 * sms / ranks;
+  std::atomic<int>& slot = known[dev][ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3];
+  int n = slot.load();
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ranks));
+  cfg.blockDim = dim3(kSampleThreads);
+  cfg.dynamicSmemBytes = 64 * 1024;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 2 * sms / ranks;
+  }
+  slot.store(n);
+  return n;
+}
+
+template <class T>
+static SamplePlan plan_sample(int64_t B, int64_t V, int sms) {
   constexpr size_t kScratch = 2 * kListCap * sizeof(u64);  // the list's weights and ids
   constexpr size_t kOne = max_dynamic<true>(1), kTwo = max_dynamic<true>(2);
-  const int64_t vec = static_cast<int64_t>(16 / elem);
+  constexpr int64_t vec = 16 / sizeof(T);
   SamplePlan p{};
   for (p.ranks = 1;; p.ranks *= 2) {
     const int64_t per = ((V + p.ranks - 1) / p.ranks + vec - 1) / vec * vec;
     p.per = static_cast<int>(per);
     // the counted entries' weights and the slice, which may start inside a vector
-    const size_t need = kCountingMax * sizeof(u64) + static_cast<size_t>(per) * elem + 16;
+    const size_t need = kCountingMax * sizeof(u64) + static_cast<size_t>(per) * sizeof(T) + 16;
     p.resident = need <= kOne && per <= Pieces<true>::kMaxSlice;
     p.smem = p.resident && need > kScratch ? need : kScratch;
     const bool wide = need <= kTwo && per <= Pieces<true>::kMaxSlice;
-    if (p.ranks == kMaxCluster || (wide && (B * p.ranks > sms || V < 2 * kMinSlice * p.ranks))) return p;
+    if (p.ranks == kMaxCluster) return p;
+    if (wide && (V < 2 * kMinSlice * p.ranks || B > clusters_at_once(sample_kernel<T, true>, 2 * p.ranks, sms))) return p;
   }
+}
+
+// Raises the kernels' shared-memory limits, once per device.
+template <class T>
+static cudaError_t raise_limits() {
+  static std::atomic<uint64_t> raised[2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (raised[(dev >> 6) & 1].load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(max_dynamic<true>(1)));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(sample_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(max_dynamic<false>(1)));
+  if (e == cudaSuccess) raised[(dev >> 6) & 1].fetch_or(bit);
+  return e;
 }
 
 template <class T, bool kResident>
@@ -1466,17 +1508,6 @@ static cudaError_t launch_sample(const void* logits, int64_t B, int64_t V, int64
                                  const fkl_sample_params& params, int32_t* token, float* logprob, const SamplePlan& pl,
                                  cudaStream_t st) {
   auto kern = sample_kernel<T, kResident>;
-  static std::atomic<uint64_t> raised[2];  // devices whose shared-memory limit is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t{1} << (dev & 63);
-  if (!(raised[(dev >> 6) & 1].load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(max_dynamic<kResident>(1)));
-    if (e != cudaSuccess) return e;
-    raised[(dev >> 6) & 1].fetch_or(bit);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B * pl.ranks));
   cfg.blockDim = dim3(kSampleThreads);
@@ -1527,7 +1558,8 @@ extern "C" fkl_status fkl_sample(const void* logits, int32_t type, int64_t B, in
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = with_type(type, [&](auto t) {
     using T = decltype(t);
-    const SamplePlan pl = plan_sample(B, V, sizeof(T), sms);
+    if (const cudaError_t e = raise_limits<T>(); e != cudaSuccess) return e;
+    const SamplePlan pl = plan_sample<T>(B, V, sms);
     return pl.resident ? launch_sample<T, true>(logits, B, V, ld, u, *params, token, logprob, pl, st)
                        : launch_sample<T, false>(logits, B, V, ld, u, *params, token, logprob, pl, st);
   });
