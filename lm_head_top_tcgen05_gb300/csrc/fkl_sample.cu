@@ -43,8 +43,10 @@ constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxSampleV = int64_t{1} << 22;  // 2^22 weights of 2^40 stay below 2^63
 constexpr int kBins = 1024;
 constexpr int kListCap = 1024;
-// The first histogram, over z: 64 bins to each halving of the weight, 36 halvings; smaller weights
-// share the last bin.
+// The first histogram, over z: 64 bins to each halving of the weight, 36 halvings.  Smaller weights
+// belong to the last bin, which is not kept: a sharp row's logits are mostly there, and adding
+// them to one address is slow (512 sharp rows of 32000, top-p 0.9: 69 us with, 62 us without).  A
+// boundary in it is left to the exact histograms.
 constexpr int kOctaveBits = 6, kOctaves = 36;
 constexpr int kZBins = kOctaves << kOctaveBits;
 constexpr float kZBinWidth = 0.6931471806f / 64.f;
@@ -798,7 +800,8 @@ struct RowCtx {
         // it, which has the octave's exponent), so that 2^15 add up in 32 bits; a longer slice's
         // bins wrap at worst, and the exact sums then refuse the bin.
         const uint32_t amount = ((((__float_as_uint(e) - 1u) & 0x7fffffu) | 0x800000u) + 64u) >> 7;
-        atomicAdd(&s.work.zhist[bin_number(rs.z_bin_of(z))], amount);
+        const int b = bin_number(rs.z_bin_of(z));
+        if (b < kZBins - 1) atomicAdd(&s.work.zhist[b], amount);
       };
       u64 sum;
       if (kPlain && kResident && !cut) {  // two logits at a time where that is one instruction
@@ -824,7 +827,8 @@ struct RowCtx {
       sum_to_part(sum, 1, s.warp_sum);
     } else {
       slice.each(lane, [&](float x, int) {
-        if (x > -INFINITY) atomicAdd(&s.work.zhist[bin_number(rs.z_bin(x))], 1u);
+        const int b = bin_number(rs.z_bin(x));
+        if (b < kZBins - 1) atomicAdd(&s.work.zhist[b], 1u);
       });
     }
     u64 want, before = 0;
