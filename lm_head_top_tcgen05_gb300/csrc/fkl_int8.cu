@@ -3,6 +3,12 @@
 //
 //     s_m = max_k |x_mk| * fl(1/127),  q_mk = rint(x_mk / s_m)
 //     y_mn = (sum_k q_mk w_nk) * s_m * t_n
+//
+// Up to 4 tokens run on the kernel below, which streams W through registers; more, or tokens
+// too long for shared memory, on the tensor cores (fkl_int8_gemm.cu).  W 201088 x 2880 on a GB300:
+// 1 token 84 us (86 us is W at the measured copy bandwidth), 4 tokens 90 us; with 8 tokens the
+// streaming kernel took 123 us, bound by its reads of the tokens from shared memory, and the
+// tensor cores 107 us.
 #include <climits>
 
 #include "fkl_gemm.cuh"
@@ -165,10 +171,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- few tokens: dp4a
-// Up to 8 tokens: each warp streams rows of W through registers, 16 bytes a lane, against the
-// tokens' integers in shared memory; the sums are exact int32.  Bound by reading W.  Every block
-// brings the tokens to 8 bits for itself (they come from L2), so a call is one launch; W's first
-// rows are prefetched into L2 meanwhile.
+// Each warp streams rows of W through registers, 16 bytes a lane, against the tokens' integers in
+// shared memory; the sums are exact int32.  Bound by reading W, so what counts is bytes in flight:
+// 2 rows x 3 pieces per lane (96 KB per SM) took 85.0 us for one token, 4 rows x 1 piece 89.5 us
+// (201088 x 2880).  Every block brings the tokens to 8 bits for itself (they come from L2), so a
+// call is one launch; the first rows' pieces are under way meanwhile.
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int64_t kFewTokens = 4;
@@ -366,8 +373,8 @@ static cudaError_t launch_few_t(const FewParams& p, int sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// One row of W per warp, with several of its pieces in flight, until every warp has rows enough;
-// then several rows, which share each read of the tokens.
+// Two rows of W per warp share each read of the tokens; with fewer rows than keep every warp busy
+// four times over, one row per warp with more of its pieces in flight.
 template <int MT>
 static cudaError_t launch_few_m(const FewParams& p, int sms, cudaStream_t st) {
   return p.N < 4 * 2 * kFewWarps * sms ? launch_few_t<MT, 1, MT == 4 ? 4 : 6>(p, sms, st)

@@ -13,6 +13,12 @@
 // their fp16 form costs no shared-memory traffic; the tokens, quantised to fp16 integers by a
 // kernel before, are the B operand in shared memory (up to 256 per tile, half per CTA).
 //
+// What bounds it (GB300, W 201088 x 2880): up to about 128 tokens the HBM reads of W, 579 MB, 86 us at
+// the measured 6.78 TB/s: 16 tokens take 106 us, 128 tokens 128 us with 103 MB of output.  Beyond,
+// the tensor pipe: 4096 tokens 2.69 ms, 1766 TFLOP/s, 91 % of a bf16 library product's burst
+// rate; a tile of more than 128 tokens has one accumulator, so its epilogue (about 1 us of 13) is
+// not hidden.
+//
 // Roles per CTA (20 warps):
 //   warps 0..7   convert: 128 rows x 128 k of int8 to fp16 in a TMEM slot; warps 0..3 take the
 //                lower 64 k, warps 4..7 the upper (a warp reaches the 32 TMEM lanes of its
@@ -519,14 +525,14 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   const int64_t tiles = (N + 255) / 256 * g.m_tiles;
   g.pairs = static_cast<int>(std::min<int64_t>(std::min(sms / 2, kMaxPairs), tiles * g.k_blocks));
   // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are
-  // cut, which costs the sums of their parts at the end.  Measured per pair: a block of 128 k takes
-  // 0.36 us (W from HBM) or nt / 256 * 0.55 us (MMAs), adding up about 3 us + nt * 0.06 us
-  // (203 x 50261 x 1456, 45 tiles beyond 2 waves: whole 48 us, cut 64 us; 9 x 4096 x 2880, 16 tiles
-  // in all: cut 9 us, whole 15 us).
+  // cut, which costs the fences and sums of their parts at the end.  Measured: a block of 128 k takes
+  // a pair 0.36 us (W from HBM) or nt / 256 * 0.55 us (MMAs), a cut about 9 us + nt * 0.06 us.  Whole
+  // against cut, in us: 9 x 4096 x 2880 14.9, 18.0; 16 x 4096 x 8192 25.3, 18.0; 64 x 12288 x 4096
+  // 18.3, 20.9; 203 x 50261 x 1456 42.8, 57.0; 128 x 201088 x 2880 128, 146.
   g.rounds = static_cast<int>(tiles / g.pairs);
   const int64_t rest = tiles - static_cast<int64_t>(g.rounds) * g.pairs;
   const double tile_us = static_cast<double>(K) / kI8K * std::max(0.36, g.nt / 256.0 * 0.55);
-  const bool cut = rest * tile_us / g.pairs + 3.0 + 0.06 * g.nt < tile_us;
+  const bool cut = rest * tile_us / g.pairs + 9.0 + 0.06 * g.nt < tile_us;
   if (rest > 0 && !cut) ++g.rounds;
   g.tiles = static_cast<int>(tiles);
   g.cut_blocks = cut ? rest * g.k_blocks : 0;

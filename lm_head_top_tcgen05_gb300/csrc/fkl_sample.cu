@@ -14,10 +14,10 @@
 //                        looks up the id in the one warp's stretch that holds it;
 //   top-k up to 512      a list: tau is a lower bound of the k-th largest logit (the least, over the
 //                        CTAs, of the k / C-th largest of their threads' maxima), the logits
-//                        >= tau (about k log-many) are gathered and the first CTA finishes;
-//   otherwise            a histogram over 2048 bins of equal width in z (of counts for top-k, of
-//                        weights rounded to 2^-17 for top-p, beside their exact sum) gives the bin of
-//                        the boundary; a second pass sums the exact weights above that bin per
+//                        >= tau, not many more than k, are gathered and the first CTA finishes;
+//   otherwise            a histogram over bins of equal width in z (of counts for top-k, of weights
+//                        in 17 bits for top-p, beside their exact sum) gives the bin of the
+//                        boundary; a second pass sums the exact weights above that bin per
 //                        warp and lists the bin's logits, from which the first CTA takes the
 //                        boundary.  The rounded histogram only proposes the bin: the exact sums
 //                        confirm it.
@@ -26,8 +26,11 @@
 // most of the row), or the bin is not confirmed, the boundary is found from exact histograms,
 // first in z and then of the logits' bits, until what is left fits a list or is all equal.
 //
-// The passes are bound by their instructions (about 15 per logit with the exponential), not by
-// memory: that is why the exact sums are kept in two 32-bit words, see WeightSum.
+// What bounds it (GB300): a row is 10 to 25 us from its load to its token, in which it is read
+// once (2 to 5 us) and passed over once or twice in shared memory at about 20 instructions a
+// logit (the exponential is half of them; 3.5 us a pass with two CTAs to an SM), with 3 to 8 cluster
+// barriers of about 1 us between; 36 rows of 201088 fp32 fit the device's shared memory at once.  64 such rows
+// take 33 us without filters, 33 us with top-k 50, 72 us with top-p 0.9; one row 9 to 20 us.
 #include <atomic>
 #include <climits>
 #include <cmath>
