@@ -244,32 +244,17 @@ static EncodeTiledFn encode_fn() {
 }
 
 // 2-D bf16 map with 128-byte swizzle; out-of-range elements of a box read as zero.
-static bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
-                          uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer) {
+bool encode_map_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {row_stride_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool encode_map_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer) {
-  return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, row_stride_bytes, box_inner, box_outer);
-}
-
-bool encode_map_f16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
-                    uint32_t box_inner, uint32_t box_outer) {
-  return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, inner, outer, row_stride_bytes, box_inner, box_outer);
-}
-
-bool encode_map_bytes(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
-                      uint32_t box_inner, uint32_t box_outer) {
-  return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, outer, row_stride_bytes, box_inner, box_outer);
 }
 
 bool encode_map_mn3d(CUtensorMap* map, const void* base, uint64_t mn_extent, uint64_t k_extent,
@@ -354,13 +339,6 @@ static fkl_status device_info(DevInfo* out) {
     return fail(FKL_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a", dev,
                 out->major, out->minor);
   return FKL_OK;
-}
-
-int require_device(int* sms) {
-  DevInfo di;
-  const fkl_status s = device_info(&di);
-  *sms = di.sms;
-  return s;
 }
 
 // Row blocks per group in the unit order of the dS recompute and the teacher cache's passes

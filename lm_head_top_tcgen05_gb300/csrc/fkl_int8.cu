@@ -12,6 +12,7 @@
 #include <climits>
 
 #include "fkl_gemm.cuh"
+#include "fkl_generate.cuh"
 #include "fkl_int8.h"
 #include "fkl_types.cuh"
 

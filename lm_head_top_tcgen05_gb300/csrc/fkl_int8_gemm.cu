@@ -40,6 +40,7 @@
 #include <algorithm>
 
 #include "fkl_gemm.cuh"
+#include "fkl_generate.cuh"
 #include "fkl_int8.h"
 #include "fkl_types.cuh"
 

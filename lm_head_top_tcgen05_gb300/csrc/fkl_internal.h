@@ -83,10 +83,6 @@ int check_device_memory(const NamedPtr (&ptrs)[N]) {
   return check_device_memory(ptrs, N);
 }
 
-// The current device must be sm_103; writes its SM count (cached per device).  FKL_OK or the
-// error, with the message in fkl_last_error().
-int require_device(int* sms);
-
 // Event pair around one GEMM launch when a trace is active on this thread (fkl_trace.cu).
 // kind: 0 forward, 1 dS recompute, 2 dW, 3 dH.
 void trace_launch_begin(cudaStream_t st);
@@ -232,11 +228,6 @@ struct F32Params {
 
 bool encode_map_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                      uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
-// 2-D map of 8-bit (bytes) or fp16 elements, 128-byte swizzle; out-of-range elements read as zero.
-bool encode_map_bytes(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
-                      uint32_t box_inner, uint32_t box_outer);
-bool encode_map_f16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
-                    uint32_t box_inner, uint32_t box_outer);
 // 3-D view of an MN-major operand stored [k][mn] (mn contiguous, mn_extent % 64 == 0 and
 // every element below mn_extent inside the buffer): dims (64, k, mn_extent / 64), box
 // (64, 64, tile_mn / 64).  Returns false if the map cannot be encoded.

@@ -35,7 +35,7 @@
 #include <climits>
 #include <cmath>
 
-#include "fkl_ptx.cuh"
+#include "fkl_generate.cuh"
 #include "fkl_types.cuh"
 
 namespace fkl {
