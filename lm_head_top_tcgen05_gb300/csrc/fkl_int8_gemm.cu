@@ -528,8 +528,8 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are
   // cut, which costs the fences and sums of their parts at the end.  Measured: a block of 128 k takes
   // a pair 0.36 us (W from HBM) or nt / 256 * 0.55 us (MMAs), a cut about 9 us + nt * 0.06 us.  Whole
-  // against cut, in us: 9 x 4096 x 2880 14.9, 18.0; 16 x 4096 x 8192 25.3, 18.0; 64 x 12288 x 4096
-  // 18.3, 20.9; 203 x 50261 x 1456 42.8, 57.0; 128 x 201088 x 2880 128, 146.
+  // against cut, in us: 9 x 4096 x 2880 14.9, 18.0; 16 x 4096 x 8192 25.3, 18 to 19; 64 x 12288 x 4096
+  // 18.3, 20.9; 64 x 25600 x 4096 31.3, 33.9; 203 x 50261 x 1456 42.8, 57.0; 128 x 201088 x 2880 128, 146.
   g.rounds = static_cast<int>(tiles / g.pairs);
   const int64_t rest = tiles - static_cast<int64_t>(g.rounds) * g.pairs;
   const double tile_us = static_cast<double>(K) / kI8K * std::max(0.36, g.nt / 256.0 * 0.55);

@@ -26,11 +26,12 @@
 // most of the row), or the bin is not confirmed, the boundary is found from exact histograms,
 // first in z and then of the logits' bits, until what is left fits a list or is all equal.
 //
-// What bounds it (GB300): a row is 10 to 25 us from its load to its token, in which it is read
-// once (2 to 5 us) and passed over once or twice in shared memory at about 20 instructions a
-// logit (the exponential is half of them; 3.5 us a pass with two CTAs to an SM), with 3 to 8 cluster
-// barriers of about 1 us between; 36 rows of 201088 fp32 fit the device's shared memory at once.  64 such rows
-// take 33 us without filters, 33 us with top-k 50, 72 us with top-p 0.9; one row 9 to 20 us.
+// What bounds it (GB300): a row is 11 to 26 us from its load to its token, in which it is read
+// once (2 to 5 us) and passed over once or twice in shared memory (a draw without filters
+// executes 36 instructions a logit in all, top-p 0.9 of flat rows 101), with 3 to 8 cluster
+// barriers of about 1 us between; 36 rows of 201088 fp32 fit the device's shared memory at once.  On the
+// device 64 such rows take 29 us without filters, 28 us with top-k 50, 68 us with top-p 0.9; one row
+// 11, 12 and 26 us.
 #include <atomic>
 #include <climits>
 #include <cmath>
