@@ -854,7 +854,13 @@ struct RowCtx {
     if (kPlain && kResident && !cut && !filter) {  // two logits at a time where that is one instruction
       WeightSum w;
       const float2 om = make_float2(-rs.m, -rs.m), it = make_float2(rs.inv_t, rs.inv_t);
+      // A logit below `low` is in a later bin (one bin to spare for the roundings), and a vector of
+      // them is passed over.  Top-p 0.9 of 512 rows of 201088 bf16, without and with: sharp rows 272,
+      // 225 us, flat rows, which keep most of theirs, 523, 526 us; one flat row of fp32 29, 31 us.
+      // Top-k comes here for so many logits that most warps have some: looking first cost 3 % there.
+      const float low = __fsub_rd(rs.m, static_cast<float>(bin + 2) * kZBinWidth / rs.inv_t);
       for (int i = slice.v0 + lane; i < slice.v1; i += 32) {
+        if (by_mass && !(vector_max<T>(slice.raw(i)) >= low)) continue;
         float v[E];
         slice.get(i, v);
 #pragma unroll
