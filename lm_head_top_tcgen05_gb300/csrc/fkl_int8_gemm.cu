@@ -511,7 +511,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 // ---------------------------------------------------------------- host side
 Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   Int8GemmPlan g;
-  g.m_tiles = static_cast<int>((M + 255) / 256);
+  // Tiles of up to 256 tokens; of up to 128, with a second accumulator that hides the epilogue, where
+  // that takes no more waves of tiles, as each wave converts W once more.  256 against 128 tokens, in
+  // us: 256 x 4096 x 4096 29.0, 22.8; 512 x 4096 x 4096 31.0, 24.4 (one wave either way);
+  // 1024 x 4096 x 4096 33.2, 38.1; 203 x 151936 x 4096 185, 218 (twice the waves).
+  const int64_t n_tiles = (N + 255) / 256, most_pairs = std::min(sms / 2, kMaxPairs);
+  const int64_t large = (M + 255) / 256, small = (M + 127) / 128;
+  const auto waves = [&](int64_t m_tiles) { return (n_tiles * m_tiles + most_pairs - 1) / most_pairs; };
+  g.m_tiles = static_cast<int>(waves(small) > waves(large) ? large : small);
   const int64_t even = (M + g.m_tiles - 1) / g.m_tiles;
   g.nt = static_cast<int>((even + 15) / 16 * 16);
   // TMEM: the accumulators, then the slots.  Blocks of 256 k (half as many hand-offs) where at
@@ -523,8 +530,8 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   g.slots = std::min(kI8MaxSlots, cols / (64 * g.sub));
   g.w_stages = std::min<int>(kI8MaxStages, (static_cast<int>(kI8Ring) - g.slots * g.sub * g.nt * kI8K) / static_cast<int>(g.sub * kI8WBytes));
   g.k_blocks = static_cast<int>((K + kI8K * g.sub - 1) / (kI8K * g.sub));
-  const int64_t tiles = (N + 255) / 256 * g.m_tiles;
-  g.pairs = static_cast<int>(std::min<int64_t>(std::min(sms / 2, kMaxPairs), tiles * g.k_blocks));
+  const int64_t tiles = n_tiles * g.m_tiles;
+  g.pairs = static_cast<int>(std::min<int64_t>(most_pairs, tiles * g.k_blocks));
   // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are
   // cut, which costs the fences and sums of their parts at the end.  Measured: a block of 128 k takes
   // a pair 0.36 us (W from HBM) or nt / 256 * 0.55 us (MMAs), a cut about 9 us + nt * 0.06 us.  Whole

@@ -115,6 +115,17 @@ def test_int8_matmul(fkl, M, N, K):
         assert_product(fkl.int8_matmul(*t, out_dtype=dtype), ops, dtype)
 
 
+# Wide enough that tiles of 128 tokens would take another wave, so the tiles hold 129 to 256: one and
+# several tiles of tokens, an odd count of either, cut and whole last waves, K in and beyond one block.
+@pytest.mark.parametrize("M,N,K", [(129, 12001, 144), (200, 12000, 256), (250, 10100, 48), (256, 19456, 272),
+                                   (257, 13001, 128), (300, 13057, 400), (400, 12290, 272), (513, 8000, 256)])
+def test_int8_matmul_wide(fkl, M, N, K):
+    ops = operands(M, N, K, M + N + K)
+    t = dev(*ops)
+    for dtype in TYPES:
+        assert_product(fkl.int8_matmul(*t, out_dtype=dtype), ops, dtype)
+
+
 @pytest.mark.parametrize("M", [1, 6, 40, 300])
 def test_int8_matmul_largest_values(fkl, M):
     # every product 128 * 128: the largest sums that K = 4096 can give
