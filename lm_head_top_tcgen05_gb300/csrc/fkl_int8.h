@@ -25,6 +25,7 @@ struct Int8GemmPlan {
   int accs, acc_cols, slots, w_stages;  // TMEM and shared memory
   int tiles, rounds;                    // tiles in all; whole tiles of a pair, at most
   int64_t cut_blocks;                   // blocks of the tiles that are cut
+  int cut_pairs;                        // pairs that share them
   size_t part_bytes;                    // their partial sums
 };
 Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms);

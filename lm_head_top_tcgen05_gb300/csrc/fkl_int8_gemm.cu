@@ -64,6 +64,7 @@ struct I8Params {
   int accs, acc_cols, slots, w_stages;
   int tiles, rounds;     // tiles in all; whole tiles of a pair, at most
   long long cut_blocks;  // blocks of the cut tiles
+  int cut_pairs;         // pairs that share them, each at least one
   const float* x_scale;
   const float* w_scale;
   void* out;
@@ -81,8 +82,8 @@ struct I8Seq {
   int round, tile, kb0, kb1;
   const int pair, pairs;
   __device__ I8Seq(const I8Params& p, int pair_, int pairs_) : pair(pair_), pairs(pairs_) {
-    at = p.cut_blocks * pair / pairs;
-    end = p.cut_blocks * (pair + 1) / pairs;
+    at = p.cut_blocks * min(pair, p.cut_pairs) / p.cut_pairs;
+    end = p.cut_blocks * min(pair + 1, p.cut_pairs) / p.cut_pairs;
     round = 0;
     set(p);
   }
@@ -346,8 +347,8 @@ __device__ __forceinline__ void i8_store_any(const I8Params& p, const float (&v)
 }
 
 // The pair whose part of the line of cut tiles holds block x.
-__device__ __forceinline__ int i8_owner(const I8Params& p, long long x, int pairs) {
-  return static_cast<int>(((x + 1) * pairs - 1) / p.cut_blocks);
+__device__ __forceinline__ int i8_owner(const I8Params& p, long long x) {
+  return static_cast<int>(((x + 1) * p.cut_pairs - 1) / p.cut_blocks);
 }
 
 __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lane) {
@@ -388,7 +389,7 @@ __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lan
     if (whole) continue;
     // a cut tile: the last part to arrive adds them all up, in their order
     const long long first = static_cast<long long>(q.tile - p.rounds * c.pairs) * p.k_blocks;
-    const int p0 = i8_owner(p, first, c.pairs), p1 = i8_owner(p, first + p.k_blocks - 1, c.pairs);
+    const int p0 = i8_owner(p, first), p1 = i8_owner(p, first + p.k_blocks - 1);
     __threadfence();
     __syncwarp();
     int before = 0;
@@ -544,6 +545,8 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   if (rest > 0 && !cut) ++g.rounds;
   g.tiles = static_cast<int>(tiles);
   g.cut_blocks = cut ? rest * g.k_blocks : 0;
+  // a pair without a block would be a part that the tile's last one waits for in vain
+  g.cut_pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(g.pairs, g.cut_blocks)));
   g.part_bytes = static_cast<size_t>(2 * g.pairs) * g.nt * 256 * 4;
   return g;
 }
@@ -588,6 +591,7 @@ cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const in
   p.tiles = g.tiles;
   p.rounds = g.rounds;
   p.cut_blocks = g.cut_blocks;
+  p.cut_pairs = g.cut_pairs;
   p.x_scale = x_scale;
   p.w_scale = w_scale;
   p.out = out;

@@ -126,6 +126,14 @@ def test_int8_matmul_wide(fkl, M, N, K):
         assert_product(fkl.int8_matmul(*t, out_dtype=dtype), ops, dtype)
 
 
+# One tile more than run at once (256 channels and tokens each, 76 at once): it is cut, into fewer
+# blocks than there are pairs to share them.
+@pytest.mark.parametrize("M,N,K", [(16, 19500, 8192), (9, 19460, 4112), (5, 38913, 8192), (140, 19500, 8000)])
+def test_int8_matmul_cut_into_few_blocks(fkl, M, N, K):
+    ops = operands(M, N, K, M + N + K)
+    assert_product(fkl.int8_matmul(*dev(*ops)), ops, torch.float32)
+
+
 @pytest.mark.parametrize("M", [1, 6, 40, 300])
 def test_int8_matmul_largest_values(fkl, M):
     # every product 128 * 128: the largest sums that K = 4096 can give
