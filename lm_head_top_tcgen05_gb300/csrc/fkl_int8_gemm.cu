@@ -512,14 +512,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 // ---------------------------------------------------------------- host side
 Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   Int8GemmPlan g;
-  // Tiles of up to 256 tokens; of up to 128, with a second accumulator that hides the epilogue, where
-  // that takes no more waves of tiles, as each wave converts W once more.  256 against 128 tokens, in
-  // us: 256 x 4096 x 4096 29.0, 22.8; 512 x 4096 x 4096 31.0, 24.4 (one wave either way);
-  // 1024 x 4096 x 4096 33.2, 38.1; 203 x 151936 x 4096 185, 218 (twice the waves).
+  // Measured: a block of 128 k takes a pair 0.36 us (W from HBM) or nt / 256 * 0.55 us (MMAs).
+  const auto tile_time = [&](int64_t nt) { return static_cast<double>(K) / kI8K * std::max(0.36, nt / 256.0 * 0.55); };
+  // Tiles of up to 256 tokens, or of up to 128 with a second accumulator that hides the epilogue: a
+  // wave of tiles then costs about 2 us beyond its blocks, not 5, but there are more waves, and each
+  // converts W once more.  256 against 128 tokens, in us: 512 x 4096 x 4096 31.0, 24.4;
+  // 512 x 50261 x 1456 89.5, 78.8; 350 x 65536 x 640 47.9, 41.2; 1024 x 4096 x 4096 33.2, 38.1;
+  // 203 x 151936 x 4096 185, 218; 640 x 20000 x 5120 104.6, 109.5.
   const int64_t n_tiles = (N + 255) / 256, most_pairs = std::min(sms / 2, kMaxPairs);
+  const auto waves_time = [&](int64_t m_tiles) {
+    const int64_t nt = (M + m_tiles - 1) / m_tiles;
+    return static_cast<double>((n_tiles * m_tiles + most_pairs - 1) / most_pairs) * (tile_time(nt) + (nt > 128 ? 5.0 : 2.0));
+  };
   const int64_t large = (M + 255) / 256, small = (M + 127) / 128;
-  const auto waves = [&](int64_t m_tiles) { return (n_tiles * m_tiles + most_pairs - 1) / most_pairs; };
-  g.m_tiles = static_cast<int>(waves(small) > waves(large) ? large : small);
+  g.m_tiles = static_cast<int>(waves_time(small) < waves_time(large) ? small : large);
   const int64_t even = (M + g.m_tiles - 1) / g.m_tiles;
   g.nt = static_cast<int>((even + 15) / 16 * 16);
   // TMEM: the accumulators, then the slots.  Blocks of 256 k (half as many hand-offs) where at
@@ -534,13 +540,12 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   const int64_t tiles = n_tiles * g.m_tiles;
   g.pairs = static_cast<int>(std::min<int64_t>(most_pairs, tiles * g.k_blocks));
   // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are
-  // cut, which costs the fences and sums of their parts at the end.  Measured: a block of 128 k takes
-  // a pair 0.36 us (W from HBM) or nt / 256 * 0.55 us (MMAs), a cut about 9 us + nt * 0.06 us.  Whole
+  // cut, which costs the fences and sums of their parts at the end, about 9 us + nt * 0.06 us.  Whole
   // against cut, in us: 9 x 4096 x 2880 14.9, 18.0; 16 x 4096 x 8192 25.3, 18 to 19; 64 x 12288 x 4096
   // 18.3, 20.9; 64 x 25600 x 4096 31.3, 33.9; 203 x 50261 x 1456 42.8, 57.0; 128 x 201088 x 2880 128, 146.
   g.rounds = static_cast<int>(tiles / g.pairs);
   const int64_t rest = tiles - static_cast<int64_t>(g.rounds) * g.pairs;
-  const double tile_us = static_cast<double>(K) / kI8K * std::max(0.36, g.nt / 256.0 * 0.55);
+  const double tile_us = tile_time(g.nt);
   const bool cut = rest * tile_us / g.pairs + 9.0 + 0.06 * g.nt < tile_us;
   if (rest > 0 && !cut) ++g.rounds;
   g.tiles = static_cast<int>(tiles);

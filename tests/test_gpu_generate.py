@@ -115,8 +115,7 @@ def test_int8_matmul(fkl, M, N, K):
         assert_product(fkl.int8_matmul(*t, out_dtype=dtype), ops, dtype)
 
 
-# Wide enough that tiles of 128 tokens would take another wave, so the tiles hold 129 to 256: one and
-# several tiles of tokens, an odd count of either, cut and whole last waves, K in and beyond one block.
+# More tiles than run at once, with several tiles of up to 128 tokens.
 @pytest.mark.parametrize("M,N,K", [(129, 12001, 144), (200, 12000, 256), (250, 10100, 48), (256, 19456, 272),
                                    (257, 13001, 128), (300, 13057, 400), (400, 12290, 272), (513, 8000, 256)])
 def test_int8_matmul_wide(fkl, M, N, K):
@@ -124,6 +123,15 @@ def test_int8_matmul_wide(fkl, M, N, K):
     t = dev(*ops)
     for dtype in TYPES:
         assert_product(fkl.int8_matmul(*t, out_dtype=dtype), ops, dtype)
+
+
+# Wide and deep enough for tiles of 129 to 256 tokens: one and several of them, an odd last one, and a
+# last wave that is cut (the last two).
+@pytest.mark.parametrize("M,N,K", [(129, 12001, 2064), (200, 12000, 1456), (250, 10100, 1296), (257, 13001, 4096),
+                                   (400, 12290, 2880), (513, 8000, 4112), (140, 19500, 8000), (200, 19500, 9008)])
+def test_int8_matmul_large_tiles(fkl, M, N, K):
+    ops = operands(M, N, K, M + N + K)
+    assert_product(fkl.int8_matmul(*dev(*ops), out_dtype=torch.bfloat16), ops, torch.bfloat16)
 
 
 # One tile more than run at once (256 channels and tokens each, 76 at once): it is cut, into fewer
