@@ -539,19 +539,23 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   g.k_blocks = static_cast<int>((K + kI8K * g.sub - 1) / (kI8K * g.sub));
   const int64_t tiles = n_tiles * g.m_tiles;
   g.pairs = static_cast<int>(std::min<int64_t>(most_pairs, tiles * g.k_blocks));
-  // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are
-  // cut, which costs the fences and sums of their parts at the end, about 9 us + nt * 0.06 us.  Whole
-  // against cut, in us: 9 x 4096 x 2880 14.9, 18.0; 16 x 4096 x 8192 25.3, 18 to 19; 64 x 12288 x 4096
-  // 18.3, 20.9; 64 x 25600 x 4096 31.3, 33.9; 203 x 50261 x 1456 42.8, 57.0; 128 x 201088 x 2880 128, 146.
+  // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are cut,
+  // which costs the fences and sums of their parts at the end: measured about 5 us + nt * 0.06 us with
+  // up to 4 parts to a tile, and more with more, which pays where each part keeps 16 blocks or so.
+  // 140 x 19500 x 8000 in 4, 8, 16 and 63 parts: 52, 62, 86 and 241 us; 16 x 256 x 40000 in 4, 16 and 76:
+  // 39, 31 and 48 us.  Whole against cut, in us: 9 x 4096 x 2880 14.7, 13.8; 16 x 4096 x 8192 24.9, 17.4;
+  // 140 x 19500 x 8000 70, 52; 64 x 25600 x 4096 31.3, 33.9; 203 x 50261 x 1456 42.8, 57.0.
   g.rounds = static_cast<int>(tiles / g.pairs);
   const int64_t rest = tiles - static_cast<int64_t>(g.rounds) * g.pairs;
+  const int64_t parts = std::min<int64_t>(std::max<int64_t>(4, K / 2048), g.k_blocks);
+  const int64_t sharing = std::max<int64_t>(1, std::min<int64_t>(g.pairs, rest * parts));
   const double tile_us = tile_time(g.nt);
-  const bool cut = rest * tile_us / g.pairs + 9.0 + 0.06 * g.nt < tile_us;
+  const bool cut = rest * tile_us / sharing + 5.0 + 0.06 * g.nt < tile_us;
   if (rest > 0 && !cut) ++g.rounds;
   g.tiles = static_cast<int>(tiles);
   g.cut_blocks = cut ? rest * g.k_blocks : 0;
   // a pair without a block would be a part that the tile's last one waits for in vain
-  g.cut_pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(g.pairs, g.cut_blocks)));
+  g.cut_pairs = static_cast<int>(sharing);
   g.part_bytes = static_cast<size_t>(2 * g.pairs) * g.nt * 256 * 4;
   return g;
 }
