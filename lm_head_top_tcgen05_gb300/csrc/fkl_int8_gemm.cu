@@ -29,10 +29,10 @@
 //   warp 18      (even CTA) issues the MMAs.
 // The work is tiles of 256 rows of W x one tile of tokens, walked in blocks of 128 or 256 k.  Tiles
 // are dealt round-robin to the pairs.  Those that would leave many pairs idle in the last wave
-// (or the only one) are a line of blocks cut into equal parts, one per pair.  A tile that is cut has its fp32 partial sums in the workspace;
-// the last of its parts to finish (per warp of the epilogue) adds them in the order of the
-// parts, so the result does not depend on which one that is.  The cut tiles come first, so
-// that adding them up overlaps the whole ones.
+// (or the only one) are a line of blocks cut into equal parts, one for each pair that shares it.  A
+// tile that is cut has its fp32 partial sums in the workspace; the last of its parts to finish (per
+// warp of the epilogue) adds them in the order of the parts, so the result does not depend on which
+// one that is.  The cut tiles come first, so that adding them up overlaps the whole ones.
 //
 // The kernel starts while the tokens are still being quantised (programmatic launch): W's first
 // blocks are loaded and converted meanwhile, and only what reads the tokens, their scales or the
