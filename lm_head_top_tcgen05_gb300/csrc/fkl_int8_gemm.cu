@@ -140,6 +140,18 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+// A wait of a whole warp, with one answer for all of its lanes.  Each lane polls for itself, so when a
+// wait runs out some may have given up while others saw the barrier complete; lanes that went on by
+// their own answers would part for good and wait for each other without a limit at the next
+// warp or block barrier.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, ctl));
+}
+// The same for two barriers in the same phase, with one vote.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t then, uint32_t parity, const WaitCtl& ctl) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, ctl) && mbar_wait_cluster(then, parity, ctl));
+}
+
 template <int SUB>
 __device__ void i8_w_producer(const CUtensorMap* tm, const I8Params& p, const I8Ctx& c) {
   int stage = 0;
@@ -201,7 +213,7 @@ __device__ void i8_convert(const I8Params& p, const I8Ctx& c, int warp, int lane
   uint32_t wphase = 0, phase = 0;
   for (I8Seq q(p, c.pair, c.pairs); q.more(p); q.next(p)) {
     for (int kb = q.kb0; kb < q.kb1; ++kb) {
-      if (!__all_sync(0xffffffffu, mbar_wait(c.wfull0 + 8 * stage, wphase, c.ctl))) return;
+      if (!warp_wait(c.wfull0 + 8 * stage, wphase, c.ctl)) return;
       const uint32_t to = c.tmem_a + lanes + static_cast<uint32_t>(slot * (64 * SUB) + upper * 32);
 #pragma unroll
       for (int j = 0; j < SUB; ++j) {
@@ -220,7 +232,7 @@ __device__ void i8_convert(const I8Params& p, const I8Ctx& c, int warp, int lane
           if (lane == 0) mbar_arrive(c.wempty0 + 8 * stage);
         }
         if (j == 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait_cluster(c.empty0 + 8 * slot, phase ^ 1u, c.ctl))) return;
+          if (!warp_wait(c.empty0 + 8 * slot, phase ^ 1u, c.ctl)) return;
           tc_fence_after();
         }
         tmem_st32(to + static_cast<uint32_t>(j * 64), h);
@@ -249,12 +261,11 @@ __device__ void i8_mma(const I8Params& p, const I8Ctx& c) {
   uint32_t phase = 0, acc_phase = 0;
   bool ok = true;
   for (I8Seq q(p, c.pair, c.pairs); ok && q.more(p); q.next(p)) {
-    if (!mbar_wait_cluster(c.tempty0 + 8 * acc, acc_phase ^ 1u, c.ctl)) { ok = false; break; }
+    if (!warp_wait(c.tempty0 + 8 * acc, acc_phase ^ 1u, c.ctl)) { ok = false; break; }
     tc_fence_after();
     const uint32_t d = c.tmem + static_cast<uint32_t>(acc * p.acc_cols);
     for (int kb = q.kb0; kb < q.kb1; ++kb) {
-      if (!mbar_wait_cluster(c.xfull0 + 8 * slot, phase, c.ctl) ||
-          !mbar_wait_cluster(c.afull0 + 8 * slot, phase, c.ctl)) {
+      if (!warp_wait(c.xfull0 + 8 * slot, c.afull0 + 8 * slot, phase, c.ctl)) {
         ok = false;
         break;
       }
@@ -366,7 +377,7 @@ __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lan
     const float ws = n < p.N ? p.w_scale[n] : 0.f;
     const bool whole = q.kb1 - q.kb0 == p.k_blocks;
     float* part = p.part + static_cast<size_t>(2 * c.pair + (q.kb0 == 0 ? 1 : 0)) * p.nt * 256 + row;
-    if (!__all_sync(0xffffffffu, mbar_wait_cluster(c.tfull0 + 8 * acc, acc_phase, c.ctl))) return;
+    if (!warp_wait(c.tfull0 + 8 * acc, acc_phase, c.ctl)) return;
     tc_fence_after();
     const uint32_t t = c.tmem + lanes + static_cast<uint32_t>(acc * p.acc_cols);
 #pragma unroll 1

@@ -98,3 +98,25 @@ def test_binding_needs_cuda_tensors():
         fkl.int8_linear(torch.zeros(2, 16), torch.zeros(3, 16, dtype=torch.int8), torch.zeros(3))
     with pytest.raises(ValueError):
         fkl.sample(torch.zeros(2, 16), torch.zeros(2))
+
+
+def _function(source, name):
+    """The text of a device function's body."""
+    at = source.index("{", source.index(f" {name}("))
+    depth, end = 0, at
+    while depth > 0 or end == at:
+        depth += {"{": 1, "}": -1}.get(source[end], 0)
+        end += 1
+    return source[at:end]
+
+
+@pytest.mark.parametrize("role", ["i8_convert", "i8_mma", "i8_epilogue"])
+def test_waits_of_whole_warps_have_one_answer(role):
+    # Lanes that leave a wait with different answers part for good, and the launch hangs at the next
+    # warp barrier; it takes a wait that runs out just as its barrier completes, so it is read here.
+    from pathlib import Path
+
+    body = _function((Path(__file__).resolve().parent.parent / "lm_head_top_tcgen05_gb300" / "csrc"
+                      / "fkl_int8_gemm.cu").read_text(), role)
+    body = body.replace("mbar_wait_drain(", "")  # made by the one lane that issues
+    assert "warp_wait(" in body and "mbar_wait" not in body
