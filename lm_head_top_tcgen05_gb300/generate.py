@@ -9,12 +9,15 @@ On-policy distillation trains on text that the student draws.  One step of drawi
 with ``h`` the hidden states [M, K] of the rows' last tokens and ``u`` one uniform random
 number per row.  ``int8_matmul`` is the product of operands that are already in 8 bits.
 ``draw_token`` is the step as one call.  None of these has a gradient.  Calls run on the
-current stream of their inputs' device and keep one workspace per stream.
+current stream.  A product without a ``workspace`` uses a buffer that the calling thread keeps for
+that stream, so calls of several threads and on several streams never share one; a ``Workspace`` that is
+given belongs to one thread and one stream at a time.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import threading
 from typing import Optional, Tuple, Union
 
 import torch
@@ -24,7 +27,7 @@ from ._lib import DTYPES, FklError, FklSampleParams, check, lib
 __all__ = ["quantize_int8", "int8_matmul", "int8_linear", "sample", "draw_token"]
 
 _Setting = Union[float, int, torch.Tensor]
-_workspaces = {}
+_local = threading.local()  # .buffers: the calling thread's default workspaces, by (device, stream)
 
 # A generation step is a handful of microseconds on the device, so the calls below keep the
 # host's part short: the raw stream without a Stream object, workspace sizes looked up by shape.
@@ -46,15 +49,20 @@ def _workspace_bytes(fn: str, M: int, N: int, K: int, device_index: int) -> int:
 
 
 def _workspace(nbytes: int, device, stream: int, given) -> torch.Tensor:
-    """`given` (a Workspace), or this module's buffer of the stream: calls queued on two streams
-    never share one."""
+    """`given` (a Workspace), or the calling thread's buffer of the stream.  A product is two
+    launches that hand the tokens over in it, and the interpreter's lock is not held meanwhile: two
+    threads that share a stream may queue their launches in any order, so they never share a buffer."""
     if given is not None:
         return given.get(nbytes, device)
+    try:
+        buffers = _local.buffers
+    except AttributeError:
+        buffers = _local.buffers = {}
     key = (device.index, stream)
-    buf = _workspaces.get(key)
+    buf = buffers.get(key)
     if buf is None or buf.numel() < nbytes:
-        _workspaces[key] = buf = None
-        _workspaces[key] = buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        buffers[key] = buf = None
+        buffers[key] = buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     return buf
 
 

@@ -120,3 +120,27 @@ def test_waits_of_whole_warps_have_one_answer(role):
                       / "fkl_int8_gemm.cu").read_text(), role)
     body = body.replace("mbar_wait_drain(", "")  # made by the one lane that issues
     assert "warp_wait(" in body and "mbar_wait" not in body
+
+
+def test_threads_do_not_share_a_default_workspace():
+    # the two launches of a product hand data over in it, and another thread's may come between
+    import threading
+
+    from lm_head_top_tcgen05_gb300 import generate
+
+    cpu, got, both = torch.device("cpu"), {}, threading.Barrier(2)
+
+    def work(name):
+        first = generate._workspace(1000, cpu, 7, None)
+        both.wait()
+        got[name] = first, generate._workspace(500, cpu, 7, None), generate._workspace(500, cpu, 8, None)
+        both.wait()
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for first, again, other in got.values():
+        assert first.numel() >= 1000 and again.data_ptr() == first.data_ptr() != other.data_ptr()
+    assert got[0][0].data_ptr() != got[1][0].data_ptr()

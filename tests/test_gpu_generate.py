@@ -587,3 +587,29 @@ def test_int8_linear_default_workspaces_of_two_streams(fkl):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(y, ref[i]) for y in got[i])
+
+
+def test_int8_linear_from_threads_of_one_stream(fkl):
+    # two threads on the default stream, tiles that are cut along K: each gets its own product
+    import threading
+
+    g = torch.Generator().manual_seed(10)
+    wq, ws = fkl.quantize_int8((torch.randn(4096, 2880, generator=g) * 0.02).cuda())
+    xs = [torch.randn(9, 2880, generator=g).cuda() for _ in range(2)]
+    ref = [fkl.int8_linear(x, wq, ws) for x in xs]
+    torch.cuda.synchronize()
+    got, start = [[], []], threading.Barrier(2)
+
+    def work(i):
+        start.wait()
+        for _ in range(300):
+            got[i].append(fkl.int8_linear(xs[i], wq, ws, out=torch.full((9, 4096), 7.0, device="cuda")))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 300 and all(torch.equal(y, ref[i]) for y in got[i])
