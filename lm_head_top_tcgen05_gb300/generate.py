@@ -10,8 +10,9 @@ with ``h`` the hidden states [M, K] of the rows' last tokens and ``u`` one unifo
 number per row.  ``int8_matmul`` is the product of operands that are already in 8 bits.
 ``draw_token`` is the step as one call.  None of these has a gradient.  Calls run on the
 current stream.  A product without a ``workspace`` uses a buffer that the calling thread keeps for
-that stream, so calls of several threads and on several streams never share one; a ``Workspace`` that is
-given belongs to one thread and one stream at a time.
+that stream, so calls of several threads and on several streams never share one; a call that is captured in
+a CUDA graph has a buffer of the graph's own memory.  A ``Workspace`` that is given belongs to one thread
+and one stream at a time, and one given to a captured call to that graph.
 """
 from __future__ import annotations
 
@@ -32,6 +33,7 @@ _local = threading.local()  # .buffers: the calling thread's default workspaces,
 # A generation step is a handful of microseconds on the device, so the calls below keep the
 # host's part short: the raw stream without a Stream object, workspace sizes looked up by shape.
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def _stream(device) -> int:
@@ -54,6 +56,9 @@ def _workspace(nbytes: int, device, stream: int, given) -> torch.Tensor:
     threads that share a stream may queue their launches in any order, so they never share a buffer."""
     if given is not None:
         return given.get(nbytes, device)
+    if _capturing():
+        # a graph keeps the address: the buffer must be the graph's, not one that a later call may drop
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     try:
         buffers = _local.buffers
     except AttributeError:

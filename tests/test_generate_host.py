@@ -122,13 +122,14 @@ def test_waits_of_whole_warps_have_one_answer(role):
     assert "warp_wait(" in body and "mbar_wait" not in body
 
 
-def test_threads_do_not_share_a_default_workspace():
+def test_threads_do_not_share_a_default_workspace(monkeypatch):
     # the two launches of a product hand data over in it, and another thread's may come between
     import threading
 
     from lm_head_top_tcgen05_gb300 import generate
 
     cpu, got, both = torch.device("cpu"), {}, threading.Barrier(2)
+    monkeypatch.setattr(generate, "_capturing", lambda: False)  # no driver to ask here
 
     def work(name):
         first = generate._workspace(1000, cpu, 7, None)
@@ -144,3 +145,18 @@ def test_threads_do_not_share_a_default_workspace():
     for first, again, other in got.values():
         assert first.numel() >= 1000 and again.data_ptr() == first.data_ptr() != other.data_ptr()
     assert got[0][0].data_ptr() != got[1][0].data_ptr()
+
+
+def test_captured_calls_do_not_keep_the_default_workspace(monkeypatch):
+    # a graph records its workspace's address, and a later call may drop the thread's buffer for a larger
+    from lm_head_top_tcgen05_gb300 import generate
+
+    cpu, capturing = torch.device("cpu"), [False]
+    monkeypatch.setattr(generate, "_capturing", lambda: capturing[0], raising=False)
+    eager = generate._workspace(1000, cpu, 9, None)
+    capturing[0] = True
+    captured = generate._workspace(1000, cpu, 9, None)
+    other = generate._workspace(1000, cpu, 9, None)
+    assert captured.numel() >= 1000 and len({t.data_ptr() for t in (eager, captured, other)}) == 3
+    capturing[0] = False
+    assert generate._workspace(1000, cpu, 9, None).data_ptr() == eager.data_ptr()

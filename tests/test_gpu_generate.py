@@ -613,3 +613,34 @@ def test_int8_linear_from_threads_of_one_stream(fkl):
     torch.cuda.synchronize()
     for i in range(2):
         assert len(got[i]) == 300 and all(torch.equal(y, ref[i]) for y in got[i])
+
+
+def test_graph_with_the_default_workspace(fkl):
+    # captured after a warm-up, replayed after a larger call and with the memory that the warm-up's
+    # workspace had in other hands
+    g = torch.Generator().manual_seed(11)
+    wq, ws = fkl.quantize_int8((torch.randn(4096, 2880, generator=g) * 0.02).cuda())
+    x, u = torch.randn(9, 2880, generator=g).cuda(), torch.rand(9, generator=g).cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(s):
+        fkl.draw_token(x, wq, ws, u, top_k=40)
+        for _ in range(2):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=s):
+                out = fkl.draw_token(x, wq, ws, u, top_k=40), fkl.int8_linear(x, wq, ws)
+        many = torch.randn(2000, 2880, generator=g).cuda()
+        fkl.int8_linear(many, wq, ws)
+        others = [torch.full((2 ** 20,), 5, dtype=torch.int32, device="cuda") for _ in range(64)]
+    s.synchronize()
+    for _ in range(2):
+        x.copy_(torch.randn(9, 2880, generator=g))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        (token, logprob), y = out
+        want = fkl.draw_token(x, wq, ws, u, top_k=40)
+        assert torch.equal(token, want[0]) and torch.equal(logprob, want[1])
+        assert torch.equal(y, fkl.int8_linear(x, wq, ws))
+        assert all((t == 5).all() for t in others)
