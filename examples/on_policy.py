@@ -61,6 +61,7 @@ def main(argv=None):
         head8 = fkl.quantize_int8(student.head)
         start = torch.randint(0, a.vocab, (a.batch,), generator=g, device=device, dtype=torch.int32)
         tokens, logs = generate(student, head8, start, a.length, g, temperature=0.9, top_p=0.95)
+        assert (tokens >= 0).all()  # -1: a row without a logit to draw from, as a failed product leaves
         seen = torch.cat([start[:, None], tokens[:, :-1]], 1).reshape(-1)  # the states the tokens came from
         ids, values = fkl.teacher_topk(teacher.hidden(seen).contiguous(), teacher.head, a.top_k)
         H = student.hidden(seen).contiguous().requires_grad_()

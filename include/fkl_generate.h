@@ -57,6 +57,9 @@ fkl_status fkl_quantize_int8(const void* x, int32_t x_type, int64_t rows, int64_
  *   out [M][N] of type out_type, rows `ldo` elements apart (ldo >= N), aligned to its type
  * xq and wq are 16-byte aligned and K is a multiple of 16 (rows are whole 16-byte units).
  * 0 <= M < 2^31, 1 <= N < 2^31, 16 <= K <= 131072.  Any value of int8, -128 included.
+ * The kernel's waits are limited (5 s each).  Should one run out, the outputs that are not finished are
+ * NaN and fkl_read_status(workspace, stream) returns FKL_ERR_TIMEOUT until the workspace's next
+ * call; fkl_sample draws -1 from such a row when all of it is NaN.
  */
 size_t fkl_int8_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
 fkl_status fkl_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, int64_t M,

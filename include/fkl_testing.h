@@ -57,6 +57,18 @@ fkl_status fkl_test_backward_plan(int64_t T, int64_t d, int64_t V, int64_t K, in
  */
 fkl_status fkl_test_wait_timeout(uint64_t limit_ns, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * fkl_int8_matmul whose tokens arrive late_ns after the tensor-core kernel has started, with its
+ * waits limited to limit_ns each (both 1 ms to 1 s), so that the path of a wait that runs out can be
+ * checked: with late_ns well above limit_ns the outputs are NaN and fkl_read_status(workspace,
+ * stream) returns FKL_ERR_TIMEOUT; with late_ns well below it the product is the usual one.  For
+ * shapes that run on the tensor cores (more than 4 tokens).
+ */
+fkl_status fkl_test_int8_matmul_late(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                                     int64_t M, int64_t N, int64_t K, int32_t out_type, void* out, int64_t ldo,
+                                     uint64_t limit_ns, uint64_t late_ns, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

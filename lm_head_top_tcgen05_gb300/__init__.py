@@ -34,7 +34,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .generate import draw_token, int8_linear, int8_matmul, quantize_int8, sample
+from .generate import default_workspace, draw_token, int8_linear, int8_matmul, quantize_int8, sample
 from ._lib import (DIVERGENCES, FKL_ACCUMULATE_DH, FKL_ACCUMULATE_DW, FKL_NORM_SEQUENCES,  # noqa: F401
                    FKL_NORM_TOKENS, FKL_OK, STATUS, FklError, FklOptions, check, lib)
 
@@ -243,10 +243,23 @@ def backward(H: torch.Tensor, W: torch.Tensor, topk_idx: torch.Tensor, topk_logi
 
 
 def read_status(workspace: Optional[Workspace] = None, device=None) -> int:
-    """Device-side status of the last call on ``workspace`` (syncs the current stream)."""
-    if workspace is None:
-        workspace = _default_ws[_norm(device or "cuda")]
-    return int(lib().fkl_read_status(_ptr(workspace.buf), _stream(workspace.buf.device)))
+    """Device-side status of the last call on ``workspace`` (syncs the current stream).  Without one:
+    of the last loss call with the device's default workspace, or, if that is 0 or there was none, of
+    the last 8-bit product with the calling thread's default workspace of the current stream (a
+    captured product has neither: what a failed one leaves unfinished is NaN)."""
+    if workspace is not None:
+        buffers = [workspace.buf]
+    else:
+        device = _norm(device or "cuda")
+        buffers = [_default_ws[device].buf] if device in _default_ws else []
+        if (drawn := default_workspace(device)) is not None:
+            buffers.append(drawn)
+        if not buffers:
+            raise KeyError(device)
+    status = FKL_OK
+    for buf in buffers:
+        status = status or int(lib().fkl_read_status(_ptr(buf), _stream(buf.device)))
+    return status
 
 
 def local_count(mask: Optional[torch.Tensor], T: int, device=None, seq_ids: Optional[torch.Tensor] = None,

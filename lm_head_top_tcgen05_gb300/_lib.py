@@ -95,6 +95,8 @@ _SIGNATURES = {
                                   _P]),
     "fkl_test_gemm": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                      ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "fkl_test_int8_matmul_late": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int32, _P, _I64,
+                                                 ctypes.c_uint64, ctypes.c_uint64, _P, ctypes.c_size_t, _P]),
     "fkl_test_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, _P, ctypes.c_size_t, _P]),
 }
 

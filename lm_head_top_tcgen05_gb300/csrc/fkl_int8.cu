@@ -11,6 +11,7 @@
 // tensor cores 107 us.
 #include <climits>
 
+#include "../../include/fkl_testing.h"
 #include "fkl_gemm.cuh"
 #include "fkl_generate.cuh"
 #include "fkl_int8.h"
@@ -169,6 +170,13 @@ __global__ void __launch_bounds__(256)
     for (int b = 0; b < 4; ++b) q[b] = static_cast<float>(static_cast<int8_t>(w >> (8 * b)));
     put4(reinterpret_cast<__half*>(x16 + i), q);
   }
+}
+
+// Test hook: holds the product's tokens back for `ns` while the product runs (fkl_testing.h).
+__global__ void late_kernel(uint64_t ns) {
+  launch_dependents();
+  const uint64_t t0 = global_timer_ns();
+  for (int i = 0; i < (1 << 21) && global_timer_ns() - t0 < ns; ++i) __nanosleep(1000);
 }
 
 // ---------------------------------------------------------------- few tokens: dp4a
@@ -470,10 +478,12 @@ extern "C" size_t fkl_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K
 
 namespace fkl {
 
-// Both products; x_type < 0: x is int8 [M][K] with the scales x_scale.
+// Both products; x_type < 0: x is int8 [M][K] with the scales x_scale.  limit_ns: of each wait of the
+// tensor-core kernel; late_ns: what a test holds the tokens back.
 static fkl_status int8_product(const char* x_name, const void* x, int32_t x_type, int64_t ldx, const float* x_scale,
                                const int8_t* wq, const float* w_scale, const Int8Shape& g, int32_t out_type, void* out,
-                               void* workspace, size_t ws_bytes, void* stream) {
+                               void* workspace, size_t ws_bytes, void* stream, uint64_t limit_ns = kWaitLimitNs,
+                               uint64_t late_ns = 0) {
   const bool given = x_type < 0;
   if (!type_ok(out_type)) return bad(FKL_ERR_INVALID_ARG, "out_type must be one of FKL_TYPE_*");
   const size_t need = int8_workspace(g.M, g.N, g.K);
@@ -531,9 +541,15 @@ static fkl_status int8_product(const char* x_name, const void* x, int32_t x_type
   } else {
     e = launch_quantize(x, x_type, g.M, g.K, ldx, x16, scale, hdr, st);
   }
+  if (e == cudaSuccess && late_ns > 0) {
+    // with its SM's memory split as the product needs it, so that every pair starts beside it
+    e = cudaFuncSetAttribute(late_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) late_kernel<<<1, 1, 0, st>>>(late_ns);
+    if (e == cudaSuccess) e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return bad(FKL_ERR_CUDA, "launch of the tokens' kernel failed");
   e = launch_int8_gemm(reinterpret_cast<const uint16_t*>(x16), scale, wq, w_scale, g, out_type, out,
-                       pl.gemm, reinterpret_cast<float*>(ws + pl.off_part), hdr, st);
+                       pl.gemm, reinterpret_cast<float*>(ws + pl.off_part), hdr, limit_ns, st);
   return e == cudaSuccess ? FKL_OK : bad(FKL_ERR_CUDA, "8-bit product launch failed");
 }
 
@@ -555,4 +571,17 @@ extern "C" fkl_status fkl_int8_linear(const void* x, int32_t x_type, int64_t ldx
   if (ldx < K) return bad(FKL_ERR_INVALID_ARG, "ldx must be at least K");
   return int8_product("x", x, x_type, ldx, nullptr, wq, w_scale, Int8Shape{M, N, K, ldo}, out_type, out, workspace,
                       ws_bytes, stream);
+}
+
+extern "C" fkl_status fkl_test_int8_matmul_late(const int8_t* xq, const float* x_scale, const int8_t* wq,
+                                                const float* w_scale, int64_t M, int64_t N, int64_t K, int32_t out_type,
+                                                void* out, int64_t ldo, uint64_t limit_ns, uint64_t late_ns,
+                                                void* workspace, size_t ws_bytes, void* stream) {
+  set_last_error_message("");
+  constexpr uint64_t kMs = 1000000;
+  if (M < 1 || few_tokens(M, K)) return bad(FKL_ERR_INVALID_ARG, "the shape must run on the tensor cores");
+  if (limit_ns < kMs || limit_ns > 1000 * kMs || late_ns < kMs || late_ns > 1000 * kMs)
+    return bad(FKL_ERR_INVALID_ARG, "limit_ns and late_ns must be 1 ms to 1 s");
+  return int8_product("xq", xq, -1, K, x_scale, wq, w_scale, Int8Shape{M, N, K, ldo}, out_type, out, workspace, ws_bytes,
+                      stream, limit_ns, late_ns);
 }

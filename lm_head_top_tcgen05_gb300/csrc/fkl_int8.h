@@ -30,9 +30,9 @@ struct Int8GemmPlan {
 };
 Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms);
 // x16: the tokens' integers as fp16 [M][K]; x_scale: 16-byte aligned; hdr zeroed before on the
-// stream.
+// stream.  Each wait of the kernel is limited to limit_ns.
 cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const int8_t* wq, const float* w_scale,
                              const Int8Shape& s, int32_t out_type, void* out, const Int8GemmPlan& g, float* part,
-                             Int8Header* hdr, cudaStream_t st);
+                             Int8Header* hdr, uint64_t limit_ns, cudaStream_t st);
 
 }  // namespace fkl

@@ -357,6 +357,26 @@ __device__ __forceinline__ void i8_store_any(const I8Params& p, const float (&v)
     i8_store<__half, C>(p, v, m0, m_end, n, ws, lane);
 }
 
+// When a wait has run out: NaN in place of what this warp of the epilogue has not stored, so that a
+// failed launch cannot pass for a result.  A tile that is cut gets it too: its parts are added up by
+// the last warp to arrive, and this one does not.
+__device__ __noinline__ void i8_unfinished(const I8Params& p, I8Seq q, int row, int half) {
+  for (; q.more(p); q.next(p)) {
+    const int n = (q.tile / p.m_tiles) * 256 + row;
+    const int m0 = (q.tile % p.m_tiles) * p.nt;
+    const int m_end = min(p.M, m0 + p.nt);
+    if (n >= p.N) continue;
+    for (int col = 32 * half; m0 + col < m_end; col += 64)
+      for (int m = m0 + col; m < min(m_end, m0 + col + 32); ++m) {
+        const int64_t at = static_cast<int64_t>(m) * p.ldo + n;
+        if (p.out_type == FKL_TYPE_F32)
+          static_cast<uint32_t*>(p.out)[at] = 0x7fffffffu;
+        else
+          static_cast<uint16_t*>(p.out)[at] = 0x7fffu;  // NaN in both 16-bit types
+      }
+  }
+}
+
 // The pair whose part of the line of cut tiles holds block x.
 __device__ __forceinline__ int i8_owner(const I8Params& p, long long x) {
   return static_cast<int>(((x + 1) * p.cut_pairs - 1) / p.cut_blocks);
@@ -377,7 +397,10 @@ __device__ void i8_epilogue(const I8Params& p, const I8Ctx& c, int warp, int lan
     const float ws = n < p.N ? p.w_scale[n] : 0.f;
     const bool whole = q.kb1 - q.kb0 == p.k_blocks;
     float* part = p.part + static_cast<size_t>(2 * c.pair + (q.kb0 == 0 ? 1 : 0)) * p.nt * 256 + row;
-    if (!warp_wait(c.tfull0 + 8 * acc, acc_phase, c.ctl)) return;
+    if (!warp_wait(c.tfull0 + 8 * acc, acc_phase, c.ctl)) {
+      i8_unfinished(p, q, row, half);
+      return;
+    }
     tc_fence_after();
     const uint32_t t = c.tmem + lanes + static_cast<uint32_t>(acc * p.acc_cols);
 #pragma unroll 1
@@ -592,7 +615,7 @@ static cudaError_t launch_int8_gemm_t(const CUtensorMap& mw, const CUtensorMap& 
 
 cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const int8_t* wq, const float* w_scale,
                              const Int8Shape& s, int32_t out_type, void* out, const Int8GemmPlan& g, float* part,
-                             Int8Header* hdr, cudaStream_t st) {
+                             Int8Header* hdr, uint64_t limit_ns, cudaStream_t st) {
   CUtensorMap mw, mx;
   if (!encode_map_bytes(&mw, wq, s.K, s.N, s.K, kI8K, 128) ||
       !encode_map_f16(&mx, x16, s.K, s.M, s.K * 2, 64, static_cast<uint32_t>(g.nt / 2)))
@@ -621,7 +644,7 @@ cudaError_t launch_int8_gemm(const uint16_t* x16, const float* x_scale, const in
   p.part = part;
   p.arrived = hdr->arrived;
   p.status = &hdr->status;
-  p.limit_ns = kWaitLimitNs;
+  p.limit_ns = limit_ns;
   return g.sub == 2 ? launch_int8_gemm_t<2>(mw, mx, p, g.pairs, st) : launch_int8_gemm_t<1>(mw, mx, p, g.pairs, st);
 }
 

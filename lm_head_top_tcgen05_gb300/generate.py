@@ -71,6 +71,12 @@ def _workspace(nbytes: int, device, stream: int, given) -> torch.Tensor:
     return buf
 
 
+def default_workspace(device: torch.device) -> Optional[torch.Tensor]:
+    """The calling thread's default workspace of the device's current stream, or None.  Its first word
+    is the status of the last product that used it (``read_status``)."""
+    return getattr(_local, "buffers", {}).get((device.index, _stream(device)))
+
+
 def _dtype(dtype: torch.dtype, name: str) -> int:
     kind = DTYPES.get(dtype)
     if kind is None:
@@ -133,7 +139,8 @@ def int8_matmul(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_sca
                 workspace=None) -> torch.Tensor:
     """out [M, N] = (xq wq^T) * x_scale[:, None] * w_scale[None, :] for int8 xq [M, K], wq [N, K].
 
-    K is a multiple of 16.  ``out`` may be given, with rows any stride apart."""
+    K is a multiple of 16.  ``out`` may be given, with rows any stride apart.  Should a wait inside the
+    kernel run out (5 s), what is not finished is NaN and ``read_status`` gives FKL_ERR_TIMEOUT."""
     if xq.dtype != torch.int8 or xq.dim() != 2 or not xq.is_cuda or not xq.is_contiguous():
         raise ValueError("xq must be a contiguous int8 CUDA tensor [M, K]")
     M, K = xq.shape

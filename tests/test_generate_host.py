@@ -160,3 +160,44 @@ def test_captured_calls_do_not_keep_the_default_workspace(monkeypatch):
     assert captured.numel() >= 1000 and len({t.data_ptr() for t in (eager, captured, other)}) == 3
     capturing[0] = False
     assert generate._workspace(1000, cpu, 9, None).data_ptr() == eager.data_ptr()
+
+
+def test_late_tokens_hook_is_checked(L):
+    def call(M=5, N=10, K=64, limit=2 * 10 ** 6, late=10 ** 6, ldo=10):
+        return L.fkl_test_int8_matmul_late(16, 16, 16, 16, M, N, K, 0, 16, ldo, limit, late, 256, 1 << 30, None)
+
+    assert call(M=4) == INVALID and call(M=0) == INVALID     # no tensor cores
+    assert call(limit=10 ** 5) == INVALID and call(limit=2 * 10 ** 9) == INVALID
+    assert call(late=0) == INVALID and call(late=2 * 10 ** 9) == INVALID
+    assert call(ldo=9) == INVALID and call(K=72) == INVALID
+
+
+def test_read_status_sees_the_default_workspaces(monkeypatch):
+    # of the loss and, after it, of the calling thread's last product on the current stream
+    import lm_head_top_tcgen05_gb300 as fkl
+    from lm_head_top_tcgen05_gb300 import generate
+
+    class Fake:
+        def fkl_read_status(self, ptr, stream):
+            word = ctypes.cast(ptr, ctypes.POINTER(ctypes.c_uint32))[0]
+            return {0: 0, 1: 6, 4: 8}[word]
+
+    cpu = torch.device("cpu")
+    monkeypatch.setattr(fkl, "lib", Fake)
+    monkeypatch.setattr(fkl, "_stream", lambda device: None)
+    monkeypatch.setattr(fkl, "_default_ws", {})
+    monkeypatch.setattr(generate, "_capturing", lambda: False)
+    monkeypatch.setattr(generate, "_stream", lambda device: 31)
+    with pytest.raises(KeyError):
+        fkl.read_status(device=cpu)
+    product = generate._workspace(256, cpu, 31, None).zero_()
+    assert fkl.read_status(device=cpu) == 0
+    product[0] = 4
+    assert fkl.read_status(device=cpu) == 8
+    loss = fkl._ws_for(None, 256, cpu).zero_()
+    assert fkl.read_status(device=cpu) == 8
+    loss[0] = 1
+    assert fkl.read_status(device=cpu) == 6
+    own = fkl.Workspace(cpu)
+    own.get(256, cpu).zero_()
+    assert fkl.read_status(own) == 0

@@ -644,3 +644,47 @@ def test_graph_with_the_default_workspace(fkl):
         assert torch.equal(token, want[0]) and torch.equal(logprob, want[1])
         assert torch.equal(y, fkl.int8_linear(x, wq, ws))
         assert all((t == 5).all() for t in others)
+
+
+def _late(fkl, ops, dtype, out, workspace, limit_ms, late_ms):
+    from lm_head_top_tcgen05_gb300._lib import DTYPES, lib
+
+    (M, K), N = ops[0].shape, ops[2].shape[0]
+    buf = workspace.get(lib().fkl_int8_matmul_workspace_size(M, N, K), "cuda")
+    st = lib().fkl_test_int8_matmul_late(*[t.data_ptr() for t in ops], M, N, K, DTYPES[dtype], out.data_ptr(),
+                                         out.stride(0), limit_ms * 10 ** 6, late_ms * 10 ** 6, buf.data_ptr(),
+                                         buf.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+
+
+# Few tokens with cut tiles, whole tiles in several rounds, tiles of more than 128 tokens.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(9, 4096, 2880), (5, 21001, 272), (300, 513, 1040), (200, 19500, 1456)])
+def test_product_whose_tokens_come_too_late(fkl, M, N, K, dtype):
+    # every wait runs out after 20 ms; the tokens are there after 200
+    ops = operands(M, N, K, M + N)
+    t, ws = dev(*ops), fkl.Workspace("cuda")
+    big = torch.full((M, N + 6), 7.0, dtype=dtype, device="cuda")
+    _late(fkl, t, dtype, big[:, 3:N + 3], ws, 20, 200)
+    assert fkl.read_status(ws) == 8  # FKL_ERR_TIMEOUT
+    assert torch.isnan(big[:, 3:N + 3]).all()
+    assert (big[:, :3] == 7).all() and (big[:, N + 3:] == 7).all()
+    token, logprob = fkl.sample(big[:, 3:N + 3], torch.rand(M, device="cuda"))
+    assert (token == -1).all() and torch.isnan(logprob).all()
+    # in time, and the usual call in the same workspace
+    _late(fkl, t, dtype, big[:, 3:N + 3], ws, 1000, 1)
+    assert fkl.read_status(ws) == 0
+    assert_product(big[:, 3:N + 3], ops, dtype)
+    assert_product(fkl.int8_matmul(*t, out_dtype=dtype, workspace=ws), ops, dtype)
+    assert fkl.read_status(ws) == 0
+
+
+def test_status_of_the_default_workspace(fkl, monkeypatch):
+    monkeypatch.setattr(fkl, "_default_ws", {})  # no loss call before
+    ops = dev(*operands(8, 300, 64, 1))
+    fkl.int8_matmul(*ops)
+    buf = fkl.default_workspace(torch.device("cuda", torch.cuda.current_device()))
+    buf[0] = 4                                   # the bit that a wait that runs out sets
+    assert fkl.read_status(device="cuda") == 8
+    fkl.int8_matmul(*ops)
+    assert buf[0] == 0
