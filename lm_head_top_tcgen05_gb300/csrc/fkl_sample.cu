@@ -125,9 +125,11 @@ struct RowScale {
     return fminf(u, 8388608.f + static_cast<float>(kZBins - 1));
   }
   __device__ __forceinline__ float z_bin(float x) const { return z_bin_of(z(x)); }
-  // Bin of the second histogram, within `bin` of the first; depends on z alone too.
+  // Bin of the second histogram, within `bin` of the first; depends on z alone too.  Its loops must all
+  // get the same bin, as one counts the entries that another writes, so each rounding is spelled
+  // out: contracted or not, the plain expression gives other bins for one logit in some hundreds.
   __device__ __forceinline__ int fine_bin(float x, int bin) const {
-    const float u = (z(x) + static_cast<float>(bin) * kZBinWidth) * (-static_cast<float>(kFineBins) / kZBinWidth);
+    const float u = __fmul_rn(__fmaf_rn(static_cast<float>(bin), kZBinWidth, z(x)), -static_cast<float>(kFineBins) / kZBinWidth);
     return static_cast<int>(fminf(fmaxf(u, 0.f), static_cast<float>(kFineBins - 1)));
   }
 };

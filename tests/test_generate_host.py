@@ -201,3 +201,14 @@ def test_read_status_sees_the_default_workspaces(monkeypatch):
     own = fkl.Workspace(cpu)
     own.get(256, cpu).zero_()
     assert fkl.read_status(own) == 0
+
+
+def test_bins_of_the_second_histogram_have_one_rounding():
+    # three loops of the sampler evaluate it and must agree; the compiler may contract a plain product
+    # and sum in one of them and not in another
+    import re
+    from pathlib import Path
+
+    body = _function((Path(__file__).resolve().parent.parent / "lm_head_top_tcgen05_gb300" / "csrc"
+                      / "fkl_sample.cu").read_text(), "fine_bin")
+    assert "__fmaf_rn(" in body and "__fmul_rn(" in body and not re.search(r" [+*] ", body)

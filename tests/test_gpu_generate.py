@@ -688,3 +688,17 @@ def test_status_of_the_default_workspace(fkl, monkeypatch):
     assert fkl.read_status(device="cuda") == 8
     fkl.int8_matmul(*ops)
     assert buf[0] == 0
+
+
+@pytest.mark.parametrize("kw", [dict(top_k=600), dict(top_k=17000), dict(top_p=0.02), dict(top_p=0.5), dict(top_p=0.97),
+                                dict(top_k=9000, top_p=0.3, min_p=0.9)])
+def test_sample_logits_at_the_edges_of_bins(fkl, kw):
+    # logits at the edges of 1/2048 of a histogram's bin (1/64 of a halving), and next to them;
+    # some thousands to a bin, more than one list holds
+    V, width = 40000, np.log(2.0) / 64
+    g = torch.Generator().manual_seed(12)
+    x = (-torch.randint(0, 8 * 2048, (4, V), generator=g).double() * width / 2048).float()
+    step = torch.randint(-1, 2, (4, V), generator=g)
+    x = torch.where(step == 0, x, torch.nextafter(x, torch.where(step > 0, 1.0, -1.0))).clamp(max=0)
+    x[:, 5] = 0
+    check_sample(fkl, x, torch.rand(4, generator=g), **kw)
