@@ -56,7 +56,7 @@ fkl_status fkl_quantize_int8(const void* x, int32_t x_type, int64_t rows, int64_
  *   xq int8 [M][K], x_scale float [M]; wq int8 [N][K], w_scale float [N]; all contiguous
  *   out [M][N] of type out_type, rows `ldo` elements apart (ldo >= N), aligned to its type
  * xq and wq are 16-byte aligned and K is a multiple of 16 (rows are whole 16-byte units).
- * 0 <= M < 2^31, 1 <= N < 2^31, 16 <= K <= 131072.  Any value of int8, -128 included.
+ * 0 <= M <= 2^31 - 512, 1 <= N <= 2^31 - 512, 16 <= K <= 131072.  Any value of int8, -128 included.
  * The kernel's waits are limited (5 s each).  Should one run out, the outputs that are not finished are
  * NaN and fkl_read_status(workspace, stream) returns FKL_ERR_TIMEOUT until the workspace's next
  * call; fkl_sample draws -1 from such a row when all of it is NaN.

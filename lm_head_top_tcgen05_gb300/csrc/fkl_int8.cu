@@ -19,7 +19,9 @@
 
 namespace fkl {
 
-constexpr int64_t kMaxInt8K = 131072;  // 128 * 128 * K stays within an int32 sum
+constexpr int64_t kMaxInt8K = 131072;
+// Largest M and N: a tile of 256 tokens or channels more stays an int.
+constexpr int64_t kMaxInt8Extent = INT32_MAX - 511;
 
 // ---------------------------------------------------------------- quantisation
 constexpr uint32_t kInfBits = 0x7f800000u;
@@ -189,6 +191,7 @@ constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int64_t kFewTokens = 4;
 constexpr int64_t kFewSmem = 96 * 1024;  // two blocks to an SM
+static_assert(128 * 128 * kFewSmem <= INT32_MAX, "the int32 sums of K <= kFewSmem products do not overflow");
 
 // V values per lane, summed over the lanes: lane l gets the sum of value l * V / 32 (V < 32: of
 // the value whose 32 / V lanes it is one of).
@@ -413,7 +416,8 @@ struct Int8Plan {
 
 // The workspace for a device of `sms` SMs.
 static bool make_int8_plan(int64_t M, int64_t N, int64_t K, int sms, Int8Plan* p) {
-  if (M < 0 || M > INT32_MAX || N < 1 || N > INT32_MAX || K < 16 || K % 16 != 0 || K > kMaxInt8K) return false;
+  if (M < 0 || M > kMaxInt8Extent || N < 1 || N > kMaxInt8Extent || K < 16 || K % 16 != 0 || K > kMaxInt8K) return false;
+  if ((M + 127) / 128 * ((N + 255) / 256) > INT32_MAX) return false;  // tiles
   p->few = few_tokens(M, K);
   size_t off = p->few ? 256 : up256(sizeof(Int8Header));  // few tokens: the status word's 256 bytes
   p->off_x16 = p->off_scale = p->off_part = off;
@@ -488,7 +492,7 @@ static fkl_status int8_product(const char* x_name, const void* x, int32_t x_type
   if (!type_ok(out_type)) return bad(FKL_ERR_INVALID_ARG, "out_type must be one of FKL_TYPE_*");
   const size_t need = int8_workspace(g.M, g.N, g.K);
   if (need == 0)
-    return bad(FKL_ERR_INVALID_ARG, "unsupported shape (need K % 16 == 0, 16 <= K <= 131072, 0 <= M < 2^31, 1 <= N < 2^31)");
+    return bad(FKL_ERR_INVALID_ARG, "unsupported shape (need K % 16 == 0, 16 <= K <= 131072, 0 <= M <= 2^31 - 512, 1 <= N <= 2^31 - 512)");
   if (g.ldo < g.N) return bad(FKL_ERR_INVALID_ARG, "ldo must be at least N");
   if (wq == nullptr || w_scale == nullptr ||
       (g.M > 0 && (x == nullptr || out == nullptr || (given && x_scale == nullptr))))

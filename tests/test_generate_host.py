@@ -212,3 +212,13 @@ def test_bins_of_the_second_histogram_have_one_rounding():
     body = _function((Path(__file__).resolve().parent.parent / "lm_head_top_tcgen05_gb300" / "csrc"
                       / "fkl_sample.cu").read_text(), "fine_bin")
     assert "__fmaf_rn(" in body and "__fmul_rn(" in body and not re.search(r" [+*] ", body)
+
+
+def test_extents_whose_tiles_pass_32_bits_are_refused(L):
+    # the kernels' row and channel numbers are ints, a whole tile beyond the last one included
+    most = 2 ** 31 - 512
+    for f in (L.fkl_int8_matmul_workspace_size, L.fkl_int8_linear_workspace_size):
+        assert f(4, most, 16) > 0 and f(most, 1, 16) > 0
+        assert f(4, most + 1, 16) == 0 and f(most + 1, 1, 16) == 0 and f(1, 2 ** 31 - 1, 64) == 0
+        assert f(most, most, 16) == 0
+    assert L.fkl_int8_matmul(16, 16, 16, 16, 4, 2 ** 31 - 1, 64, 0, 16, 2 ** 31, 256, 1 << 40, None) == INVALID
