@@ -61,6 +61,8 @@ fkl_status fkl_quantize_int8(const void* x, int32_t x_type, int64_t rows, int64_
  * NaN and fkl_read_status(workspace, stream) returns FKL_ERR_TIMEOUT until the workspace's next
  * call; fkl_sample draws -1 from such a row when all of it is NaN.
  */
+/* Bytes for this shape on the current device.  Not monotone: partial sums are kept only for shapes
+ * whose tiles are cut along K, so a buffer for several shapes takes the largest of their sizes. */
 size_t fkl_int8_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
 fkl_status fkl_int8_matmul(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, int64_t M,
                            int64_t N, int64_t K, int32_t out_type, void* out, int64_t ldo, void* workspace,

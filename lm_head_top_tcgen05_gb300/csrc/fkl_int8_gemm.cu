@@ -70,7 +70,7 @@ struct I8Params {
   void* out;
   int64_t ldo;
   int out_type, paired;  // paired: two adjacent 16-bit outputs share an aligned word
-  float* part;   // [2 * pairs][nt][256]
+  float* part;   // [2 * cut_pairs][nt][256], where tiles are cut
   int* arrived;  // [pairs][16]
   uint32_t* status;
   uint64_t limit_ns;
@@ -590,7 +590,8 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   g.cut_blocks = cut ? rest * g.k_blocks : 0;
   // a pair without a block would be a part that the tile's last one waits for in vain
   g.cut_pairs = static_cast<int>(sharing);
-  g.part_bytes = static_cast<size_t>(2 * g.pairs) * g.nt * 256 * 4;
+  // two parts of each pair that shares the line: the end of one tile, the start of the next
+  g.part_bytes = g.cut_blocks > 0 ? static_cast<size_t>(2 * g.cut_pairs) * g.nt * 256 * 4 : 0;
   return g;
 }
 

@@ -222,3 +222,11 @@ def test_extents_whose_tiles_pass_32_bits_are_refused(L):
         assert f(4, most + 1, 16) == 0 and f(most + 1, 1, 16) == 0 and f(1, 2 ** 31 - 1, 64) == 0
         assert f(most, most, 16) == 0
     assert L.fkl_int8_matmul(16, 16, 16, 16, 4, 2 ** 31 - 1, 64, 0, 16, 2 ** 31, 256, 1 << 40, None) == INVALID
+
+
+def test_workspace_holds_partial_sums_only_of_cut_tiles(L):
+    # otherwise the header (at most 16 KB), the tokens in fp16 and their scales, each rounded up to 256
+    for M, N, K in ((4096, 201088, 2880), (64, 151936, 4096), (203, 50261, 1456), (8192, 4096, 4096)):
+        assert L.fkl_int8_linear_workspace_size(M, N, K) <= 16384 + 2 * M * K + 4 * M + 512
+    for M, N, K in ((9, 4096, 2880), (16, 4096, 8192), (140, 19500, 8000)):
+        assert L.fkl_int8_linear_workspace_size(M, N, K) > 16384 + 2 * M * K + 4 * M + 512
