@@ -230,3 +230,13 @@ def test_workspace_holds_partial_sums_only_of_cut_tiles(L):
         assert L.fkl_int8_linear_workspace_size(M, N, K) <= 16384 + 2 * M * K + 4 * M + 512
     for M, N, K in ((9, 4096, 2880), (16, 4096, 8192), (140, 19500, 8000)):
         assert L.fkl_int8_linear_workspace_size(M, N, K) > 16384 + 2 * M * K + 4 * M + 512
+
+
+def test_product_reads_nothing_as_constant_data():
+    # it starts beside the kernel that writes the tokens and their scales: the path for data that is
+    # constant during a launch (__ldg) may give what was there before
+    from pathlib import Path
+
+    source = (Path(__file__).resolve().parent.parent / "lm_head_top_tcgen05_gb300" / "csrc" / "fkl_int8_gemm.cu").read_text()
+    code = "\n".join(line.split("//")[0] for line in source.splitlines())
+    assert "__ldg(" not in code and ".nc." not in code and "__restrict__" not in code
