@@ -57,7 +57,7 @@ constexpr float kZBinWidth = 0.6931471806f / 64.f;
 constexpr int kFineBins = 2048;        // of the second histogram, over one bin of the first
 constexpr int kGroups = 32;            // groups of bins that are added up before they are exchanged
 constexpr int kFew = 32;
-constexpr int kCountingMax = 160;      // longest list that is ranked by counting, not sorted
+constexpr int kCountingMax = 160;      // longest list that is ranked by counting, not sorted (see kTwoSlice)
 
 using u64 = unsigned long long;
 
@@ -1449,6 +1449,14 @@ template <bool kResident>
 constexpr size_t max_dynamic(int n) {
   return ((n == 1 ? 227 * 1024 : 228 * 1024 / n - 1024) - sizeof(SampleShared<kResident>)) / 16 * 16;
 }
+
+// The longest slice, in bytes, of which an SM holds two beside the counted entries' weights and a
+// vector that it may start inside: 8 of them are a row of 201088 fp32 logits.  Longer rows have one
+// CTA to an SM, half as many rows at once.  On the device, 64 rows of 201088 and of 201089 fp32: 29
+// and 44 us without filters, 28 and 44 with top-k 50, 74 and 128 with flat rows' top-p 0.9; 16 rows: 14
+// and 19, 15 and 19, 36 and 52.  A larger SampleShared or kCountingMax moves that step to shorter rows.
+constexpr size_t kTwoSlice = 100544;
+static_assert(max_dynamic<true>(2) >= kCountingMax * sizeof(u64) + kTwoSlice + sizeof(uint4), "two such slices to an SM");
 
 // Fewest logits that a CTA gets a slice of.
 constexpr int64_t kMinSlice = 4096;
