@@ -52,7 +52,8 @@ fkl_status fkl_quantize_int8(const void* x, int32_t x_type, int64_t rows, int64_
  * Product of 8-bit integers with a scale per token and per channel:
  *     out[m][n] = (sum_k xq[m][k] * wq[n][k]) * x_scale[m] * w_scale[n]
  * rounded once to out_type.  The sum is exact while its partial sums stay below 2^24 in
- * magnitude (always for K <= 1024) and within fp32 rounding of the exact sum beyond.
+ * magnitude (always for K <= 1024), and for up to 4 tokens with K <= 24576.  Beyond, each 16-deep step
+ * of the tensor cores' fp32 accumulation loses at most 2^-23 of the partial sum.
  *   xq int8 [M][K], x_scale float [M]; wq int8 [N][K], w_scale float [N]; all contiguous
  *   out [M][N] of type out_type, rows `ldo` elements apart (ldo >= N), aligned to its type
  * xq and wq are 16-byte aligned and K is a multiple of 16 (rows are whole 16-byte units).

@@ -8,7 +8,7 @@
 // too long for shared memory, on the tensor cores (fkl_int8_gemm.cu).  W 201088 x 2880 on a GB300:
 // 1 token 84 us (86 us is W at the measured copy bandwidth), 4 tokens 90 us; with 8 tokens the
 // streaming kernel took 123 us, bound by its reads of the tokens from shared memory, and the
-// tensor cores 107 us.
+// tensor cores take 103 to 106 us.
 #include <climits>
 
 #include "../../include/fkl_testing.h"

@@ -14,10 +14,10 @@
 // kernel before, are the B operand in shared memory (up to 256 per tile, half per CTA).
 //
 // What bounds it (GB300, W 201088 x 2880): up to about 128 tokens the HBM reads of W, 579 MB, 86 us at
-// the measured 6.78 TB/s: 16 tokens take 106 us, 128 tokens 128 us with 103 MB of output.  Beyond,
-// the tensor pipe: 4096 tokens 2.69 ms, 1766 TFLOP/s, 91 % of a bf16 library product's burst
-// rate; a tile of more than 128 tokens has one accumulator, so its epilogue (about 1 us of 13) is
-// not hidden.
+// the measured 6.78 TB/s: 16 tokens take 102 us on the device, 128 tokens 124 us with 103 MB of
+// output.  Beyond, the tensor pipe: 4096 tokens 2.54 to 2.70 ms, as the clock under the power cap
+// allows, 1760 to 1870 TFLOP/s (a bf16 library product: 1932 in a burst, 1704 sustained); a tile of
+// more than 128 tokens has one accumulator, so its epilogue (about 1 us of 13) is not hidden.
 //
 // Roles per CTA (20 warps):
 //   warps 0..7   convert: 128 rows x 128 k of int8 to fp16 in a TMEM slot; warps 0..3 take the
@@ -556,9 +556,10 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   const auto tile_time = [&](int64_t nt) { return static_cast<double>(K) / kI8K * std::max(0.36, nt / 256.0 * 0.55); };
   // Tiles of up to 256 tokens, or of up to 128 with a second accumulator that hides the epilogue: a
   // wave of tiles then costs about 2 us beyond its blocks, not 5, but there are more waves, and each
-  // converts W once more.  256 against 128 tokens, in us: 512 x 4096 x 4096 31.0, 24.4;
-  // 512 x 50261 x 1456 89.5, 78.8; 350 x 65536 x 640 47.9, 41.2; 1024 x 4096 x 4096 33.2, 38.1;
-  // 203 x 151936 x 4096 185, 218; 640 x 20000 x 5120 104.6, 109.5.
+  // converts W once more.  256 against 128 tokens, in us on the device: 512 x 4096 x 4096 27.2, 21.5;
+  // 512 x 50261 x 1456 94.2, 74.8; 350 x 65536 x 640 44.5, 38.8; 1024 x 4096 x 4096 30.3, 37.0;
+  // 203 x 151936 x 4096 177, 225; 640 x 20000 x 5120 98.0, 108.7.  It misses where a tile has somewhat
+  // more than 200 tokens and few blocks: 700 x 50261 x 1456 gets 256 (121.4, 105.0).
   const int64_t n_tiles = (N + 255) / 256, most_pairs = std::min(sms / 2, kMaxPairs);
   const auto waves_time = [&](int64_t m_tiles) {
     const int64_t nt = (M + m_tiles - 1) / m_tiles;
@@ -582,9 +583,10 @@ Int8GemmPlan plan_int8_gemm(int64_t M, int64_t N, int64_t K, int sms) {
   // Tiles beyond whole waves of pairs either leave pairs idle for part of a tile's time or are cut,
   // which costs the fences and sums of their parts at the end: measured about 5 us + nt * 0.06 us with
   // up to 4 parts to a tile, and more with more, which pays where each part keeps 16 blocks or so.
-  // 140 x 19500 x 8000 in 4, 8, 16 and 63 parts: 52, 62, 86 and 241 us; 16 x 256 x 40000 in 4, 16 and 76:
-  // 39, 31 and 48 us.  Whole against cut, in us: 9 x 4096 x 2880 14.7, 13.8; 16 x 4096 x 8192 24.9, 17.4;
-  // 140 x 19500 x 8000 70, 52; 64 x 25600 x 4096 31.3, 33.9; 203 x 50261 x 1456 42.8, 57.0.
+  // 140 x 19500 x 8000 in 4, 8, 16 and 63 parts: 48, 57, 81 and 232 us; 16 x 256 x 40000 in 4, 16 and 76:
+  // 36, 28 and 47 us.  Whole against cut, in us on the device: 9 x 4096 x 2880 12.4, 11.3;
+  // 16 x 4096 x 8192 22.2, 13.6; 140 x 19500 x 8000 67.9, 47.9; 64 x 25600 x 4096 29.3, 31.4;
+  // 203 x 50261 x 1456 40.9, 57.9.
   g.rounds = static_cast<int>(tiles / g.pairs);
   const int64_t rest = tiles - static_cast<int64_t>(g.rounds) * g.pairs;
   const int64_t parts = std::min<int64_t>(std::max<int64_t>(4, K / 2048), g.k_blocks);

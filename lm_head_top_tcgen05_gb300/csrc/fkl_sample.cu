@@ -28,8 +28,9 @@
 //
 // What bounds it (GB300): a row is 11 to 26 us from its load to its token, in which it is read
 // once (2 to 5 us) and passed over once or twice in shared memory (a draw without filters
-// executes 36 instructions a logit in all, top-p 0.9 of flat rows 101), with 3 to 8 cluster
-// barriers of about 1 us between; 36 rows of 201088 fp32 fit the device's shared memory at once.  On the
+// executes 36 instructions a logit in all, top-p 0.9 of flat rows 101), with cluster barriers of about
+// 1 us between: 3 with a list, 4 without filters, 10 with top-p, up to 18 with a top-k too large for
+// a list before it; 36 rows of 201088 fp32 fit the device's shared memory at once.  On the
 // device 64 such rows take 29 us without filters, 28 us with top-k 50, 68 us with top-p 0.9; one row
 // 11, 12 and 26 us.
 #include <atomic>

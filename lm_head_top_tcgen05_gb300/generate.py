@@ -8,8 +8,8 @@ On-policy distillation trains on text that the student draws.  One step of drawi
 
 with ``h`` the hidden states [M, K] of the rows' last tokens and ``u`` one uniform random
 number per row.  ``int8_matmul`` is the product of operands that are already in 8 bits.
-``draw_token`` is the step as one call.  None of these has a gradient.  Calls run on the
-current stream.  A product without a ``workspace`` uses a buffer that the calling thread keeps for
+``draw_token`` is the step as one call.  None of these has a gradient.  Inputs are on the
+current device, and calls run on its current stream.  A product without a ``workspace`` uses a buffer that the calling thread keeps for
 that stream, so calls of several threads and on several streams never share one; a call that is captured in
 a CUDA graph has a buffer of the graph's own memory.  A ``Workspace`` that is given belongs to one thread
 and one stream at a time, and one given to a captured call to that graph.
@@ -108,7 +108,7 @@ def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> i
 def quantize_int8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """(q int8 [M, K], scale float32 [M]): each row of x in 8-bit integers, x ~ q * scale.
 
-    scale = largest magnitude / 127, q rounded to nearest even.  A row with a NaN or an infinity
+    scale = largest magnitude * fl(1/127), q = x / scale rounded to nearest even.  A row with a NaN or an infinity
     has scale NaN."""
     M, K, ld = _rows(x, "x")
     kind = _dtype(x.dtype, "x")
