@@ -1,5 +1,5 @@
-"""ctypes loader of the in-tree CUDA library ``libfkl.so`` (C ABI in include/fkl.h and
-include/fkl_generate.h).
+"""ctypes loader of the in-tree CUDA library ``libfkl.so`` (C ABI in include/fkl.h,
+include/fkl_generate.h, include/fkl_score.h and include/fkl_cache.h).
 
 There is no fallback: if the library is missing or cannot be loaded, every call raises.
 """
@@ -93,6 +93,20 @@ _SIGNATURES = {
                                        _P, ctypes.c_size_t, _P]),
     "fkl_sample": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _I64, _I64, _P, ctypes.POINTER(FklSampleParams), _P, _P,
                                   _P]),
+    "fkl_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _I64, _I64, _P, ctypes.c_int32, _P, ctypes.c_float,
+                                          _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P]),
+    "fkl_token_logprobs_backward": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _I64, _I64, _P, ctypes.c_int32, _P,
+                                                   ctypes.c_float, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "fkl_logprob_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "fkl_logprob_forward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P,
+                                           _P, ctypes.c_size_t, _P]),
+    "fkl_logprob_backward_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, ctypes.c_int32]),
+    "fkl_logprob_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _I64, _I64, _I64,
+                                            ctypes.c_float, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
+                                            ctypes.c_size_t, _P]),
+    "fkl_cache_words": (ctypes.c_int32, [_I64, _I64, ctypes.c_int32]),
+    "fkl_cache_pack": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, ctypes.c_int32, _P, _P]),
+    "fkl_cache_unpack": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.c_int32, _P, _P, _P]),
     "fkl_test_gemm": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                      ctypes.c_int, _P, ctypes.c_size_t, _P]),
     "fkl_test_int8_matmul_late": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int32, _P, _I64,

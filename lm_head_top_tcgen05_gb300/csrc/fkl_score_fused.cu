@@ -1,0 +1,575 @@
+// Scores given tokens from hidden states (fkl_logprob_forward) and the gradients in the hidden states and
+// the LM head (fkl_logprob_backward), on the two-SM tensor-core product of fkl_gemm2.cuh.
+//
+// Forward: the logits s = H W^T live in tensor memory, a tile at a time.  Each (row, vocabulary split) keeps
+// a base-2 reference m, l = sum of 2^a and u = sum of 2^a a with a = s log2(e) / tau - m, as the loss's
+// forward keeps m and l, and the split that holds the row's token stores its logit.  A kernel over the
+// rows then joins the splits: lse = ln 2 (M + log2 L), entropy = ln 2 (log2 L - U / L).
+//
+// Backward: dS_tv = q_tv (c0_t + c1_t log2 q_tv) + k_t [v = v*_t] with c0 = -(a + b entropy) / tau,
+// c1 = -b ln 2 / tau, k = a / tau, rounded to bf16 and written block by block (tokens x a vocabulary slab),
+// then dW[slab] += dS^T H and dH[block] += dS W[slab] in fp32, in a fixed order: the blocks are those of the
+// loss's backward, planned by the same functions, and both products run its kernels.  The bf16 of dS (half a step
+// is 2^-8 of each value) is what the tensor cores multiply; sums stay fp32.
+//
+// The tensor pipe bounds both: 2 T V d operations forward, 6 T V d backward.
+#include <cmath>
+
+#include "../../include/fkl_score.h"
+#include "fkl_gemm2.cuh"
+#include "fkl_generate.cuh"
+#include "fkl_score.cuh"
+
+namespace fkl {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool on_boundary(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// ---------------------------------------------------------------- forward epilogue
+struct ScoreFwdParams {
+  TokenIds tokens;
+  const uint8_t* mask;
+  float* part;       // [3][nsplit][T]: reference, sum, weighted sum
+  float* token_s;    // [T]: the token's logit
+  int T, V, nsplit;
+  float scale2;      // log2(e) / tau
+};
+
+struct EpiScore {
+  using Params = ScoreFwdParams;
+  const Params& p;
+  int t, tok;
+  bool row_ok;
+  float m, l, u;
+
+  __device__ explicit EpiScore(const Params& prm) : p(prm) {}
+
+  __device__ __forceinline__ void begin_unit(int row0, int, int, int row) {
+    t = row0 + row;
+    row_ok = t < p.T;
+    tok = row_ok && (p.mask == nullptr || p.mask[t] != 0) ? p.tokens.get(t, p.V) : -1;
+    m = -INFINITY;
+    l = u = 0.f;
+  }
+
+  // Adds the chunk's terms at reference m; the sum of its weights.
+  __device__ __forceinline__ float sums(const float (&v)[32], float ref, float& weighted) const {
+    const float2 sc = make_float2(p.scale2, p.scale2), om = make_float2(-ref, -ref);
+    float2 t0 = make_float2(0.f, 0.f), t1 = t0, w0 = t0, w1 = t0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float2 a0 = ffma2(make_float2(v[j], v[j + 1]), sc, om), a1 = ffma2(make_float2(v[j + 2], v[j + 3]), sc, om);
+      const float2 e0 = make_float2(ex2_approx(a0.x), ex2_approx(a0.y)), e1 = make_float2(ex2_approx(a1.x), ex2_approx(a1.y));
+      t0 = fadd2(t0, e0);
+      t1 = fadd2(t1, e1);
+      w0 = ffma2(e0, a0, w0);
+      w1 = ffma2(e1, a1, w1);
+    }
+    weighted = (w0.x + w0.y) + (w1.x + w1.y);
+    return (t0.x + t0.y) + (t1.x + t1.y);
+  }
+
+  __device__ __forceinline__ void chunk(float (&v)[32], int col0) {
+    if (col0 >= p.V) return;
+    if (tok >= col0 && tok < col0 + 32) p.token_s[t] = pick(v, tok - col0);
+    if (col0 + 32 > p.V) {  // the last columns: weight 0 at a finite exponent (0 * -inf is not 0)
+      const float low = ((m != -INFINITY ? m : v[0] * p.scale2) - 400.f) / p.scale2;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col0 + j >= p.V) v[j] = low;
+    }
+    float weighted;
+    if (m != -INFINITY) {
+      // A reference 2^10 below a term would cost the entropy 10 binary orders of its last digits: log2 L
+      // and U / L then cancel.  It moves before that.
+      const float sum = sums(v, m, weighted);
+      if (sum < 1024.f) {
+        l += sum;
+        u += weighted;
+        return;
+      }
+    }
+    float c0 = fmax3(v[0], v[1], v[2]), c1 = fmax3(v[3], v[4], v[5]);
+#pragma unroll
+    for (int j = 6; j < 30; j += 4) {
+      c0 = fmax3(c0, v[j], v[j + 1]);
+      c1 = fmax3(c1, v[j + 2], v[j + 3]);
+    }
+    const float to = fmaxf(m, fmax3(c0, c1, fmaxf(v[30], v[31])) * p.scale2);
+    const float sum = sums(v, to, weighted);
+    if (m == -INFINITY) {
+      l = sum;
+      u = weighted;
+    } else {
+      const float r = m - to, f = ex2_approx(r);
+      u = fmaf(fmaf(r, l, u), f, weighted);
+      l = fmaf(l, f, sum);
+    }
+    m = to;
+  }
+
+  template <int BN>
+  __device__ __forceinline__ void tile(uint32_t taddr, int n, int) {
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; c += 2) {
+      float v0[32], v1[32];
+      tmem_ld32(taddr + c * 32, v0);
+      tmem_ld32(taddr + c * 32 + 32, v1);
+      tmem_wait_ld();
+      pin(v0);
+      pin(v1);
+      chunk(v0, n * BN + c * 32);
+      chunk(v1, n * BN + c * 32 + 32);
+    }
+  }
+
+  __device__ __forceinline__ void end_unit(int split, int) {
+    if (!row_ok) return;
+    const size_t plane = static_cast<size_t>(p.nsplit) * p.T, i = static_cast<size_t>(split) * p.T + t;
+    p.part[i] = m;
+    p.part[plane + i] = l;
+    p.part[2 * plane + i] = u;
+  }
+};
+
+// ---------------------------------------------------------------- backward epilogue
+struct ScoreDsParams {
+  TokenIds tokens;            // of all tokens: row t of the block is token r0 + t
+  int64_t r0;
+  const float *c0, *c1, *at;  // of the block's tokens; a row left out has zeros
+  const float* lse;
+  uint16_t* ds;
+  int64_t ld_ds;
+  int T, V, v0, slab_w;
+  float scale2;
+};
+
+struct EpiScoreDs {
+  using Params = ScoreDsParams;
+  const Params& p;
+  bool row_ok, off;
+  int tok;
+  float c0, c1, at, shift;
+  uint16_t* dst;
+
+  __device__ explicit EpiScoreDs(const Params& prm) : p(prm) {}
+
+  __device__ __forceinline__ void begin_unit(int row0, int, int, int row) {
+    const int t = row0 + row;
+    row_ok = t < p.T;
+    off = true;
+    tok = -1;
+    c0 = c1 = at = shift = 0.f;
+    dst = nullptr;
+    if (row_ok) {
+      c0 = p.c0[t];
+      c1 = p.c1[t];
+      at = p.at[t];
+      off = c0 == 0.f && c1 == 0.f && at == 0.f;
+      shift = -p.lse[t] * kLog2e;
+      if (!off) tok = p.tokens.get(p.r0 + t, p.V);
+      dst = p.ds + static_cast<size_t>(t) * p.ld_ds;
+    }
+  }
+
+  __device__ __forceinline__ void chunk(float (&v)[32], int cl0) {
+    if (!row_ok) return;
+    uint16_t* o = dst + cl0;
+    if (off) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) st_v8(o + 16 * j, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u);
+      return;
+    }
+    {
+      const float2 sc = make_float2(p.scale2, p.scale2), sh = make_float2(shift, shift);
+      const float2 k0 = make_float2(c0, c0), k1 = make_float2(c1, c1);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 a = ffma2(make_float2(v[j], v[j + 1]), sc, sh);  // log2 q
+        const float2 y = fmul2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), ffma2(k1, a, k0));
+        v[j] = y.x;
+        v[j + 1] = y.y;
+      }
+    }
+    const int jt = tok - (p.v0 + cl0);
+    if (jt >= 0 && jt < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] += j == jt ? at : 0.f;
+    }
+    if (cl0 + 32 > p.slab_w) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (cl0 + j >= p.slab_w) v[j] = 0.f;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      st_v8(o + 16 * j, w[8 * j], w[8 * j + 1], w[8 * j + 2], w[8 * j + 3], w[8 * j + 4], w[8 * j + 5], w[8 * j + 6],
+            w[8 * j + 7]);
+  }
+
+  template <int BN>
+  __device__ __forceinline__ void tile(uint32_t taddr, int n, int) {
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; c += 2) {
+      float v0[32], v1[32];
+      tmem_ld32(taddr + c * 32, v0);
+      tmem_ld32(taddr + c * 32 + 32, v1);
+      tmem_wait_ld();
+      pin(v0);
+      pin(v1);
+      chunk(v0, n * BN + c * 32);
+      chunk(v1, n * BN + c * 32 + 32);
+    }
+  }
+
+  __device__ __forceinline__ void end_unit(int, int) {}
+};
+
+// ---------------------------------------------------------------- kernels over the rows
+constexpr int kRowThreads = 256;
+
+// Joins a row's splits.  The weights between splits are fp32, the same for L and U; the sums and the two
+// terms of the entropy, which may cancel, are fp64.
+__global__ void __launch_bounds__(kRowThreads)
+    score_rows_kernel(const float* __restrict__ part, int nsplit, const float* __restrict__ token_s, TokenIds tokens,
+                      const uint8_t* __restrict__ mask, int64_t T, int V, float inv_tau, uint32_t* status,
+                      float* __restrict__ logprob, float* __restrict__ entropy, float* __restrict__ lse) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
+  if (t >= T) return;
+  const size_t plane = static_cast<size_t>(nsplit) * T;
+  float M = -INFINITY;
+  for (int s = 0; s < nsplit; ++s) M = fmaxf(M, part[static_cast<size_t>(s) * T + t]);
+  double L = 0.0, U = 0.0;
+  for (int s = 0; s < nsplit; ++s) {
+    const size_t i = static_cast<size_t>(s) * T + t;
+    const float a = fmaxf(part[i] - M, -1000.f);
+    const double f = exp2f(a), l = part[plane + i];
+    L += f * l;
+    U += f * (part[2 * plane + i] + a * l);
+  }
+  const double log2_sum = log2(L);
+  const bool late = (*reinterpret_cast<const volatile uint32_t*>(status) & kStatusTimeoutBit) != 0;
+  const double ln2 = 0.69314718055994530942;
+  const double z = late ? NAN : (static_cast<double>(M) + log2_sum) * ln2;
+  lse[t] = static_cast<float>(z);
+  if (mask != nullptr && mask[t] == 0) {
+    logprob[t] = late ? NAN : 0.f;
+    entropy[t] = late ? NAN : 0.f;
+    return;
+  }
+  const int tok = tokens.get(t, V);
+  if (tok < 0) atomicOr(status, kStatusBadIdBit);
+  logprob[t] = tok < 0 ? NAN : static_cast<float>(static_cast<double>(token_s[t]) * inv_tau - z);
+  entropy[t] = late ? NAN : static_cast<float>((log2_sum - U / L) * ln2);
+}
+
+// The three factors of each token's dS; a token outside the vocabulary is recorded.
+__global__ void __launch_bounds__(kRowThreads)
+    score_factors_kernel(TokenIds tokens, const uint8_t* __restrict__ mask, const float* __restrict__ entropy,
+                         const float* __restrict__ grad_logprob, const float* __restrict__ grad_entropy, int64_t T, int V,
+                         float inv_tau, uint32_t* __restrict__ status, float* __restrict__ c0, float* __restrict__ c1,
+                         float* __restrict__ at) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
+  if (t >= T) return;
+  float a = 0.f, b = 0.f, h = 0.f;
+  if (mask == nullptr || mask[t] != 0) {
+    if (tokens.get(t, V) < 0) atomicOr(status, kStatusBadIdBit);
+    if (grad_logprob != nullptr) a = grad_logprob[t];
+    if (grad_entropy != nullptr) b = grad_entropy[t];
+    if (b != 0.f) h = entropy[t];
+  }
+  c0[t] = -fmaf(b, h, a) * inv_tau;
+  c1[t] = -b * kLn2 * inv_tau;
+  at[t] = a * inv_tau;
+}
+
+unsigned row_blocks(int64_t T) { return static_cast<unsigned>((T + kRowThreads - 1) / kRowThreads); }
+
+// ---------------------------------------------------------------- planning
+// The loss's plan for one pair a row: its areas of T floats (or more) hold the token's logit and the factors
+// of dS, its partials and dS buffer what they hold there.
+bool score_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, bool bf16, Plan* p) {
+  return make_plan(T, d, V, 1, chunk, p, bf16);
+}
+
+// Tile width along d of dW and dH: the one with the least time, by columns (padded ones too) and the measured
+// time per column of each width.  256-wide tiles read the fewest operand bytes per product, so narrower ones
+// (1.23 and 1.3 times the time a column) pay only where 256 pads far more.
+int tile_width(int64_t d) {
+  int best = 256;
+  double least = 1e300;
+  const struct { int bn; double cost; } widths[] = {{256, 1.0}, {192, 1.23}, {128, 1.3}};
+  for (const auto& w : widths) {
+    const double time = static_cast<double>(ceil_div(d, w.bn) * w.bn) * w.cost;
+    if (time < least) {
+      least = time;
+      best = w.bn;
+    }
+  }
+  return best;
+}
+
+// Map of an operand whose contiguous axis is the product's N (H for dW, the W slab for dH), half a tile
+// wide: one 3-D box where the extent allows, 2-D boxes elsewhere; 64-byte swizzle for 96-wide halves.
+bool map_columns(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, int bn, bool* box3d) {
+  const bool narrow = (bn / 2) % 64 != 0;
+  *box3d = narrow ? encode_map_mn3d_sw64(map, base, cols, rows, cols * 2, bn / 2)
+                  : encode_map_mn3d(map, base, cols, rows, cols * 2, bn / 2);
+  if (*box3d) return true;
+  return narrow ? encode_map_bf16_sw64(map, base, cols, rows, cols * 2)
+                : encode_map_bf16(map, base, cols, rows, cols * 2, 64, 64);
+}
+
+fkl_status fused_fail(fkl_status st, const char* msg) {
+  set_last_error_message(msg);
+  return st;
+}
+fkl_status fused_cuda(cudaError_t e) { return fused_fail(FKL_ERR_CUDA, cudaGetErrorString(e)); }
+
+// Destination of a product that is summed over `count` blocks, of which this is number `at`: the caller's
+// fp32 gradient, or fp32 sums in the workspace that the last block rounds to bf16.
+F32Params destination(int64_t rows, int64_t d, int64_t at, int64_t count, float* out32, uint16_t* out16, float* sums,
+                      bool accumulate) {
+  F32Params p;
+  p.ldo = d;
+  p.M = static_cast<int>(rows);
+  p.N = static_cast<int>(d);
+  p.out = out16 == nullptr ? out32 : sums;
+  p.accumulate = at > 0 || (out16 == nullptr && accumulate) ? 1 : 0;
+  p.vec_ok = on_boundary(p.out, 32) && d % 8 == 0 ? 1 : 0;
+  if (out16 != nullptr && at == count - 1) {
+    p.out16 = out16;
+    p.ldo16 = d;
+    p.vec16_ok = on_boundary(out16, 16) ? 1 : 0;
+  }
+  return p;
+}
+
+struct Backward {
+  const uint16_t *H, *W;
+  TokenIds tokens;
+  const float* lse;
+  int64_t T, d, V;
+  float tau;
+  int accumulate;
+  bool bf16;
+  void *dH, *dW;
+  uint8_t* ws;
+  int sms;
+  cudaStream_t st;
+  Plan pl;
+};
+
+// One block: tokens [b Ct, ...) x vocabulary columns [j Vc, ...).
+fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
+  const Plan& pl = c.pl;
+  const int64_t d = c.d, Vc = pl.Vc, r0 = b * pl.Ct, v0 = j * Vc;
+  const int64_t rows = c.T - r0 < pl.Ct ? c.T - r0 : pl.Ct, w = c.V - v0 < Vc ? c.V - v0 : Vc;
+  const uint16_t *Hb = c.H + r0 * d, *Wj = c.W + v0 * d;
+  uint16_t* ds = reinterpret_cast<uint16_t*>(c.ws + pl.off_ds);
+  uint32_t* status = reinterpret_cast<uint32_t*>(c.ws);
+  float* kpart = reinterpret_cast<float*>(c.ws + pl.off_kpart);
+  const int bn = tile_width(d), pairs = c.sms / 2;
+  CUtensorMap h_rows, h_cols, w_rows, w_cols, ds_cols, ds_rows;
+  bool h3d = false, w3d = false;
+  // dS has zeros in the columns [w, round_up(w, 256)) of every row, so its 3-D view may span round_up(w, 64)
+  const bool ds3d = encode_map_mn3d(&ds_cols, ds, ceil_div(w, 64) * 64, rows, Vc * 2, 128);
+  if (!encode_map_bf16(&h_rows, Hb, d, rows, d * 2, 64, 128) || !map_columns(&h_cols, Hb, d, rows, bn, &h3d) ||
+      !encode_map_bf16(&w_rows, Wj, d, w, d * 2, 64, kVocabTile / 2) || !map_columns(&w_cols, Wj, d, w, bn, &w3d) ||
+      (!ds3d && !encode_map_bf16(&ds_cols, ds, w, rows, Vc * 2, 64, 64)) ||
+      !encode_map_bf16(&ds_rows, ds, w, rows, Vc * 2, 64, 128))
+    return fused_fail(FKL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+
+  const int m_tiles = static_cast<int>(ceil_div(rows, 256)), n_tiles = static_cast<int>(ceil_div(w, kVocabTile));
+  GemmShape g = make_shape(rows, w, d, kVocabTile, plan_splits(m_tiles, n_tiles, pairs, group_rows(m_tiles)), status, 256);
+  g.group_m = group_rows(m_tiles);
+  ScoreDsParams p;
+  p.tokens = c.tokens;
+  p.r0 = r0;
+  p.c0 = reinterpret_cast<const float*>(c.ws + pl.off_crow) + r0;
+  p.c1 = reinterpret_cast<const float*>(c.ws + pl.off_wrow) + r0;
+  p.at = reinterpret_cast<const float*>(c.ws + pl.off_arow) + r0;
+  p.lse = c.lse + r0;
+  p.ds = ds;
+  p.ld_ds = Vc;
+  p.T = static_cast<int>(rows);
+  p.V = static_cast<int>(c.V);
+  p.v0 = static_cast<int>(v0);
+  p.slab_w = static_cast<int>(w);
+  p.scale2 = kLog2e / c.tau;
+  cudaError_t e = launch_gemm2_t<kVocabTile, false, false, EpiScoreDs>(h_rows, w_rows, g, p, c.sms, c.st);
+  if (e != cudaSuccess) return fused_cuda(e);
+
+  if (c.dW != nullptr) {  // dW[slab] (+)= dS[block]^T H[block], token blocks in order
+    float* wsum = reinterpret_cast<float*>(c.ws + pl.off_wsum) + (pl.slab_outer ? 0 : v0 * d);
+    GemmShape gw = make_shape(w, d, rows, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
+    gw.a_box3d = ds3d ? 1 : 0;
+    gw.b_box3d = h3d ? 1 : 0;
+    const F32Params pw = destination(w, d, b, pl.nt, static_cast<float*>(c.dW) + (c.bf16 ? 0 : v0 * d),
+                                     c.bf16 ? static_cast<uint16_t*>(c.dW) + v0 * d : nullptr, wsum,
+                                     (c.accumulate & FKL_ACCUMULATE_DW) != 0);
+    plan_ksplit(&gw, pairs, kpart, kKsplitSlots);
+    if ((e = launch_gemm2_f32(bn, true, true, ds_cols, h_cols, gw, pw, c.sms, c.st)) != cudaSuccess ||
+        (e = launch_ksplit_fixup(bn, gw, pw, c.st)) != cudaSuccess)
+      return fused_cuda(e);
+  }
+  if (c.dH == nullptr) return FKL_OK;
+
+  // dH[block] (+)= dS[block] W[slab], slabs in order
+  float* hsum = reinterpret_cast<float*>(c.ws + pl.off_hsum) + (pl.slab_outer ? r0 * d : 0);
+  GemmShape gh = make_shape(rows, d, w, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
+  gh.b_box3d = w3d ? 1 : 0;
+  const F32Params ph = destination(rows, d, j, pl.nslabs, static_cast<float*>(c.dH) + (c.bf16 ? 0 : r0 * d),
+                                   c.bf16 ? static_cast<uint16_t*>(c.dH) + r0 * d : nullptr, hsum,
+                                   (c.accumulate & FKL_ACCUMULATE_DH) != 0);
+  plan_ksplit(&gh, pairs, kpart, kKsplitSlots);
+  if ((e = launch_gemm2_f32(bn, false, true, ds_rows, w_cols, gh, ph, c.sms, c.st)) != cudaSuccess ||
+      (e = launch_ksplit_fixup(bn, gh, ph, c.st)) != cudaSuccess)
+    return fused_cuda(e);
+  return FKL_OK;
+}
+
+// What both directions check.
+fkl_status check_fused(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes, int64_t T,
+                       float tau, const void* ws, size_t ws_bytes, size_t need) {
+  if (!(tau > 0.f) || !std::isfinite(tau)) return fused_fail(FKL_ERR_INVALID_ARG, "tau must be finite and > 0");
+  if (token_bytes != 4 && token_bytes != 8) return fused_fail(FKL_ERR_INVALID_ARG, "token_bytes must be 4 or 8");
+  if (W == nullptr || (T > 0 && (H == nullptr || tokens == nullptr)))
+    return fused_fail(FKL_ERR_INVALID_ARG, "H, W and tokens must not be NULL");
+  if (!on_boundary(H, 16) || !on_boundary(W, 16)) return fused_fail(FKL_ERR_ALIGNMENT, "H and W must be 16-byte aligned");
+  if (!on_boundary(tokens, token_bytes)) return fused_fail(FKL_ERR_ALIGNMENT, "tokens must be aligned to their type");
+  if (ws == nullptr || ws_bytes < need) return fused_fail(FKL_ERR_WORKSPACE, "workspace missing or too small");
+  if (!on_boundary(ws, 256)) return fused_fail(FKL_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  return FKL_OK;
+}
+constexpr char kShapeRule[] = "unsupported shape (need 0 <= T < 2^31, d % 8 == 0, 8 <= d < 2^20, 1 <= V <= 2^30, chunk >= 1)";
+
+// Workspace of the forward: the status, the partials of the splits and the tokens' logits.
+struct ForwardPlan {
+  size_t part, token_s, total;
+};
+bool forward_plan(int64_t T, int64_t d, int64_t V, ForwardPlan* p) {
+  Plan pl;
+  if (!score_plan(T, d, V, 1, false, &pl)) return false;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  p->part = 256;
+  p->token_s = up(p->part + static_cast<size_t>(T) * 3 * kMaxSplit * 4);
+  p->total = up(p->token_s + static_cast<size_t>(T) * 4);
+  return true;
+}
+
+}  // namespace
+}  // namespace fkl
+
+using namespace fkl;
+
+extern "C" size_t fkl_logprob_workspace_size(int64_t T, int64_t d, int64_t V) {
+  ForwardPlan p;
+  return forward_plan(T, d, V, &p) ? p.total : 0;
+}
+
+extern "C" size_t fkl_logprob_backward_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t grad_bf16) {
+  Plan p;
+  return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? p.total : 0;
+}
+
+extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
+                                          const uint8_t* mask, int64_t T, int64_t d, int64_t V, float tau,
+                                          float* logprob, float* entropy, float* lse, void* workspace, size_t ws_bytes,
+                                          void* stream) {
+  set_last_error_message("");
+  ForwardPlan pl;
+  if (!forward_plan(T, d, V, &pl)) return fused_fail(FKL_ERR_INVALID_ARG, kShapeRule);
+  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, pl.total);
+  if (s != FKL_OK) return s;
+  if (T > 0 && (logprob == nullptr || entropy == nullptr || lse == nullptr))
+    return fused_fail(FKL_ERR_INVALID_ARG, "logprob, entropy and lse must not be NULL");
+  if (!on_boundary(logprob, 4) || !on_boundary(entropy, 4) || !on_boundary(lse, 4))
+    return fused_fail(FKL_ERR_ALIGNMENT, "logprob, entropy and lse must be 4-byte aligned");
+  int sms = 0;
+  if (const int e = require_device(&sms); e != FKL_OK) return static_cast<fkl_status>(e);
+  const NamedPtr ptrs[] = {{H, "H"}, {W, "W"}, {tokens, "tokens"}, {mask, "mask"}, {logprob, "logprob"},
+                           {entropy, "entropy"}, {lse, "lse"}, {workspace, "workspace"}};
+  if (const int e = check_device_memory(ptrs); e != FKL_OK) return static_cast<fkl_status>(e);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  if (e != cudaSuccess) return fused_cuda(e);
+  if (T == 0) return FKL_OK;
+  CUtensorMap mH, mW;
+  if (!encode_map_bf16(&mH, H, d, T, d * 2, 64, 128) || !encode_map_bf16(&mW, W, d, V, d * 2, 64, kVocabTile / 2))
+    return fused_fail(FKL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  const int m_tiles = static_cast<int>(ceil_div(T, 256)), n_tiles = static_cast<int>(ceil_div(V, kVocabTile));
+  GemmShape g = make_shape(T, V, d, kVocabTile, dynamic_splits(m_tiles, n_tiles, sms / 2), &hdr->status, 256);
+  g.group_m = fwd_group_rows(m_tiles, sms / 2);
+  g.sched = &hdr->items_taken;
+  ScoreFwdParams p;
+  p.tokens = TokenIds{tokens, token_bytes};
+  p.mask = mask;
+  p.part = reinterpret_cast<float*>(ws + pl.part);
+  p.token_s = reinterpret_cast<float*>(ws + pl.token_s);
+  p.T = static_cast<int>(T);
+  p.V = static_cast<int>(V);
+  p.nsplit = g.nsplit;
+  p.scale2 = kLog2e / tau;
+  if ((e = launch_gemm2_t<kVocabTile, false, false, EpiScore>(mH, mW, g, p, sms, st)) != cudaSuccess) return fused_cuda(e);
+  score_rows_kernel<<<row_blocks(T), kRowThreads, 0, st>>>(p.part, p.nsplit, p.token_s, p.tokens, mask, T, p.V, 1.f / tau,
+                                                           &hdr->status, logprob, entropy, lse);
+  if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
+  return FKL_OK;
+}
+
+extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
+                                           const uint8_t* mask, const float* lse, const float* entropy,
+                                           const float* grad_logprob, const float* grad_entropy, int64_t T, int64_t d,
+                                           int64_t V, float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate,
+                                           void* dH, void* dW, void* workspace, size_t ws_bytes, void* stream) {
+  set_last_error_message("");
+  if (grad_bf16 != 0 && grad_bf16 != 1) return fused_fail(FKL_ERR_INVALID_ARG, "grad_bf16 must be 0 or 1");
+  Backward c{H, W, TokenIds{tokens, token_bytes}, lse, T, d, V, tau, accumulate, grad_bf16 == 1, dH, dW,
+             static_cast<uint8_t*>(workspace), 0, static_cast<cudaStream_t>(stream), Plan{}};
+  if (!score_plan(T, d, V, chunk, c.bf16, &c.pl)) return fused_fail(FKL_ERR_INVALID_ARG, kShapeRule);
+  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, c.pl.total);
+  if (s != FKL_OK) return s;
+  if (accumulate < 0 || accumulate > 3) return fused_fail(FKL_ERR_INVALID_ARG, "bad accumulate");
+  if (c.bf16 && accumulate != 0) return fused_fail(FKL_ERR_INVALID_ARG, "bf16 gradients do not accumulate");
+  if ((dW == nullptr && dH == nullptr) || (T > 0 && (lse == nullptr || entropy == nullptr)))
+    return fused_fail(FKL_ERR_INVALID_ARG, "lse, entropy and one of dH and dW must not be NULL");
+  if (!on_boundary(dH, 16) || !on_boundary(dW, 16)) return fused_fail(FKL_ERR_ALIGNMENT, "dH and dW must be 16-byte aligned");
+  if (!on_boundary(lse, 4) || !on_boundary(entropy, 4) || !on_boundary(grad_logprob, 4) || !on_boundary(grad_entropy, 4))
+    return fused_fail(FKL_ERR_ALIGNMENT, "lse, entropy and the gradients must be 4-byte aligned");
+  if (const int e = require_device(&c.sms); e != FKL_OK) return static_cast<fkl_status>(e);
+  const NamedPtr ptrs[] = {{H, "H"}, {W, "W"}, {tokens, "tokens"}, {mask, "mask"}, {lse, "lse"}, {entropy, "entropy"},
+                           {grad_logprob, "grad_logprob"}, {grad_entropy, "grad_entropy"}, {dH, "dH"}, {dW, "dW"},
+                           {workspace, "workspace"}};
+  if (const int e = check_device_memory(ptrs); e != FKL_OK) return static_cast<fkl_status>(e);
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(c.ws);
+  cudaError_t e = cudaMemsetAsync(c.ws, 0, 256, c.st);
+  if (e != cudaSuccess) return fused_cuda(e);
+  if (T == 0) {
+    if (dW != nullptr && !(accumulate & FKL_ACCUMULATE_DW) &&
+        (e = cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * d * (c.bf16 ? 2 : 4), c.st)) != cudaSuccess)
+      return fused_cuda(e);
+    return FKL_OK;
+  }
+  choose_slab_width(&c.pl, c.sms / 2);
+  score_factors_kernel<<<row_blocks(T), kRowThreads, 0, c.st>>>(
+      c.tokens, mask, entropy, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau, &hdr->status,
+      reinterpret_cast<float*>(c.ws + c.pl.off_crow), reinterpret_cast<float*>(c.ws + c.pl.off_wrow),
+      reinterpret_cast<float*>(c.ws + c.pl.off_arow));
+  if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
+  const Plan& pl = c.pl;
+  for (int64_t o = 0; o < (pl.slab_outer ? pl.nslabs : pl.nt); ++o)
+    for (int64_t i = 0; i < (pl.slab_outer ? pl.nt : pl.nslabs); ++i)
+      if ((s = score_block(c, pl.slab_outer ? i : o, pl.slab_outer ? o : i)) != FKL_OK) return s;
+  const int64_t nh = dH != nullptr ? T * d : 0, nw = dW != nullptr ? V * d : 0;
+  e = c.bf16 ? launch_poison16(static_cast<uint16_t*>(dH), nh, static_cast<uint16_t*>(dW), nw, &hdr->status, c.sms, c.st)
+             : launch_poison(static_cast<float*>(dH), nh, static_cast<float*>(dW), nw, &hdr->status, c.sms, c.st);
+  if (e != cudaSuccess) return fused_cuda(e);
+  return FKL_OK;
+}

@@ -1,0 +1,270 @@
+"""Scoring: log-probabilities of given tokens, entropies and alternatives (C ABI in include/fkl_score.h).
+
+Text that was drawn (``sample``, ``draw_token``) is scored from logits in memory,
+
+    r = token_logprobs(logits, tokens, temperature=0.8, top_n=20)
+    r.logprob, r.entropy, r.top_ids, r.top_logprobs
+
+or straight from hidden states and the LM head, whose logits are never written,
+
+    logprob, entropy = fused_logprobs(H, W, tokens, mask)
+
+Both are differentiable (``logprob`` and ``entropy``; in the logits, or in H and W), for a policy
+gradient, a cross-entropy or an entropy bonus on the drawn text:
+
+    loss = -(advantage * logprob).sum() / n - 0.01 * entropy.sum() / n
+    loss.backward()
+
+``logprob_forward`` and ``logprob_backward`` are the explicit calls of the fused form.  Inputs are on the
+current device, and calls run on its current stream.  A call without a ``workspace`` takes its scratch from
+PyTorch's allocator for as long as it runs, so calls of several threads, streams and captured graphs share none.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional, Tuple, Union
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from ._lib import FKL_ACCUMULATE_DH, FKL_ACCUMULATE_DW, FklError, check, lib
+from .generate import _dtype, _rows, _stream, _vector
+
+__all__ = ["TokenLogprobs", "token_logprobs", "fused_logprobs", "logprob_forward", "logprob_backward"]
+
+_TOKEN_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``token_logprobs`` returns; the last two are None without alternatives (top_n = 0)."""
+
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    top_ids: Optional[torch.Tensor]
+    top_logprobs: Optional[torch.Tensor]
+
+
+def _tokens(tokens: torch.Tensor, n: int, device) -> int:
+    """Bytes of a token id, of checked tokens."""
+    size = _TOKEN_BYTES.get(tokens.dtype)
+    if size is None or tokens.shape != (n,) or tokens.device != device or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous int32 or int64 tensor of shape [{n}] on {device}")
+    return size
+
+
+def _mask(mask: Optional[torch.Tensor], n: int, device) -> Optional[torch.Tensor]:
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.uint8, torch.bool) or mask.shape != (n,) or mask.device != device:
+        raise ValueError(f"mask must be a uint8 or bool tensor of shape [{n}] on {device}")
+    return mask.contiguous()
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _temperature(temperature, n: int, device):
+    """(number, address of the rows' values or None)."""
+    if isinstance(temperature, torch.Tensor):
+        return 1.0, _vector(temperature, "temperature", torch.float32, n, device)
+    return float(temperature), None
+
+
+# ---------------------------------------------------------------- logits in memory
+def _score(logits, tokens, temperature, top_n, mask, want_stats):
+    B, V, ld = _rows(logits, "logits")
+    kind = _dtype(logits.dtype, "logits")
+    device = logits.device
+    size = _tokens(tokens, B, device)
+    mask = _mask(mask, B, device)
+    number, per_row = _temperature(temperature, B, device)
+    logprob = torch.empty(B, dtype=torch.float32, device=device)
+    entropy = torch.empty(B, dtype=torch.float32, device=device)
+    stats = torch.empty((B, 2), dtype=torch.float32, device=device) if want_stats else None
+    ids = logs = None
+    if top_n > 0:
+        ids = torch.empty((B, top_n), dtype=torch.int32, device=device)
+        logs = torch.empty((B, top_n), dtype=torch.float32, device=device)
+    st = lib().fkl_token_logprobs(logits.data_ptr(), kind, B, V, ld, tokens.data_ptr(), size, _address(mask), number,
+                                  per_row, top_n, logprob.data_ptr(), entropy.data_ptr(), _address(stats),
+                                  _address(ids), _address(logs), _stream(device))
+    check(st, "fkl_token_logprobs")
+    return logprob, entropy, ids, logs, stats
+
+
+def _grad_like(logits: torch.Tensor) -> torch.Tensor:
+    """A tensor for the logits' gradient whose rows lie in 16-byte vectors as the logits' do, where they can."""
+    B, V = logits.shape
+    unit = 16 // logits.element_size()
+    if V % unit and B > 1 and logits.stride(0) % unit == 0:
+        wide = torch.empty((B, (V + unit - 1) // unit * unit), dtype=logits.dtype, device=logits.device)
+        return wide[:, :V]
+    return torch.empty((B, V), dtype=logits.dtype, device=logits.device)
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature, top_n, mask):
+        logprob, entropy, ids, logs, stats = _score(logits, tokens, temperature, top_n, mask, True)
+        rows = temperature if isinstance(temperature, torch.Tensor) else None
+        ctx.save_for_backward(logits, tokens, entropy, stats, mask, rows)
+        ctx.number = 1.0 if rows is not None else float(temperature)
+        ctx.set_materialize_grads(False)
+        if ids is not None:
+            ctx.mark_non_differentiable(ids, logs)
+        return logprob, entropy, ids, logs
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_logprob, grad_entropy, _ids, _logs):
+        logits, tokens, entropy, stats, mask, rows = ctx.saved_tensors
+        if grad_logprob is None and grad_entropy is None:
+            return None, None, None, None, None
+        B, V, ld = _rows(logits, "logits")
+        mask = _mask(mask, B, logits.device)
+        out = _grad_like(logits)
+        if grad_logprob is not None:
+            grad_logprob = grad_logprob.contiguous()
+        if grad_entropy is not None:
+            grad_entropy = grad_entropy.contiguous()
+        st = lib().fkl_token_logprobs_backward(
+            logits.data_ptr(), _dtype(logits.dtype, "logits"), B, V, ld, tokens.data_ptr(), _TOKEN_BYTES[tokens.dtype],
+            _address(mask), ctx.number, _address(rows), stats.data_ptr(), entropy.data_ptr(), _address(grad_logprob),
+            _address(grad_entropy), out.data_ptr(), out.stride(0) if B > 1 else V, _stream(logits.device))
+        check(st, "fkl_token_logprobs_backward")
+        return out, None, None, None, None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: Union[float, torch.Tensor] = 1.0,
+                   top_n: int = 0, mask: Optional[torch.Tensor] = None) -> TokenLogprobs:
+    """Scores ``tokens`` [B] (int32 or int64) under softmax(logits / temperature), logits [B, V] (float32,
+    bfloat16 or float16; rows any stride apart): the tokens' log-probability and the distribution's entropy
+    (float32 [B], differentiable in the logits) and the ``top_n`` (at most 128) likeliest ids, int32 and
+    float32 [B, top_n], likeliest first, ties by the lower id.
+
+    ``temperature`` is one number or a float32 tensor [B].  ``mask`` (uint8 or bool [B]) leaves rows out: log-probability,
+    entropy and gradient 0, ids -1.  -inf bans an id, NaN counts as -inf, +inf ids share all the
+    probability.  A token outside [0, V) in another row gives NaN, in its log-probability and its row of
+    the gradient; so does a row without any logit, and a temperature in a tensor that is not finite and above 0."""
+    if not 0 <= top_n <= 128:
+        raise ValueError("top_n must be between 0 and 128")
+    if logits.requires_grad and torch.is_grad_enabled():
+        return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, top_n, mask))
+    return TokenLogprobs(*_score(logits, tokens, temperature, top_n, mask, False)[:4])
+
+
+# ---------------------------------------------------------------- hidden states and head
+def _operands(H, W, tokens, mask):
+    if not (H.is_cuda and W.is_cuda) or H.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise TypeError("H and W must be bfloat16 CUDA tensors")
+    if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1] or not (H.is_contiguous() and W.is_contiguous()):
+        raise ValueError("H must be [T, d] and W [V, d], contiguous")
+    if W.device != H.device:
+        raise ValueError("H and W must be on one device")
+    T = H.shape[0]
+    return _tokens(tokens, T, H.device), _mask(mask, T, H.device)
+
+
+def _scratch(workspace, nbytes: int, device) -> torch.Tensor:
+    return workspace.get(nbytes, device) if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _floats(t: Optional[torch.Tensor], name: str, T: int, device) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.shape != (T,) or t.device != device:
+        raise ValueError(f"{name} must be a float32 tensor of shape [{T}] on {device}")
+    return t.detach().contiguous()
+
+
+def logprob_forward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                    tau: float = 1.0, workspace=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(logprob, entropy, lse), float32 [T], of ``tokens`` [T] under softmax(H W^T / tau); lse is that of every row,
+    the masked ones included, and belongs to the backward.  A wait of the product that runs out makes them NaN, as a token
+    outside [0, V) does in its row; ``read_status(workspace)`` tells."""
+    size, mask = _operands(H, W, tokens, mask)
+    (T, d), V, device = H.shape, W.shape[0], H.device
+    n = lib().fkl_logprob_workspace_size(T, d, V)
+    if n == 0:
+        raise FklError(1, "fkl_logprob_workspace_size", f"unsupported shape T={T} d={d} V={V}")
+    ws = _scratch(workspace, int(n), device)
+    out = [torch.empty(T, dtype=torch.float32, device=device) for _ in range(3)]
+    st = lib().fkl_logprob_forward(H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), T, d, V,
+                                   float(tau), *(t.data_ptr() for t in out), ws.data_ptr(), ws.numel(), _stream(device))
+    check(st, "fkl_logprob_forward")
+    return tuple(out)
+
+
+def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor],
+                     lse: torch.Tensor, entropy: torch.Tensor, grad_logprob: Optional[torch.Tensor] = None,
+                     grad_entropy: Optional[torch.Tensor] = None, tau: float = 1.0, chunk: int = 2048, workspace=None,
+                     out: Optional[Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]] = None,
+                     accumulate: bool = False, grad_dtype: torch.dtype = torch.float32,
+                     ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """dH [T, d] and dW [V, d], the gradient of sum(grad_logprob * logprob + grad_entropy * entropy) (float32 [T]
+    each; None = 0), in float32 or, with ``grad_dtype=torch.bfloat16``, in bfloat16 (fp32 sums rounded once).
+
+    ``lse`` and ``entropy`` are the forward's; ``chunk`` bounds the buffer of the logits' gradient as in
+    ``backward``.  ``out`` gives the tensors to write, one of them None if it is not wanted (a frozen head:
+    ``(dH, None)``); ``accumulate=True`` adds into them (float32)."""
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("grad_dtype must be torch.float32 or torch.bfloat16")
+    bf16 = grad_dtype == torch.bfloat16
+    if accumulate and (bf16 or out is None):
+        raise ValueError("accumulate=True adds into float32 gradients given in `out`")
+    size, mask = _operands(H, W, tokens, mask)
+    (T, d), V, device = H.shape, W.shape[0], H.device
+    lse, entropy = _floats(lse, "lse", T, device), _floats(entropy, "entropy", T, device)
+    grad_logprob = _floats(grad_logprob, "grad_logprob", T, device)
+    grad_entropy = _floats(grad_entropy, "grad_entropy", T, device)
+    if out is None:
+        out = tuple(torch.empty(t.shape, dtype=grad_dtype, device=device) for t in (H, W))
+    for g, t in zip(out, (H, W)):
+        if g is not None and (g.dtype != grad_dtype or g.shape != t.shape or not g.is_contiguous() or g.device != device):
+            raise ValueError(f"out gradients must be contiguous {grad_dtype} {tuple(t.shape)} on {device}")
+    n = lib().fkl_logprob_backward_workspace_size(T, d, V, chunk, int(bf16))
+    if n == 0:
+        raise FklError(1, "fkl_logprob_backward_workspace_size", f"unsupported shape T={T} d={d} V={V} chunk={chunk}")
+    ws = _scratch(workspace, int(n), device)
+    flags = (FKL_ACCUMULATE_DH | FKL_ACCUMULATE_DW) if accumulate else 0
+    st = lib().fkl_logprob_backward(
+        H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), lse.data_ptr(), entropy.data_ptr(),
+        _address(grad_logprob), _address(grad_entropy), T, d, V, float(tau), chunk, int(bf16), flags, _address(out[0]),
+        _address(out[1]), ws.data_ptr(), ws.numel(), _stream(device))
+    check(st, "fkl_logprob_backward")
+    return out
+
+
+class _FusedLogprobs(torch.autograd.Function):
+    """Saves lse and the entropies; the backward recomputes the projection block by block."""
+
+    @staticmethod
+    def forward(ctx, H, W, tokens, mask, tau, chunk):
+        logprob, entropy, lse = logprob_forward(H, W, tokens, mask, tau)
+        ctx.save_for_backward(H, W, tokens, mask, lse, entropy)
+        ctx.tau, ctx.chunk = tau, chunk
+        ctx.set_materialize_grads(False)
+        return logprob, entropy
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_logprob, grad_entropy):
+        H, W, tokens, mask, lse, entropy = ctx.saved_tensors
+        if grad_logprob is None and grad_entropy is None:
+            return None, None, None, None, None, None
+        out = tuple(torch.empty_like(t) if need else None for t, need in zip((H, W), ctx.needs_input_grad))
+        dH, dW = logprob_backward(H, W, tokens, mask, lse, entropy, grad_logprob, grad_entropy, ctx.tau, ctx.chunk,
+                                  out=out, grad_dtype=torch.bfloat16)
+        return dH, dW, None, None, None, None
+
+
+def fused_logprobs(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                   tau: float = 1.0, chunk: int = 2048) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(logprob, entropy), float32 [T], of ``tokens`` [T] (int32 or int64) under softmax(H W^T / tau) for hidden
+    states H [T, d] and LM head W [V, d] (bfloat16), without the [T, V] logits in memory; differentiable in H and W.
+
+    ``mask`` (uint8 or bool [T]) leaves tokens out: log-probability, entropy and gradient 0.  A token outside [0, V) in another row
+    gives NaN there, and NaN gradients.  ``chunk`` bounds the backward's buffer as in ``fused_kl``."""
+    if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
+        return _FusedLogprobs.apply(H, W, tokens, mask, tau, chunk)
+    return logprob_forward(H, W, tokens, mask, tau)[:2]

@@ -1,0 +1,266 @@
+"""Scores and gradients from hidden states and the LM head (fused_logprobs) against the float64 oracle.
+
+Tolerances.  The tensor cores add products in fp32, 16 deep: each step loses at most 2^-23 of the partial sum, which
+is below sum |h w|, so a logit is off by s_tol = (d / 16 + 2) 2^-22 max sum |h w|, and log q by twice that over tau
+and the sums' error (2^-20).  dS is rounded to bf16 (half a step: 2^-8), its products are summed in fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import score as oracle
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fkl(cuda_device):
+    from lm_head_top_tcgen05_gb300 import build
+
+    build.build()
+    import lm_head_top_tcgen05_gb300 as m
+
+    return m
+
+
+def make(T, d, V, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    W = torch.randn(V, d, generator=g) / d ** 0.5
+    tok = torch.randint(0, V, (T,), generator=g)
+    H = torch.randn(T, d, generator=g) * 1.5 + 6 * torch.rand(T, 1, generator=g) * W[tok]
+    return H.bfloat16().cuda(), W.bfloat16().cuda(), tok.cuda(), (torch.rand(T, generator=g) > 0.2).cuda()
+
+
+class Exact:
+    def __init__(self, H, W, tok, mask, tau):
+        self.H, self.W = H.float().cpu().double().numpy(), W.float().cpu().double().numpy()
+        self.tok, self.tau = tok.cpu().numpy(), float(np.float32(tau))
+        self.keep = None if mask is None else mask.cpu().numpy().astype(bool)
+        T, d = self.H.shape
+        self.x = self.H @ self.W.T
+        self.lp, self.ent, self.logq, self.q = oracle.score(self.x, self.tok, self.tau, self.keep)
+        size = (np.abs(self.H) @ np.abs(self.W).T).max() if T else 0.0
+        self.log_tol = 2 * (d / 16 + 2) * 2.0 ** -22 * size / self.tau + 2.0 ** -20 * (2 + np.log(W.shape[0] + 1))
+
+    def check_scores(self, lp, ent):
+        lp, ent = lp.cpu().double().numpy(), ent.cpu().double().numpy()
+        ok = np.isfinite(self.lp)
+        assert (np.isnan(lp) == np.isnan(self.lp)).all() and (np.isnan(ent) == np.isnan(self.ent)).all()
+        assert (np.abs(lp - self.lp)[ok] <= self.log_tol + 2.0 ** -22 * np.abs(self.lp[ok])).all()
+        ok = np.isfinite(self.ent)
+        # entropy = E[-log q]: log q's error, and that of the weights, relative, times the spread of log q
+        spread = 1 + self.ent[ok] + np.log(self.q.shape[1] + 1)
+        assert (np.abs(ent - self.ent)[ok] <= self.log_tol * (1 + spread)).all()
+
+    def check_gradients(self, dH, dW, a, b, bf16, base=(0.0, 0.0)):
+        a, b = a.cpu().double().numpy(), b.cpu().double().numpy()
+        dS = oracle.score_gradient(self.logq, self.q, self.ent, self.tok, a, b, self.tau, self.keep)
+        keep = np.ones(len(a), bool) if self.keep is None else self.keep
+        lq = np.where(self.q > 0, np.abs(np.nan_to_num(self.logq)), 0)
+        terms = (np.abs(a)[:, None] + np.abs(b)[:, None] * (lq + np.nan_to_num(self.ent)[:, None] + 1)) / self.tau
+        off = np.where(keep[:, None], np.nan_to_num(self.q) * terms * 4 * self.log_tol, 0) + 2.0 ** -8 * np.abs(dS)
+        for got, want, room, start in ((dH, dS @ self.W, (off + 2.0 ** -18 * np.abs(dS)) @ np.abs(self.W), base[0]),
+                                       (dW, dS.T @ self.H, (off + 2.0 ** -18 * np.abs(dS)).T @ np.abs(self.H), base[1])):
+            if got is None:
+                continue
+            got = got.float().cpu().double().numpy()
+            want = want + start
+            lim = room + (2.0 ** -8 if bf16 else 2.0 ** -22) * np.abs(want) + 1e-30
+            assert (np.abs(got - want) <= lim).all(), (np.abs(got - want) / lim).max()
+
+
+@pytest.mark.parametrize("T,d,V,tau", [(1, 8, 1, 1.0), (1, 64, 300, 0.5), (3, 8, 17, 2.0), (130, 64, 257, 1.0),
+                                       (257, 72, 1000, 0.8), (300, 128, 4099, 1.0), (64, 256, 30011, 1.3),
+                                       (700, 40, 513, 1.0), (0, 16, 50, 1.0)])
+def test_scores_and_gradients(fkl, T, d, V, tau):
+    H, W, tok, mask = make(T, d, V, seed=T + V)
+    for m, ids in ((None, tok), (mask, tok.int())):
+        e = Exact(H, W, tok, m, tau)
+        Hl, Wl = H.clone().requires_grad_(), W.clone().requires_grad_()
+        lp, ent = fkl.fused_logprobs(Hl, Wl, ids, m, tau=tau, chunk=128)
+        e.check_scores(lp.detach(), ent.detach())
+        a, b = torch.randn(T).cuda(), torch.randn(T).cuda() * 0.3
+        dH, dW = torch.autograd.grad((lp, ent), (Hl, Wl), (a, b))
+        assert dH.dtype == dW.dtype == torch.bfloat16
+        e.check_gradients(dH, dW, a, b, True)
+
+
+def test_explicit_calls(fkl):
+    """fp32 gradients, accumulation, one gradient alone, chunks of every size, a workspace that is kept."""
+    T, d, V, tau = 520, 96, 3001, 0.9
+    H, W, tok, mask = make(T, d, V, seed=1)
+    e = Exact(H, W, tok, mask, tau)
+    ws = fkl.Workspace()
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, mask, tau, workspace=ws)
+    e.check_scores(lp, ent)
+    want = torch.logsumexp(torch.tensor(e.x) / tau, 1)
+    assert (lse.cpu().double() - want).abs().max() <= e.log_tol + 2.0 ** -22 * want.abs().max()
+    a, b = torch.randn(T).cuda(), torch.randn(T).cuda()
+    first = None
+    for chunk in (1, 64, 2048, 10 ** 6):
+        dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, chunk, workspace=ws)
+        e.check_gradients(dH, dW, a, b, False)
+        if chunk == 2048:
+            first = dH, dW
+    again = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 2048)
+    assert all(torch.equal(x, y) for x, y in zip(first, again))  # the same bits
+    half = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 2048, grad_dtype=torch.bfloat16)
+    assert all(torch.equal(x.bfloat16(), y) for x, y in zip(first, half))  # fp32 sums rounded once
+    base = torch.randn(T, d).cuda(), torch.randn(V, d).cuda()
+    out = base[0].clone(), base[1].clone()
+    fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 512, out=out, accumulate=True)
+    e.check_gradients(*out, a, b, False, base=tuple(x.cpu().double().numpy() for x in base))
+    for only in (0, 1):
+        out = [torch.full((T, d), 7.0).cuda(), torch.full((V, d), 7.0).cuda()]
+        out[1 - only] = None
+        got = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 2048, out=tuple(out))
+        assert torch.equal(got[only], first[only]) and got[1 - only] is None
+    dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, None, tau)
+    e.check_gradients(dH, dW, a, torch.zeros(T), False)
+    dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, None, b, tau)
+    e.check_gradients(dH, dW, torch.zeros(T), b, False)
+    assert fkl.read_status(ws) == 0
+
+
+def test_frozen_head_and_frozen_states(fkl):
+    H, W, tok, _ = make(90, 64, 700, seed=3)
+    Hl, Wl = H.clone().requires_grad_(), W.clone().requires_grad_()
+    lp, ent = fkl.fused_logprobs(Hl, Wl, tok)
+    both = torch.autograd.grad(lp.sum() + ent.mean(), (Hl, Wl))
+    lp, ent = fkl.fused_logprobs(Hl, W, tok)
+    (lp.sum() + ent.mean()).backward()
+    assert torch.equal(Hl.grad, both[0])
+    lp, ent = fkl.fused_logprobs(H, Wl, tok)
+    (lp.sum() + ent.mean()).backward()
+    assert torch.equal(Wl.grad, both[1])
+    lp, ent = fkl.fused_logprobs(H, Wl, tok)
+    assert torch.autograd.grad(lp.sum(), Wl)[0].shape == W.shape  # entropy unused
+
+
+def test_several_token_blocks(fkl):
+    """A long batch against a small vocabulary: the backward takes several token blocks, in either loop order."""
+    T, d, V = 9000, 64, 900
+    H, W, tok, mask = make(T, d, V, seed=5)
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, mask)
+    e = Exact(H, W, tok, mask, 1.0)
+    e.check_scores(lp, ent)
+    a, b = torch.randn(T).cuda() / 30, torch.randn(T).cuda() / 90
+    for dtype in (torch.float32, torch.bfloat16):
+        for chunk in (100, 4096):
+            dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, chunk=chunk, grad_dtype=dtype)
+            e.check_gradients(dH, dW, a, b, dtype == torch.bfloat16)
+
+
+def test_sharp_rows(fkl):
+    """Logits far above the rest: the reference moves, probabilities underflow."""
+    H, W, tok, _ = make(200, 128, 5000, seed=9)
+    H = (H.float() * 3).bfloat16()
+    e = Exact(H, W, tok, None, 0.5)
+    lp, ent = fkl.fused_logprobs(H, W, tok, tau=0.5)
+    e.check_scores(lp, ent)
+
+
+def test_tokens_outside_and_rows_left_out(fkl):
+    H, W, tok, _ = make(300, 64, 500, seed=4)
+    tok[7], tok[8] = -1, 500
+    ws = fkl.Workspace()
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, workspace=ws)
+    assert fkl.read_status(ws) == 6
+    assert torch.isnan(lp[7:9]).all() and torch.isfinite(lp[:7]).all() and torch.isfinite(lp[9:]).all()
+    assert torch.isfinite(ent).all()
+    one = torch.ones(300).cuda()
+    dH, dW = fkl.logprob_backward(H, W, tok, None, lse, ent, one, None, workspace=ws)
+    assert fkl.read_status(ws) == 6 and torch.isnan(dH).all() and torch.isnan(dW).all()
+    mask = torch.ones(300, dtype=torch.uint8).cuda()
+    mask[7:9] = 0
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, mask, workspace=ws)
+    assert fkl.read_status(ws) == 0 and (lp[7:9] == 0).all() and (ent[7:9] == 0).all()
+    dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, one, one, workspace=ws)
+    assert fkl.read_status(ws) == 0 and (dH[7:9] == 0).all() and torch.isfinite(dW).all()
+    none = torch.zeros(300, dtype=torch.bool).cuda()
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, none)
+    dH, dW = fkl.logprob_backward(H, W, tok, none, lse, ent, one, one)
+    assert (lp == 0).all() and (ent == 0).all() and (dH == 0).all() and (dW == 0).all()
+
+
+def test_refusals(fkl):
+    H, W, tok, mask = make(20, 64, 100)
+    with pytest.raises(TypeError):
+        fkl.fused_logprobs(H.float(), W, tok)
+    with pytest.raises(ValueError):
+        fkl.fused_logprobs(H, W[:, :32], tok)
+    with pytest.raises(ValueError):
+        fkl.fused_logprobs(H, W, tok[:5])
+    with pytest.raises(ValueError):
+        fkl.fused_logprobs(H, W, tok, mask[:5])
+    with pytest.raises(fkl.FklError):
+        fkl.fused_logprobs(H, W, tok, tau=0.0)
+    with pytest.raises(fkl.FklError):
+        fkl.fused_logprobs(H[:, :12].contiguous(), W[:, :12].contiguous(), tok)
+    lp, ent, lse = fkl.logprob_forward(H, W, tok)
+    with pytest.raises(ValueError):
+        fkl.logprob_backward(H, W, tok, None, lse[:3], ent)
+    with pytest.raises(ValueError):
+        fkl.logprob_backward(H, W, tok, None, lse, ent, ent.double())
+    with pytest.raises(fkl.FklError):
+        fkl.logprob_backward(H, W, tok, None, lse, ent, ent, chunk=0)
+    with pytest.raises(fkl.FklError):
+        fkl.logprob_backward(H, W, tok, None, lse, ent, ent, out=(None, None))
+
+
+def test_another_stream_and_a_graph(fkl):
+    H, W, tok, mask = make(300, 64, 2000, seed=6)
+    want = fkl.fused_logprobs(H, W, tok, mask)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = fkl.fused_logprobs(H, W, tok, mask)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    a, b = torch.randn(300).cuda(), torch.randn(300).cuda()
+    h = H.clone()
+
+    def step(h):
+        lp, ent, lse = fkl.logprob_forward(h, W, tok, mask)
+        return (lp, ent) + fkl.logprob_backward(h, W, tok, mask, lse, ent, a, b, grad_dtype=torch.bfloat16)
+
+    step(h)  # one eager call of the shape, as for the loss
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = []
+    for g in graphs:  # two graphs share no scratch
+        with torch.cuda.graph(g):
+            outs.append(step(h))
+    for seed in (1, 2):
+        h.copy_(make(300, 64, 2000, seed=seed)[0])
+        for g in graphs:
+            g.replay()
+        eager = step(h)
+        for o in outs:
+            assert all(torch.equal(x, y) for x, y in zip(o, eager))
+
+
+# ---------------------------------------------------------------- together
+def test_draw_score_and_train(fkl):
+    """What a server and an on-policy step do: draw through an 8-bit head, score from its logits, then a policy gradient
+    from the hidden states whose scores agree with the logits'."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    T, d, V = 256, 128, 4000
+    H = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    W = (torch.randn(V, d, generator=g, device="cuda") * 0.2).bfloat16()
+    wq, ws = fkl.quantize_int8(W)
+    logits = torch.empty(T, V, device="cuda")
+    token, drawn = fkl.draw_token(H, wq, ws, torch.rand(T, generator=g, device="cuda"), temperature=0.8, logits=logits)
+    r = fkl.token_logprobs(logits, token, temperature=0.8, top_n=5)
+    # without filters the sampler's log-probability is the scored one: whole weights of 2^-40 and fp32 sums
+    assert (r.logprob - drawn).abs().max() < 2.0 ** -24 * 64 + 2 * (2.0 ** -22 + 32 * 2.0 ** -23 + 44 * 2.0 ** -24)
+    assert (r.top_logprobs[:, 0] >= r.logprob).all()
+    Hl, Wl = H.clone().requires_grad_(), W.clone().requires_grad_()
+    lp, ent = fkl.fused_logprobs(Hl, Wl, token, tau=0.8)
+    x = H.float() @ W.float().t()
+    full = fkl.token_logprobs(x, token, temperature=0.8)
+    e = Exact(H, W, token.long(), None, 0.8)
+    e.check_scores(lp.detach(), ent.detach())
+    assert (full.logprob - lp.detach()).abs().max() < 2 * e.log_tol + 2.0 ** -22 * 20
+    adv = torch.randn(T, generator=g, device="cuda")
+    (-(adv * lp).mean() - 0.01 * ent.mean()).backward()
+    e.check_gradients(Hl.grad, Wl.grad, -adv / T, torch.full((T,), -0.01 / T), True)
