@@ -1,10 +1,15 @@
 // The teacher cache in few bits: fkl_cache_pack and fkl_cache_unpack (format in include/fkl_cache.h).
 //
-// A warp per row, a lane per slot of the 32 that share a scale: the group's largest and smallest logit are
-// warp reductions, and a part's words are put together from the lanes by shuffles.  Both directions read and
-// write each byte once; HBM bounds them.
+// A thread per group of 32 slots: it has the group's logits in registers, so largest, smallest and codes are
+// its own, and it puts words together bit by bit, at positions that are the same in every thread of the warp.  Rows
+// pass through shared memory, the slots of a group 36 words from the next group's: four words at a time, eight
+// threads that walk their groups together then touch all 32 banks once.  A block's rows, and its records, are
+// one stretch of memory each, moved 16 bytes a thread where K and the pointers allow it, else 4.
+// A lane per slot, with warp reductions for a group's range and shuffles to assemble words, was the first form: 250
+// instructions to 32 slots against about 30 here, and the instructions were what it took its time for.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/fkl_cache.h"
 #include "fkl_generate.cuh"
@@ -15,10 +20,12 @@ namespace {
 constexpr int kGroup = 32;        // slots that share a scale
 constexpr int kMaxK = 1024;
 constexpr float kSpan = 4096.f;   // a logit further below its row's largest is stored as -inf
-constexpr int kWarps = 8;
+constexpr int kThreads = 128;     // groups of a block's rows (one row at least: up to 32 groups)
+constexpr int kStride = kGroup + 4;
 
 struct Format {
   int K, V, bits, id_bits, groups, code_words, id_words, words;
+  int rows;  // of a block: kThreads groups, and records that fit their slots' shared memory
 };
 
 bool make_format(int64_t K, int64_t V, int32_t bits, Format* f) {
@@ -32,122 +39,277 @@ bool make_format(int64_t K, int64_t V, int32_t bits, Format* f) {
   f->code_words = static_cast<int>((K * bits + 31) / 32);
   f->id_words = static_cast<int>((K * f->id_bits + 31) / 32);
   f->words = 2 * f->groups + f->code_words + f->id_words;
+  f->rows = kThreads / f->groups;
+  if (f->rows * f->words > kThreads * kStride) f->rows = kThreads * kStride / f->words;
+  if (f->rows > 4) f->rows = f->rows / 4 * 4;  // whole 16-byte units of records
   return true;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+// 4 bytes from global to shared memory by the calling thread (see copy_async_wait).
+__device__ __forceinline__ void copy4_async(void* dst_smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst_smem)), "l"(src) : "memory");
 }
-__device__ __forceinline__ float warp_min(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fminf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN where one of them is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
-// Word `lane` of the 32 lanes' values of `width` bits (1 to 31) laid one after the other: the values
-// that overlap bits [32 lane, 32 lane + 32).
-__device__ __forceinline__ uint32_t gather_bits(uint32_t value, int width, int lane) {
-  const int first = 32 * lane / width;  // the value that holds the word's first bit
-  uint32_t word = 0;
-  for (int k = 0, n = 31 / width + 2; k < n; ++k) {
-    const int from = first + k;
-    const uint32_t v = __shfl_sync(0xffffffffu, value, from & 31);
-    const int at = from * width - 32 * lane;  // its first bit in the word
-    if (from < 32 && at < 32) word |= at >= 0 ? v << at : v >> -at;
+// The level nearest to z, from the definition: in fp64 the product is exact, and so is a tie.
+__device__ __noinline__ uint32_t exact_level(float top, float z, float low, float levels) {
+  const double down = static_cast<double>(top) - z, span = static_cast<double>(top) - low;
+  return static_cast<uint32_t>(rint(down * levels / span));
+}
+
+// Calls f(unit, place) for the thread's share of a block's slots, which are one stretch of memory: units of kUnit
+// slots, and where the unit lies among the groups in shared memory.
+template <int kUnit, class F>
+__device__ __forceinline__ void for_slots(const Format& f, int rows, F&& fn) {
+  const int per_row = f.K / kUnit, units = rows * per_row;
+  const int rows_on = kThreads / per_row, on = kThreads - rows_on * per_row;  // what a step of kThreads units moves
+  int r = static_cast<int>(threadIdx.x) / per_row, k = static_cast<int>(threadIdx.x) - r * per_row;
+  for (int u = static_cast<int>(threadIdx.x); u < units; u += kThreads) {
+    const int slot = k * kUnit;
+    fn(u * kUnit, (r * f.groups + slot / kGroup) * kStride + slot % kGroup);
+    r += rows_on;
+    k += on;
+    if (k >= per_row) {
+      k -= per_row;
+      ++r;
+    }
   }
-  return word;
 }
 
-// The lane's value of `width` bits (1 to 31) of words that lie one to a lane.
-__device__ __forceinline__ uint32_t spread_bits(uint32_t word, int width, int lane) {
-  const int at = lane * width;
-  const uint32_t lo = __shfl_sync(0xffffffffu, word, at >> 5), hi = __shfl_sync(0xffffffffu, word, ((at >> 5) + 1) & 31);
-  return __funnelshift_r(lo, hi, at) & ((1u << width) - 1u);
-}
-
-// round((top - z) levels / (top - low)), a tie to the even one.  In fp32 the quotient is off by less than 2^-14
-// of a level (four roundings of at most 254); only where that leaves the nearest level open, or per_level =
-// levels / (top - low) is no number, is it taken again in fp64: there the product is exact, and so is a tie.
-__device__ __forceinline__ uint32_t level_of(float top, float z, float low, float levels, float per_level) {
-  const float t = (top - z) * per_level;
-  float r = rintf(t);
-  if (!(per_level < INFINITY) || fabsf(fabsf(t - r) - 0.5f) < 0x1p-10f) {
-    const double down = static_cast<double>(top) - z, span = static_cast<double>(top) - low;
-    r = static_cast<float>(rint(down * levels / span));
-  }
-  return static_cast<uint32_t>(fminf(fmaxf(r, 0.f), levels));
-}
-
-__global__ void __launch_bounds__(kWarps * 32)
+// kVec: K, the pointers and a block's records are whole 16-byte units (`whole_units` below).
+template <int kBits, bool kVec>
+__global__ void __launch_bounds__(kThreads, 6)
     pack_kernel(const int32_t* __restrict__ idx, const float* __restrict__ logits, int64_t T, const Format f,
                 uint32_t* __restrict__ records) {
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= T) return;  // uniform per warp
-  const int32_t* ri = idx + t * f.K;
-  const float* rz = logits + t * f.K;
-  uint32_t* out = records + t * f.words;
-  const float levels = static_cast<float>((1 << f.bits) - 2);
-  const uint32_t none = (1u << f.bits) - 1u, no_id = (1u << f.id_bits) - 1u;
-
-  float row_max = -INFINITY;
-  bool bad = false;
-  for (int k = lane; k < f.K; k += 32) {
-    const float z = rz[k];
-    row_max = fmaxf(row_max, z);
-    bad |= !(z < INFINITY);  // NaN, +inf
-  }
-  row_max = warp_max(row_max);
-  bad = __any_sync(0xffffffffu, bad);
-  const float least = row_max - kSpan;
-
-  for (int g = 0; g < f.groups; ++g) {
-    const int k = g * kGroup + lane, slots = min(kGroup, f.K - g * kGroup);
-    const bool in = lane < slots;
-    const float z = in ? rz[k] : -INFINITY;
-    const int id = in ? ri[k] : 0;
-    const bool has = z >= least && z > -INFINITY && !bad;
-    const float top = warp_max(has ? z : -INFINITY), low = warp_min(has ? z : INFINITY);
-    const bool some = top > -INFINITY;
-    const float span = some ? top - low : 0.f;
-    if (lane == 0) {
-      out[2 * g] = __float_as_uint(bad ? NAN : some ? top : 0.f);
-      out[2 * g + 1] = __float_as_uint(__fdiv_rn(span, levels));
+  __shared__ __align__(16) float z_part[kThreads * kStride];  // logits by group, then the records
+  __shared__ __align__(16) int32_t id_part[kThreads * kStride];
+  __shared__ float group_max[kThreads];
+  constexpr float kLevels = static_cast<float>((1 << kBits) - 2);
+  constexpr uint32_t kNone = (1u << kBits) - 1u;
+  constexpr int kPerWord = 32 / kBits;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * f.rows;
+  const int rows = static_cast<int>(T - t0 < f.rows ? T - t0 : f.rows);
+  const int r = tid / f.groups, g = tid - r * f.groups;
+  const bool on = r < rows;  // a row of the block, and of the cache
+  const int slots = on ? min(kGroup, f.K - g * kGroup) : 0;
+  const float* zr = logits + t0 * f.K;
+  const int32_t* ir = idx + t0 * f.K;
+  for_slots<kVec ? 4 : 1>(f, rows, [&](int i, int at) {
+    if (kVec) {
+      copy16_async(z_part + at, zr + i);
+      copy16_async(id_part + at, ir + i);
+    } else {
+      copy4_async(z_part + at, zr + i);
+      copy4_async(id_part + at, ir + i);
     }
-    uint32_t code = none;
-    if (has) code = span > 0.f ? level_of(top, z, low, levels, levels / span) : 0u;
-    const uint32_t codes = gather_bits(in ? code : 0u, f.bits, lane);
-    const int cw = (slots * f.bits + 31) / 32, iw = (slots * f.id_bits + 31) / 32;
-    if (lane < cw) out[2 * f.groups + g * f.bits + lane] = codes;
-    const uint32_t stored = id >= 0 && id < f.V ? static_cast<uint32_t>(id) : no_id;
-    const uint32_t ids = gather_bits(in ? stored : 0u, f.id_bits, lane);
-    if (lane < iw) out[2 * f.groups + f.code_words + g * f.id_bits + lane] = ids;
+  });
+  for (int j = slots; j < kGroup; ++j) z_part[tid * kStride + j] = -INFINITY;  // behind the row's last slot
+  copy_async_wait();
+  __syncthreads();
+
+  const float4* mine = reinterpret_cast<const float4*>(&z_part[tid * kStride]);
+  float largest = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kGroup / 4; ++j) {
+    const float4 v = mine[j];
+    largest = max_nan(max_nan(largest, max_nan(v.x, v.y)), max_nan(v.z, v.w));
   }
+  group_max[tid] = largest;
+  __syncthreads();
+  float row_max = -INFINITY;
+  if (on)
+    for (int i = 0; i < f.groups; ++i) row_max = max_nan(row_max, group_max[r * f.groups + i]);
+  const bool bad = !(row_max < INFINITY);                               // a NaN or +inf
+  const float least = fmaxf(row_max - kSpan, -3.40282347e38f);          // -inf does not reach it
+  const bool some = !bad && largest >= least;
+  float low = INFINITY;
+#pragma unroll
+  for (int j = 0; j < kGroup / 4; ++j) {
+    const float4 v = mine[j];
+    low = fminf(fminf(low, v.x >= least ? v.x : INFINITY), v.y >= least ? v.y : INFINITY);
+    low = fminf(fminf(low, v.z >= least ? v.z : INFINITY), v.w >= least ? v.w : INFINITY);
+  }
+  const float top = some ? largest : 0.f, span = some ? top - low : 0.f;
+  const float floor = some ? least : NAN;  // no slot reaches it where there is none
+  const float per_level = span > 0.f ? kLevels / span : 0.f;
+  // Nearest levels: adding 1.5 2^23 leaves the whole number in a float's low bits, and the words are sums of
+  // those floats' bits in their places, less the bits of 1.5 2^23.  In fp32 the quotient is off by less
+  // than four roundings of at most kLevels; the slots (`open`) that this leaves between two levels, and all where
+  // levels / span is no number, are decided in fp64.
+  constexpr float kRound = 12582912.f;
+  constexpr uint32_t kRoundBits = 0x4B400000u;
+  constexpr float kNear = 0.5f - kLevels * 0x1p-21f;
+  auto level = [&](float x, float& t) {  // each operation rounded by itself: both calls give the same bits
+    t = __fmul_rn(__fsub_rn(top, x), per_level);
+    return __fadd_rn(t, kRound);
+  };
+  uint32_t codes[kBits], open = 0;
+#pragma unroll
+  for (int w = 0; w < kBits; ++w) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int q = 0; q < kPerWord; q += 4) {
+      const float4 v = mine[(w * kPerWord + q) / 4];
+      const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float t;
+        const float n = level(x[i], t);
+        const bool has = x[i] >= floor;
+        if (has && !(fabsf(t - (n - kRound)) < kNear)) open |= 1u << (w * kPerWord + q + i);
+        word += ((has ? __float_as_uint(n) : kRoundBits + kNone) - kRoundBits) << ((q + i) * kBits);
+      }
+    }
+    codes[w] = word;
+  }
+  while (open != 0) {
+    const int j = __ffs(open) - 1;
+    open &= open - 1;
+    const float x = z_part[tid * kStride + j];
+    float t;
+    const uint32_t fix = (exact_level(top, x, low, kLevels) - (__float_as_uint(level(x, t)) - kRoundBits)) << (j % kPerWord * kBits);
+#pragma unroll
+    for (int w = 0; w < kBits; ++w) codes[w] += w == j / kPerWord ? fix : 0u;
+  }
+  __syncthreads();  // the logits are read: their memory is free for the records
+  if (on) {
+    uint32_t* out = reinterpret_cast<uint32_t*>(z_part) + r * f.words;
+    out[2 * g] = __float_as_uint(bad ? NAN : top);
+    out[2 * g + 1] = __float_as_uint(__fdiv_rn(span, kLevels));
+#pragma unroll
+    for (int w = 0; w < kBits; ++w) {
+      const int bits = slots * kBits - w * 32;  // of the word that slots have
+      if (bits > 0) out[2 * f.groups + g * kBits + w] = bits < 32 ? codes[w] & ((1u << bits) - 1u) : codes[w];
+    }
+    const uint32_t no_id = (1u << f.id_bits) - 1u, V = static_cast<uint32_t>(f.V);
+    uint32_t* to = out + 2 * f.groups + f.code_words + g * f.id_bits;
+    uint64_t held = 0;
+    int fill = 0;
+    auto put = [&](uint32_t id) {
+      held += static_cast<uint64_t>(id < V ? id : no_id) * (1u << fill);
+      fill += f.id_bits;
+      if (fill >= 32) {
+        *to++ = static_cast<uint32_t>(held);
+        held >>= 32;
+        fill -= 32;
+      }
+    };
+    const int32_t* from = &id_part[tid * kStride];
+    int j = 0;
+    for (; j + 4 <= slots; j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(from + j);
+      put(v.x);
+      put(v.y);
+      put(v.z);
+      put(v.w);
+    }
+    for (; j < slots; ++j) put(static_cast<uint32_t>(from[j]));
+    if (fill > 0) *to = static_cast<uint32_t>(held);
+  }
+  __syncthreads();
+  uint32_t* record = records + t0 * f.words;
+  const int total = rows * f.words;
+  int done = 0;
+  if (kVec) {
+    done = total / 4 * 4;
+    for (int i = tid * 4; i < done; i += kThreads * 4)
+      *reinterpret_cast<uint4*>(record + i) = *reinterpret_cast<const uint4*>(z_part + i);
+  }
+  for (int i = done + tid; i < total; i += kThreads) record[i] = __float_as_uint(z_part[i]);
 }
 
-__global__ void __launch_bounds__(kWarps * 32)
+template <int kBits, bool kVec>
+__global__ void __launch_bounds__(kThreads, 6)
     unpack_kernel(const uint32_t* __restrict__ records, int64_t T, const Format f, int32_t* __restrict__ idx,
                   float* __restrict__ logits) {
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= T) return;  // uniform per warp
-  const uint32_t* in = records + t * f.words;
-  const uint32_t none = (1u << f.bits) - 1u;
-  for (int g = 0; g < f.groups; ++g) {
-    const int k = g * kGroup + lane, slots = min(kGroup, f.K - g * kGroup);
-    const int cw = (slots * f.bits + 31) / 32, iw = (slots * f.id_bits + 31) / 32;
-    const float top = __uint_as_float(in[2 * g]), step = __uint_as_float(in[2 * g + 1]);
-    const uint32_t cword = lane < cw ? in[2 * f.groups + g * f.bits + lane] : 0u;
-    const uint32_t iword = lane < iw ? in[2 * f.groups + f.code_words + g * f.id_bits + lane] : 0u;
-    const uint32_t code = spread_bits(cword, f.bits, lane), id = spread_bits(iword, f.id_bits, lane);
-    if (lane < slots) {
-      const float z = __fsub_rn(top, __fmul_rn(static_cast<float>(code), step));
-      logits[t * f.K + k] = code == none && top == top ? -INFINITY : z;
-      idx[t * f.K + k] = id < static_cast<uint32_t>(f.V) ? static_cast<int32_t>(id) : -1;
+  __shared__ __align__(16) uint32_t part[kThreads * kStride];  // the records, then the logits by group
+  __shared__ __align__(16) int32_t id_part[kThreads * kStride];
+  constexpr uint32_t kNone = (1u << kBits) - 1u;
+  constexpr int kPerWord = 32 / kBits;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * f.rows;
+  const int rows = static_cast<int>(T - t0 < f.rows ? T - t0 : f.rows);
+  const uint32_t* record = records + t0 * f.words;
+  const int total = rows * f.words;
+  int done = 0;
+  if (kVec) {
+    done = total / 4 * 4;
+    for (int i = tid * 4; i < done; i += kThreads * 4) copy16_async(part + i, record + i);
+  }
+  for (int i = done + tid; i < total; i += kThreads) copy4_async(part + i, record + i);
+  copy_async_wait();
+  __syncthreads();
+
+  const int r = tid / f.groups, g = tid - r * f.groups;
+  const int slots = r < rows ? min(kGroup, f.K - g * kGroup) : 0;
+  float top = 0.f, step = 0.f;
+  uint32_t codes[kBits];
+  if (slots > 0) {
+    const uint32_t* in = part + r * f.words;
+    top = __uint_as_float(in[2 * g]);
+    step = __uint_as_float(in[2 * g + 1]);
+#pragma unroll
+    for (int w = 0; w < kBits; ++w) codes[w] = w * 32 < slots * kBits ? in[2 * f.groups + g * kBits + w] : 0u;
+    const uint32_t* from = in + 2 * f.groups + f.code_words + g * f.id_bits;
+    const uint32_t mask = (1u << f.id_bits) - 1u, V = static_cast<uint32_t>(f.V);
+    uint64_t held = 0;
+    int fill = 0;
+    auto take = [&]() {
+      if (fill < f.id_bits) {
+        held += static_cast<uint64_t>(*from++) * (1u << fill);
+        fill += 32;
+      }
+      const uint32_t id = static_cast<uint32_t>(held) & mask;
+      held >>= f.id_bits;
+      fill -= f.id_bits;
+      return id < V ? static_cast<int32_t>(id) : -1;
+    };
+    int32_t* to = &id_part[tid * kStride];
+    int j = 0;
+    for (; j + 4 <= slots; j += 4) {
+      int4 v;
+      v.x = take();
+      v.y = take();
+      v.z = take();
+      v.w = take();
+      *reinterpret_cast<int4*>(to + j) = v;
+    }
+    for (; j < slots; ++j) to[j] = take();
+  }
+  __syncthreads();  // every record is read: its memory is free for the logits
+  if (slots > 0) {
+    float* z = reinterpret_cast<float*>(part) + tid * kStride;
+    const float none = top == top ? -INFINITY : NAN;
+#pragma unroll
+    for (int j = 0; j < kGroup; j += 4) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t code = codes[(j + i) / kPerWord] >> ((j + i) % kPerWord * kBits) & kNone;
+        // 2^23 + code has the code in its low bits: a subtraction instead of a conversion
+        const float level = __uint_as_float(0x4B000000u | code) - 8388608.f;
+        v[i] = code == kNone ? none : __fsub_rn(top, __fmul_rn(level, step));
+      }
+      *reinterpret_cast<float4*>(z + j) = make_float4(v[0], v[1], v[2], v[3]);
     }
   }
+  __syncthreads();
+  float* zr = logits + t0 * f.K;
+  int32_t* ir = idx + t0 * f.K;
+  for_slots<kVec ? 4 : 1>(f, rows, [&](int i, int at) {
+    if (kVec) {
+      *reinterpret_cast<uint4*>(zr + i) = *reinterpret_cast<const uint4*>(part + at);
+      *reinterpret_cast<int4*>(ir + i) = *reinterpret_cast<const int4*>(id_part + at);
+    } else {
+      zr[i] = __uint_as_float(part[at]);
+      ir[i] = id_part[at];
+    }
+  });
 }
 
 fkl_status cache_fail(fkl_status st, const char* msg) {
@@ -172,7 +334,25 @@ fkl_status check_cache(const void* records, const void* idx, const void* logits,
   return static_cast<fkl_status>(check_device_memory(ptrs));
 }
 
-unsigned cache_blocks(int64_t T) { return static_cast<unsigned>((T + kWarps - 1) / kWarps); }
+unsigned cache_blocks(int64_t T, const Format& f) { return static_cast<unsigned>((T + f.rows - 1) / f.rows); }
+
+// Whether rows of slots and the blocks' records start and end at 16-byte units.
+bool whole_units(const Format& f, const void* records, const void* idx, const void* logits) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(records) | reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(logits);
+  return all % 16 == 0 && f.K % 4 == 0 && f.rows * f.words % 4 == 0;
+}
+
+// Calls fn with the two template arguments of a kernel as constants.
+template <class F>
+void with_variant(const Format& f, bool vec, F&& fn) {
+  using yes = std::true_type;
+  using no = std::false_type;
+  if (f.bits == 8) {
+    if (vec) fn(std::integral_constant<int, 8>{}, yes{}); else fn(std::integral_constant<int, 8>{}, no{});
+  } else {
+    if (vec) fn(std::integral_constant<int, 4>{}, yes{}); else fn(std::integral_constant<int, 4>{}, no{});
+  }
+}
 
 fkl_status cache_done() {
   const cudaError_t e = cudaGetLastError();
@@ -195,7 +375,10 @@ extern "C" fkl_status fkl_cache_pack(const int32_t* topk_idx, const float* topk_
   Format f;
   const fkl_status s = check_cache(records, topk_idx, topk_logits, T, K, V, bits, &f);
   if (s != FKL_OK || T == 0) return s;
-  pack_kernel<<<cache_blocks(T), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(topk_idx, topk_logits, T, f, records);
+  with_variant(f, whole_units(f, records, topk_idx, topk_logits), [&](auto b, auto vec) {
+    pack_kernel<decltype(b)::value, decltype(vec)::value>
+        <<<cache_blocks(T, f), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(topk_idx, topk_logits, T, f, records);
+  });
   return cache_done();
 }
 
@@ -205,6 +388,9 @@ extern "C" fkl_status fkl_cache_unpack(const uint32_t* records, int64_t T, int64
   Format f;
   const fkl_status s = check_cache(records, topk_idx, topk_logits, T, K, V, bits, &f);
   if (s != FKL_OK || T == 0) return s;
-  unpack_kernel<<<cache_blocks(T), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(records, T, f, topk_idx, topk_logits);
+  with_variant(f, whole_units(f, records, topk_idx, topk_logits), [&](auto b, auto vec) {
+    unpack_kernel<decltype(b)::value, decltype(vec)::value>
+        <<<cache_blocks(T, f), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(records, T, f, topk_idx, topk_logits);
+  });
   return cache_done();
 }
