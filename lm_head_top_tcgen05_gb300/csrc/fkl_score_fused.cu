@@ -232,28 +232,44 @@ struct EpiScoreDs {
 // ---------------------------------------------------------------- kernels over the rows
 constexpr int kRowThreads = 256;
 
-// Joins a row's splits.  The weights between splits are fp32, the same for L and U; the sums and the two
-// terms of the entropy, which may cancel, are fp64.
+// Joins the splits of 32 rows, a row to a lane, a share of the splits to a warp.  The weights between splits are
+// fp32, the same for L and U; the sums and the two terms of the entropy, which may cancel, are fp64.
 __global__ void __launch_bounds__(kRowThreads)
     score_rows_kernel(const float* __restrict__ part, int nsplit, const float* __restrict__ token_s, TokenIds tokens,
                       const uint8_t* __restrict__ mask, int64_t T, int V, float inv_tau, uint32_t* status,
                       float* __restrict__ logprob, float* __restrict__ entropy, float* __restrict__ lse) {
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (t >= T) return;
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ float warp_m[kWarps][32];
+  __shared__ double warp_l[kWarps][32], warp_u[kWarps][32];
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const size_t plane = static_cast<size_t>(nsplit) * T;
   float M = -INFINITY;
-  for (int s = 0; s < nsplit; ++s) M = fmaxf(M, part[static_cast<size_t>(s) * T + t]);
+  if (t < T)
+    for (int s = warp; s < nsplit; s += kWarps) M = fmaxf(M, part[static_cast<size_t>(s) * T + t]);
+  warp_m[warp][lane] = M;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, warp_m[w][lane]);
   double L = 0.0, U = 0.0;
-  for (int s = 0; s < nsplit; ++s) {
-    const size_t i = static_cast<size_t>(s) * T + t;
-    const float a = fmaxf(part[i] - M, -1000.f);
-    const double f = exp2f(a), l = part[plane + i];
-    L += f * l;
-    U += f * (part[2 * plane + i] + a * l);
+  if (t < T) {
+    for (int s = warp; s < nsplit; s += kWarps) {
+      const size_t i = static_cast<size_t>(s) * T + t;
+      const float a = fmaxf(part[i] - M, -1000.f);
+      const double f = exp2f(a), l = part[plane + i];
+      L += f * l;
+      U += f * (part[2 * plane + i] + a * l);
+    }
   }
-  const double log2_sum = log2(L);
+  warp_l[warp][lane] = L;
+  warp_u[warp][lane] = U;
+  __syncthreads();
+  if (warp != 0 || t >= T) return;
+  for (int w = 1; w < kWarps; ++w) {
+    L += warp_l[w][lane];
+    U += warp_u[w][lane];
+  }
+  const double ln2 = 0.69314718055994530942, log2_sum = log2(L);
   const bool late = (*reinterpret_cast<const volatile uint32_t*>(status) & kStatusTimeoutBit) != 0;
-  const double ln2 = 0.69314718055994530942;
   const double z = late ? NAN : (static_cast<double>(M) + log2_sum) * ln2;
   lse[t] = static_cast<float>(z);
   if (mask != nullptr && mask[t] == 0) {
@@ -518,7 +534,7 @@ extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, 
   p.nsplit = g.nsplit;
   p.scale2 = kLog2e / tau;
   if ((e = launch_gemm2_t<kVocabTile, false, false, EpiScore>(mH, mW, g, p, sms, st)) != cudaSuccess) return fused_cuda(e);
-  score_rows_kernel<<<row_blocks(T), kRowThreads, 0, st>>>(p.part, p.nsplit, p.token_s, p.tokens, mask, T, p.V, 1.f / tau,
+  score_rows_kernel<<<static_cast<unsigned>(ceil_div(T, 32)), kRowThreads, 0, st>>>(p.part, p.nsplit, p.token_s, p.tokens, mask, T, p.V, 1.f / tau,
                                                            &hdr->status, logprob, entropy, lse);
   if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
   return FKL_OK;

@@ -102,9 +102,33 @@ def _grad_like(logits: torch.Tensor) -> torch.Tensor:
     return torch.empty((B, V), dtype=logits.dtype, device=logits.device)
 
 
+def _score_backward(ctx, grad_logprob, grad_entropy, _ids, _logs):
+    logits, tokens, entropy, stats, mask, rows = ctx.saved_tensors
+    if grad_logprob is None and grad_entropy is None:
+        return None, None, None, None, None
+    B, V, ld = _rows(logits, "logits")
+    out = _grad_like(logits)
+    if grad_logprob is not None:
+        grad_logprob = grad_logprob.contiguous()
+    if grad_entropy is not None:
+        grad_entropy = grad_entropy.contiguous()
+    st = lib().fkl_token_logprobs_backward(
+        logits.data_ptr(), _dtype(logits.dtype, "logits"), B, V, ld, tokens.data_ptr(), _TOKEN_BYTES[tokens.dtype],
+        _address(mask), ctx.number, _address(rows), stats.data_ptr(), entropy.data_ptr(), _address(grad_logprob),
+        _address(grad_entropy), out.data_ptr(), out.stride(0) if B > 1 else V, _stream(logits.device))
+    check(st, "fkl_token_logprobs_backward")
+    return out, None, None, None, None
+
+
+# The engine's thread calls a backward, and a short one is mostly Python: the wrapper that makes a second
+# derivative an error (about 10 us) is only taken where one can be asked for (create_graph=True).
+_score_backward_once = once_differentiable(_score_backward)
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, temperature, top_n, mask):
+        mask = _mask(mask, logits.shape[0], logits.device)
         logprob, entropy, ids, logs, stats = _score(logits, tokens, temperature, top_n, mask, True)
         rows = temperature if isinstance(temperature, torch.Tensor) else None
         ctx.save_for_backward(logits, tokens, entropy, stats, mask, rows)
@@ -115,24 +139,8 @@ class _TokenLogprobs(torch.autograd.Function):
         return logprob, entropy, ids, logs
 
     @staticmethod
-    @once_differentiable
-    def backward(ctx, grad_logprob, grad_entropy, _ids, _logs):
-        logits, tokens, entropy, stats, mask, rows = ctx.saved_tensors
-        if grad_logprob is None and grad_entropy is None:
-            return None, None, None, None, None
-        B, V, ld = _rows(logits, "logits")
-        mask = _mask(mask, B, logits.device)
-        out = _grad_like(logits)
-        if grad_logprob is not None:
-            grad_logprob = grad_logprob.contiguous()
-        if grad_entropy is not None:
-            grad_entropy = grad_entropy.contiguous()
-        st = lib().fkl_token_logprobs_backward(
-            logits.data_ptr(), _dtype(logits.dtype, "logits"), B, V, ld, tokens.data_ptr(), _TOKEN_BYTES[tokens.dtype],
-            _address(mask), ctx.number, _address(rows), stats.data_ptr(), entropy.data_ptr(), _address(grad_logprob),
-            _address(grad_entropy), out.data_ptr(), out.stride(0) if B > 1 else V, _stream(logits.device))
-        check(st, "fkl_token_logprobs_backward")
-        return out, None, None, None, None
+    def backward(ctx, *grads):
+        return _score_backward_once(ctx, *grads) if torch.is_grad_enabled() else _score_backward(ctx, *grads)
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: Union[float, torch.Tensor] = 1.0,

@@ -358,3 +358,14 @@ def test_on_another_stream_and_in_a_graph(fkl):
         for a, b in zip(r, e):
             assert torch.equal(a, b)
         assert torch.equal(dx, de)
+
+
+def test_a_second_derivative_is_refused(fkl):
+    x, tok = make(3, 100, torch.float32)
+    leaf = x.clone().requires_grad_()
+    r = fkl.token_logprobs(leaf, tok)
+    dx, = torch.autograd.grad(r.logprob.sum(), leaf, create_graph=True)
+    want, = torch.autograd.grad(fkl.token_logprobs(leaf, tok).logprob.sum(), leaf)
+    assert torch.equal(dx.detach(), want)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
