@@ -153,7 +153,7 @@ struct ScoreShared<true> : ScoreShared<false> {
   u64 top[kMaxTop];                // this CTA's largest, in order
   u64 tops[kMaxRanks * kMaxTop];   // in the first CTA: every CTA's, n each, 0 behind the last
   uint16_t hot[kMostThreads];
-  int hot_count, list_count;
+  int hot_count, list_count, bound;
   uint32_t hist[256];
   u64 prefix;
   int want;
@@ -273,18 +273,46 @@ __device__ __forceinline__ int select_top(ScoreShared<true>& s, const RowView<T>
   static_assert(kInFlight * kN <= 32, "a bit for each logit in flight");
   const int tid = static_cast<int>(threadIdx.x);
   // The largest 16-bit bound that n threads reach.  It mostly lies within 255 of the CTA's largest (two binary
-  // orders of a logit); one count asks, and 8 more find it there, else 16 do.
+  // orders of a logit): a histogram of the distances, which the first warp adds up.  Where fewer than n threads
+  // lie so near, a search by bits.
   const uint32_t key = order_bits(mine) >> 16, most = order_bits(largest) >> 16;
-  uint32_t bound = most > 255u ? most - 255u : 0u;
-  int bit = 7;
-  if (__syncthreads_count(key >= bound) < n) {
-    bound = 0u;
-    bit = 15;
+  if (most - key < 256u) atomicAdd(&s.hist[most - key], 1u);
+  __syncthreads();
+  if (tid < 32) {
+    uint32_t bins[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += bins[i] = s.hist[tid * 8 + i];
+    uint32_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (tid >= o) upto += y;
+    }
+    const unsigned reached = __ballot_sync(0xffffffffu, upto >= static_cast<uint32_t>(n));
+    if (reached == 0) {
+      if (tid == 0) s.bound = -1;
+    } else if (tid == __ffs(reached) - 1) {
+      uint32_t before = upto - sum;
+      int i = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i == k && before + bins[k] < static_cast<uint32_t>(n)) {
+          before += bins[k];
+          ++i;
+        }
+      }
+      s.bound = static_cast<int>(most) - (tid * 8 + i);
+    }
   }
+  __syncthreads();
+  uint32_t bound = static_cast<uint32_t>(max(s.bound, 0));
+  if (s.bound < 0) {
+    bound = 0u;
 #pragma unroll 1
-  for (; bit >= 0; --bit) {
-    const uint32_t next = bound + (1u << bit);
-    if (__syncthreads_count(key >= next) >= n) bound = next;
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t next = bound + (1u << bit);
+      if (__syncthreads_count(key >= next) >= n) bound = next;
+    }
   }
   const bool is_hot = key >= bound && mine > -INFINITY;
   if (is_hot) s.hot[atomicAdd(&s.hot_count, 1)] = static_cast<uint16_t>(tid);
@@ -384,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   if (ranks > 1) cluster_arrive();  // this CTA runs: its shared memory may be written from now on
   if constexpr (kTop) {
     if (tid == 0) s.hot_count = s.list_count = 0;  // seen after the barriers of the sums
+    if (tid < 256) s.hist[tid] = 0;
   }
   const float lead = 8.f / sc;
   const RowView<T> row(static_cast<const T*>(g.logits) + b * g.ld, g.V);
@@ -481,21 +510,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
     __syncthreads();
   }
 
-  float M = -INFINITY;
-  for (int c = 0; c < ranks; ++c) M = fmaxf(M, s.part[c].largest);
-  float L = 0.f, U = 0.f;
-  int total = 0;
-  for (int c = 0; c < ranks; ++c) {
-    const Part p = s.part[c];
-    total += p.listed;
-    if (M == INFINITY) {
-      L += static_cast<float>(p.infinite);
-    } else if (p.largest > -INFINITY) {
-      const float a = fmaxf((p.largest - M) * sc, -1000.f), f = ex2_approx(a);
-      L = fmaf(p.l, f, L);
-      U = fmaf(fmaf(a, p.l, p.u), f, U);
-    }
-  }
+  // a lane per CTA (the lanes beyond repeat the first's sums with weight 0)
+  const Part p = s.part[lane < ranks ? lane : 0];
+  const float M = warp_max(p.largest);
+  const float a = M < INFINITY && p.largest > -INFINITY ? fmaxf((p.largest - M) * sc, -1000.f) : 0.f;
+  const float f = lane < ranks && p.largest > -INFINITY ? ex2_approx(a) : 0.f;
+  const float L = warp_sum(M == INFINITY ? (lane < ranks ? static_cast<float>(p.infinite) : 0.f) : f > 0.f ? f * p.l : 0.f);
+  const float U = warp_sum(M == INFINITY || !(f > 0.f) ? 0.f : f * fmaf(a, p.l, p.u));
+  const int total = __reduce_add_sync(0xffffffffu, lane < ranks ? p.listed : 0);
   const float log_sum = M > -INFINITY ? logf(L) : NAN;
   auto logprob_of = [&](float x) {  // NaN where the row has nothing to produce
     if (M == INFINITY) return x == INFINITY ? -log_sum : -INFINITY;
