@@ -19,8 +19,8 @@
  * anything is enqueued, and gives the same bits for the same inputs.
  *
  * Rows.  `mask` (uint8, 1 = valid; NULL = all valid) leaves rows out: their logprob and entropy
- * are 0, their gradient is 0, and their token is not looked at.  In the others a token outside
- * [0, V) gives logprob NaN.
+ * are 0, their gradient is 0, and neither their token nor what their logits or hidden states hold (NaN, say)
+ * reaches anything else.  In the others a token outside [0, V) gives logprob NaN.
  */
 #ifndef FKL_SCORE_H_
 #define FKL_SCORE_H_

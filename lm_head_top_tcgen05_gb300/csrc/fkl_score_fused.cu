@@ -303,6 +303,18 @@ __global__ void __launch_bounds__(kRowThreads)
   at[t] = a * inv_tau;
 }
 
+// A block's hidden states for dW, with zeros in the rows that the mask leaves out: their dS is 0, but 0 times
+// the NaN or infinity that such a row may hold would be none.  8 values a thread.
+__global__ void __launch_bounds__(kRowThreads)
+    clean_rows_kernel(const uint4* __restrict__ H, const uint8_t* __restrict__ mask, int64_t rows, int per_row,
+                      uint4* __restrict__ out) {
+  for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
+    const bool on = mask[t] != 0;
+    for (int i = static_cast<int>(threadIdx.x); i < per_row; i += kRowThreads)
+      out[t * per_row + i] = on ? H[t * per_row + i] : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 unsigned row_blocks(int64_t T) { return static_cast<unsigned>((T + kRowThreads - 1) / kRowThreads); }
 
 // ---------------------------------------------------------------- planning
@@ -311,6 +323,9 @@ unsigned row_blocks(int64_t T) { return static_cast<unsigned>((T + kRowThreads -
 bool score_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, bool bf16, Plan* p) {
   return make_plan(T, d, V, 1, chunk, p, bf16);
 }
+
+// Workspace of the backward: the plan's, and a block's hidden states without the rows that a mask leaves out.
+size_t backward_bytes(const Plan& p) { return p.total + (static_cast<size_t>(p.Ct) * p.d * 2 + 255) / 256 * 256; }
 
 // Tile width along d of dW and dH: the one with the least time, by columns (padded ones too) and the measured
 // time per column of each width.  256-wide tiles read the fewest operand bytes per product, so narrower ones
@@ -368,6 +383,7 @@ F32Params destination(int64_t rows, int64_t d, int64_t at, int64_t count, float*
 struct Backward {
   const uint16_t *H, *W;
   TokenIds tokens;
+  const uint8_t* mask;
   const float* lse;
   int64_t T, d, V;
   float tau;
@@ -390,11 +406,21 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   uint32_t* status = reinterpret_cast<uint32_t*>(c.ws);
   float* kpart = reinterpret_cast<float*>(c.ws + pl.off_kpart);
   const int bn = tile_width(d), pairs = c.sms / 2;
+  const uint16_t* Hw = Hb;  // what dW multiplies
+  if (c.mask != nullptr && c.dW != nullptr) {
+    uint16_t* clean = reinterpret_cast<uint16_t*>(c.ws + pl.total);
+    Hw = clean;
+    if (j == 0 || (pl.slab_outer && pl.nt > 1)) {  // else it still holds this block's
+      clean_rows_kernel<<<static_cast<unsigned>(rows < 8 * c.sms ? rows : 8 * c.sms), kRowThreads, 0, c.st>>>(
+          reinterpret_cast<const uint4*>(Hb), c.mask + r0, rows, static_cast<int>(d / 8), reinterpret_cast<uint4*>(clean));
+      if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return fused_cuda(e);
+    }
+  }
   CUtensorMap h_rows, h_cols, w_rows, w_cols, ds_cols, ds_rows;
   bool h3d = false, w3d = false;
   // dS has zeros in the columns [w, round_up(w, 256)) of every row, so its 3-D view may span round_up(w, 64)
   const bool ds3d = encode_map_mn3d(&ds_cols, ds, ceil_div(w, 64) * 64, rows, Vc * 2, 128);
-  if (!encode_map_bf16(&h_rows, Hb, d, rows, d * 2, 64, 128) || !map_columns(&h_cols, Hb, d, rows, bn, &h3d) ||
+  if (!encode_map_bf16(&h_rows, Hb, d, rows, d * 2, 64, 128) || !map_columns(&h_cols, Hw, d, rows, bn, &h3d) ||
       !encode_map_bf16(&w_rows, Wj, d, w, d * 2, 64, kVocabTile / 2) || !map_columns(&w_cols, Wj, d, w, bn, &w3d) ||
       (!ds3d && !encode_map_bf16(&ds_cols, ds, w, rows, Vc * 2, 64, 64)) ||
       !encode_map_bf16(&ds_rows, ds, w, rows, Vc * 2, 64, 128))
@@ -490,7 +516,7 @@ extern "C" size_t fkl_logprob_workspace_size(int64_t T, int64_t d, int64_t V) {
 
 extern "C" size_t fkl_logprob_backward_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t grad_bf16) {
   Plan p;
-  return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? p.total : 0;
+  return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? backward_bytes(p) : 0;
 }
 
 extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
@@ -547,10 +573,10 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
                                            void* dH, void* dW, void* workspace, size_t ws_bytes, void* stream) {
   set_last_error_message("");
   if (grad_bf16 != 0 && grad_bf16 != 1) return fused_fail(FKL_ERR_INVALID_ARG, "grad_bf16 must be 0 or 1");
-  Backward c{H, W, TokenIds{tokens, token_bytes}, lse, T, d, V, tau, accumulate, grad_bf16 == 1, dH, dW,
+  Backward c{H, W, TokenIds{tokens, token_bytes}, mask, lse, T, d, V, tau, accumulate, grad_bf16 == 1, dH, dW,
              static_cast<uint8_t*>(workspace), 0, static_cast<cudaStream_t>(stream), Plan{}};
   if (!score_plan(T, d, V, chunk, c.bf16, &c.pl)) return fused_fail(FKL_ERR_INVALID_ARG, kShapeRule);
-  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, c.pl.total);
+  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, backward_bytes(c.pl));
   if (s != FKL_OK) return s;
   if (accumulate < 0 || accumulate > 3) return fused_fail(FKL_ERR_INVALID_ARG, "bad accumulate");
   if (c.bf16 && accumulate != 0) return fused_fail(FKL_ERR_INVALID_ARG, "bf16 gradients do not accumulate");

@@ -230,6 +230,8 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
     for g, t in zip(out, (H, W)):
         if g is not None and (g.dtype != grad_dtype or g.shape != t.shape or not g.is_contiguous() or g.device != device):
             raise ValueError(f"out gradients must be contiguous {grad_dtype} {tuple(t.shape)} on {device}")
+    if T == 0 and out[1] is None:  # nothing to write, and no address to say so with
+        return out
     n = lib().fkl_logprob_backward_workspace_size(T, d, V, chunk, int(bf16))
     if n == 0:
         raise FklError(1, "fkl_logprob_backward_workspace_size", f"unsupported shape T={T} d={d} V={V} chunk={chunk}")

@@ -107,6 +107,29 @@ def test_many_rows(fkl):
     assert torch.equal(i2, ids[1000:1003]) and torch.equal(z2, got[1000:1003])
 
 
+@pytest.mark.parametrize("K", [4, 7, 100])
+def test_any_alignment(fkl, K):
+    """Tensors and records that start anywhere."""
+    T, V = 37, 5000
+    ids, z = make(T, K, V, seed=K)
+    want = oracle.cache_pack(ids, z, V, 8)
+    W = want.shape[1]
+    for off in (0, 1, 2, 3):
+        i = torch.empty(off + T * K, dtype=torch.int32, device="cuda")[off:].view(T, K)
+        f = torch.empty(off + T * K, device="cuda")[off:].view(T, K)
+        i.copy_(torch.tensor(ids))
+        f.copy_(torch.tensor(z))
+        got = fkl.quantize_cache(i, f, V)
+        assert (got.data.cpu().numpy().view(np.uint32) == want).all()
+        data = torch.empty(off + T * W, dtype=torch.int32, device="cuda")[off:].view(T, W)
+        data.copy_(got.data)
+        i.zero_()
+        f.zero_()
+        fkl.dequantize_cache(fkl.QuantizedCache(data, K, V, 8), out=(i, f))
+        assert (i.cpu().numpy() == ids).all()
+        np.testing.assert_array_equal(f.cpu().numpy(), oracle.cache_unpack(want, K, V, 8)[1])
+
+
 def test_empty_and_out(fkl):
     cache = fkl.quantize_cache(torch.zeros(0, 5, dtype=torch.int32).cuda(), torch.zeros(0, 5).cuda(), 10)
     assert len(cache) == 0 and fkl.dequantize_cache(cache)[0].shape == (0, 5)

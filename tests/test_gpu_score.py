@@ -309,6 +309,20 @@ def test_offsets_beyond_32_bits(fkl):
     assert torch.equal(r.top_ids[-1].long() - (V - 1000), s.top_ids[0].long())
 
 
+def test_more_rows_than_a_grid_has(fkl):
+    x, tok = make(70000, 5, torch.bfloat16, seed=3)
+    r = fkl.token_logprobs(x, tok, top_n=2)
+    rows = torch.tensor([0, 1, 65534, 65535, 65536, 69999]).cuda()
+    s = fkl.token_logprobs(x[rows].contiguous(), tok[rows], top_n=2)
+    for a, b in zip(r, s):
+        assert torch.equal(a[rows], b)
+    leaf = x.clone().requires_grad_()
+    few = x[rows].clone().requires_grad_()
+    da, = torch.autograd.grad(fkl.token_logprobs(leaf, tok).logprob.sum(), leaf)
+    db, = torch.autograd.grad(fkl.token_logprobs(few, tok[rows]).logprob.sum(), few)
+    assert torch.equal(da[rows], db)
+
+
 def test_refusals(fkl):
     x, tok = make(3, 50, torch.float32)
     with pytest.raises(ValueError):

@@ -183,6 +183,35 @@ def test_tokens_outside_and_rows_left_out(fkl):
     assert (lp == 0).all() and (ent == 0).all() and (dH == 0).all() and (dW == 0).all()
 
 
+@pytest.mark.parametrize("T,V", [(300, 500), (9000, 900)])
+def test_rows_left_out_may_hold_anything(fkl, T, V):
+    """NaN and infinities in the hidden states of masked rows reach neither the other rows nor dW."""
+    H, W, tok, mask = make(T, 64, V, seed=12)
+    a, b = torch.randn(T).cuda(), torch.randn(T).cuda()
+    bad = H.clone()
+    bad[~mask] = torch.tensor([float("nan"), float("inf")], device="cuda").bfloat16().repeat(32)
+    for dtype in (torch.float32, torch.bfloat16):
+        for chunk in (100, 4096):
+            outs = []
+            for h in (H, bad):
+                lp, ent, lse = fkl.logprob_forward(h, W, tok, mask)
+                outs.append((lp, ent) + fkl.logprob_backward(h, W, tok, mask, lse, ent, a, b, chunk=chunk, grad_dtype=dtype))
+            for x, y in zip(*outs):
+                assert torch.isfinite(y).all() and torch.equal(x, y)
+
+
+def test_empty_batch_with_a_frozen_head(fkl):
+    H, W, tok, _ = make(0, 16, 50)
+    Hl = H.requires_grad_()
+    lp, ent = fkl.fused_logprobs(Hl, W, tok)
+    lp.sum().backward()
+    assert Hl.grad.shape == (0, 16)
+    Wl = W.clone().requires_grad_()
+    lp, ent = fkl.fused_logprobs(H.detach(), Wl, tok)
+    lp.sum().backward()
+    assert (Wl.grad == 0).all()
+
+
 def test_refusals(fkl):
     H, W, tok, mask = make(20, 64, 100)
     with pytest.raises(TypeError):
