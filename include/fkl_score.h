@@ -94,7 +94,7 @@ fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void*
  * its product is left out (a frozen head, say).  The logits are recomputed block by block as in fkl_backward, and `chunk` bounds the buffer of their gradient in the same
  * way: at most chunk * V bfloat16 values.
  *   grad_logprob, grad_entropy   float [T]; NULL = 0
- *   lse, entropy                 the forward's
+ *   logprob, entropy, lse        the forward's
  *   accumulate   FKL_ACCUMULATE_DH and/or FKL_ACCUMULATE_DW add into float gradients (0 with grad_bf16)
  *   workspace    fkl_logprob_backward_workspace_size bytes, 256-byte aligned
  * A token outside [0, V) in a valid row (FKL_ERR_BAD_TOPK_ID) and a wait that runs out (FKL_ERR_TIMEOUT) fill
@@ -102,7 +102,7 @@ fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void*
  */
 size_t fkl_logprob_backward_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t grad_bf16);
 fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
-                                const uint8_t* mask, const float* lse, const float* entropy,
+                                const uint8_t* mask, const float* logprob, const float* entropy, const float* lse,
                                 const float* grad_logprob, const float* grad_entropy, int64_t T, int64_t d, int64_t V,
                                 float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate, void* dH, void* dW,
                                 void* workspace, size_t ws_bytes, void* stream);

@@ -21,7 +21,7 @@ INCLUDE = PKG.parent / "include"
 LIB = PKG / "libfkl.so"
 SOURCES = ["fkl_api.cu", "fkl_small.cu", "fkl_gemm_loss.cu", "fkl_gemm_f32.cu", "fkl_noalloc.cu", "fkl_trace.cu", "fkl_gemm2.cu",
            "fkl_topk.cu", "fkl_generate.cu", "fkl_int8.cu", "fkl_int8_gemm.cu", "fkl_sample.cu",
-           "fkl_score.cu", "fkl_score_fused.cu", "fkl_cache.cu"]
+           "fkl_score.cu", "fkl_score_fused.cu", "fkl_score_dw.cu", "fkl_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", str(INCLUDE)]

@@ -9,8 +9,11 @@
 // Backward: dS_tv = q_tv (c0_t + c1_t log2 q_tv) + k_t [v = v*_t] with c0 = -(a + b entropy) / tau,
 // c1 = -b ln 2 / tau, k = a / tau, rounded to bf16 and written block by block (tokens x a vocabulary slab),
 // then dW[slab] += dS^T H and dH[block] += dS W[slab] in fp32, in a fixed order: the blocks are those of the
-// loss's backward, planned by the same functions, and both products run its kernels.  The bf16 of dS (half a step
-// is 2^-8 of each value) is what the tensor cores multiply; sums stay fp32.
+// loss's backward, planned by the same functions.  The bf16 of dS (half a step is 2^-8 of each value) is what
+// the tensor cores multiply; sums stay fp32.  A row's largest entry mostly is the one of its token, so what
+// rounding takes from that one, r_t, is not lost: dH's sums start at r_t W[v*_t], and dW's rows add r_t H_t before
+// they are rounded (fkl_score_dw.cu).  Without, both gradients were 1.4 times as far from exact ones as their
+// own rounding to bf16 makes them.
 //
 // The tensor pipe bounds both: 2 T V d operations forward, 6 T V d backward.
 #include <cmath>
@@ -19,6 +22,7 @@
 #include "fkl_gemm2.cuh"
 #include "fkl_generate.cuh"
 #include "fkl_score.cuh"
+#include "fkl_score_dw.cuh"
 
 namespace fkl {
 namespace {
@@ -137,7 +141,8 @@ struct EpiScore {
 struct ScoreDsParams {
   TokenIds tokens;            // of all tokens: row t of the block is token r0 + t
   int64_t r0;
-  const float *c0, *c1, *at;  // of the block's tokens; a row left out has zeros
+  const float *c0, *c1;       // of the block's tokens; a row left out has zeros
+  const float* hit;           // the token's entry, rounded (0 in a row left out)
   const float* lse;
   uint16_t* ds;
   int64_t ld_ds;
@@ -150,7 +155,7 @@ struct EpiScoreDs {
   const Params& p;
   bool row_ok, off;
   int tok;
-  float c0, c1, at, shift;
+  float c0, c1, hit, shift;
   uint16_t* dst;
 
   __device__ explicit EpiScoreDs(const Params& prm) : p(prm) {}
@@ -160,13 +165,13 @@ struct EpiScoreDs {
     row_ok = t < p.T;
     off = true;
     tok = -1;
-    c0 = c1 = at = shift = 0.f;
+    c0 = c1 = hit = shift = 0.f;
     dst = nullptr;
     if (row_ok) {
       c0 = p.c0[t];
       c1 = p.c1[t];
-      at = p.at[t];
-      off = c0 == 0.f && c1 == 0.f && at == 0.f;
+      hit = p.hit[t];
+      off = c0 == 0.f && c1 == 0.f && hit == 0.f;
       shift = -p.lse[t] * kLog2e;
       if (!off) tok = p.tokens.get(p.r0 + t, p.V);
       dst = p.ds + static_cast<size_t>(t) * p.ld_ds;
@@ -195,7 +200,7 @@ struct EpiScoreDs {
     const int jt = tok - (p.v0 + cl0);
     if (jt >= 0 && jt < 32) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] += j == jt ? at : 0.f;
+      for (int j = 0; j < 32; ++j) v[j] = j == jt ? hit : v[j];
     }
     if (cl0 + 32 > p.slab_w) {
 #pragma unroll
@@ -283,24 +288,65 @@ __global__ void __launch_bounds__(kRowThreads)
   entropy[t] = late ? NAN : static_cast<float>((log2_sum - U / L) * ln2);
 }
 
-// The three factors of each token's dS; a token outside the vocabulary is recorded.
+// The factors of each token's dS, its entry at the token with what rounding takes from it, and the tokens of each
+// vocabulary row that few have (TargetRows); a token outside the vocabulary is recorded.
 __global__ void __launch_bounds__(kRowThreads)
-    score_factors_kernel(TokenIds tokens, const uint8_t* __restrict__ mask, const float* __restrict__ entropy,
-                         const float* __restrict__ grad_logprob, const float* __restrict__ grad_entropy, int64_t T, int V,
-                         float inv_tau, uint32_t* __restrict__ status, float* __restrict__ c0, float* __restrict__ c1,
-                         float* __restrict__ at) {
+    score_factors_kernel(TokenIds tokens, const uint8_t* __restrict__ mask, const float* __restrict__ logprob,
+                         const float* __restrict__ entropy, const float* __restrict__ grad_logprob,
+                         const float* __restrict__ grad_entropy, int64_t T, int V, float inv_tau,
+                         uint32_t* __restrict__ status, float* __restrict__ c0, float* __restrict__ c1,
+                         float* __restrict__ hit, float* __restrict__ rest, int* __restrict__ count,
+                         int* __restrict__ token_of) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
   if (t >= T) return;
-  float a = 0.f, b = 0.f, h = 0.f;
+  float a = 0.f, b = 0.f, h = 0.f, log2_q = 0.f;
+  int tok = -1;
   if (mask == nullptr || mask[t] != 0) {
-    if (tokens.get(t, V) < 0) atomicOr(status, kStatusBadIdBit);
+    tok = tokens.get(t, V);
+    if (tok < 0) atomicOr(status, kStatusBadIdBit);
     if (grad_logprob != nullptr) a = grad_logprob[t];
     if (grad_entropy != nullptr) b = grad_entropy[t];
     if (b != 0.f) h = entropy[t];
+    log2_q = fmaxf(logprob[t], -1000.f) * kLog2e;  // below that q is 0, and 0 * -inf would be none
   }
-  c0[t] = -fmaf(b, h, a) * inv_tau;
-  c1[t] = -b * kLn2 * inv_tau;
-  at[t] = a * inv_tau;
+  const float f0 = -fmaf(b, h, a) * inv_tau, f1 = -b * kLn2 * inv_tau;
+  const float entry = fmaf(exp2f(log2_q), fmaf(f1, log2_q, f0), a * inv_tau);
+  const float rounded = __uint_as_float(pack_bf16x2(entry, 0.f) << 16);
+  c0[t] = f0;
+  c1[t] = f1;
+  hit[t] = rounded;
+  rest[t] = entry - rounded;
+  if (tok >= 0 && (f0 != 0.f || f1 != 0.f)) {
+    const int n = atomicAdd(&count[tok], 1);
+    if (n < kMaxTargets) token_of[static_cast<size_t>(tok) * kMaxTargets + n] = static_cast<int>(t);
+  }
+}
+
+// Where dH's sums start: rest_t W[v*_t] (added to what is there where `add`).  8 values a thread.
+__global__ void __launch_bounds__(kRowThreads)
+    start_rows_kernel(const uint4* __restrict__ W, TokenIds tokens, int64_t r0, const float* __restrict__ rest, int64_t rows,
+                      int per_row, int V, int add, float4* __restrict__ out) {
+  for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
+    const float r = rest[t];
+    const int tok = r != 0.f ? tokens.get(r0 + t, V) : -1;
+    for (int i = static_cast<int>(threadIdx.x); i < per_row; i += kRowThreads) {
+      float4* o = out + (t * per_row + i) * 2;
+      float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+      if (add) {
+        lo = o[0];
+        hi = o[1];
+      }
+      if (tok >= 0) {
+        const uint4 w = W[static_cast<int64_t>(tok) * per_row + i];
+        add_bf16x2(lo.x, lo.y, w.x, r);
+        add_bf16x2(lo.z, lo.w, w.y, r);
+        add_bf16x2(hi.x, hi.y, w.z, r);
+        add_bf16x2(hi.z, hi.w, w.w, r);
+      }
+      o[0] = lo;
+      o[1] = hi;
+    }
+  }
 }
 
 // A block's hidden states for dW, with zeros in the rows that the mask leaves out: their dS is 0, but 0 times
@@ -324,8 +370,41 @@ bool score_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, bool bf16, Plan*
   return make_plan(T, d, V, 1, chunk, p, bf16);
 }
 
-// Workspace of the backward: the plan's, and a block's hidden states without the rows that a mask leaves out.
-size_t backward_bytes(const Plan& p) { return p.total + (static_cast<size_t>(p.Ct) * p.d * 2 + 255) / 256 * 256; }
+// Workspace of the backward behind the plan's: a block's hidden states without the rows that a mask leaves
+// out, what rounding takes from the tokens' entries, and the tokens of each vocabulary row.
+struct BackwardAreas {
+  size_t clean, rest, count, token_of, total;
+};
+BackwardAreas backward_areas(const Plan& p) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  BackwardAreas a;
+  a.clean = p.total;
+  a.rest = up(a.clean + static_cast<size_t>(p.Ct) * p.d * 2);
+  a.count = up(a.rest + static_cast<size_t>(p.T) * 4);
+  a.token_of = up(a.count + static_cast<size_t>(p.V) * 4);
+  a.total = up(a.token_of + static_cast<size_t>(p.V) * kMaxTargets * 4);
+  return a;
+}
+
+// Splits of a row block's vocabulary for the forward.  Up to four row blocks have a unit to each CTA pair and
+// block: the loss's rule, made for many blocks, leaves pairs idle there (1024 x 201088 x 2880: 724 us with its 64
+// splits, 681 with 76; 300 tokens 376 and 350).
+constexpr int kFewBlocks = 4, kFewSplits = 80;
+int split_room(int64_t T) { return ceil_div(T, 256) <= kFewBlocks ? kFewSplits : kMaxSplit; }
+int forward_splits(int m_tiles, int n_tiles, int pairs) {
+  if (m_tiles > kFewBlocks) return dynamic_splits(m_tiles, n_tiles, pairs);
+  const int s = pairs < kFewSplits ? pairs : kFewSplits;
+  return s < n_tiles ? s : n_tiles;
+}
+
+// Splits of the logits' recompute in the backward, whose units are dealt round-robin: the loss's, at most 32,
+// unless that is less than a unit to a pair.
+int recompute_splits(int m_tiles, int n_tiles, int pairs) {
+  const int s = plan_splits(m_tiles, n_tiles, pairs, group_rows(m_tiles));
+  if (m_tiles * s >= pairs) return s;
+  const int all = (pairs + m_tiles - 1) / m_tiles;
+  return all < n_tiles ? all : n_tiles;
+}
 
 // Tile width along d of dW and dH: the one with the least time, by columns (padded ones too) and the measured
 // time per column of each width.  256-wide tiles read the fewest operand bytes per product, so narrower ones
@@ -362,7 +441,7 @@ fkl_status fused_fail(fkl_status st, const char* msg) {
 fkl_status fused_cuda(cudaError_t e) { return fused_fail(FKL_ERR_CUDA, cudaGetErrorString(e)); }
 
 // Destination of a product that is summed over `count` blocks, of which this is number `at`: the caller's
-// fp32 gradient, or fp32 sums in the workspace that the last block rounds to bf16.
+// fp32 gradient, or fp32 sums in the workspace that the last block rounds to bf16.  accumulate: the first adds too.
 F32Params destination(int64_t rows, int64_t d, int64_t at, int64_t count, float* out32, uint16_t* out16, float* sums,
                       bool accumulate) {
   F32Params p;
@@ -370,7 +449,7 @@ F32Params destination(int64_t rows, int64_t d, int64_t at, int64_t count, float*
   p.M = static_cast<int>(rows);
   p.N = static_cast<int>(d);
   p.out = out16 == nullptr ? out32 : sums;
-  p.accumulate = at > 0 || (out16 == nullptr && accumulate) ? 1 : 0;
+  p.accumulate = at > 0 || accumulate ? 1 : 0;
   p.vec_ok = on_boundary(p.out, 32) && d % 8 == 0 ? 1 : 0;
   if (out16 != nullptr && at == count - 1) {
     p.out16 = out16;
@@ -394,6 +473,7 @@ struct Backward {
   int sms;
   cudaStream_t st;
   Plan pl;
+  BackwardAreas areas;
 };
 
 // One block: tokens [b Ct, ...) x vocabulary columns [j Vc, ...).
@@ -408,7 +488,7 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   const int bn = tile_width(d), pairs = c.sms / 2;
   const uint16_t* Hw = Hb;  // what dW multiplies
   if (c.mask != nullptr && c.dW != nullptr) {
-    uint16_t* clean = reinterpret_cast<uint16_t*>(c.ws + pl.total);
+    uint16_t* clean = reinterpret_cast<uint16_t*>(c.ws + c.areas.clean);
     Hw = clean;
     if (j == 0 || (pl.slab_outer && pl.nt > 1)) {  // else it still holds this block's
       clean_rows_kernel<<<static_cast<unsigned>(rows < 8 * c.sms ? rows : 8 * c.sms), kRowThreads, 0, c.st>>>(
@@ -427,14 +507,14 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
     return fused_fail(FKL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 
   const int m_tiles = static_cast<int>(ceil_div(rows, 256)), n_tiles = static_cast<int>(ceil_div(w, kVocabTile));
-  GemmShape g = make_shape(rows, w, d, kVocabTile, plan_splits(m_tiles, n_tiles, pairs, group_rows(m_tiles)), status, 256);
+  GemmShape g = make_shape(rows, w, d, kVocabTile, recompute_splits(m_tiles, n_tiles, pairs), status, 256);
   g.group_m = group_rows(m_tiles);
   ScoreDsParams p;
   p.tokens = c.tokens;
   p.r0 = r0;
   p.c0 = reinterpret_cast<const float*>(c.ws + pl.off_crow) + r0;
   p.c1 = reinterpret_cast<const float*>(c.ws + pl.off_wrow) + r0;
-  p.at = reinterpret_cast<const float*>(c.ws + pl.off_arow) + r0;
+  p.hit = reinterpret_cast<const float*>(c.ws + pl.off_arow) + r0;
   p.lse = c.lse + r0;
   p.ds = ds;
   p.ld_ds = Vc;
@@ -451,23 +531,33 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
     GemmShape gw = make_shape(w, d, rows, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
     gw.a_box3d = ds3d ? 1 : 0;
     gw.b_box3d = h3d ? 1 : 0;
-    const F32Params pw = destination(w, d, b, pl.nt, static_cast<float*>(c.dW) + (c.bf16 ? 0 : v0 * d),
-                                     c.bf16 ? static_cast<uint16_t*>(c.dW) + v0 * d : nullptr, wsum,
-                                     (c.accumulate & FKL_ACCUMULATE_DW) != 0);
-    plan_ksplit(&gw, pairs, kpart, kKsplitSlots);
-    if ((e = launch_gemm2_f32(bn, true, true, ds_cols, h_cols, gw, pw, c.sms, c.st)) != cudaSuccess ||
-        (e = launch_ksplit_fixup(bn, gw, pw, c.st)) != cudaSuccess)
-      return fused_cuda(e);
+    DwParams pw;
+    pw.to = destination(w, d, b, pl.nt, static_cast<float*>(c.dW) + (c.bf16 ? 0 : v0 * d),
+                        c.bf16 ? static_cast<uint16_t*>(c.dW) + v0 * d : nullptr, wsum,
+                        !c.bf16 && (c.accumulate & FKL_ACCUMULATE_DW) != 0);
+    pw.wide16 = on_boundary(pw.to.out16, 32) && d % 16 == 0 ? 1 : 0;
+    pw.H = c.H;
+    pw.rest = reinterpret_cast<const float*>(c.ws + c.areas.rest);
+    // what rounding took is added with the last block's sums
+    pw.count = b == pl.nt - 1 ? reinterpret_cast<const int*>(c.ws + c.areas.count) + v0 : nullptr;
+    pw.token_of = reinterpret_cast<const int*>(c.ws + c.areas.token_of) + v0 * kMaxTargets;
+    if ((e = launch_score_dw(bn, ds_cols, h_cols, gw, pw, c.sms, c.st)) != cudaSuccess) return fused_cuda(e);
   }
   if (c.dH == nullptr) return FKL_OK;
 
-  // dH[block] (+)= dS[block] W[slab], slabs in order
+  // dH[block] = what rounding took from the tokens' entries, + dS[block] W[slab], slabs in order
   float* hsum = reinterpret_cast<float*>(c.ws + pl.off_hsum) + (pl.slab_outer ? r0 * d : 0);
   GemmShape gh = make_shape(rows, d, w, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
   gh.b_box3d = w3d ? 1 : 0;
   const F32Params ph = destination(rows, d, j, pl.nslabs, static_cast<float*>(c.dH) + (c.bf16 ? 0 : r0 * d),
-                                   c.bf16 ? static_cast<uint16_t*>(c.dH) + r0 * d : nullptr, hsum,
-                                   (c.accumulate & FKL_ACCUMULATE_DH) != 0);
+                                   c.bf16 ? static_cast<uint16_t*>(c.dH) + r0 * d : nullptr, hsum, true);
+  if (j == 0) {
+    start_rows_kernel<<<static_cast<unsigned>(rows < 8 * c.sms ? rows : 8 * c.sms), kRowThreads, 0, c.st>>>(
+        reinterpret_cast<const uint4*>(c.W), c.tokens, r0, reinterpret_cast<const float*>(c.ws + c.areas.rest) + r0, rows,
+        static_cast<int>(d / 8), static_cast<int>(c.V), !c.bf16 && (c.accumulate & FKL_ACCUMULATE_DH) != 0 ? 1 : 0,
+        reinterpret_cast<float4*>(ph.out));
+    if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
+  }
   plan_ksplit(&gh, pairs, kpart, kKsplitSlots);
   if ((e = launch_gemm2_f32(bn, false, true, ds_rows, w_cols, gh, ph, c.sms, c.st)) != cudaSuccess ||
       (e = launch_ksplit_fixup(bn, gh, ph, c.st)) != cudaSuccess)
@@ -499,7 +589,7 @@ bool forward_plan(int64_t T, int64_t d, int64_t V, ForwardPlan* p) {
   if (!score_plan(T, d, V, 1, false, &pl)) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p->part = 256;
-  p->token_s = up(p->part + static_cast<size_t>(T) * 3 * kMaxSplit * 4);
+  p->token_s = up(p->part + static_cast<size_t>(T) * 3 * split_room(T) * 4);
   p->total = up(p->token_s + static_cast<size_t>(T) * 4);
   return true;
 }
@@ -516,7 +606,7 @@ extern "C" size_t fkl_logprob_workspace_size(int64_t T, int64_t d, int64_t V) {
 
 extern "C" size_t fkl_logprob_backward_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t grad_bf16) {
   Plan p;
-  return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? backward_bytes(p) : 0;
+  return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? backward_areas(p).total : 0;
 }
 
 extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
@@ -547,7 +637,7 @@ extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, 
   if (!encode_map_bf16(&mH, H, d, T, d * 2, 64, 128) || !encode_map_bf16(&mW, W, d, V, d * 2, 64, kVocabTile / 2))
     return fused_fail(FKL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   const int m_tiles = static_cast<int>(ceil_div(T, 256)), n_tiles = static_cast<int>(ceil_div(V, kVocabTile));
-  GemmShape g = make_shape(T, V, d, kVocabTile, dynamic_splits(m_tiles, n_tiles, sms / 2), &hdr->status, 256);
+  GemmShape g = make_shape(T, V, d, kVocabTile, forward_splits(m_tiles, n_tiles, sms / 2), &hdr->status, 256);
   g.group_m = fwd_group_rows(m_tiles, sms / 2);
   g.sched = &hdr->items_taken;
   ScoreFwdParams p;
@@ -567,26 +657,27 @@ extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, 
 }
 
 extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
-                                           const uint8_t* mask, const float* lse, const float* entropy,
-                                           const float* grad_logprob, const float* grad_entropy, int64_t T, int64_t d,
-                                           int64_t V, float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate,
+                                           const uint8_t* mask, const float* logprob, const float* entropy,
+                                           const float* lse, const float* grad_logprob, const float* grad_entropy,
+                                           int64_t T, int64_t d, int64_t V, float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate,
                                            void* dH, void* dW, void* workspace, size_t ws_bytes, void* stream) {
   set_last_error_message("");
   if (grad_bf16 != 0 && grad_bf16 != 1) return fused_fail(FKL_ERR_INVALID_ARG, "grad_bf16 must be 0 or 1");
   Backward c{H, W, TokenIds{tokens, token_bytes}, mask, lse, T, d, V, tau, accumulate, grad_bf16 == 1, dH, dW,
-             static_cast<uint8_t*>(workspace), 0, static_cast<cudaStream_t>(stream), Plan{}};
+             static_cast<uint8_t*>(workspace), 0, static_cast<cudaStream_t>(stream), Plan{}, BackwardAreas{}};
   if (!score_plan(T, d, V, chunk, c.bf16, &c.pl)) return fused_fail(FKL_ERR_INVALID_ARG, kShapeRule);
-  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, backward_bytes(c.pl));
+  c.areas = backward_areas(c.pl);
+  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, c.areas.total);
   if (s != FKL_OK) return s;
   if (accumulate < 0 || accumulate > 3) return fused_fail(FKL_ERR_INVALID_ARG, "bad accumulate");
   if (c.bf16 && accumulate != 0) return fused_fail(FKL_ERR_INVALID_ARG, "bf16 gradients do not accumulate");
-  if ((dW == nullptr && dH == nullptr) || (T > 0 && (lse == nullptr || entropy == nullptr)))
-    return fused_fail(FKL_ERR_INVALID_ARG, "lse, entropy and one of dH and dW must not be NULL");
+  if ((dW == nullptr && dH == nullptr) || (T > 0 && (logprob == nullptr || entropy == nullptr || lse == nullptr)))
+    return fused_fail(FKL_ERR_INVALID_ARG, "logprob, entropy, lse and one of dH and dW must not be NULL");
   if (!on_boundary(dH, 16) || !on_boundary(dW, 16)) return fused_fail(FKL_ERR_ALIGNMENT, "dH and dW must be 16-byte aligned");
-  if (!on_boundary(lse, 4) || !on_boundary(entropy, 4) || !on_boundary(grad_logprob, 4) || !on_boundary(grad_entropy, 4))
-    return fused_fail(FKL_ERR_ALIGNMENT, "lse, entropy and the gradients must be 4-byte aligned");
+  if (!on_boundary(logprob, 4) || !on_boundary(lse, 4) || !on_boundary(entropy, 4) || !on_boundary(grad_logprob, 4) || !on_boundary(grad_entropy, 4))
+    return fused_fail(FKL_ERR_ALIGNMENT, "logprob, entropy, lse and the gradients must be 4-byte aligned");
   if (const int e = require_device(&c.sms); e != FKL_OK) return static_cast<fkl_status>(e);
-  const NamedPtr ptrs[] = {{H, "H"}, {W, "W"}, {tokens, "tokens"}, {mask, "mask"}, {lse, "lse"}, {entropy, "entropy"},
+  const NamedPtr ptrs[] = {{H, "H"}, {W, "W"}, {tokens, "tokens"}, {mask, "mask"}, {logprob, "logprob"}, {lse, "lse"}, {entropy, "entropy"},
                            {grad_logprob, "grad_logprob"}, {grad_entropy, "grad_entropy"}, {dH, "dH"}, {dW, "dW"},
                            {workspace, "workspace"}};
   if (const int e = check_device_memory(ptrs); e != FKL_OK) return static_cast<fkl_status>(e);
@@ -600,10 +691,13 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
     return FKL_OK;
   }
   choose_slab_width(&c.pl, c.sms / 2);
+  const BackwardAreas& ar = c.areas;
+  if ((e = cudaMemsetAsync(c.ws + ar.count, 0, static_cast<size_t>(V) * 4, c.st)) != cudaSuccess) return fused_cuda(e);
   score_factors_kernel<<<row_blocks(T), kRowThreads, 0, c.st>>>(
-      c.tokens, mask, entropy, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau, &hdr->status,
+      c.tokens, mask, logprob, entropy, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau, &hdr->status,
       reinterpret_cast<float*>(c.ws + c.pl.off_crow), reinterpret_cast<float*>(c.ws + c.pl.off_wrow),
-      reinterpret_cast<float*>(c.ws + c.pl.off_arow));
+      reinterpret_cast<float*>(c.ws + c.pl.off_arow), reinterpret_cast<float*>(c.ws + ar.rest),
+      reinterpret_cast<int*>(c.ws + ar.count), reinterpret_cast<int*>(c.ws + ar.token_of));
   if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
   const Plan& pl = c.pl;
   for (int64_t o = 0; o < (pl.slab_outer ? pl.nslabs : pl.nt); ++o)

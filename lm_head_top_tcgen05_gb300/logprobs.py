@@ -204,15 +204,15 @@ def logprob_forward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask
 
 
 def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor],
-                     lse: torch.Tensor, entropy: torch.Tensor, grad_logprob: Optional[torch.Tensor] = None,
-                     grad_entropy: Optional[torch.Tensor] = None, tau: float = 1.0, chunk: int = 2048, workspace=None,
+                     logprob: torch.Tensor, entropy: torch.Tensor, lse: torch.Tensor,
+                     grad_logprob: Optional[torch.Tensor] = None, grad_entropy: Optional[torch.Tensor] = None, tau: float = 1.0, chunk: int = 2048, workspace=None,
                      out: Optional[Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]] = None,
                      accumulate: bool = False, grad_dtype: torch.dtype = torch.float32,
                      ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
     """dH [T, d] and dW [V, d], the gradient of sum(grad_logprob * logprob + grad_entropy * entropy) (float32 [T]
     each; None = 0), in float32 or, with ``grad_dtype=torch.bfloat16``, in bfloat16 (fp32 sums rounded once).
 
-    ``lse`` and ``entropy`` are the forward's; ``chunk`` bounds the buffer of the logits' gradient as in
+    ``logprob``, ``entropy`` and ``lse`` are the forward's; ``chunk`` bounds the buffer of the logits' gradient as in
     ``backward``.  ``out`` gives the tensors to write, one of them None if it is not wanted (a frozen head:
     ``(dH, None)``); ``accumulate=True`` adds into them (float32)."""
     if grad_dtype not in (torch.float32, torch.bfloat16):
@@ -222,7 +222,8 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
         raise ValueError("accumulate=True adds into float32 gradients given in `out`")
     size, mask = _operands(H, W, tokens, mask)
     (T, d), V, device = H.shape, W.shape[0], H.device
-    lse, entropy = _floats(lse, "lse", T, device), _floats(entropy, "entropy", T, device)
+    logprob, entropy = _floats(logprob, "logprob", T, device), _floats(entropy, "entropy", T, device)
+    lse = _floats(lse, "lse", T, device)
     grad_logprob = _floats(grad_logprob, "grad_logprob", T, device)
     grad_entropy = _floats(grad_entropy, "grad_entropy", T, device)
     if out is None:
@@ -238,8 +239,8 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
     ws = _scratch(workspace, int(n), device)
     flags = (FKL_ACCUMULATE_DH | FKL_ACCUMULATE_DW) if accumulate else 0
     st = lib().fkl_logprob_backward(
-        H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), lse.data_ptr(), entropy.data_ptr(),
-        _address(grad_logprob), _address(grad_entropy), T, d, V, float(tau), chunk, int(bf16), flags, _address(out[0]),
+        H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), logprob.data_ptr(), entropy.data_ptr(),
+        lse.data_ptr(), _address(grad_logprob), _address(grad_entropy), T, d, V, float(tau), chunk, int(bf16), flags, _address(out[0]),
         _address(out[1]), ws.data_ptr(), ws.numel(), _stream(device))
     check(st, "fkl_logprob_backward")
     return out
@@ -251,7 +252,7 @@ class _FusedLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, tokens, mask, tau, chunk):
         logprob, entropy, lse = logprob_forward(H, W, tokens, mask, tau)
-        ctx.save_for_backward(H, W, tokens, mask, lse, entropy)
+        ctx.save_for_backward(H, W, tokens, mask, logprob, entropy, lse)
         ctx.tau, ctx.chunk = tau, chunk
         ctx.set_materialize_grads(False)
         return logprob, entropy
@@ -259,12 +260,12 @@ class _FusedLogprobs(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_logprob, grad_entropy):
-        H, W, tokens, mask, lse, entropy = ctx.saved_tensors
+        H, W, tokens, mask, logprob, entropy, lse = ctx.saved_tensors
         if grad_logprob is None and grad_entropy is None:
             return None, None, None, None, None, None
         out = tuple(torch.empty_like(t) if need else None for t, need in zip((H, W), ctx.needs_input_grad))
-        dH, dW = logprob_backward(H, W, tokens, mask, lse, entropy, grad_logprob, grad_entropy, ctx.tau, ctx.chunk,
-                                  out=out, grad_dtype=torch.bfloat16)
+        dH, dW = logprob_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, ctx.tau,
+                                  ctx.chunk, out=out, grad_dtype=torch.bfloat16)
         return dH, dW, None, None, None, None
 
 

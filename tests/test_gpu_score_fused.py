@@ -2,7 +2,8 @@
 
 Tolerances.  The tensor cores add products in fp32, 16 deep: each step loses at most 2^-23 of the partial sum, which
 is below sum |h w|, so a logit is off by s_tol = (d / 16 + 2) 2^-22 max sum |h w|, and log q by twice that over tau
-and the sums' error (2^-20).  dS is rounded to bf16 (half a step: 2^-8), its products are summed in fp32.
+and the sums' error (2^-20).  dS is rounded to bf16 (half a step: 2^-8; not its entries at the tokens), its
+products are summed in fp32.
 """
 import numpy as np
 import pytest
@@ -58,9 +59,15 @@ class Exact:
         keep = np.ones(len(a), bool) if self.keep is None else self.keep
         lq = np.where(self.q > 0, np.abs(np.nan_to_num(self.logq)), 0)
         terms = (np.abs(a)[:, None] + np.abs(b)[:, None] * (lq + np.nan_to_num(self.ent)[:, None] + 1)) / self.tau
-        off = np.where(keep[:, None], np.nan_to_num(self.q) * terms * 4 * self.log_tol, 0) + 2.0 ** -8 * np.abs(dS)
-        for got, want, room, start in ((dH, dS @ self.W, (off + 2.0 ** -18 * np.abs(dS)) @ np.abs(self.W), base[0]),
-                                       (dW, dS.T @ self.H, (off + 2.0 ** -18 * np.abs(dS)).T @ np.abs(self.H), base[1])):
+        off = np.where(keep[:, None], np.nan_to_num(self.q) * terms * 4 * self.log_tol, 0) + 2.0 ** -18 * np.abs(dS)
+        # what rounding takes from the tokens' own entries is added back: in dW where at most 4 tokens share a row
+        rows, used = np.arange(len(a))[keep], self.tok[keep]
+        round_h, round_w = 2.0 ** -8 * np.abs(dS), 2.0 ** -8 * np.abs(dS)
+        round_h[rows, used] = 0
+        few = np.bincount(used, minlength=dS.shape[1])[used] <= 4
+        round_w[rows[few], used[few]] = 0
+        for got, want, room, start in ((dH, dS @ self.W, (off + round_h) @ np.abs(self.W), base[0]),
+                                       (dW, dS.T @ self.H, (off + round_w).T @ np.abs(self.H), base[1])):
             if got is None:
                 continue
             got = got.float().cpu().double().numpy()
@@ -98,28 +105,46 @@ def test_explicit_calls(fkl):
     a, b = torch.randn(T).cuda(), torch.randn(T).cuda()
     first = None
     for chunk in (1, 64, 2048, 10 ** 6):
-        dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, chunk, workspace=ws)
+        dH, dW = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, tau, chunk, workspace=ws)
         e.check_gradients(dH, dW, a, b, False)
         if chunk == 2048:
             first = dH, dW
-    again = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 2048)
+    again = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, tau, 2048)
     assert all(torch.equal(x, y) for x, y in zip(first, again))  # the same bits
-    half = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 2048, grad_dtype=torch.bfloat16)
+    half = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, tau, 2048, grad_dtype=torch.bfloat16)
     assert all(torch.equal(x.bfloat16(), y) for x, y in zip(first, half))  # fp32 sums rounded once
     base = torch.randn(T, d).cuda(), torch.randn(V, d).cuda()
     out = base[0].clone(), base[1].clone()
-    fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 512, out=out, accumulate=True)
+    fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, tau, 512, out=out, accumulate=True)
     e.check_gradients(*out, a, b, False, base=tuple(x.cpu().double().numpy() for x in base))
     for only in (0, 1):
         out = [torch.full((T, d), 7.0).cuda(), torch.full((V, d), 7.0).cuda()]
         out[1 - only] = None
-        got = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, tau, 2048, out=tuple(out))
+        got = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, tau, 2048, out=tuple(out))
         assert torch.equal(got[only], first[only]) and got[1 - only] is None
-    dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, None, tau)
+    dH, dW = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, None, tau)
     e.check_gradients(dH, dW, a, torch.zeros(T), False)
-    dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, None, b, tau)
+    dH, dW = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, None, b, tau)
     e.check_gradients(dH, dW, torch.zeros(T), b, False)
     assert fkl.read_status(ws) == 0
+
+
+def test_tokens_that_many_share(fkl):
+    """One to many tokens of a vocabulary row, the same bits each time."""
+    T, d, V = 600, 64, 40
+    H, W, tok, mask = make(T, d, V, seed=2)
+    tok = torch.arange(T).cuda() % 3
+    tok[:30] = torch.arange(30).cuda() // 4 + 10  # rows of 4 tokens, one of 2
+    tok[30:35] = 30                               # one of 5
+    a, b = torch.randn(T).cuda(), torch.randn(T).cuda()
+    for m in (None, mask):
+        e = Exact(H, W, tok, m, 1.0)
+        lp, ent, lse = fkl.logprob_forward(H, W, tok, m)
+        for dtype in (torch.float32, torch.bfloat16):
+            got = fkl.logprob_backward(H, W, tok, m, lp, ent, lse, a, b, grad_dtype=dtype)
+            e.check_gradients(*got, a, b, dtype == torch.bfloat16)
+            again = fkl.logprob_backward(H, W, tok, m, lp, ent, lse, a, b, grad_dtype=dtype)
+            assert all(torch.equal(x, y) for x, y in zip(got, again))
 
 
 def test_frozen_head_and_frozen_states(fkl):
@@ -147,7 +172,7 @@ def test_several_token_blocks(fkl):
     a, b = torch.randn(T).cuda() / 30, torch.randn(T).cuda() / 90
     for dtype in (torch.float32, torch.bfloat16):
         for chunk in (100, 4096):
-            dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, a, b, chunk=chunk, grad_dtype=dtype)
+            dH, dW = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, chunk=chunk, grad_dtype=dtype)
             e.check_gradients(dH, dW, a, b, dtype == torch.bfloat16)
 
 
@@ -169,17 +194,17 @@ def test_tokens_outside_and_rows_left_out(fkl):
     assert torch.isnan(lp[7:9]).all() and torch.isfinite(lp[:7]).all() and torch.isfinite(lp[9:]).all()
     assert torch.isfinite(ent).all()
     one = torch.ones(300).cuda()
-    dH, dW = fkl.logprob_backward(H, W, tok, None, lse, ent, one, None, workspace=ws)
+    dH, dW = fkl.logprob_backward(H, W, tok, None, lp, ent, lse, one, None, workspace=ws)
     assert fkl.read_status(ws) == 6 and torch.isnan(dH).all() and torch.isnan(dW).all()
     mask = torch.ones(300, dtype=torch.uint8).cuda()
     mask[7:9] = 0
     lp, ent, lse = fkl.logprob_forward(H, W, tok, mask, workspace=ws)
     assert fkl.read_status(ws) == 0 and (lp[7:9] == 0).all() and (ent[7:9] == 0).all()
-    dH, dW = fkl.logprob_backward(H, W, tok, mask, lse, ent, one, one, workspace=ws)
+    dH, dW = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, one, one, workspace=ws)
     assert fkl.read_status(ws) == 0 and (dH[7:9] == 0).all() and torch.isfinite(dW).all()
     none = torch.zeros(300, dtype=torch.bool).cuda()
     lp, ent, lse = fkl.logprob_forward(H, W, tok, none)
-    dH, dW = fkl.logprob_backward(H, W, tok, none, lse, ent, one, one)
+    dH, dW = fkl.logprob_backward(H, W, tok, none, lp, ent, lse, one, one)
     assert (lp == 0).all() and (ent == 0).all() and (dH == 0).all() and (dW == 0).all()
 
 
@@ -195,7 +220,7 @@ def test_rows_left_out_may_hold_anything(fkl, T, V):
             outs = []
             for h in (H, bad):
                 lp, ent, lse = fkl.logprob_forward(h, W, tok, mask)
-                outs.append((lp, ent) + fkl.logprob_backward(h, W, tok, mask, lse, ent, a, b, chunk=chunk, grad_dtype=dtype))
+                outs.append((lp, ent) + fkl.logprob_backward(h, W, tok, mask, lp, ent, lse, a, b, chunk=chunk, grad_dtype=dtype))
             for x, y in zip(*outs):
                 assert torch.isfinite(y).all() and torch.equal(x, y)
 
@@ -228,13 +253,13 @@ def test_refusals(fkl):
         fkl.fused_logprobs(H[:, :12].contiguous(), W[:, :12].contiguous(), tok)
     lp, ent, lse = fkl.logprob_forward(H, W, tok)
     with pytest.raises(ValueError):
-        fkl.logprob_backward(H, W, tok, None, lse[:3], ent)
+        fkl.logprob_backward(H, W, tok, None, lp, ent, lse[:3])
     with pytest.raises(ValueError):
-        fkl.logprob_backward(H, W, tok, None, lse, ent, ent.double())
+        fkl.logprob_backward(H, W, tok, None, lp, ent, lse, ent.double())
     with pytest.raises(fkl.FklError):
-        fkl.logprob_backward(H, W, tok, None, lse, ent, ent, chunk=0)
+        fkl.logprob_backward(H, W, tok, None, lp, ent, lse, ent, chunk=0)
     with pytest.raises(fkl.FklError):
-        fkl.logprob_backward(H, W, tok, None, lse, ent, ent, out=(None, None))
+        fkl.logprob_backward(H, W, tok, None, lp, ent, lse, ent, out=(None, None))
 
 
 def test_another_stream_and_a_graph(fkl):
@@ -251,7 +276,7 @@ def test_another_stream_and_a_graph(fkl):
 
     def step(h):
         lp, ent, lse = fkl.logprob_forward(h, W, tok, mask)
-        return (lp, ent) + fkl.logprob_backward(h, W, tok, mask, lse, ent, a, b, grad_dtype=torch.bfloat16)
+        return (lp, ent) + fkl.logprob_backward(h, W, tok, mask, lp, ent, lse, a, b, grad_dtype=torch.bfloat16)
 
     step(h)  # one eager call of the shape, as for the loss
     graphs = [torch.cuda.CUDAGraph() for _ in range(2)]

@@ -57,9 +57,9 @@ def test_fused_sizes_and_checks(L):
             nbytes=1 << 30):
         return L.fkl_logprob_forward(H, W, tok, size, mask, T, d, V, tau, lp, ent, lse, ws, nbytes, None)
 
-    def bwd(H=16, W=16, tok=16, size=4, mask=None, lse=16, ent=16, ga=16, gb=16, T=256, d=256, V=4096, tau=1.0, chunk=64,
+    def bwd(H=16, W=16, tok=16, size=4, mask=None, lp=16, ent=16, lse=16, ga=16, gb=16, T=256, d=256, V=4096, tau=1.0, chunk=64,
             bf16=0, acc=0, dH=16, dW=16, ws=256, nbytes=1 << 40):
-        return L.fkl_logprob_backward(H, W, tok, size, mask, lse, ent, ga, gb, T, d, V, tau, chunk, bf16, acc, dH, dW, ws,
+        return L.fkl_logprob_backward(H, W, tok, size, mask, lp, ent, lse, ga, gb, T, d, V, tau, chunk, bf16, acc, dH, dW, ws,
                                       nbytes, None)
 
     for f in (fwd, bwd):
@@ -68,7 +68,7 @@ def test_fused_sizes_and_checks(L):
         assert f(H=None) == INVALID and f(W=None) == INVALID and f(tok=None) == INVALID and f(lse=None) == INVALID
         assert f(H=24) == ALIGN and f(W=24) == ALIGN and f(tok=18) == ALIGN and f(lse=18) == ALIGN
         assert f(ws=None) == WS and f(nbytes=64) == WS and f(ws=128) == ALIGN
-    assert fwd(lp=None) == INVALID and fwd(ent=None) == INVALID and fwd(lp=18) == ALIGN
+        assert f(lp=None) == INVALID and f(ent=None) == INVALID and f(lp=18) == ALIGN
     assert bwd(chunk=0) == INVALID and bwd(bf16=2) == INVALID and bwd(acc=4) == INVALID and bwd(bf16=1, acc=1) == INVALID
     assert bwd(dH=None, dW=None) == INVALID and bwd(dH=24) == ALIGN and bwd(dW=24) == ALIGN and bwd(ga=18) == ALIGN
 
@@ -109,9 +109,9 @@ def test_binding_refuses_on_the_host():
     with pytest.raises(TypeError):
         fkl.fused_logprobs(torch.zeros(2, 8), torch.zeros(5, 8), tok)
     with pytest.raises(ValueError):
-        fkl.logprob_backward(x, x, tok, None, x, x, accumulate=True)
+        fkl.logprob_backward(x, x, tok, None, x, x, x, accumulate=True)
     with pytest.raises(ValueError):
-        fkl.logprob_backward(x, x, tok, None, x, x, grad_dtype=torch.float16)
+        fkl.logprob_backward(x, x, tok, None, x, x, x, grad_dtype=torch.float16)
     with pytest.raises(ValueError):
         fkl.quantize_cache(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3), 10)
     data = torch.zeros(6, 4, dtype=torch.int32)
