@@ -92,7 +92,7 @@ fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void*
  * The gradient of sum_t (a_t logprob_t + b_t entropy_t): dH [T][d] and dW [V][d], as float or, with
  * grad_bf16 = 1, as bfloat16 bit patterns (fp32 sums rounded once), 16-byte aligned.  One of them may be NULL:
  * its product is left out (a frozen head, say).  The logits are recomputed block by block as in fkl_backward, and `chunk` bounds the buffer of their gradient in the same
- * way: at most chunk * V bfloat16 values.
+ * way: at most chunk * V bfloat16 values (V rounded up to whole tiles of 256).
  *   grad_logprob, grad_entropy   float [T]; NULL = 0
  *   logprob, entropy, lse        the forward's
  *   accumulate   FKL_ACCUMULATE_DH and/or FKL_ACCUMULATE_DW add into float gradients (0 with grad_bf16)

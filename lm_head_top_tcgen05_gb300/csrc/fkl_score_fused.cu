@@ -364,26 +364,78 @@ __global__ void __launch_bounds__(kRowThreads)
 unsigned row_blocks(int64_t T) { return static_cast<unsigned>((T + kRowThreads - 1) / kRowThreads); }
 
 // ---------------------------------------------------------------- planning
-// The loss's plan for one pair a row: its areas of T floats (or more) hold the token's logit and the factors
-// of dS, its partials and dS buffer what they hold there.
+// The loss's plan of the backward's blocks (with one pair a row, whose area is not used here).  It rounds slabs
+// down to whole tiles; a batch that `chunk` takes at once has the whole vocabulary in one slab, rounded up,
+// for the few columns that are left would cost a slab's launches of their own (54 us of 830 for 64 tokens).
 bool score_plan(int64_t T, int64_t d, int64_t V, int64_t chunk, bool bf16, Plan* p) {
-  return make_plan(T, d, V, 1, chunk, p, bf16);
+  if (!make_plan(T, d, V, 1, chunk, p, bf16)) return false;
+  if (T > 0 && T <= chunk && p->nt == 1) {
+    p->Vmax = p->Vc = ceil_div(V, kVocabTile) * kVocabTile;
+    p->nslabs = 1;
+  }
+  return true;
 }
 
-// Workspace of the backward behind the plan's: a block's hidden states without the rows that a mask leaves
-// out, what rounding takes from the tokens' entries, and the tokens of each vocabulary row.
-struct BackwardAreas {
-  size_t clean, rest, count, token_of, total;
+// Partial tiles that dH's units may be cut into.
+constexpr int kPieces = 160;
+
+// The backward's workspace.
+struct Areas {
+  size_t c0, c1, hit, rest;   // float [T]: the factors of dS, its entry at the token and what rounding takes from it
+  size_t count, token_of;     // int [V], int [V][kMaxTargets]: the tokens of each vocabulary row
+  size_t clean;               // bf16 [Ct][d]: a block's hidden states without the rows that a mask leaves out
+  size_t ds;                  // bf16 [Ct][Vmax]
+  size_t pieces;              // fp32 [kPieces][256][256]
+  size_t hsum, wsum;          // bf16 gradients: fp32 sums of dH over slabs and of dW over token blocks (see Plan)
+  size_t total;
 };
-BackwardAreas backward_areas(const Plan& p) {
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  BackwardAreas a;
-  a.clean = p.total;
-  a.rest = up(a.clean + static_cast<size_t>(p.Ct) * p.d * 2);
-  a.count = up(a.rest + static_cast<size_t>(p.T) * 4);
-  a.token_of = up(a.count + static_cast<size_t>(p.V) * 4);
-  a.total = up(a.token_of + static_cast<size_t>(p.V) * kMaxTargets * 4);
+Areas backward_areas(const Plan& p, bool bf16) {
+  size_t off = 256;  // status
+  auto take = [&](int64_t elements, size_t bytes) {
+    const size_t at = off;
+    off = (off + static_cast<size_t>(elements) * bytes + 255) / 256 * 256;
+    return at;
+  };
+  const bool sums = bf16 && p.T > 0;
+  Areas a;
+  a.c0 = take(p.T, 4);
+  a.c1 = take(p.T, 4);
+  a.hit = take(p.T, 4);
+  a.rest = take(p.T, 4);
+  a.count = take(p.V, 4);
+  a.token_of = take(p.V * kMaxTargets, 4);
+  a.clean = take(p.Ct * p.d, 2);
+  a.ds = take(p.Ct * p.Vmax, 2);
+  a.pieces = take(p.T > 0 ? int64_t{kPieces} * 256 * 256 : 0, 4);
+  a.hsum = take(sums ? (p.slab_outer ? p.T : p.Ct) * p.d : 0, 4);
+  a.wsum = take(sums && p.nt > 1 ? (p.slab_outer ? p.Vmax : p.V) * p.d : 0, 4);
+  a.total = off;
   return a;
+}
+
+// Cuts dH's units along K.  Where there are more units than CTA pairs, the last wave's, as in the loss.  Else all of
+// them, into the number of pieces with the least time by this count: a wave's 64-deep steps at 645 cycles with 2500
+// for a tile's start and end, and a pass that adds the pieces up (1024 tokens: 48 units on 76 pairs, 851 us
+// whole and 585 in three pieces each).
+void plan_pieces(GemmShape* g, int pairs, float* pieces) {
+  if (g->num_units >= pairs) {
+    plan_ksplit(g, pairs, pieces, kKsplitSlots);
+    return;
+  }
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= 64 && s * g->num_units <= kPieces && (s == 1 || s * kKsplitMinBlocks <= g->k_blocks); ++s) {
+    const double waves = static_cast<double>(ceil_div(static_cast<int64_t>(g->num_units) * s, pairs));
+    const double time = waves * (ceil_div(g->k_blocks, s) * 645.0 + 2500.0) + (s > 1 ? 8000.0 + 1900.0 * s : 0.0);
+    if (time < least) {
+      least = time;
+      best = s;
+    }
+  }
+  if (best == 1) return;
+  g->split_from = 0;
+  g->ksplit = best;
+  g->kpart = pieces;
 }
 
 // Splits of a row block's vocabulary for the forward.  Up to four row blocks have a unit to each CTA pair and
@@ -473,7 +525,9 @@ struct Backward {
   int sms;
   cudaStream_t st;
   Plan pl;
-  BackwardAreas areas;
+  Areas at;
+  template <class P>
+  P* area(size_t off) const { return reinterpret_cast<P*>(ws + off); }
 };
 
 // One block: tokens [b Ct, ...) x vocabulary columns [j Vc, ...).
@@ -482,13 +536,13 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   const int64_t d = c.d, Vc = pl.Vc, r0 = b * pl.Ct, v0 = j * Vc;
   const int64_t rows = c.T - r0 < pl.Ct ? c.T - r0 : pl.Ct, w = c.V - v0 < Vc ? c.V - v0 : Vc;
   const uint16_t *Hb = c.H + r0 * d, *Wj = c.W + v0 * d;
-  uint16_t* ds = reinterpret_cast<uint16_t*>(c.ws + pl.off_ds);
+  uint16_t* ds = c.area<uint16_t>(c.at.ds);
   uint32_t* status = reinterpret_cast<uint32_t*>(c.ws);
-  float* kpart = reinterpret_cast<float*>(c.ws + pl.off_kpart);
+  float* pieces = c.area<float>(c.at.pieces);
   const int bn = tile_width(d), pairs = c.sms / 2;
   const uint16_t* Hw = Hb;  // what dW multiplies
   if (c.mask != nullptr && c.dW != nullptr) {
-    uint16_t* clean = reinterpret_cast<uint16_t*>(c.ws + c.areas.clean);
+    uint16_t* clean = c.area<uint16_t>(c.at.clean);
     Hw = clean;
     if (j == 0 || (pl.slab_outer && pl.nt > 1)) {  // else it still holds this block's
       clean_rows_kernel<<<static_cast<unsigned>(rows < 8 * c.sms ? rows : 8 * c.sms), kRowThreads, 0, c.st>>>(
@@ -512,9 +566,9 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   ScoreDsParams p;
   p.tokens = c.tokens;
   p.r0 = r0;
-  p.c0 = reinterpret_cast<const float*>(c.ws + pl.off_crow) + r0;
-  p.c1 = reinterpret_cast<const float*>(c.ws + pl.off_wrow) + r0;
-  p.hit = reinterpret_cast<const float*>(c.ws + pl.off_arow) + r0;
+  p.c0 = c.area<const float>(c.at.c0) + r0;
+  p.c1 = c.area<const float>(c.at.c1) + r0;
+  p.hit = c.area<const float>(c.at.hit) + r0;
   p.lse = c.lse + r0;
   p.ds = ds;
   p.ld_ds = Vc;
@@ -527,7 +581,7 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   if (e != cudaSuccess) return fused_cuda(e);
 
   if (c.dW != nullptr) {  // dW[slab] (+)= dS[block]^T H[block], token blocks in order
-    float* wsum = reinterpret_cast<float*>(c.ws + pl.off_wsum) + (pl.slab_outer ? 0 : v0 * d);
+    float* wsum = c.area<float>(c.at.wsum) + (pl.slab_outer ? 0 : v0 * d);
     GemmShape gw = make_shape(w, d, rows, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
     gw.a_box3d = ds3d ? 1 : 0;
     gw.b_box3d = h3d ? 1 : 0;
@@ -537,28 +591,28 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
                         !c.bf16 && (c.accumulate & FKL_ACCUMULATE_DW) != 0);
     pw.wide16 = on_boundary(pw.to.out16, 32) && d % 16 == 0 ? 1 : 0;
     pw.H = c.H;
-    pw.rest = reinterpret_cast<const float*>(c.ws + c.areas.rest);
+    pw.rest = c.area<const float>(c.at.rest);
     // what rounding took is added with the last block's sums
-    pw.count = b == pl.nt - 1 ? reinterpret_cast<const int*>(c.ws + c.areas.count) + v0 : nullptr;
-    pw.token_of = reinterpret_cast<const int*>(c.ws + c.areas.token_of) + v0 * kMaxTargets;
+    pw.count = b == pl.nt - 1 ? c.area<const int>(c.at.count) + v0 : nullptr;
+    pw.token_of = c.area<const int>(c.at.token_of) + v0 * kMaxTargets;
     if ((e = launch_score_dw(bn, ds_cols, h_cols, gw, pw, c.sms, c.st)) != cudaSuccess) return fused_cuda(e);
   }
   if (c.dH == nullptr) return FKL_OK;
 
   // dH[block] = what rounding took from the tokens' entries, + dS[block] W[slab], slabs in order
-  float* hsum = reinterpret_cast<float*>(c.ws + pl.off_hsum) + (pl.slab_outer ? r0 * d : 0);
+  float* hsum = c.area<float>(c.at.hsum) + (pl.slab_outer ? r0 * d : 0);
   GemmShape gh = make_shape(rows, d, w, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
   gh.b_box3d = w3d ? 1 : 0;
   const F32Params ph = destination(rows, d, j, pl.nslabs, static_cast<float*>(c.dH) + (c.bf16 ? 0 : r0 * d),
                                    c.bf16 ? static_cast<uint16_t*>(c.dH) + r0 * d : nullptr, hsum, true);
   if (j == 0) {
     start_rows_kernel<<<static_cast<unsigned>(rows < 8 * c.sms ? rows : 8 * c.sms), kRowThreads, 0, c.st>>>(
-        reinterpret_cast<const uint4*>(c.W), c.tokens, r0, reinterpret_cast<const float*>(c.ws + c.areas.rest) + r0, rows,
+        reinterpret_cast<const uint4*>(c.W), c.tokens, r0, c.area<const float>(c.at.rest) + r0, rows,
         static_cast<int>(d / 8), static_cast<int>(c.V), !c.bf16 && (c.accumulate & FKL_ACCUMULATE_DH) != 0 ? 1 : 0,
         reinterpret_cast<float4*>(ph.out));
     if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
   }
-  plan_ksplit(&gh, pairs, kpart, kKsplitSlots);
+  plan_pieces(&gh, pairs, pieces);
   if ((e = launch_gemm2_f32(bn, false, true, ds_rows, w_cols, gh, ph, c.sms, c.st)) != cudaSuccess ||
       (e = launch_ksplit_fixup(bn, gh, ph, c.st)) != cudaSuccess)
     return fused_cuda(e);
@@ -606,7 +660,7 @@ extern "C" size_t fkl_logprob_workspace_size(int64_t T, int64_t d, int64_t V) {
 
 extern "C" size_t fkl_logprob_backward_workspace_size(int64_t T, int64_t d, int64_t V, int64_t chunk, int32_t grad_bf16) {
   Plan p;
-  return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? backward_areas(p).total : 0;
+  return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? backward_areas(p, grad_bf16 != 0).total : 0;
 }
 
 extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
@@ -664,10 +718,10 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
   set_last_error_message("");
   if (grad_bf16 != 0 && grad_bf16 != 1) return fused_fail(FKL_ERR_INVALID_ARG, "grad_bf16 must be 0 or 1");
   Backward c{H, W, TokenIds{tokens, token_bytes}, mask, lse, T, d, V, tau, accumulate, grad_bf16 == 1, dH, dW,
-             static_cast<uint8_t*>(workspace), 0, static_cast<cudaStream_t>(stream), Plan{}, BackwardAreas{}};
+             static_cast<uint8_t*>(workspace), 0, static_cast<cudaStream_t>(stream), Plan{}, Areas{}};
   if (!score_plan(T, d, V, chunk, c.bf16, &c.pl)) return fused_fail(FKL_ERR_INVALID_ARG, kShapeRule);
-  c.areas = backward_areas(c.pl);
-  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, c.areas.total);
+  c.at = backward_areas(c.pl, c.bf16);
+  fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, c.at.total);
   if (s != FKL_OK) return s;
   if (accumulate < 0 || accumulate > 3) return fused_fail(FKL_ERR_INVALID_ARG, "bad accumulate");
   if (c.bf16 && accumulate != 0) return fused_fail(FKL_ERR_INVALID_ARG, "bf16 gradients do not accumulate");
@@ -691,13 +745,11 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
     return FKL_OK;
   }
   choose_slab_width(&c.pl, c.sms / 2);
-  const BackwardAreas& ar = c.areas;
-  if ((e = cudaMemsetAsync(c.ws + ar.count, 0, static_cast<size_t>(V) * 4, c.st)) != cudaSuccess) return fused_cuda(e);
+  if ((e = cudaMemsetAsync(c.ws + c.at.count, 0, static_cast<size_t>(V) * 4, c.st)) != cudaSuccess) return fused_cuda(e);
   score_factors_kernel<<<row_blocks(T), kRowThreads, 0, c.st>>>(
       c.tokens, mask, logprob, entropy, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau, &hdr->status,
-      reinterpret_cast<float*>(c.ws + c.pl.off_crow), reinterpret_cast<float*>(c.ws + c.pl.off_wrow),
-      reinterpret_cast<float*>(c.ws + c.pl.off_arow), reinterpret_cast<float*>(c.ws + ar.rest),
-      reinterpret_cast<int*>(c.ws + ar.count), reinterpret_cast<int*>(c.ws + ar.token_of));
+      c.area<float>(c.at.c0), c.area<float>(c.at.c1), c.area<float>(c.at.hit), c.area<float>(c.at.rest),
+      c.area<int>(c.at.count), c.area<int>(c.at.token_of));
   if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
   const Plan& pl = c.pl;
   for (int64_t o = 0; o < (pl.slab_outer ? pl.nslabs : pl.nt); ++o)
