@@ -322,6 +322,15 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// Few tokens' hidden states with rows of zeros behind them, kLeastRows in all.
+constexpr int kLeastRows = 64;
+__global__ void __launch_bounds__(kRowThreads)
+    pad_rows_kernel(const uint4* __restrict__ H, int rows, int per_row, uint4* __restrict__ out) {
+  const int t = static_cast<int>(blockIdx.x);
+  for (int i = static_cast<int>(threadIdx.x); i < per_row; i += kRowThreads)
+    out[t * per_row + i] = t < rows ? H[t * per_row + i] : make_uint4(0u, 0u, 0u, 0u);
+}
+
 // Where dH's sums start: rest_t W[v*_t] (added to what is there where `add`).  8 values a thread.
 __global__ void __launch_bounds__(kRowThreads)
     start_rows_kernel(const uint4* __restrict__ W, TokenIds tokens, int64_t r0, const float* __restrict__ rest, int64_t rows,
@@ -383,6 +392,7 @@ constexpr int kPieces = 160;
 struct Areas {
   size_t c0, c1, hit, rest;   // float [T]: the factors of dS, its entry at the token and what rounding takes from it
   size_t count, token_of;     // int [V], int [V][kMaxTargets]: the tokens of each vocabulary row
+  size_t few;                 // bf16 [kLeastRows][d]: see map_tokens
   size_t clean;               // bf16 [Ct][d]: a block's hidden states without the rows that a mask leaves out
   size_t ds;                  // bf16 [Ct][Vmax]
   size_t pieces;              // fp32 [kPieces][256][256]
@@ -404,6 +414,7 @@ Areas backward_areas(const Plan& p, bool bf16) {
   a.rest = take(p.T, 4);
   a.count = take(p.V, 4);
   a.token_of = take(p.V * kMaxTargets, 4);
+  a.few = take(p.T > 0 ? kLeastRows * p.d : 0, 2);
   a.clean = take(p.Ct * p.d, 2);
   a.ds = take(p.Ct * p.Vmax, 2);
   a.pieces = take(p.T > 0 ? int64_t{kPieces} * 256 * 256 : 0, 4);
@@ -436,6 +447,20 @@ void plan_pieces(GemmShape* g, int pairs, float* pieces) {
   g->split_from = 0;
   g->ksplit = best;
   g->kpart = pieces;
+}
+
+// Map of the hidden states as the projection's A operand.  Few tokens are padded in the workspace (`room`:
+// kLeastRows x d): loading the same few rows for every tile, the product of one token with a 201088 x 2880 head took 282
+// us, of 64 tokens 199.
+cudaError_t map_tokens(CUtensorMap* map, const uint16_t* H, int64_t rows, int64_t d, uint16_t* room, cudaStream_t st) {
+  if (rows < kLeastRows) {
+    pad_rows_kernel<<<kLeastRows, kRowThreads, 0, st>>>(reinterpret_cast<const uint4*>(H), static_cast<int>(rows),
+                                                        static_cast<int>(d / 8), reinterpret_cast<uint4*>(room));
+    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    H = room;
+    rows = kLeastRows;
+  }
+  return encode_map_bf16(map, H, d, rows, d * 2, 64, 128) ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 // Splits of a row block's vocabulary for the forward.  Up to four row blocks have a unit to each CTA pair and
@@ -554,7 +579,9 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   bool h3d = false, w3d = false;
   // dS has zeros in the columns [w, round_up(w, 256)) of every row, so its 3-D view may span round_up(w, 64)
   const bool ds3d = encode_map_mn3d(&ds_cols, ds, ceil_div(w, 64) * 64, rows, Vc * 2, 128);
-  if (!encode_map_bf16(&h_rows, Hb, d, rows, d * 2, 64, 128) || !map_columns(&h_cols, Hw, d, rows, bn, &h3d) ||
+  cudaError_t e = map_tokens(&h_rows, Hb, rows, d, c.area<uint16_t>(c.at.few), c.st);
+  if (e != cudaSuccess) return fused_cuda(e);
+  if (!map_columns(&h_cols, Hw, d, rows, bn, &h3d) ||
       !encode_map_bf16(&w_rows, Wj, d, w, d * 2, 64, kVocabTile / 2) || !map_columns(&w_cols, Wj, d, w, bn, &w3d) ||
       (!ds3d && !encode_map_bf16(&ds_cols, ds, w, rows, Vc * 2, 64, 64)) ||
       !encode_map_bf16(&ds_rows, ds, w, rows, Vc * 2, 64, 128))
@@ -577,12 +604,15 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   p.v0 = static_cast<int>(v0);
   p.slab_w = static_cast<int>(w);
   p.scale2 = kLog2e / c.tau;
-  cudaError_t e = launch_gemm2_t<kVocabTile, false, false, EpiScoreDs>(h_rows, w_rows, g, p, c.sms, c.st);
-  if (e != cudaSuccess) return fused_cuda(e);
+  if ((e = launch_gemm2_t<kVocabTile, false, false, EpiScoreDs>(h_rows, w_rows, g, p, c.sms, c.st)) != cudaSuccess)
+    return fused_cuda(e);
 
   if (c.dW != nullptr) {  // dW[slab] (+)= dS[block]^T H[block], token blocks in order
     float* wsum = c.area<float>(c.at.wsum) + (pl.slab_outer ? 0 : v0 * d);
-    GemmShape gw = make_shape(w, d, rows, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
+    // Few tokens' tiles are short: four to a unit share its start (64 tokens, dW alone 557 -> 502 us; beyond
+    // 256 tokens a unit of one tile balances better, 512 tokens 798 against 833).
+    const int64_t d_tiles = ceil_div(d, bn);
+    GemmShape gw = make_shape(w, d, rows, bn, static_cast<int>(rows <= 256 ? ceil_div(d_tiles, 4) : d_tiles), status, 256);
     gw.a_box3d = ds3d ? 1 : 0;
     gw.b_box3d = h3d ? 1 : 0;
     DwParams pw;
@@ -636,7 +666,7 @@ constexpr char kShapeRule[] = "unsupported shape (need 0 <= T < 2^31, d % 8 == 0
 
 // Workspace of the forward: the status, the partials of the splits and the tokens' logits.
 struct ForwardPlan {
-  size_t part, token_s, total;
+  size_t part, token_s, few, total;
 };
 bool forward_plan(int64_t T, int64_t d, int64_t V, ForwardPlan* p) {
   Plan pl;
@@ -644,7 +674,8 @@ bool forward_plan(int64_t T, int64_t d, int64_t V, ForwardPlan* p) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p->part = 256;
   p->token_s = up(p->part + static_cast<size_t>(T) * 3 * split_room(T) * 4);
-  p->total = up(p->token_s + static_cast<size_t>(T) * 4);
+  p->few = up(p->token_s + static_cast<size_t>(T) * 4);
+  p->total = up(p->few + (T > 0 ? static_cast<size_t>(kLeastRows) * d * 2 : 0));
   return true;
 }
 
@@ -688,7 +719,8 @@ extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, 
   if (e != cudaSuccess) return fused_cuda(e);
   if (T == 0) return FKL_OK;
   CUtensorMap mH, mW;
-  if (!encode_map_bf16(&mH, H, d, T, d * 2, 64, 128) || !encode_map_bf16(&mW, W, d, V, d * 2, 64, kVocabTile / 2))
+  if ((e = map_tokens(&mH, H, T, d, reinterpret_cast<uint16_t*>(ws + pl.few), st)) != cudaSuccess) return fused_cuda(e);
+  if (!encode_map_bf16(&mW, W, d, V, d * 2, 64, kVocabTile / 2))
     return fused_fail(FKL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   const int m_tiles = static_cast<int>(ceil_div(T, 256)), n_tiles = static_cast<int>(ceil_div(V, kVocabTile));
   GemmShape g = make_shape(T, V, d, kVocabTile, forward_splits(m_tiles, n_tiles, sms / 2), &hdr->status, 256);
