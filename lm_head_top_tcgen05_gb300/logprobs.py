@@ -21,6 +21,7 @@ PyTorch's allocator for as long as it runs, so calls of several threads, streams
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
@@ -185,6 +186,22 @@ def _floats(t: Optional[torch.Tensor], name: str, T: int, device) -> Optional[to
     return t.detach().contiguous()
 
 
+@functools.lru_cache(maxsize=1024)
+def _forward_bytes(T: int, d: int, V: int) -> int:
+    n = lib().fkl_logprob_workspace_size(T, d, V)
+    if n == 0:
+        raise FklError(1, "fkl_logprob_workspace_size", f"unsupported shape T={T} d={d} V={V}")
+    return n
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_bytes(T: int, d: int, V: int, chunk: int, bf16: int) -> int:
+    n = lib().fkl_logprob_backward_workspace_size(T, d, V, chunk, bf16)
+    if n == 0:
+        raise FklError(1, "fkl_logprob_backward_workspace_size", f"unsupported shape T={T} d={d} V={V} chunk={chunk}")
+    return n
+
+
 def logprob_forward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor] = None,
                     tau: float = 1.0, workspace=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(logprob, entropy, lse), float32 [T], of ``tokens`` [T] under softmax(H W^T / tau); lse is that of every row,
@@ -192,15 +209,28 @@ def logprob_forward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask
     outside [0, V) does in its row; ``read_status(workspace)`` tells."""
     size, mask = _operands(H, W, tokens, mask)
     (T, d), V, device = H.shape, W.shape[0], H.device
-    n = lib().fkl_logprob_workspace_size(T, d, V)
-    if n == 0:
-        raise FklError(1, "fkl_logprob_workspace_size", f"unsupported shape T={T} d={d} V={V}")
-    ws = _scratch(workspace, int(n), device)
-    out = [torch.empty(T, dtype=torch.float32, device=device) for _ in range(3)]
+    ws = _scratch(workspace, _forward_bytes(T, d, V), device)
+    logprob = torch.empty(T, dtype=torch.float32, device=device)
+    entropy = torch.empty(T, dtype=torch.float32, device=device)
+    lse = torch.empty(T, dtype=torch.float32, device=device)
     st = lib().fkl_logprob_forward(H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), T, d, V,
-                                   float(tau), *(t.data_ptr() for t in out), ws.data_ptr(), ws.numel(), _stream(device))
+                                   float(tau), logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                   ws.numel(), _stream(device))
     check(st, "fkl_logprob_forward")
-    return tuple(out)
+    return logprob, entropy, lse
+
+
+def _launch_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, tau, chunk, out, bf16, flags,
+                     workspace):
+    (T, d), V, device = H.shape, W.shape[0], H.device
+    if T == 0 and out[1] is None:  # nothing to write, and no address to say so with
+        return
+    ws = _scratch(workspace, _backward_bytes(T, d, V, chunk, bf16), device)
+    st = lib().fkl_logprob_backward(
+        H.data_ptr(), W.data_ptr(), tokens.data_ptr(), _TOKEN_BYTES[tokens.dtype], _address(mask), logprob.data_ptr(),
+        entropy.data_ptr(), lse.data_ptr(), _address(grad_logprob), _address(grad_entropy), T, d, V, float(tau), chunk, bf16,
+        flags, _address(out[0]), _address(out[1]), ws.data_ptr(), ws.numel(), _stream(device))
+    check(st, "fkl_logprob_backward")
 
 
 def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor],
@@ -220,8 +250,8 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
     bf16 = grad_dtype == torch.bfloat16
     if accumulate and (bf16 or out is None):
         raise ValueError("accumulate=True adds into float32 gradients given in `out`")
-    size, mask = _operands(H, W, tokens, mask)
-    (T, d), V, device = H.shape, W.shape[0], H.device
+    _, mask = _operands(H, W, tokens, mask)
+    T, device = H.shape[0], H.device
     logprob, entropy = _floats(logprob, "logprob", T, device), _floats(entropy, "entropy", T, device)
     lse = _floats(lse, "lse", T, device)
     grad_logprob = _floats(grad_logprob, "grad_logprob", T, device)
@@ -231,42 +261,42 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
     for g, t in zip(out, (H, W)):
         if g is not None and (g.dtype != grad_dtype or g.shape != t.shape or not g.is_contiguous() or g.device != device):
             raise ValueError(f"out gradients must be contiguous {grad_dtype} {tuple(t.shape)} on {device}")
-    if T == 0 and out[1] is None:  # nothing to write, and no address to say so with
-        return out
-    n = lib().fkl_logprob_backward_workspace_size(T, d, V, chunk, int(bf16))
-    if n == 0:
-        raise FklError(1, "fkl_logprob_backward_workspace_size", f"unsupported shape T={T} d={d} V={V} chunk={chunk}")
-    ws = _scratch(workspace, int(n), device)
     flags = (FKL_ACCUMULATE_DH | FKL_ACCUMULATE_DW) if accumulate else 0
-    st = lib().fkl_logprob_backward(
-        H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), logprob.data_ptr(), entropy.data_ptr(),
-        lse.data_ptr(), _address(grad_logprob), _address(grad_entropy), T, d, V, float(tau), chunk, int(bf16), flags, _address(out[0]),
-        _address(out[1]), ws.data_ptr(), ws.numel(), _stream(device))
-    check(st, "fkl_logprob_backward")
+    _launch_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, tau, chunk, out, int(bf16),
+                     flags, workspace)
     return out
 
 
+def _fused_backward(ctx, grad_logprob, grad_entropy):
+    H, W, tokens, mask, logprob, entropy, lse = ctx.saved_tensors
+    if grad_logprob is None and grad_entropy is None:
+        return None, None, None, None, None, None
+    need = ctx.needs_input_grad
+    out = (torch.empty_like(H) if need[0] else None, torch.empty_like(W) if need[1] else None)
+    grad_logprob = None if grad_logprob is None else grad_logprob.contiguous()
+    grad_entropy = None if grad_entropy is None else grad_entropy.contiguous()
+    _launch_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, ctx.tau, ctx.chunk, out, 1, 0,
+                     None)
+    return out[0], out[1], None, None, None, None
+
+
+_fused_backward_once = once_differentiable(_fused_backward)
+
+
 class _FusedLogprobs(torch.autograd.Function):
-    """Saves lse and the entropies; the backward recomputes the projection block by block."""
+    """Saves the forward's three vectors; the backward recomputes the projection block by block."""
 
     @staticmethod
     def forward(ctx, H, W, tokens, mask, tau, chunk):
         logprob, entropy, lse = logprob_forward(H, W, tokens, mask, tau)
-        ctx.save_for_backward(H, W, tokens, mask, logprob, entropy, lse)
+        ctx.save_for_backward(H, W, tokens, _mask(mask, H.shape[0], H.device), logprob, entropy, lse)
         ctx.tau, ctx.chunk = tau, chunk
         ctx.set_materialize_grads(False)
         return logprob, entropy
 
     @staticmethod
-    @once_differentiable
-    def backward(ctx, grad_logprob, grad_entropy):
-        H, W, tokens, mask, logprob, entropy, lse = ctx.saved_tensors
-        if grad_logprob is None and grad_entropy is None:
-            return None, None, None, None, None, None
-        out = tuple(torch.empty_like(t) if need else None for t, need in zip((H, W), ctx.needs_input_grad))
-        dH, dW = logprob_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, ctx.tau,
-                                  ctx.chunk, out=out, grad_dtype=torch.bfloat16)
-        return dH, dW, None, None, None, None
+    def backward(ctx, *grads):
+        return _fused_backward_once(ctx, *grads) if torch.is_grad_enabled() else _fused_backward(ctx, *grads)
 
 
 def fused_logprobs(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor] = None,

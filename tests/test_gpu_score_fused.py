@@ -237,6 +237,14 @@ def test_empty_batch_with_a_frozen_head(fkl):
     assert (Wl.grad == 0).all()
 
 
+def test_a_second_derivative_is_refused(fkl):
+    H, W, tok, _ = make(20, 64, 100)
+    Hl = H.clone().requires_grad_()
+    dH, = torch.autograd.grad(fkl.fused_logprobs(Hl, W, tok)[0].sum(), Hl, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dH.float().sum().backward()
+
+
 def test_refusals(fkl):
     H, W, tok, mask = make(20, 64, 100)
     with pytest.raises(TypeError):
