@@ -1,13 +1,15 @@
 """On-policy distillation in small: a student draws its own text through an 8-bit head, a
 teacher scores the positions, and the student takes a step of the fused KL loss on them.
 
-    python examples/on_policy.py [--steps 3] [--batch 8] [--length 64]
+    python examples/on_policy.py [--steps 3] [--batch 8] [--length 64] [--cache-bits 8] [--entropy 0.01]
 
 The "models" are random tables, one hidden state per previous token, so that the example shows
 the calls and not a network: what a real trunk would compute is `hidden(tokens)`.  Each drawn
 token is one `draw_token` (8-bit product of the LM head, then the sampler); the teacher's
-top-K cache comes from `teacher_topk`, and `fused_kl` gives the loss and the gradients of the
-student's hidden states and head.  After each step the head is brought to 8 bits again.
+top-K cache comes from `teacher_topk` (or, with --cache-bits 8 or 4, packed from `teacher_cache`), and
+`fused_kl` gives the loss and the gradients of the student's hidden states and head.  With --entropy B the
+step adds B times the student's mean entropy (`fused_logprobs`).  After each step the head is brought to
+8 bits again.
 """
 import argparse
 import os
@@ -52,6 +54,8 @@ def main(argv=None):
     a.add_argument("--width", type=int, default=256)
     a.add_argument("--top-k", type=int, default=64)
     a.add_argument("--lr", type=float, default=20.0)
+    a.add_argument("--cache-bits", type=int, default=0, choices=(0, 4, 8))
+    a.add_argument("--entropy", type=float, default=0.0)
     a = a.parse_args(argv)
     device = torch.device("cuda", torch.cuda.current_device())
     g = torch.Generator(device=device).manual_seed(0)
@@ -63,17 +67,26 @@ def main(argv=None):
         tokens, logs = generate(student, head8, start, a.length, g, temperature=0.9, top_p=0.95)
         assert (tokens >= 0).all()  # -1: a row without a logit to draw from, as a failed product leaves
         seen = torch.cat([start[:, None], tokens[:, :-1]], 1).reshape(-1)  # the states the tokens came from
-        ids, values = fkl.teacher_topk(teacher.hidden(seen).contiguous(), teacher.head, a.top_k)
+        Ht = teacher.hidden(seen).contiguous()
+        if a.cache_bits:
+            cache = (fkl.teacher_cache(Ht, teacher.head, a.top_k, bits=a.cache_bits),)
+        else:
+            cache = fkl.teacher_topk(Ht, teacher.head, a.top_k)
         H = student.hidden(seen).contiguous().requires_grad_()
         W = student.head.clone().requires_grad_()
-        loss = fkl.fused_kl(H, W, ids, values)
-        loss.backward()
+        loss = fkl.fused_kl(H, W, *cache)
+        total = loss
+        if a.entropy:
+            total = loss - a.entropy * fkl.fused_logprobs(H, W, tokens.reshape(-1))[1].mean()
+        total.backward()
         assert fkl.read_status(device=device) == 0
         with torch.no_grad():
             student.head = (student.head.float() - a.lr * W.grad.float()).to(torch.bfloat16)
             student.rows.index_add_(0, seen.long(), (-a.lr * H.grad.float()).to(torch.bfloat16))
         losses.append(loss.item())
-        print(f"step {step}: loss {losses[-1]:.4f}, drawn log-probability {logs.mean().item():.3f}")
+        judged, _ = fkl.fused_logprobs(Ht, teacher.head, tokens.reshape(-1))
+        print(f"step {step}: loss {losses[-1]:.4f}, drawn log-probability {logs.mean().item():.3f}, "
+              f"the teacher's {judged.mean().item():.3f}")
     return losses
 
 
