@@ -6,7 +6,8 @@
 // threads that walk their groups together then touch all 32 banks once.  A block's rows, and its records, are
 // one stretch of memory each, moved 16 bytes a thread where K and the pointers allow it, else 4.
 // A lane per slot, with warp reductions for a group's range and shuffles to assemble words, was the first form: 250
-// instructions to 32 slots against about 30 here, and the instructions were what it took its time for.
+// instructions to 32 slots against about 50 here, and the instructions were what it took its time for.  They
+// still are (63 % of issue slots): 262144 x 100 slots in 8 bits take 70 us to write (4.3 TB/s) and 58 to read (5.2).
 #include <climits>
 #include <cmath>
 #include <type_traits>

@@ -17,6 +17,11 @@
 //
 // Backward.  dx_v = ( q_v (c0 + c1 log2 q_v) + a 1[v = v*] ) / T with c0 = -(a + b entropy), c1 = -b ln 2,
 // q_v = 2^((x_v - M) log2(e) / T - log2 L), one pass that reads the logits and writes their gradient.
+//
+// What bounds it (GB300, on the device).  Many rows: HBM for fp32 (512 x 201088: 61 us, 6.7 TB/s), for 16 bits the 9
+// instructions of a logit beside it (2048 x 128256 bf16: 87 us, 6.0 TB/s; 512 x 151936: 31 us, 5.0 TB/s, as all
+// rows run at once and end together).  Few rows: latency (1 x 201088 fp32 4.4 us, with 20 alternatives 7.8).  The
+// gradient runs at the rate of a copy (2048 x 128256 bf16: 149 us, 7.1 TB/s).
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -70,8 +75,8 @@ __device__ __forceinline__ u64 rank_key(float x, int id) {
 __device__ __forceinline__ float key_logit(u64 k) { return order_value(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int key_id(u64 k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
-// A row as 16-byte vectors.  The row may start inside a vector and end inside one: those two
-// (`skip` > 0, `tail` > 0) are read element by element, the others lie in [first, last).
+// A row as 16-byte vectors.  The row may start inside a vector (`skip` elements from its start) and end inside
+// one: those two are read element by element, the others lie in [first, last).
 template <class T>
 struct RowView {
   static constexpr int kN = 16 / static_cast<int>(sizeof(T));
