@@ -7,7 +7,7 @@
 // one stretch of memory each, moved 16 bytes a thread where K and the pointers allow it, else 4.
 // A lane per slot, with warp reductions for a group's range and shuffles to assemble words, was the first form: 250
 // instructions to 32 slots against about 50 here, and the instructions were what it took its time for.  They
-// still are (63 % of issue slots): 262144 x 100 slots in 8 bits take 70 us to write (4.3 TB/s) and 58 to read (5.2).
+// still are (63 % of issue slots): 262144 x 100 slots in 8 bits take 62 us to write (4.9 TB/s) and 56 to read (5.4).
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -26,6 +26,7 @@ constexpr int kStride = kGroup + 4;
 
 struct Format {
   int K, V, bits, id_bits, groups, code_words, id_words, words;
+  int full;  // groups of a row with all of their slots
   int rows;  // of a block: kThreads groups, and records that fit their slots' shared memory
 };
 
@@ -37,6 +38,7 @@ bool make_format(int64_t K, int64_t V, int32_t bits, Format* f) {
   f->id_bits = 1;
   while ((int64_t{1} << f->id_bits) <= V) ++f->id_bits;  // at most 31
   f->groups = static_cast<int>((K + kGroup - 1) / kGroup);
+  f->full = static_cast<int>(K / kGroup);
   f->code_words = static_cast<int>((K * bits + 31) / 32);
   f->id_words = static_cast<int>((K * f->id_bits + 31) / 32);
   f->words = 2 * f->groups + f->code_words + f->id_words;
@@ -62,6 +64,19 @@ __device__ __noinline__ uint32_t exact_level(float top, float z, float low, floa
   return static_cast<uint32_t>(rint(down * levels / span));
 }
 
+// A block's groups in the order of its threads: the full groups of its rows, then each row's last, shorter one, so that
+// whole warps have the short ones and stop early.
+struct Task {
+  int r, g, slots;
+  __device__ __forceinline__ Task(const Format& f, int rows) {
+    const int tid = static_cast<int>(threadIdx.x), fulls = f.rows * f.full;
+    r = tid < fulls ? tid / f.full : tid - fulls;
+    g = tid < fulls ? tid - r * f.full : f.full;
+    slots = r < rows ? max(min(kGroup, f.K - g * kGroup), 0) : 0;
+  }
+};
+__device__ __forceinline__ int task_of(const Format& f, int r, int g) { return g < f.full ? r * f.full + g : f.rows * f.full + r; }
+
 // Calls f(unit, place) for the thread's share of a block's slots, which are one stretch of memory: units of kUnit
 // slots, and where the unit lies among the groups in shared memory.
 template <int kUnit, class F>
@@ -71,7 +86,7 @@ __device__ __forceinline__ void for_slots(const Format& f, int rows, F&& fn) {
   int r = static_cast<int>(threadIdx.x) / per_row, k = static_cast<int>(threadIdx.x) - r * per_row;
   for (int u = static_cast<int>(threadIdx.x); u < units; u += kThreads) {
     const int slot = k * kUnit;
-    fn(u * kUnit, (r * f.groups + slot / kGroup) * kStride + slot % kGroup);
+    fn(u * kUnit, task_of(f, r, slot / kGroup) * kStride + slot % kGroup);
     r += rows_on;
     k += on;
     if (k >= per_row) {
@@ -95,9 +110,9 @@ __global__ void __launch_bounds__(kThreads, 6)
   const int tid = static_cast<int>(threadIdx.x);
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * f.rows;
   const int rows = static_cast<int>(T - t0 < f.rows ? T - t0 : f.rows);
-  const int r = tid / f.groups, g = tid - r * f.groups;
-  const bool on = r < rows;  // a row of the block, and of the cache
-  const int slots = on ? min(kGroup, f.K - g * kGroup) : 0;
+  const Task task(f, rows);
+  const int r = task.r, g = task.g, slots = task.slots, quads = (slots + 3) / 4;
+  const bool on = slots > 0;
   const float* zr = logits + t0 * f.K;
   const int32_t* ir = idx + t0 * f.K;
   for_slots<kVec ? 4 : 1>(f, rows, [&](int i, int at) {
@@ -109,32 +124,40 @@ __global__ void __launch_bounds__(kThreads, 6)
       copy4_async(id_part + at, ir + i);
     }
   });
-  for (int j = slots; j < kGroup; ++j) z_part[tid * kStride + j] = -INFINITY;  // behind the row's last slot
+  for (int j = slots; j < 4 * quads; ++j) z_part[tid * kStride + j] = -INFINITY;  // behind the row's last slot
   copy_async_wait();
   __syncthreads();
 
   const float4* mine = reinterpret_cast<const float4*>(&z_part[tid * kStride]);
-  float largest = -INFINITY;
+  // Calls fn(j, slots 4 j to 4 j + 3), straight through in a warp of full groups.
+  const bool fulls = __all_sync(0xffffffffu, quads == kGroup / 4);
+  auto for_quads = [&](auto&& fn) {
+    if (fulls) {
 #pragma unroll
-  for (int j = 0; j < kGroup / 4; ++j) {
-    const float4 v = mine[j];
-    largest = max_nan(max_nan(largest, max_nan(v.x, v.y)), max_nan(v.z, v.w));
-  }
+      for (int j = 0; j < kGroup / 4; ++j) fn(j, mine[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kGroup / 4; ++j) {
+        if (j >= quads) break;
+        fn(j, mine[j]);
+      }
+    }
+  };
+  float largest = -INFINITY;
+  for_quads([&](int, const float4& v) { largest = max_nan(max_nan(largest, max_nan(v.x, v.y)), max_nan(v.z, v.w)); });
   group_max[tid] = largest;
   __syncthreads();
   float row_max = -INFINITY;
   if (on)
-    for (int i = 0; i < f.groups; ++i) row_max = max_nan(row_max, group_max[r * f.groups + i]);
+    for (int i = 0; i < f.groups; ++i) row_max = max_nan(row_max, group_max[task_of(f, r, i)]);
   const bool bad = !(row_max < INFINITY);                               // a NaN or +inf
   const float least = fmaxf(row_max - kSpan, -3.40282347e38f);          // -inf does not reach it
   const bool some = !bad && largest >= least;
   float low = INFINITY;
-#pragma unroll
-  for (int j = 0; j < kGroup / 4; ++j) {
-    const float4 v = mine[j];
+  for_quads([&](int, const float4& v) {
     low = fminf(fminf(low, v.x >= least ? v.x : INFINITY), v.y >= least ? v.y : INFINITY);
     low = fminf(fminf(low, v.z >= least ? v.z : INFINITY), v.w >= least ? v.w : INFINITY);
-  }
+  });
   const float top = some ? largest : 0.f, span = some ? top - low : 0.f;
   const float floor = some ? least : NAN;  // no slot reaches it where there is none
   const float per_level = span > 0.f ? kLevels / span : 0.f;
@@ -151,23 +174,20 @@ __global__ void __launch_bounds__(kThreads, 6)
   };
   uint32_t codes[kBits], open = 0;
 #pragma unroll
-  for (int w = 0; w < kBits; ++w) {
+  for (int w = 0; w < kBits; ++w) codes[w] = 0;
+  for_quads([&](int quad, const float4& v) {
+    const float x[4] = {v.x, v.y, v.z, v.w};
     uint32_t word = 0;
 #pragma unroll
-    for (int q = 0; q < kPerWord; q += 4) {
-      const float4 v = mine[(w * kPerWord + q) / 4];
-      const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float t;
-        const float n = level(x[i], t);
-        const bool has = x[i] >= floor;
-        if (has && !(fabsf(t - (n - kRound)) < kNear)) open |= 1u << (w * kPerWord + q + i);
-        word += ((has ? __float_as_uint(n) : kRoundBits + kNone) - kRoundBits) << ((q + i) * kBits);
-      }
+    for (int i = 0; i < 4; ++i) {
+      float t;
+      const float n = level(x[i], t);
+      const bool has = x[i] >= floor;
+      if (has && !(fabsf(t - (n - kRound)) < kNear)) open |= 1u << (quad * 4 + i);
+      word += ((has ? __float_as_uint(n) : kRoundBits + kNone) - kRoundBits) << (i * kBits);
     }
-    codes[w] = word;
-  }
+    codes[quad * 4 / kPerWord] += word << (quad * 4 % kPerWord * kBits);
+  });
   while (open != 0) {
     const int j = __ffs(open) - 1;
     open &= open - 1;
@@ -246,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 6)
   copy_async_wait();
   __syncthreads();
 
-  const int r = tid / f.groups, g = tid - r * f.groups;
-  const int slots = r < rows ? min(kGroup, f.K - g * kGroup) : 0;
+  const Task task(f, rows);
+  const int r = task.r, g = task.g, slots = task.slots;
   float top = 0.f, step = 0.f;
   uint32_t codes[kBits];
   if (slots > 0) {
@@ -288,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 6)
     const float none = top == top ? -INFINITY : NAN;
 #pragma unroll
     for (int j = 0; j < kGroup; j += 4) {
+      if (j >= slots) break;
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

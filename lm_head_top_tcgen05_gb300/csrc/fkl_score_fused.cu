@@ -410,11 +410,11 @@ Areas backward_areas(const Plan& p, bool bf16) {
   };
   const bool sums = bf16 && p.T > 0;
   Areas a;
+  a.count = take(p.V, 4);  // zeroed with the status before it
   a.c0 = take(p.T, 4);
   a.c1 = take(p.T, 4);
   a.hit = take(p.T, 4);
   a.rest = take(p.T, 4);
-  a.count = take(p.V, 4);
   a.token_of = take(p.V * kMaxTargets, 4);
   a.few = take(p.T > 0 ? kLeastRows * p.d : 0, 2);
   a.clean = take(p.Ct * p.d, 2);
@@ -770,7 +770,7 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
                            {workspace, "workspace"}};
   if (const int e = check_device_memory(ptrs); e != FKL_OK) return static_cast<fkl_status>(e);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(c.ws);
-  cudaError_t e = cudaMemsetAsync(c.ws, 0, 256, c.st);
+  cudaError_t e = cudaMemsetAsync(c.ws, 0, T > 0 ? c.at.count + static_cast<size_t>(V) * 4 : 256, c.st);
   if (e != cudaSuccess) return fused_cuda(e);
   if (T == 0) {
     if (dW != nullptr && !(accumulate & FKL_ACCUMULATE_DW) &&
@@ -779,7 +779,6 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
     return FKL_OK;
   }
   choose_slab_width(&c.pl, c.sms / 2);
-  if ((e = cudaMemsetAsync(c.ws + c.at.count, 0, static_cast<size_t>(V) * 4, c.st)) != cudaSuccess) return fused_cuda(e);
   score_factors_kernel<<<row_blocks(T), kRowThreads, 0, c.st>>>(
       c.tokens, mask, logprob, entropy, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau, &hdr->status,
       c.area<float>(c.at.c0), c.area<float>(c.at.c1), c.area<float>(c.at.hit), c.area<float>(c.at.rest),
