@@ -324,52 +324,67 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// Few tokens' hidden states with rows of zeros behind them, kLeastRows in all.
+// A product of few rows loads the same few lines for every tile: such rows are padded with zeros to kLeastRows (one
+// token against a 201088 x 2880 head took 282 us, 64 tokens 199).
 constexpr int kLeastRows = 64;
-__global__ void __launch_bounds__(kRowThreads)
-    pad_rows_kernel(const uint4* __restrict__ H, int rows, int per_row, uint4* __restrict__ out) {
-  const int t = static_cast<int>(blockIdx.x);
-  for (int i = static_cast<int>(threadIdx.x); i < per_row; i += kRowThreads)
-    out[t * per_row + i] = t < rows ? H[t * per_row + i] : make_uint4(0u, 0u, 0u, 0u);
-}
 
-// Where dH's sums start: rest_t W[v*_t] (added to what is there where `add`).  8 values a thread.
-__global__ void __launch_bounds__(kRowThreads)
-    start_rows_kernel(const uint4* __restrict__ W, TokenIds tokens, int64_t r0, const float* __restrict__ rest, int64_t rows,
-                      int per_row, int V, int add, float4* __restrict__ out) {
-  for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
-    const float r = rest[t];
-    const int tok = r != 0.f ? tokens.get(r0 + t, V) : -1;
-    for (int i = static_cast<int>(threadIdx.x); i < per_row; i += kRowThreads) {
-      float4* o = out + (t * per_row + i) * 2;
-      float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-      if (add) {
-        lo = o[0];
-        hi = o[1];
+// What is laid out for a block of tokens before its products; each part is left out where its destination is NULL.
+struct RowJobs {
+  const uint4* H;        // [rows][per_row], 8 values each
+  const uint8_t* mask;   // of these rows, or NULL
+  int64_t rows;
+  int per_row;
+  uint4* few;            // [kLeastRows][per_row]: H, padded
+  // [rows][per_row]: H for dW, with zeros in the rows that the mask leaves out: their dS is 0, but 0 times
+  // the NaN or infinity that such a row may hold would be none
+  uint4* clean;
+  // [rows][per_row] fp32: where dH's sums start, rest_t W[v*_t] (added to what is there where `add`)
+  float4* start;
+  const uint4* W;
+  TokenIds tokens;       // of all tokens: row t is token r0 + t
+  int64_t r0;
+  const float* rest;     // of these rows
+  int V, add;
+};
+
+__global__ void __launch_bounds__(kRowThreads) row_jobs_kernel(const RowJobs p) {
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t all = p.few != nullptr && p.rows < kLeastRows ? kLeastRows : p.rows;
+  for (int64_t t = blockIdx.x; t < all; t += gridDim.x) {
+    const bool in = t < p.rows, on = in && (p.mask == nullptr || p.mask[t] != 0);
+    const float r = p.start != nullptr && in ? p.rest[t] : 0.f;
+    const int tok = r != 0.f ? p.tokens.get(p.r0 + t, p.V) : -1;
+    for (int i = static_cast<int>(threadIdx.x); i < p.per_row; i += kRowThreads) {
+      const int64_t at = t * p.per_row + i;
+      if (p.few != nullptr) p.few[at] = in ? p.H[at] : zero;
+      if (!in) continue;
+      if (p.clean != nullptr) p.clean[at] = on ? p.H[at] : zero;
+      if (p.start != nullptr) {
+        float4* o = p.start + at * 2;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        if (p.add) {
+          lo = o[0];
+          hi = o[1];
+        }
+        if (tok >= 0) {
+          const uint4 w = p.W[static_cast<int64_t>(tok) * p.per_row + i];
+          add_bf16x2(lo.x, lo.y, w.x, r);
+          add_bf16x2(lo.z, lo.w, w.y, r);
+          add_bf16x2(hi.x, hi.y, w.z, r);
+          add_bf16x2(hi.z, hi.w, w.w, r);
+        }
+        o[0] = lo;
+        o[1] = hi;
       }
-      if (tok >= 0) {
-        const uint4 w = W[static_cast<int64_t>(tok) * per_row + i];
-        add_bf16x2(lo.x, lo.y, w.x, r);
-        add_bf16x2(lo.z, lo.w, w.y, r);
-        add_bf16x2(hi.x, hi.y, w.z, r);
-        add_bf16x2(hi.z, hi.w, w.w, r);
-      }
-      o[0] = lo;
-      o[1] = hi;
     }
   }
 }
 
-// A block's hidden states for dW, with zeros in the rows that the mask leaves out: their dS is 0, but 0 times
-// the NaN or infinity that such a row may hold would be none.  8 values a thread.
-__global__ void __launch_bounds__(kRowThreads)
-    clean_rows_kernel(const uint4* __restrict__ H, const uint8_t* __restrict__ mask, int64_t rows, int per_row,
-                      uint4* __restrict__ out) {
-  for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
-    const bool on = mask[t] != 0;
-    for (int i = static_cast<int>(threadIdx.x); i < per_row; i += kRowThreads)
-      out[t * per_row + i] = on ? H[t * per_row + i] : make_uint4(0u, 0u, 0u, 0u);
-  }
+cudaError_t launch_row_jobs(const RowJobs& p, int sms, cudaStream_t st) {
+  if (p.few == nullptr && p.clean == nullptr && p.start == nullptr) return cudaSuccess;
+  const int64_t rows = p.rows < kLeastRows ? kLeastRows : p.rows;
+  row_jobs_kernel<<<static_cast<unsigned>(rows < 8 * sms ? rows : 8 * sms), kRowThreads, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 unsigned row_blocks(int64_t T) { return static_cast<unsigned>((T + kRowThreads - 1) / kRowThreads); }
@@ -394,7 +409,7 @@ constexpr int kPieces = 160;
 struct Areas {
   size_t c0, c1, hit, rest;   // float [T]: the factors of dS, its entry at the token and what rounding takes from it
   size_t count, token_of;     // int [V], int [V][kMaxTargets]: the tokens of each vocabulary row
-  size_t few;                 // bf16 [kLeastRows][d]: see map_tokens
+  size_t few;                 // bf16 [kLeastRows][d]: see kLeastRows
   size_t clean;               // bf16 [Ct][d]: a block's hidden states without the rows that a mask leaves out
   size_t ds;                  // bf16 [Ct][Vmax]
   size_t pieces;              // fp32 [kPieces][256][256]
@@ -449,20 +464,6 @@ void plan_pieces(GemmShape* g, int pairs, float* pieces) {
   g->split_from = 0;
   g->ksplit = best;
   g->kpart = pieces;
-}
-
-// Map of the hidden states as the projection's A operand.  Few tokens are padded in the workspace (`room`:
-// kLeastRows x d): loading the same few rows for every tile, the product of one token with a 201088 x 2880 head took 282
-// us, of 64 tokens 199.
-cudaError_t map_tokens(CUtensorMap* map, const uint16_t* H, int64_t rows, int64_t d, uint16_t* room, cudaStream_t st) {
-  if (rows < kLeastRows) {
-    pad_rows_kernel<<<kLeastRows, kRowThreads, 0, st>>>(reinterpret_cast<const uint4*>(H), static_cast<int>(rows),
-                                                        static_cast<int>(d / 8), reinterpret_cast<uint4*>(room));
-    if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    H = room;
-    rows = kLeastRows;
-  }
-  return encode_map_bf16(map, H, d, rows, d * 2, 64, 128) ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 // Splits of a row block's vocabulary for the forward.  Up to four row blocks have a unit to each CTA pair and
@@ -567,23 +568,34 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   uint32_t* status = reinterpret_cast<uint32_t*>(c.ws);
   float* pieces = c.area<float>(c.at.pieces);
   const int bn = tile_width(d), pairs = c.sms / 2;
-  const uint16_t* Hw = Hb;  // what dW multiplies
-  if (c.mask != nullptr && c.dW != nullptr) {
-    uint16_t* clean = c.area<uint16_t>(c.at.clean);
-    Hw = clean;
-    if (j == 0 || (pl.slab_outer && pl.nt > 1)) {  // else it still holds this block's
-      clean_rows_kernel<<<static_cast<unsigned>(rows < 8 * c.sms ? rows : 8 * c.sms), kRowThreads, 0, c.st>>>(
-          reinterpret_cast<const uint4*>(Hb), c.mask + r0, rows, static_cast<int>(d / 8), reinterpret_cast<uint4*>(clean));
-      if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return fused_cuda(e);
-    }
-  }
+  const bool padded = rows < kLeastRows, cleaned = c.mask != nullptr && c.dW != nullptr;
+  // slabs outer: the areas of a token block may hold another block's rows by now
+  const bool again = pl.slab_outer && pl.nt > 1;
+  const F32Params ph = destination(rows, d, j, pl.nslabs, static_cast<float*>(c.dH) + (c.bf16 ? 0 : r0 * d),
+                                   c.bf16 ? static_cast<uint16_t*>(c.dH) + r0 * d : nullptr,
+                                   c.area<float>(c.at.hsum) + (pl.slab_outer ? r0 * d : 0), true);
+  RowJobs jobs{};
+  jobs.H = reinterpret_cast<const uint4*>(Hb);
+  jobs.mask = c.mask != nullptr ? c.mask + r0 : nullptr;
+  jobs.rows = rows;
+  jobs.per_row = static_cast<int>(d / 8);
+  jobs.few = padded && (j == 0 || again) ? c.area<uint4>(c.at.few) : nullptr;
+  jobs.clean = cleaned && (j == 0 || again) ? c.area<uint4>(c.at.clean) : nullptr;
+  jobs.start = c.dH != nullptr && j == 0 ? reinterpret_cast<float4*>(ph.out) : nullptr;
+  jobs.W = reinterpret_cast<const uint4*>(c.W);
+  jobs.tokens = c.tokens;
+  jobs.r0 = r0;
+  jobs.rest = c.area<const float>(c.at.rest) + r0;
+  jobs.V = static_cast<int>(c.V);
+  jobs.add = !c.bf16 && (c.accumulate & FKL_ACCUMULATE_DH) != 0 ? 1 : 0;
+  cudaError_t e = launch_row_jobs(jobs, c.sms, c.st);
+  if (e != cudaSuccess) return fused_cuda(e);
+  const uint16_t *Ha = padded ? c.area<const uint16_t>(c.at.few) : Hb, *Hw = cleaned ? c.area<const uint16_t>(c.at.clean) : Hb;
   CUtensorMap h_rows, h_cols, w_rows, w_cols, ds_cols, ds_rows;
   bool h3d = false, w3d = false;
   // dS has zeros in the columns [w, round_up(w, 256)) of every row, so its 3-D view may span round_up(w, 64)
   const bool ds3d = encode_map_mn3d(&ds_cols, ds, ceil_div(w, 64) * 64, rows, Vc * 2, 128);
-  cudaError_t e = map_tokens(&h_rows, Hb, rows, d, c.area<uint16_t>(c.at.few), c.st);
-  if (e != cudaSuccess) return fused_cuda(e);
-  if (!map_columns(&h_cols, Hw, d, rows, bn, &h3d) ||
+  if (!encode_map_bf16(&h_rows, Ha, d, padded ? kLeastRows : rows, d * 2, 64, 128) || !map_columns(&h_cols, Hw, d, rows, bn, &h3d) ||
       !encode_map_bf16(&w_rows, Wj, d, w, d * 2, 64, kVocabTile / 2) || !map_columns(&w_cols, Wj, d, w, bn, &w3d) ||
       (!ds3d && !encode_map_bf16(&ds_cols, ds, w, rows, Vc * 2, 64, 64)) ||
       !encode_map_bf16(&ds_rows, ds, w, rows, Vc * 2, 64, 128))
@@ -631,19 +643,9 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   }
   if (c.dH == nullptr) return FKL_OK;
 
-  // dH[block] = what rounding took from the tokens' entries, + dS[block] W[slab], slabs in order
-  float* hsum = c.area<float>(c.at.hsum) + (pl.slab_outer ? r0 * d : 0);
+  // dH[block] (what rounding took from the tokens' entries, above) += dS[block] W[slab], slabs in order
   GemmShape gh = make_shape(rows, d, w, bn, static_cast<int>(ceil_div(d, bn)), status, 256);
   gh.b_box3d = w3d ? 1 : 0;
-  const F32Params ph = destination(rows, d, j, pl.nslabs, static_cast<float*>(c.dH) + (c.bf16 ? 0 : r0 * d),
-                                   c.bf16 ? static_cast<uint16_t*>(c.dH) + r0 * d : nullptr, hsum, true);
-  if (j == 0) {
-    start_rows_kernel<<<static_cast<unsigned>(rows < 8 * c.sms ? rows : 8 * c.sms), kRowThreads, 0, c.st>>>(
-        reinterpret_cast<const uint4*>(c.W), c.tokens, r0, c.area<const float>(c.at.rest) + r0, rows,
-        static_cast<int>(d / 8), static_cast<int>(c.V), !c.bf16 && (c.accumulate & FKL_ACCUMULATE_DH) != 0 ? 1 : 0,
-        reinterpret_cast<float4*>(ph.out));
-    if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
-  }
   plan_pieces(&gh, pairs, pieces);
   if ((e = launch_gemm2_f32(bn, false, true, ds_rows, w_cols, gh, ph, c.sms, c.st)) != cudaSuccess ||
       (e = launch_ksplit_fixup(bn, gh, ph, c.st)) != cudaSuccess)
@@ -721,8 +723,15 @@ extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, 
   if (e != cudaSuccess) return fused_cuda(e);
   if (T == 0) return FKL_OK;
   CUtensorMap mH, mW;
-  if ((e = map_tokens(&mH, H, T, d, reinterpret_cast<uint16_t*>(ws + pl.few), st)) != cudaSuccess) return fused_cuda(e);
-  if (!encode_map_bf16(&mW, W, d, V, d * 2, 64, kVocabTile / 2))
+  RowJobs jobs{};
+  jobs.H = reinterpret_cast<const uint4*>(H);
+  jobs.rows = T;
+  jobs.per_row = static_cast<int>(d / 8);
+  jobs.few = T < kLeastRows ? reinterpret_cast<uint4*>(ws + pl.few) : nullptr;
+  if ((e = launch_row_jobs(jobs, sms, st)) != cudaSuccess) return fused_cuda(e);
+  if (!encode_map_bf16(&mH, jobs.few != nullptr ? reinterpret_cast<const uint16_t*>(jobs.few) : H, d,
+                       jobs.few != nullptr ? kLeastRows : T, d * 2, 64, 128) ||
+      !encode_map_bf16(&mW, W, d, V, d * 2, 64, kVocabTile / 2))
     return fused_fail(FKL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   const int m_tiles = static_cast<int>(ceil_div(T, 256)), n_tiles = static_cast<int>(ceil_div(V, kVocabTile));
   GemmShape g = make_shape(T, V, d, kVocabTile, forward_splits(m_tiles, n_tiles, sms / 2), &hdr->status, 256);
