@@ -78,7 +78,9 @@ class Exact:
 
 @pytest.mark.parametrize("T,d,V,tau", [(1, 8, 1, 1.0), (1, 64, 300, 0.5), (3, 8, 17, 2.0), (130, 64, 257, 1.0),
                                        (257, 72, 1000, 0.8), (300, 128, 4099, 1.0), (64, 256, 30011, 1.3),
-                                       (700, 40, 513, 1.0), (0, 16, 50, 1.0)])
+                                       (700, 40, 513, 1.0), (0, 16, 50, 1.0), (63, 160, 1500, 1.0),
+                                       (64, 576, 900, 0.9), (65, 136, 769, 1.0), (256, 48, 2000, 1.0),
+                                       (513, 192, 300, 1.0)])
 def test_scores_and_gradients(fkl, T, d, V, tau):
     H, W, tok, mask = make(T, d, V, seed=T + V)
     for m, ids in ((None, tok), (mask, tok.int())):
@@ -127,6 +129,22 @@ def test_explicit_calls(fkl):
     dH, dW = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, None, b, tau)
     e.check_gradients(dH, dW, torch.zeros(T), b, False)
     assert fkl.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_at_any_16_bytes(fkl, dtype):
+    """Outputs that start 16 bytes into a 32-byte unit, and what lies around them."""
+    T, d, V = 100, 64, 777
+    H, W, tok, mask = make(T, d, V, seed=13)
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, mask)
+    a, b = torch.randn(T).cuda(), torch.randn(T).cuda()
+    want = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, grad_dtype=dtype)
+    off = 16 // want[0].element_size()
+    bufs = [torch.full((n * d + 2 * off,), 7.0, dtype=dtype, device="cuda") for n in (T, V)]
+    out = tuple(x[off:-off].view(-1, d) for x in bufs)
+    fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, grad_dtype=dtype, out=out)
+    for x, y, z in zip(out, want, bufs):
+        assert torch.equal(x, y) and (z[:off] == 7).all() and (z[-off:] == 7).all()
 
 
 def test_tokens_that_many_share(fkl):
