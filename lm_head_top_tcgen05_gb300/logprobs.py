@@ -18,6 +18,8 @@ gradient, a cross-entropy or an entropy bonus on the drawn text:
 ``logprob_forward`` and ``logprob_backward`` are the explicit calls of the fused form.  Inputs are on the
 current device, and calls run on its current stream.  A call without a ``workspace`` takes its scratch from
 PyTorch's allocator for as long as it runs, so calls of several threads, streams and captured graphs share none.
+A step that is captured in a CUDA graph takes its gradients with ``torch.autograd.grad`` or the explicit calls;
+``backward()`` would add into leaves on the stream of an eager graph that they still belong to.
 """
 from __future__ import annotations
 

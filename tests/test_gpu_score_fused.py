@@ -319,6 +319,39 @@ def test_another_stream_and_a_graph(fkl):
             assert all(torch.equal(x, y) for x, y in zip(o, eager))
 
 
+def test_several_threads(fkl):
+    """Threads on streams of their own, and on one stream, share no scratch."""
+    import threading
+
+    H, W, tok, mask = make(200, 64, 3000, seed=14)
+    x = (H.float() @ W.float().t()).bfloat16()
+    a = torch.randn(200).cuda()
+
+    def step():
+        Hl, Wl = H.clone().requires_grad_(), W.clone().requires_grad_()
+        lp, ent = fkl.fused_logprobs(Hl, Wl, tok, mask)
+        return (lp.detach(),) + torch.autograd.grad((lp, ent), (Hl, Wl), (a, a)) + tuple(fkl.token_logprobs(x, tok, top_n=7))
+
+    want = step()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(stream):
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = step()
+                stream.synchronize()
+                wrong.extend(1 for u, v in zip(got, want) if not torch.equal(u, v))
+
+    shared = torch.cuda.Stream()
+    threads = [threading.Thread(target=work, args=(s,)) for s in (torch.cuda.Stream(), torch.cuda.Stream(), shared, shared)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 # ---------------------------------------------------------------- together
 def test_draw_score_and_train(fkl):
     """What a server and an on-policy step do: draw through an 8-bit head, score from its logits, then a policy gradient
