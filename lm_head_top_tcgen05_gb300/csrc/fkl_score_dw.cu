@@ -3,8 +3,9 @@
 // Its epilogue adds, in fp32 and in the order of tokens, what the rounding of dS took from the tokens' own
 // entries, and rounds once.  A lane has a row of the tile, so each of its stores is a separate line: 32-byte
 // stores move the bf16 tile in half the instructions of 16-byte ones, which is what a short batch's
-// product waits for (64 x 201088 x 2880: 466 us with 16-byte stores, 335 with these, 300 with four tiles to a unit;
-// writing dW at the copy rate would be 170).
+// product waits for (64 x 201088 x 2880: 466 us with 16-byte stores, 335 with these, 300 with four tiles to a unit; a
+// plain fill of dW takes 287, as HBM takes writes alone at 4.0 TB/s).  Boxes of 32 rows in shared memory that leave
+// by TMA stores took 340: they leave room for 128-wide tiles only, and A is read again for each.
 #include "fkl_score_dw.cuh"
 
 #include "fkl_gemm2.cuh"

@@ -17,7 +17,7 @@
 //
 // The tensor pipe bounds both: 2 T V d operations forward, 6 T V d backward.  4096 x 201088 x 2880: 2.7 ms forward
 // (1730 TFLOP/s), 8.8 ms backward (1610), as the loss of the same shape.  Few tokens wait for the head's bytes: 64
-// tokens 200 us forward (5.8 TB/s) and 688 backward, of which reading the head twice and writing its gradient are 511.
+// tokens 200 us forward (5.8 TB/s) and 679 backward, of which reading the head twice and filling its gradient are 627.
 #include <cmath>
 
 #include "../../include/fkl_score.h"
