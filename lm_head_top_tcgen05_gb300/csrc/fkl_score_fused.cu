@@ -104,9 +104,9 @@ struct EpiScore {
     }
     const float to = fmaxf(m, fmax3(c0, c1, fmaxf(v[30], v[31])) * p.scale2);
     const float sum = sums(v, to, weighted);
-    if (m == -INFINITY) {
-      l = sum;
-      u = weighted;
+    if (m == -INFINITY) {  // nothing yet, or only NaN, which stays
+      l += sum;
+      u += weighted;
     } else {
       const float r = m - to, f = ex2_approx(r);
       u = fmaf(fmaf(r, l, u), f, weighted);

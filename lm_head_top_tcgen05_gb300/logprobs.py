@@ -150,7 +150,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: Unio
                    top_n: int = 0, mask: Optional[torch.Tensor] = None) -> TokenLogprobs:
     """Scores ``tokens`` [B] (int32 or int64) under softmax(logits / temperature), logits [B, V] (float32,
     bfloat16 or float16; rows any stride apart): the tokens' log-probability and the distribution's entropy
-    (float32 [B], differentiable in the logits) and the ``top_n`` (at most 128) likeliest ids, int32 and
+    (float32 [B], differentiable in the logits) and the ``top_n`` (at most 128, and V) likeliest ids, int32 and
     float32 [B, top_n], likeliest first, ties by the lower id.
 
     ``temperature`` is one number or a float32 tensor [B].  ``mask`` (uint8 or bool [B]) leaves rows out: log-probability,
@@ -307,7 +307,7 @@ def fused_logprobs(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask:
     states H [T, d] and LM head W [V, d] (bfloat16), without the [T, V] logits in memory; differentiable in H and W.
 
     ``mask`` (uint8 or bool [T]) leaves tokens out: log-probability, entropy and gradient 0.  A token outside [0, V) in another row
-    gives NaN there, and NaN gradients.  ``chunk`` bounds the backward's buffer as in ``fused_kl``."""
+    gives NaN there, and NaN gradients; so does a NaN among a row's logits.  ``chunk`` bounds the backward's buffer as in ``fused_kl``."""
     if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
         return _FusedLogprobs.apply(H, W, tokens, mask, tau, chunk)
     return logprob_forward(H, W, tokens, mask, tau)[:2]

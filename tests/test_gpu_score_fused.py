@@ -243,6 +243,27 @@ def test_rows_left_out_may_hold_anything(fkl, T, V):
                 assert torch.isfinite(y).all() and torch.equal(x, y)
 
 
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("start,n", [(0, 32), (0, 256), (256, 64), (1000, 1), (2990, 10)])
+def test_nan_in_the_head_is_not_lost(fkl, T, start, n):
+    """A NaN among a row's logits makes its scores NaN, also where it is all that the row begins with."""
+    H, W, tok, _ = make(T, 64, 3000, seed=15)
+    W[start:start + n] = float("nan")
+    lp, ent = fkl.fused_logprobs(H, W, tok)
+    assert lp.isnan().all() and ent.isnan().all()
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_nan_in_one_row_stays_there(fkl, T):
+    H, W, tok, _ = make(T, 64, 3000, seed=16)
+    want = fkl.fused_logprobs(H, W, tok)
+    H[2, 3] = float("nan")
+    got = fkl.fused_logprobs(H, W, tok)
+    rest = torch.arange(T, device="cuda") != 2
+    for g, w in zip(got, want):
+        assert g[2].isnan() and torch.equal(g[rest], w[rest])
+
+
 def test_empty_batch_with_a_frozen_head(fkl):
     H, W, tok, _ = make(0, 16, 50)
     Hl = H.requires_grad_()
