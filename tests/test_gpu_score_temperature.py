@@ -1,0 +1,67 @@
+"""Scores and gradients from hidden states at temperatures far from 1, against the float64 oracle.
+
+Hidden states and head hold multiples of 1/16 and 1/32, so that every logit and every partial sum of it is a whole number of
+1/512 below 2^24 of them: the tensor cores' logits are exact, and no tolerance below is divided by the temperature.
+
+Tolerances.  A weight is 2^a with a = (s - m) log2(e) / tau: the difference is exact, the constant and the product round
+(2^-23 |a| ln 2, at most 2^-22 ln V where q counts), the exponential is off by 2^-22.  fp32 sums lose 2^-24 at each
+addition: V / 32 of them in a row, 16 in a chunk and across splits.  That is tol(V), of the sum and of log q;
+what log q itself is large in rounds relatively (2^-22).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import score as oracle
+
+pytestmark = pytest.mark.gpu
+
+LOW = [1e-1, 1e-2, 1e-3, 1e-4, 1e-5, 1e-6]
+
+
+@pytest.fixture(scope="module")
+def fkl(cuda_device):
+    from lm_head_top_tcgen05_gb300 import build
+
+    build.build()
+    import lm_head_top_tcgen05_gb300 as m
+
+    return m
+
+
+def tol(V):
+    return 2.0 ** -22 * (4 + math.log(V)) + (V / 32 + 16) * 2.0 ** -24
+
+
+def make(T, d, V, seed):
+    """Exact logits up to about 40; half of the vocabulary twice, so that the likeliest token mostly shares its
+    logit; half of the tokens the likeliest."""
+    g = torch.Generator().manual_seed(seed)
+    H = torch.randint(-128, 129, (T, d), generator=g).float() / 16
+    W = torch.randint(-16, 17, (V, d), generator=g).float() / 32
+    W[V // 2:V // 2 * 2] = W[:V // 2]
+    x = H.double() @ W.double().t()
+    tok = torch.where(torch.rand(T, generator=g) < 0.5, x.argmax(1), torch.randint(0, V, (T,), generator=g))
+    assert (H.bfloat16().float() == H).all() and (W.bfloat16().float() == W).all()
+    return H.bfloat16().cuda(), W.bfloat16().cuda(), tok.cuda(), x.numpy()
+
+
+def check_scores(x, tok, tau, lp, ent):
+    V = x.shape[1]
+    want_lp, want_ent, logq, q = oracle.score(x, tok.cpu().numpy(), float(np.float32(tau)))
+    lp, ent = lp.detach().cpu().double().numpy(), ent.detach().cpu().double().numpy()
+    assert (lp <= 0).all() and (ent >= 0).all()
+    assert (np.abs(lp - want_lp) <= tol(V) + 2.0 ** -22 * np.abs(want_lp)).all(), np.abs(lp - want_lp).max()
+    # entropy = E[-log q]: the error of log q, and that of the weights times the spread of log q around it
+    assert (np.abs(ent - want_ent) <= tol(V) * (4 + 2 * math.log(V))).all(), np.abs(ent - want_ent).max()
+    return logq, q, want_ent
+
+
+@pytest.mark.parametrize("tau", [1.0, *LOW, 1e-9, 1e-20, 1e-35, 1e4, 1e36, 3e38])
+@pytest.mark.parametrize("T,V", [(70, 32), (300, 1504), (70, 20000)])
+def test_scores(fkl, T, V, tau):
+    H, W, tok, x = make(T, 64, V, seed=V)
+    lp, ent = fkl.fused_logprobs(H, W, tok, tau=tau)
+    check_scores(x, tok, tau, lp, ent)
