@@ -80,8 +80,9 @@ fkl_status fkl_token_logprobs_backward(const void* logits, int32_t type, int64_t
  *   logprob, entropy, lse   float [T]; lse (natural log of sum_v exp(x_v / tau)) is written for every row,
  *           those left out included, and the backward reads it
  *   workspace   fkl_logprob_workspace_size bytes, 256-byte aligned
- * A token outside [0, V) is recorded for fkl_read_status (FKL_ERR_BAD_TOPK_ID) beside its NaN; a wait that
- * runs out (FKL_ERR_TIMEOUT) makes every output NaN.
+ * A logit that overflows to -inf has no weight; NaN or +inf among a row's logits makes its outputs NaN.  A token
+ * outside [0, V) is recorded for fkl_read_status (FKL_ERR_BAD_TOPK_ID) beside its NaN; a wait that runs out
+ * (FKL_ERR_TIMEOUT) makes every output NaN.
  */
 size_t fkl_logprob_workspace_size(int64_t T, int64_t d, int64_t V);
 fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,

@@ -52,11 +52,6 @@ bool make_format(int64_t K, int64_t V, int32_t bits, Format* f) {
 __device__ __forceinline__ void copy4_async(void* dst_smem, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst_smem)), "l"(src) : "memory");
 }
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN where one of them is
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
 
 // The level nearest to z, from the definition: in fp64 the product is exact, and so is a tie.
 __device__ __noinline__ uint32_t exact_level(float top, float z, float low, float levels) {

@@ -16,6 +16,13 @@ bool encode_map_bytes(CUtensorMap* map, const void* base, uint64_t inner, uint64
 bool encode_map_f16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
                     uint32_t box_inner, uint32_t box_outer);
 
+// The larger of two values, NaN where one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

@@ -35,6 +35,8 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool on_boundary(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+constexpr float kFloor = -200.f;  // exponents below it are 0: 2^-200 is below fp32
+
 // ---------------------------------------------------------------- forward epilogue
 struct ScoreFwdParams {
   TokenIds tokens;
@@ -62,10 +64,15 @@ struct EpiScore {
     l = u = 0.f;
   }
 
-  // Adds the chunk's terms at reference m; the sum of its weights.
+  // The sum of the chunk's weights at reference `ref`, and their weighted sum.  kGuard: a logit of -inf, whose
+  // exponent is -inf too, has weight 0 in both (0 * -inf would be NaN); NaN stays.
+  template <bool kGuard>
   __device__ __forceinline__ float sums(const float (&v)[32], float ref, float& weighted) const {
     const float2 sc = make_float2(p.scale2, p.scale2), om = make_float2(-ref, -ref);
-    auto exponent = [&](float x, float y) { return fmul2(fadd2(make_float2(x, y), om), sc); };
+    auto exponent = [&](float x, float y) {
+      const float2 a = fmul2(fadd2(make_float2(x, y), om), sc);
+      return kGuard ? make_float2(max_nan(a.x, kFloor), max_nan(a.y, kFloor)) : a;
+    };
     float2 t0 = make_float2(0.f, 0.f), t1 = t0, w0 = t0, w1 = t0;
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
@@ -83,18 +90,18 @@ struct EpiScore {
   __device__ __forceinline__ void chunk(float (&v)[32], int col0) {
     if (col0 >= p.V) return;
     if (tok >= col0 && tok < col0 + 32) p.token_s[t] = pick(v, tok - col0);
-    if (col0 + 32 > p.V) {  // the last columns: weight 0 at a finite exponent (0 * -inf is not 0)
-      const float low = (m != -INFINITY ? m : v[0]) - 400.f / p.scale2;
+    const bool whole = col0 + 32 <= p.V;
+    if (!whole) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (col0 + j >= p.V) v[j] = low;
+        if (col0 + j >= p.V) v[j] = -INFINITY;
     }
     float weighted;
-    if (m != -INFINITY) {
+    if (whole && m != -INFINITY) {
       // A reference 2^10 below a term would cost the entropy 10 binary orders of its last digits: log2 L
-      // and U / L then cancel.  It moves before that.
-      const float sum = sums(v, m, weighted);
-      if (sum < 1024.f) {
+      // and U / L then cancel.  It moves before that.  A weighted sum of NaN has a logit of -inf, or NaN, in it.
+      const float sum = sums<false>(v, m, weighted);
+      if (sum < 1024.f && weighted == weighted) {
         l += sum;
         u += weighted;
         return;
@@ -107,15 +114,11 @@ struct EpiScore {
       c1 = fmax3(c1, v[j + 2], v[j + 3]);
     }
     const float to = fmaxf(m, fmax3(c0, c1, fmaxf(v[30], v[31])));
-    const float sum = sums(v, to, weighted);
-    if (m == -INFINITY) {  // nothing yet, or only NaN, which stays
-      l += sum;
-      u += weighted;
-    } else {
-      const float r = fmaxf((m - to) * p.scale2, -1000.f), f = ex2_approx(r);
-      u = fmaf(fmaf(r, l, u), f, weighted);
-      l = fmaf(l, f, sum);
-    }
+    const float ref = to > -INFINITY ? to : 0.f;  // no logit yet: sums of 0, or NaN, which stays
+    const float sum = sums<true>(v, ref, weighted);
+    const float r = fmaxf((m - ref) * p.scale2, -1000.f), f = ex2_approx(r);
+    u = fmaf(fmaf(r, l, u), f, weighted);
+    l = fmaf(l, f, sum);
     m = to;
   }
 

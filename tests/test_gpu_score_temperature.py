@@ -60,8 +60,31 @@ def check_scores(x, tok, tau, lp, ent):
 
 
 @pytest.mark.parametrize("tau", [1.0, *LOW, 1e-9, 1e-20, 1e-35, 1e4, 1e36, 3e38])
-@pytest.mark.parametrize("T,V", [(70, 32), (300, 1504), (70, 20000)])
+@pytest.mark.parametrize("T,V", [(70, 32), (300, 1504), (70, 20000), (70, 1), (5, 33), (300, 1505), (70, 20001)])
 def test_scores(fkl, T, V, tau):
     H, W, tok, x = make(T, 64, V, seed=V)
     lp, ent = fkl.fused_logprobs(H, W, tok, tau=tau)
     check_scores(x, tok, tau, lp, ent)
+    if V == 1:
+        assert (lp == 0).all() and (ent == 0).all()
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_not_finite_logits(fkl, T):
+    """What a hidden state of 2^127 makes of a head with signs: -inf has no weight, +inf and NaN make the row NaN."""
+    H, W, tok, _ = make(T, 64, 1505, seed=4)
+    W[:, 0] = 0.0
+    W[3:40, 0], W[200, 0] = -8.0, -8.0
+    tok[:] = 1
+    want = fkl.fused_logprobs(H, W, tok)
+    H[:, 0] = 0.0
+    H[2, 0] = 2.0 ** 127
+    lp, ent = fkl.fused_logprobs(H, W, tok)
+    x = H.cpu().double().numpy() @ W.cpu().double().numpy().T
+    x[2, np.abs(x[2]) > 3e38] = -np.inf
+    e_lp, e_ent, _, _ = oracle.score(x, tok.cpu().numpy())
+    assert abs(lp[2].item() - e_lp[2]) < 1e-4 and abs(ent[2].item() - e_ent[2]) < 1e-4
+    W[300, 0] = 8.0
+    lp, ent = fkl.fused_logprobs(H, W, tok)
+    assert lp[2].isnan() and ent[2].isnan() and torch.isfinite(lp[:2]).all() and torch.isfinite(lp[3:]).all()
+    assert torch.isfinite(want[0]).all()
