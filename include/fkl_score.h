@@ -78,24 +78,36 @@ fkl_status fkl_token_logprobs_backward(const void* logits, int32_t type, int64_t
  *   H  bf16 [T][d], W bf16 [V][d], 16-byte aligned, d a multiple of 8
  *   tokens  int32 or int64 [T] (token_bytes 4 or 8);  mask uint8 [T] or NULL
  *   logprob, entropy, lse   float [T]; lse (natural log of sum_v exp(x_v / tau)) is written for every row,
- *           those left out included, and the backward reads it
+ *           those left out included
  *   workspace   fkl_logprob_workspace_size bytes, 256-byte aligned
  * A logit that overflows to -inf has no weight; NaN or +inf among a row's logits makes its outputs NaN.  A token
  * outside [0, V) is recorded for fkl_read_status (FKL_ERR_BAD_TOPK_ID) beside its NaN; a wait that runs out
  * (FKL_ERR_TIMEOUT) makes every output NaN.
+ *
+ * fkl_logprob_forward_ex also writes `stats` (float [T][2], or NULL) for the backward: a reference logit m (one that is
+ * at most 10 tau ln 2 below the row's largest) and log sum_v exp((x_v - m) / tau).  Its lse may be NULL.
  */
 size_t fkl_logprob_workspace_size(int64_t T, int64_t d, int64_t V);
 fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
                                const uint8_t* mask, int64_t T, int64_t d, int64_t V, float tau, float* logprob,
                                float* entropy, float* lse, void* workspace, size_t ws_bytes, void* stream);
+fkl_status fkl_logprob_forward_ex(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
+                                  const uint8_t* mask, int64_t T, int64_t d, int64_t V, float tau, float* logprob,
+                                  float* entropy, float* lse, float* stats, void* workspace, size_t ws_bytes,
+                                  void* stream);
 
 /*
  * The gradient of sum_t (a_t logprob_t + b_t entropy_t): dH [T][d] and dW [V][d], as float or, with
  * grad_bf16 = 1, as bfloat16 bit patterns (fp32 sums rounded once), 16-byte aligned.  One of them may be NULL:
- * its product is left out (a frozen head, say).  The logits are recomputed block by block as in fkl_backward, and `chunk` bounds the buffer of their gradient in the same
- * way: at most chunk * V bfloat16 values (V rounded up to whole tiles of 256).
+ * its product is left out (a frozen head, say).  The logits are recomputed block by block as in fkl_backward, and
+ * `chunk` bounds the buffer of their gradient in the same way: at most chunk * V bfloat16 values (V rounded up to
+ * whole tiles of 256).
  *   grad_logprob, grad_entropy   float [T]; NULL = 0
- *   logprob, entropy, lse        the forward's
+ *   logprob, entropy   the forward's
+ *   lse, stats   the forward's; one of them may be NULL in fkl_logprob_backward_ex.  With `stats` q is right at any
+ *           tau.  Without, it is taken from lse, whose rounding is 2^-24 |lse| of it: a row whose |lse| is above 2^15,
+ *           where that passes the rounding of the logits' gradient to bf16 (logits of 30 below tau = 1e-3), has NaN
+ *           gradients, unless it is left out or its a_t and b_t are 0
  *   accumulate   FKL_ACCUMULATE_DH and/or FKL_ACCUMULATE_DW add into float gradients (0 with grad_bf16)
  *   workspace    fkl_logprob_backward_workspace_size bytes, 256-byte aligned
  * A token outside [0, V) in a valid row (FKL_ERR_BAD_TOPK_ID) and a wait that runs out (FKL_ERR_TIMEOUT) fill
@@ -107,6 +119,11 @@ fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W, const void
                                 const float* grad_logprob, const float* grad_entropy, int64_t T, int64_t d, int64_t V,
                                 float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate, void* dH, void* dW,
                                 void* workspace, size_t ws_bytes, void* stream);
+fkl_status fkl_logprob_backward_ex(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
+                                   const uint8_t* mask, const float* logprob, const float* entropy, const float* lse,
+                                   const float* stats, const float* grad_logprob, const float* grad_entropy, int64_t T,
+                                   int64_t d, int64_t V, float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate,
+                                   void* dH, void* dW, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

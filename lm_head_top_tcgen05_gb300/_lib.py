@@ -100,10 +100,15 @@ _SIGNATURES = {
     "fkl_logprob_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "fkl_logprob_forward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P,
                                            _P, ctypes.c_size_t, _P]),
+    "fkl_logprob_forward_ex": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _I64, _I64, _I64, ctypes.c_float, _P, _P,
+                                              _P, _P, _P, ctypes.c_size_t, _P]),
     "fkl_logprob_backward_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64, _I64, ctypes.c_int32]),
     "fkl_logprob_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64,
                                             ctypes.c_float, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
                                             ctypes.c_size_t, _P]),
+    "fkl_logprob_backward_ex": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _I64, _I64,
+                                               _I64, ctypes.c_float, _I64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
+                                               ctypes.c_size_t, _P]),
     "fkl_cache_words": (ctypes.c_int32, [_I64, _I64, ctypes.c_int32]),
     "fkl_cache_pack": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, ctypes.c_int32, _P, _P]),
     "fkl_cache_unpack": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.c_int32, _P, _P, _P]),

@@ -9,7 +9,9 @@
 // what a row's likeliest token scores at a low temperature (4e-3 above 0 at tau = 1e-4).  It takes an addition and a
 // product where one multiply-add would do: 2 % of the time at d = 128 to 512, 1 % at 1024, none beyond.
 //
-// Backward: dS_tv = q_tv (c0_t + c1_t log2 q_tv) + k_t [v = v*_t] with c0 = -(a + b entropy) / tau,
+// Backward: log2 q_tv = c (s_tv - M_t) - log2 L_t with the forward's reference and sum (statistics of a row; from
+// lse, their rounded sum, q would be off by 2^-24 lse of itself, 2 % for a logit of 30 at tau = 1e-4), and
+// dS_tv = q_tv (c0_t + c1_t log2 q_tv) + k_t [v = v*_t] with c0 = -(a + b entropy) / tau,
 // c1 = -b ln 2 / tau, k = a / tau, rounded to bf16 and written block by block (tokens x a vocabulary slab),
 // then dW[slab] += dS^T H and dH[block] += dS W[slab] in fp32, in a fixed order: the blocks are those of the
 // loss's backward, planned by the same functions.  The bf16 of dS (half a step is 2^-8 of each value) is what
@@ -152,7 +154,7 @@ struct ScoreDsParams {
   int64_t r0;
   const float *c0, *c1;       // of the block's tokens; a row left out has zeros
   const float* hit;           // the token's entry, rounded (0 in a row left out)
-  const float* lse;
+  const float2* ref;          // reference logit and log2 of the sum of the weights at it
   uint16_t* ds;
   int64_t ld_ds;
   int T, V, v0, slab_w;
@@ -164,7 +166,8 @@ struct EpiScoreDs {
   const Params& p;
   bool row_ok, off;
   int tok;
-  float c0, c1, hit, shift;
+  float c0, c1, hit;
+  float2 ref;
   uint16_t* dst;
 
   __device__ explicit EpiScoreDs(const Params& prm) : p(prm) {}
@@ -174,14 +177,15 @@ struct EpiScoreDs {
     row_ok = t < p.T;
     off = true;
     tok = -1;
-    c0 = c1 = hit = shift = 0.f;
+    c0 = c1 = hit = 0.f;
+    ref = make_float2(0.f, 0.f);
     dst = nullptr;
     if (row_ok) {
       c0 = p.c0[t];
       c1 = p.c1[t];
       hit = p.hit[t];
       off = c0 == 0.f && c1 == 0.f && hit == 0.f;
-      shift = -p.lse[t] * kLog2e;
+      ref = p.ref[t];
       if (!off) tok = p.tokens.get(p.r0 + t, p.V);
       dst = p.ds + static_cast<size_t>(t) * p.ld_ds;
     }
@@ -196,11 +200,13 @@ struct EpiScoreDs {
       return;
     }
     {
-      const float2 sc = make_float2(p.scale2, p.scale2), sh = make_float2(shift, shift);
+      const float2 sc = make_float2(p.scale2, p.scale2);
+      const float2 nm = make_float2(-ref.x, -ref.x), sh = make_float2(-ref.y, -ref.y);
       const float2 k0 = make_float2(c0, c0), k1 = make_float2(c1, c1);
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
-        const float2 a = ffma2(make_float2(v[j], v[j + 1]), sc, sh);  // log2 q
+        float2 a = ffma2(fadd2(make_float2(v[j], v[j + 1]), nm), sc, sh);  // log2 q
+        a = make_float2(max_nan(a.x, kFloor), max_nan(a.y, kFloor));       // 0 * -inf would be NaN
         const float2 y = fmul2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), ffma2(k1, a, k0));
         v[j] = y.x;
         v[j + 1] = y.y;
@@ -253,7 +259,8 @@ constexpr int kRowThreads = 256;
 __global__ void __launch_bounds__(kRowThreads)
     score_rows_kernel(const float* __restrict__ part, int nsplit, const float* __restrict__ token_s, TokenIds tokens,
                       const uint8_t* __restrict__ mask, int64_t T, int V, float scale2, uint32_t* status,
-                      float* __restrict__ logprob, float* __restrict__ entropy, float* __restrict__ lse) {
+                      float* __restrict__ logprob, float* __restrict__ entropy, float* __restrict__ lse,
+                      float* __restrict__ stats) {
   constexpr int kWarps = kRowThreads / 32;
   __shared__ float warp_m[kWarps][32];
   __shared__ double warp_l[kWarps][32], warp_u[kWarps][32];
@@ -286,7 +293,11 @@ __global__ void __launch_bounds__(kRowThreads)
   }
   const double ln2 = 0.69314718055994530942, log2_sum = log2(L);
   const bool late = (*reinterpret_cast<const volatile uint32_t*>(status) & kStatusTimeoutBit) != 0;
-  lse[t] = late ? NAN : static_cast<float>((static_cast<double>(M) * scale2 + log2_sum) * ln2);
+  if (lse != nullptr) lse[t] = late ? NAN : static_cast<float>((static_cast<double>(M) * scale2 + log2_sum) * ln2);
+  if (stats != nullptr) {
+    stats[2 * t] = late ? NAN : M;
+    stats[2 * t + 1] = late ? NAN : static_cast<float>(log2_sum * ln2);
+  }
   if (mask != nullptr && mask[t] == 0) {
     logprob[t] = late ? NAN : 0.f;
     entropy[t] = late ? NAN : 0.f;
@@ -300,15 +311,20 @@ __global__ void __launch_bounds__(kRowThreads)
   entropy[t] = ent < 0.0 ? 0.f : static_cast<float>(ent);
 }
 
-// The factors of each token's dS, its entry at the token with what rounding takes from it, and the tokens of each
-// vocabulary row that few have (TargetRows); a token outside the vocabulary is recorded.
+// Without the rows' statistics log q is a logit less lse, off by 2^-24 lse.  Above this lse that passes what
+// rounding to bf16 takes from dS (2^-9), and the row is NaN.
+constexpr float kMaxLse = 32768.f;
+
+// The factors of each token's dS, its entry at the token with what rounding takes from it, where its log q is counted
+// from, and the tokens of each vocabulary row that few have; a token outside the vocabulary is recorded.
 __global__ void __launch_bounds__(kRowThreads)
     score_factors_kernel(TokenIds tokens, const uint8_t* __restrict__ mask, const float* __restrict__ logprob,
-                         const float* __restrict__ entropy, const float* __restrict__ grad_logprob,
+                         const float* __restrict__ entropy, const float* __restrict__ lse,
+                         const float* __restrict__ stats, const float* __restrict__ grad_logprob,
                          const float* __restrict__ grad_entropy, int64_t T, int V, float inv_tau,
                          uint32_t* __restrict__ status, float* __restrict__ c0, float* __restrict__ c1,
-                         float* __restrict__ hit, float* __restrict__ rest, int* __restrict__ count,
-                         int* __restrict__ token_of) {
+                         float* __restrict__ hit, float* __restrict__ rest, float2* __restrict__ ref,
+                         int* __restrict__ count, int* __restrict__ token_of) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
   if (t >= T) return;
   float a = 0.f, b = 0.f, h = 0.f, log2_q = 0.f;
@@ -328,6 +344,10 @@ __global__ void __launch_bounds__(kRowThreads)
   c1[t] = f1;
   hit[t] = rounded;
   rest[t] = entry - rounded;
+  if (stats != nullptr)
+    ref[t] = make_float2(stats[2 * t], stats[2 * t + 1] * kLog2e);
+  else
+    ref[t] = make_float2(0.f, fabsf(lse[t]) <= kMaxLse ? lse[t] * kLog2e : NAN);
   if (tok >= 0 && (f0 != 0.f || f1 != 0.f)) {
     const int n = atomicAdd(&count[tok], 1);
     if (n < kMaxTargets) token_of[static_cast<size_t>(tok) * kMaxTargets + n] = static_cast<int>(t);
@@ -418,6 +438,7 @@ constexpr int kPieces = 160;
 // The backward's workspace.
 struct Areas {
   size_t c0, c1, hit, rest;   // float [T]: the factors of dS, its entry at the token and what rounding takes from it
+  size_t ref;                 // float2 [T]: reference logit and log2 of the sum
   size_t count, token_of;     // int [V], int [V][kMaxTargets]: the tokens of each vocabulary row
   size_t few;                 // bf16 [kLeastRows][d]: see kLeastRows
   size_t clean;               // bf16 [Ct][d]: a block's hidden states without the rows that a mask leaves out
@@ -440,6 +461,7 @@ Areas backward_areas(const Plan& p, bool bf16) {
   a.c1 = take(p.T, 4);
   a.hit = take(p.T, 4);
   a.rest = take(p.T, 4);
+  a.ref = take(p.T, 8);
   a.token_of = take(p.V * kMaxTargets, 4);
   a.few = take(p.T > 0 ? kLeastRows * p.d : 0, 2);
   a.clean = take(p.Ct * p.d, 2);
@@ -553,7 +575,6 @@ struct Backward {
   const uint16_t *H, *W;
   TokenIds tokens;
   const uint8_t* mask;
-  const float* lse;
   int64_t T, d, V;
   float tau;
   int accumulate;
@@ -620,7 +641,7 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   p.c0 = c.area<const float>(c.at.c0) + r0;
   p.c1 = c.area<const float>(c.at.c1) + r0;
   p.hit = c.area<const float>(c.at.hit) + r0;
-  p.lse = c.lse + r0;
+  p.ref = c.area<const float2>(c.at.ref) + r0;
   p.ds = ds;
   p.ld_ds = Vc;
   p.T = static_cast<int>(rows);
@@ -708,23 +729,23 @@ extern "C" size_t fkl_logprob_backward_workspace_size(int64_t T, int64_t d, int6
   return score_plan(T, d, V, chunk, grad_bf16 != 0, &p) ? backward_areas(p, grad_bf16 != 0).total : 0;
 }
 
-extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
-                                          const uint8_t* mask, int64_t T, int64_t d, int64_t V, float tau,
-                                          float* logprob, float* entropy, float* lse, void* workspace, size_t ws_bytes,
-                                          void* stream) {
+extern "C" fkl_status fkl_logprob_forward_ex(const uint16_t* H, const uint16_t* W, const void* tokens,
+                                             int32_t token_bytes, const uint8_t* mask, int64_t T, int64_t d, int64_t V,
+                                             float tau, float* logprob, float* entropy, float* lse, float* stats,
+                                             void* workspace, size_t ws_bytes, void* stream) {
   set_last_error_message("");
   ForwardPlan pl;
   if (!forward_plan(T, d, V, &pl)) return fused_fail(FKL_ERR_INVALID_ARG, kShapeRule);
   fkl_status s = check_fused(H, W, tokens, token_bytes, T, tau, workspace, ws_bytes, pl.total);
   if (s != FKL_OK) return s;
-  if (T > 0 && (logprob == nullptr || entropy == nullptr || lse == nullptr))
-    return fused_fail(FKL_ERR_INVALID_ARG, "logprob, entropy and lse must not be NULL");
-  if (!on_boundary(logprob, 4) || !on_boundary(entropy, 4) || !on_boundary(lse, 4))
-    return fused_fail(FKL_ERR_ALIGNMENT, "logprob, entropy and lse must be 4-byte aligned");
+  if (T > 0 && (logprob == nullptr || entropy == nullptr))
+    return fused_fail(FKL_ERR_INVALID_ARG, "logprob and entropy must not be NULL");
+  if (!on_boundary(logprob, 4) || !on_boundary(entropy, 4) || !on_boundary(lse, 4) || !on_boundary(stats, 4))
+    return fused_fail(FKL_ERR_ALIGNMENT, "logprob, entropy, lse and stats must be 4-byte aligned");
   int sms = 0;
   if (const int e = require_device(&sms); e != FKL_OK) return static_cast<fkl_status>(e);
   const NamedPtr ptrs[] = {{H, "H"}, {W, "W"}, {tokens, "tokens"}, {mask, "mask"}, {logprob, "logprob"},
-                           {entropy, "entropy"}, {lse, "lse"}, {workspace, "workspace"}};
+                           {entropy, "entropy"}, {lse, "lse"}, {stats, "stats"}, {workspace, "workspace"}};
   if (const int e = check_device_memory(ptrs); e != FKL_OK) return static_cast<fkl_status>(e);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -758,19 +779,29 @@ extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, 
   p.scale2 = kLog2e / tau;
   if ((e = launch_gemm2_t<kVocabTile, false, false, EpiScore>(mH, mW, g, p, sms, st)) != cudaSuccess) return fused_cuda(e);
   score_rows_kernel<<<static_cast<unsigned>(ceil_div(T, 32)), kRowThreads, 0, st>>>(
-      p.part, p.nsplit, p.token_s, p.tokens, mask, T, p.V, p.scale2, &hdr->status, logprob, entropy, lse);
+      p.part, p.nsplit, p.token_s, p.tokens, mask, T, p.V, p.scale2, &hdr->status, logprob, entropy, lse, stats);
   if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
   return FKL_OK;
 }
 
-extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
-                                           const uint8_t* mask, const float* logprob, const float* entropy,
-                                           const float* lse, const float* grad_logprob, const float* grad_entropy,
-                                           int64_t T, int64_t d, int64_t V, float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate,
-                                           void* dH, void* dW, void* workspace, size_t ws_bytes, void* stream) {
+extern "C" fkl_status fkl_logprob_forward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
+                                          const uint8_t* mask, int64_t T, int64_t d, int64_t V, float tau,
+                                          float* logprob, float* entropy, float* lse, void* workspace, size_t ws_bytes,
+                                          void* stream) {
+  if (T > 0 && lse == nullptr) return fused_fail(FKL_ERR_INVALID_ARG, "lse must not be NULL");
+  return fkl_logprob_forward_ex(H, W, tokens, token_bytes, mask, T, d, V, tau, logprob, entropy, lse, nullptr, workspace,
+                                ws_bytes, stream);
+}
+
+extern "C" fkl_status fkl_logprob_backward_ex(const uint16_t* H, const uint16_t* W, const void* tokens,
+                                              int32_t token_bytes, const uint8_t* mask, const float* logprob,
+                                              const float* entropy, const float* lse, const float* stats,
+                                              const float* grad_logprob, const float* grad_entropy, int64_t T, int64_t d,
+                                              int64_t V, float tau, int64_t chunk, int32_t grad_bf16, int32_t accumulate,
+                                              void* dH, void* dW, void* workspace, size_t ws_bytes, void* stream) {
   set_last_error_message("");
   if (grad_bf16 != 0 && grad_bf16 != 1) return fused_fail(FKL_ERR_INVALID_ARG, "grad_bf16 must be 0 or 1");
-  Backward c{H, W, TokenIds{tokens, token_bytes}, mask, lse, T, d, V, tau, accumulate, grad_bf16 == 1, dH, dW,
+  Backward c{H, W, TokenIds{tokens, token_bytes}, mask, T, d, V, tau, accumulate, grad_bf16 == 1, dH, dW,
              static_cast<uint8_t*>(workspace), 0, static_cast<cudaStream_t>(stream), Plan{}, Areas{}};
   if (!score_plan(T, d, V, chunk, c.bf16, &c.pl)) return fused_fail(FKL_ERR_INVALID_ARG, kShapeRule);
   c.at = backward_areas(c.pl, c.bf16);
@@ -778,14 +809,16 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
   if (s != FKL_OK) return s;
   if (accumulate < 0 || accumulate > 3) return fused_fail(FKL_ERR_INVALID_ARG, "bad accumulate");
   if (c.bf16 && accumulate != 0) return fused_fail(FKL_ERR_INVALID_ARG, "bf16 gradients do not accumulate");
-  if ((dW == nullptr && dH == nullptr) || (T > 0 && (logprob == nullptr || entropy == nullptr || lse == nullptr)))
-    return fused_fail(FKL_ERR_INVALID_ARG, "logprob, entropy, lse and one of dH and dW must not be NULL");
+  if ((dW == nullptr && dH == nullptr) ||
+      (T > 0 && (logprob == nullptr || entropy == nullptr || (lse == nullptr && stats == nullptr))))
+    return fused_fail(FKL_ERR_INVALID_ARG, "logprob, entropy, one of lse and stats and one of dH and dW must not be NULL");
   if (!on_boundary(dH, 16) || !on_boundary(dW, 16)) return fused_fail(FKL_ERR_ALIGNMENT, "dH and dW must be 16-byte aligned");
-  if (!on_boundary(logprob, 4) || !on_boundary(lse, 4) || !on_boundary(entropy, 4) || !on_boundary(grad_logprob, 4) || !on_boundary(grad_entropy, 4))
-    return fused_fail(FKL_ERR_ALIGNMENT, "logprob, entropy, lse and the gradients must be 4-byte aligned");
+  if (!on_boundary(logprob, 4) || !on_boundary(lse, 4) || !on_boundary(stats, 4) || !on_boundary(entropy, 4) ||
+      !on_boundary(grad_logprob, 4) || !on_boundary(grad_entropy, 4))
+    return fused_fail(FKL_ERR_ALIGNMENT, "logprob, entropy, lse, stats and the gradients must be 4-byte aligned");
   if (const int e = require_device(&c.sms); e != FKL_OK) return static_cast<fkl_status>(e);
-  const NamedPtr ptrs[] = {{H, "H"}, {W, "W"}, {tokens, "tokens"}, {mask, "mask"}, {logprob, "logprob"}, {lse, "lse"}, {entropy, "entropy"},
-                           {grad_logprob, "grad_logprob"}, {grad_entropy, "grad_entropy"}, {dH, "dH"}, {dW, "dW"},
+  const NamedPtr ptrs[] = {{H, "H"}, {W, "W"}, {tokens, "tokens"}, {mask, "mask"}, {logprob, "logprob"},
+                           {lse, "lse"}, {stats, "stats"}, {entropy, "entropy"}, {grad_logprob, "grad_logprob"}, {grad_entropy, "grad_entropy"}, {dH, "dH"}, {dW, "dW"},
                            {workspace, "workspace"}};
   if (const int e = check_device_memory(ptrs); e != FKL_OK) return static_cast<fkl_status>(e);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(c.ws);
@@ -799,9 +832,9 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
   }
   choose_slab_width(&c.pl, c.sms / 2);
   score_factors_kernel<<<row_blocks(T), kRowThreads, 0, c.st>>>(
-      c.tokens, mask, logprob, entropy, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau, &hdr->status,
-      c.area<float>(c.at.c0), c.area<float>(c.at.c1), c.area<float>(c.at.hit), c.area<float>(c.at.rest),
-      c.area<int>(c.at.count), c.area<int>(c.at.token_of));
+      c.tokens, mask, logprob, entropy, lse, stats, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau,
+      &hdr->status, c.area<float>(c.at.c0), c.area<float>(c.at.c1), c.area<float>(c.at.hit), c.area<float>(c.at.rest),
+      c.area<float2>(c.at.ref), c.area<int>(c.at.count), c.area<int>(c.at.token_of));
   if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
   const Plan& pl = c.pl;
   for (int64_t o = 0; o < (pl.slab_outer ? pl.nslabs : pl.nt); ++o)
@@ -812,4 +845,15 @@ extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W,
              : launch_poison(static_cast<float*>(dH), nh, static_cast<float*>(dW), nw, &hdr->status, c.sms, c.st);
   if (e != cudaSuccess) return fused_cuda(e);
   return FKL_OK;
+}
+
+extern "C" fkl_status fkl_logprob_backward(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes,
+                                           const uint8_t* mask, const float* logprob, const float* entropy,
+                                           const float* lse, const float* grad_logprob, const float* grad_entropy,
+                                           int64_t T, int64_t d, int64_t V, float tau, int64_t chunk, int32_t grad_bf16,
+                                           int32_t accumulate, void* dH, void* dW, void* workspace, size_t ws_bytes,
+                                           void* stream) {
+  return fkl_logprob_backward_ex(H, W, tokens, token_bytes, mask, logprob, entropy, lse, nullptr, grad_logprob,
+                                 grad_entropy, T, d, V, tau, chunk, grad_bf16, accumulate, dH, dW, workspace, ws_bytes,
+                                 stream);
 }

@@ -204,47 +204,65 @@ def _backward_bytes(T: int, d: int, V: int, chunk: int, bf16: int) -> int:
     return n
 
 
-def logprob_forward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor] = None,
-                    tau: float = 1.0, workspace=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    """(logprob, entropy, lse), float32 [T], of ``tokens`` [T] under softmax(H W^T / tau); lse is that of every row,
-    the masked ones included, and belongs to the backward.  A wait of the product that runs out makes them NaN, as a token
-    outside [0, V) does in its row; ``read_status(workspace)`` tells."""
-    size, mask = _operands(H, W, tokens, mask)
+def _stats(t: Optional[torch.Tensor], T: int, device) -> Optional[torch.Tensor]:
+    if t is not None and (t.dtype != torch.float32 or t.shape != (T, 2) or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"stats must be a contiguous float32 tensor of shape [{T}, 2] on {device}")
+    return t
+
+
+def _launch_forward(H, W, tokens, size, mask, tau, workspace, lse, stats):
     (T, d), V, device = H.shape, W.shape[0], H.device
     ws = _scratch(workspace, _forward_bytes(T, d, V), device)
     logprob = torch.empty(T, dtype=torch.float32, device=device)
     entropy = torch.empty(T, dtype=torch.float32, device=device)
-    lse = torch.empty(T, dtype=torch.float32, device=device)
-    st = lib().fkl_logprob_forward(H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), T, d, V,
-                                   float(tau), logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                   ws.numel(), _stream(device))
-    check(st, "fkl_logprob_forward")
+    st = lib().fkl_logprob_forward_ex(H.data_ptr(), W.data_ptr(), tokens.data_ptr(), size, _address(mask), T, d, V,
+                                      float(tau), logprob.data_ptr(), entropy.data_ptr(), _address(lse),
+                                      _address(stats), ws.data_ptr(), ws.numel(), _stream(device))
+    check(st, "fkl_logprob_forward_ex")
+    return logprob, entropy
+
+
+def logprob_forward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                    tau: float = 1.0, workspace=None, stats: Optional[torch.Tensor] = None,
+                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(logprob, entropy, lse), float32 [T], of ``tokens`` [T] under softmax(H W^T / tau); lse is that of every row,
+    the masked ones included.  ``stats`` (float32 [T, 2], optional) receives each row's reference logit and the log of
+    its sum, from which the backward knows q at any temperature.  A wait of the product that runs out makes
+    all of them NaN, as a token outside [0, V) does its log-probability; ``read_status(workspace)`` tells."""
+    size, mask = _operands(H, W, tokens, mask)
+    T = H.shape[0]
+    lse = torch.empty(T, dtype=torch.float32, device=H.device)
+    logprob, entropy = _launch_forward(H, W, tokens, size, mask, tau, workspace, lse, _stats(stats, T, H.device))
     return logprob, entropy, lse
 
 
-def _launch_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, tau, chunk, out, bf16, flags,
-                     workspace):
+def _launch_backward(H, W, tokens, mask, logprob, entropy, lse, stats, grad_logprob, grad_entropy, tau, chunk, out, bf16,
+                     flags, workspace):
     (T, d), V, device = H.shape, W.shape[0], H.device
     if T == 0 and out[1] is None:  # nothing to write, and no address to say so with
         return
     ws = _scratch(workspace, _backward_bytes(T, d, V, chunk, bf16), device)
-    st = lib().fkl_logprob_backward(
+    st = lib().fkl_logprob_backward_ex(
         H.data_ptr(), W.data_ptr(), tokens.data_ptr(), _TOKEN_BYTES[tokens.dtype], _address(mask), logprob.data_ptr(),
-        entropy.data_ptr(), lse.data_ptr(), _address(grad_logprob), _address(grad_entropy), T, d, V, float(tau), chunk, bf16,
-        flags, _address(out[0]), _address(out[1]), ws.data_ptr(), ws.numel(), _stream(device))
-    check(st, "fkl_logprob_backward")
+        entropy.data_ptr(), _address(lse), _address(stats), _address(grad_logprob), _address(grad_entropy), T, d, V,
+        float(tau), chunk, bf16, flags, _address(out[0]), _address(out[1]), ws.data_ptr(), ws.numel(), _stream(device))
+    check(st, "fkl_logprob_backward_ex")
 
 
 def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask: Optional[torch.Tensor],
-                     logprob: torch.Tensor, entropy: torch.Tensor, lse: torch.Tensor,
-                     grad_logprob: Optional[torch.Tensor] = None, grad_entropy: Optional[torch.Tensor] = None, tau: float = 1.0, chunk: int = 2048, workspace=None,
+                     logprob: torch.Tensor, entropy: torch.Tensor, lse: Optional[torch.Tensor],
+                     grad_logprob: Optional[torch.Tensor] = None, grad_entropy: Optional[torch.Tensor] = None,
+                     tau: float = 1.0, chunk: int = 2048, workspace=None,
                      out: Optional[Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]] = None,
                      accumulate: bool = False, grad_dtype: torch.dtype = torch.float32,
+                     stats: Optional[torch.Tensor] = None,
                      ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
     """dH [T, d] and dW [V, d], the gradient of sum(grad_logprob * logprob + grad_entropy * entropy) (float32 [T]
     each; None = 0), in float32 or, with ``grad_dtype=torch.bfloat16``, in bfloat16 (fp32 sums rounded once).
 
-    ``logprob``, ``entropy`` and ``lse`` are the forward's; ``chunk`` bounds the buffer of the logits' gradient as in
+    ``logprob``, ``entropy``, ``lse`` and ``stats`` are the forward's (with ``stats`` lse may be None).  Without ``stats``
+    the probabilities come from lse, whose rounding is 2^-24 |lse| of them, and a row with |lse| above 32768 (low
+    temperatures: logits of 30 below tau = 1e-3) has NaN gradients.  ``chunk`` bounds the buffer of the logits' gradient as in
     ``backward``.  ``out`` gives the tensors to write, one of them None if it is not wanted (a frozen head:
     ``(dH, None)``); ``accumulate=True`` adds into them (float32)."""
     if grad_dtype not in (torch.float32, torch.bfloat16):
@@ -255,7 +273,7 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
     _, mask = _operands(H, W, tokens, mask)
     T, device = H.shape[0], H.device
     logprob, entropy = _floats(logprob, "logprob", T, device), _floats(entropy, "entropy", T, device)
-    lse = _floats(lse, "lse", T, device)
+    lse, stats = _floats(lse, "lse", T, device), _stats(stats, T, device)
     grad_logprob = _floats(grad_logprob, "grad_logprob", T, device)
     grad_entropy = _floats(grad_entropy, "grad_entropy", T, device)
     if out is None:
@@ -264,21 +282,21 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
         if g is not None and (g.dtype != grad_dtype or g.shape != t.shape or not g.is_contiguous() or g.device != device):
             raise ValueError(f"out gradients must be contiguous {grad_dtype} {tuple(t.shape)} on {device}")
     flags = (FKL_ACCUMULATE_DH | FKL_ACCUMULATE_DW) if accumulate else 0
-    _launch_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, tau, chunk, out, int(bf16),
-                     flags, workspace)
+    _launch_backward(H, W, tokens, mask, logprob, entropy, lse, stats, grad_logprob, grad_entropy, tau, chunk, out,
+                     int(bf16), flags, workspace)
     return out
 
 
 def _fused_backward(ctx, grad_logprob, grad_entropy):
-    H, W, tokens, mask, logprob, entropy, lse = ctx.saved_tensors
+    H, W, tokens, mask, logprob, entropy, stats = ctx.saved_tensors
     if grad_logprob is None and grad_entropy is None:
         return None, None, None, None, None, None
     need = ctx.needs_input_grad
     out = (torch.empty_like(H) if need[0] else None, torch.empty_like(W) if need[1] else None)
     grad_logprob = None if grad_logprob is None else grad_logprob.contiguous()
     grad_entropy = None if grad_entropy is None else grad_entropy.contiguous()
-    _launch_backward(H, W, tokens, mask, logprob, entropy, lse, grad_logprob, grad_entropy, ctx.tau, ctx.chunk, out, 1, 0,
-                     None)
+    _launch_backward(H, W, tokens, mask, logprob, entropy, None, stats, grad_logprob, grad_entropy, ctx.tau, ctx.chunk,
+                     out, 1, 0, None)
     return out[0], out[1], None, None, None, None
 
 
@@ -286,12 +304,14 @@ _fused_backward_once = once_differentiable(_fused_backward)
 
 
 class _FusedLogprobs(torch.autograd.Function):
-    """Saves the forward's three vectors; the backward recomputes the projection block by block."""
+    """Saves the forward's scores and statistics; the backward recomputes the projection block by block."""
 
     @staticmethod
     def forward(ctx, H, W, tokens, mask, tau, chunk):
-        logprob, entropy, lse = logprob_forward(H, W, tokens, mask, tau)
-        ctx.save_for_backward(H, W, tokens, _mask(mask, H.shape[0], H.device), logprob, entropy, lse)
+        size, mask = _operands(H, W, tokens, mask)
+        stats = torch.empty((H.shape[0], 2), dtype=torch.float32, device=H.device)
+        logprob, entropy = _launch_forward(H, W, tokens, size, mask, tau, None, None, stats)
+        ctx.save_for_backward(H, W, tokens, mask, logprob, entropy, stats)
         ctx.tau, ctx.chunk = tau, chunk
         ctx.set_materialize_grads(False)
         return logprob, entropy
@@ -310,4 +330,5 @@ def fused_logprobs(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask:
     gives NaN there, and NaN gradients; so does a NaN among a row's logits.  ``chunk`` bounds the backward's buffer as in ``fused_kl``."""
     if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
         return _FusedLogprobs.apply(H, W, tokens, mask, tau, chunk)
-    return logprob_forward(H, W, tokens, mask, tau)[:2]
+    size, mask = _operands(H, W, tokens, mask)
+    return _launch_forward(H, W, tokens, size, mask, tau, None, None, None)

@@ -88,3 +88,83 @@ def test_not_finite_logits(fkl, T):
     lp, ent = fkl.fused_logprobs(H, W, tok)
     assert lp[2].isnan() and ent[2].isnan() and torch.isfinite(lp[:2]).all() and torch.isfinite(lp[3:]).all()
     assert torch.isfinite(want[0]).all()
+
+
+def check_gradients(x, H, W, tok, tau, a, b, logq, q, ent, got, half):
+    H, W = H.float().cpu().double().numpy(), W.float().cpu().double().numpy()
+    a, b, tau = a.cpu().double().numpy(), b.cpu().double().numpy(), float(np.float32(tau))
+    dS = oracle.score_gradient(logq, q, ent, tok.cpu().numpy(), a, b, tau)
+    lq = np.where(q > 0, np.abs(logq), 0)
+    terms = (np.abs(a)[:, None] + np.abs(b)[:, None] * (lq + ent[:, None] + 1)) / tau
+    # q's relative error is log q's; dS is rounded to bf16 (2^-8) but where the token is; there a (1 - q) / tau is a
+    # difference in fp32; products are summed in fp32, 16 deep
+    room = q * terms * (4 * tol(x.shape[1]) + 2.0 ** -22 * lq) + 2.0 ** -8 * np.abs(dS)
+    rows = np.arange(len(a))
+    t = tok.cpu().numpy()
+    room[rows, t] += 2.0 ** -22 * terms[rows, t] - 2.0 ** -8 * np.abs(dS[rows, t])
+    room += 2.0 ** -18 * np.abs(dS)
+    for g, want, lim in zip(got, (dS @ W, dS.T @ H), (room @ np.abs(W), room.T @ np.abs(H))):
+        g = g.float().cpu().double().numpy()
+        lim = lim + (2.0 ** -8 if half else 2.0 ** -22) * np.abs(want) + 1e-30
+        assert (np.abs(g - want) <= lim).all(), (np.abs(g - want) / lim).max()
+
+
+@pytest.mark.parametrize("tau", [1.0, *LOW])
+@pytest.mark.parametrize("T,V", [(5, 33), (300, 1505)])
+def test_gradients(fkl, T, V, tau):
+    H, W, tok, x = make(T, 64, V, seed=V + 1)
+    g = torch.Generator().manual_seed(3)
+    a, b = torch.randn(T, generator=g).cuda(), torch.randn(T, generator=g).cuda() * 0.3
+    Hl, Wl = H.clone().requires_grad_(), W.clone().requires_grad_()
+    lp, ent = fkl.fused_logprobs(Hl, Wl, tok, tau=tau)
+    logq, q, want_ent = check_scores(x, tok, tau, lp, ent)
+    got = torch.autograd.grad((lp, ent), (Hl, Wl), (a, b))
+    check_gradients(x, H, W, tok, tau, a, b, logq, q, want_ent, got, True)
+
+
+@pytest.mark.parametrize("tau", [1.0, 1e-3, 1e-6])
+def test_explicit_gradients(fkl, tau):
+    """The explicit calls hand the row's statistics on; from lse alone a row whose lse no longer tells q is NaN."""
+    T, V = 300, 1505
+    H, W, tok, x = make(T, 64, V, seed=9)
+    a, b = torch.randn(T).cuda(), torch.randn(T).cuda() * 0.3
+    stats = torch.empty(T, 2, device="cuda")
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, tau=tau, stats=stats)
+    logq, q, want_ent = check_scores(x, tok, tau, lp, ent)
+    want = torch.logsumexp(torch.tensor(x) / float(np.float32(tau)), 1)
+    assert ((lse.cpu().double() - want).abs() <= tol(V) + 2.0 ** -22 * want.abs()).all()
+    # the reference is a logit at most 10 binary orders below the row's largest, and the sum is the one above it
+    m, log_sum = stats.cpu().double().unbind(1)
+    top = torch.tensor(x).amax(1)
+    assert ((m <= top) & (top - m <= 10 * math.log(2) * tau + 1e-9)).all()
+    assert ((m / float(np.float32(tau)) + log_sum - want).abs() <= tol(V) + 2.0 ** -22 * want.abs()).all()
+    got = fkl.logprob_backward(H, W, tok, None, lp, ent, lse, a, b, tau, stats=stats)
+    check_gradients(x, H, W, tok, tau, a, b, logq, q, want_ent, got, False)
+    plain = fkl.logprob_backward(H, W, tok, None, lp, ent, lse, a, b, tau)
+    off = lse.abs() > 2 ** 15
+    assert (tau < 1e-4) == bool(off.all()) and plain[0].isnan().any(1).equal(off)
+    if tau == 1.0:
+        check_gradients(x, H, W, tok, tau, a, b, logq, q, want_ent, plain, False)
+    # a row that takes no part is not spoiled by its lse
+    mask = torch.zeros(T, dtype=torch.bool, device="cuda")
+    none = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a, b, tau)
+    assert (none[0] == 0).all() and (none[1] == 0).all()
+    with pytest.raises(ValueError):
+        fkl.logprob_forward(H, W, tok, tau=tau, stats=stats[:, :1])
+    with pytest.raises(ValueError):
+        fkl.logprob_backward(H, W, tok, None, lp, ent, lse, a, b, tau, stats=stats[:5])
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_gradients_beside_logits_of_minus_infinity(fkl, T):
+    H, W, tok, _ = make(T, 64, 1505, seed=4)
+    W[:, 0] = 0.0
+    W[3:40, 0], W[200, 0] = -8.0, -8.0
+    tok[:] = 1
+    H[:, 0] = 0.0
+    H[2, 0] = 2.0 ** 127
+    for b in (0.0, 1.0):
+        Hl = H.clone().requires_grad_()
+        lp, ent = fkl.fused_logprobs(Hl, W, tok)
+        dH, = torch.autograd.grad(lp.sum() + b * ent.sum(), Hl)
+        assert torch.isfinite(dH).all()

@@ -1,0 +1,32 @@
+"""What the scoring operators cannot take is refused by the call that is given it."""
+import pytest
+import torch
+
+INVALID, ALIGN = 1, 2
+
+
+@pytest.fixture(scope="module")
+def fkl():
+    from lm_head_top_tcgen05_gb300 import build
+
+    build.build()
+    import lm_head_top_tcgen05_gb300 as m
+
+    return m
+
+
+def test_the_backward_needs_lse_or_statistics(fkl):
+    from lm_head_top_tcgen05_gb300._lib import lib
+
+    L = lib()
+
+    def fwd(lse=None, stats=None):
+        return L.fkl_logprob_forward_ex(16, 16, 16, 4, None, 256, 256, 4096, 1.0, 16, 16, lse, stats, 256, 1 << 30, None)
+
+    def bwd(lse=None, stats=None):
+        return L.fkl_logprob_backward_ex(16, 16, 16, 4, None, 16, 16, lse, stats, 16, 16, 256, 256, 4096, 1.0, 64, 0, 0, 16,
+                                         16, 256, 1 << 40, None)
+
+    assert bwd() == INVALID and b"stats" in L.fkl_last_error()
+    for f in (fwd, bwd):
+        assert f(stats=18) == ALIGN and f(lse=18) == ALIGN and f(lse=16, stats=18) == ALIGN
