@@ -1,7 +1,9 @@
 // dW (+)= dS^T H of the scores from hidden states (fkl_score_fused.cu), on the two-SM product of fkl_gemm2.cuh.
 //
 // Its epilogue adds, in fp32 and in the order of tokens, what the rounding of dS took from the tokens' own
-// entries, and rounds once.  A lane has a row of the tile, so each of its stores is a separate line: 32-byte
+// entries, and rounds once; rows that more than kMaxTargets tokens share it leaves in fp32 for the kernel behind it
+// (reading a sum made beforehand cost a warp a load's latency for each 32 columns: 64 tokens, 20 of one row, 279 us
+// without and 310 with it).  A lane has a row of the tile, so each of its stores is a separate line: 32-byte
 // stores move the bf16 tile in half the instructions of 16-byte ones, which is what a short batch's
 // product waits for (64 x 201088 x 2880: 466 us with 16-byte stores, 335 with these, 300 with four tiles to a unit; a
 // plain fill of dW takes 287, as HBM takes writes alone at 4.0 TB/s).  Boxes of 32 rows in shared memory that leave
@@ -23,6 +25,7 @@ struct EpiDw {
   int n;
   int token[kMaxTargets];
   float rest[kMaxTargets];
+  float* held;  // where a shared row's fp32 values go in place of bf16, or NULL
 
   __device__ explicit EpiDw(const Params& prm) : p(prm) {}
 
@@ -33,7 +36,11 @@ struct EpiDw {
     rowp = p.to.out != nullptr ? p.to.out + rr * p.to.ldo : nullptr;
     rowp16 = kBf16 ? p.to.out16 + rr * p.to.ldo16 : nullptr;
     n = row_ok && p.count != nullptr ? p.count[rr] : 0;
-    if (n > kMaxTargets) n = 0;
+    held = nullptr;
+    if (n > kMaxTargets) {
+      if (kBf16) held = p.held + static_cast<size_t>(p.slot_of[rr]) * p.to.N;
+      n = 0;
+    }
 #pragma unroll
     for (int k = 0; k < kMaxTargets; ++k) token[k] = k < n ? p.token_of[rr * kMaxTargets + k] : INT_MAX;
     // the tokens came in any order; a fixed one gives the same sums every time
@@ -89,7 +96,15 @@ struct EpiDw {
           }
         }
       }
-      if (kBf16) {
+      if (kBf16 && held != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (8 * j < left)
+            st_v8(held + col0 + 8 * j, __float_as_uint(v[8 * j]), __float_as_uint(v[8 * j + 1]), __float_as_uint(v[8 * j + 2]),
+                  __float_as_uint(v[8 * j + 3]), __float_as_uint(v[8 * j + 4]), __float_as_uint(v[8 * j + 5]),
+                  __float_as_uint(v[8 * j + 6]), __float_as_uint(v[8 * j + 7]));
+        }
+      } else if (kBf16) {
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);

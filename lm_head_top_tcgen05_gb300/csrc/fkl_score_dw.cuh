@@ -5,8 +5,9 @@
 
 namespace fkl {
 
-// Most tokens of one vocabulary row for which what rounding took from their entries is added back.  Where more
-// tokens share a row, their rounding errors average out.
+// What rounding took from the tokens' entries is added back to dW's rows: by the product's epilogue in rows of at
+// most this many tokens, by a kernel behind it in rows that more tokens share.  It does not average out there: tokens of
+// one weight and a small q have entries that round alike (500 tokens, a = 1 / 3001: 0.2 % of their sum).
 constexpr int kMaxTargets = 4;
 
 // Tile of dW (+)= dS^T H: F32Params, the row's tokens (up to kMaxTargets, in any order) and what
@@ -16,6 +17,8 @@ struct DwParams {
   int wide16;           // out16 and its row stride allow 32-byte vectors
   const int* count;     // tokens of each row, or NULL: nothing to add
   const int* token_of;  // [row][kMaxTargets]
+  const int* slot_of;   // [row], where there are more than kMaxTargets tokens
+  float* held;          // [slot][N]: such a row of a bf16 gradient, not rounded yet
   const float* rest;    // by token
   const uint16_t* H;    // [T][N]
 };

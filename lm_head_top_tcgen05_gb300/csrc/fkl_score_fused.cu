@@ -16,14 +16,16 @@
 // then dW[slab] += dS^T H and dH[block] += dS W[slab] in fp32, in a fixed order: the blocks are those of the
 // loss's backward, planned by the same functions.  The bf16 of dS (half a step is 2^-8 of each value) is what
 // the tensor cores multiply; sums stay fp32.  A row's largest entry mostly is the one of its token, so what
-// rounding takes from that one, r_t, is not lost: dH's sums start at r_t W[v*_t], and dW's rows add r_t H_t before
-// they are rounded (fkl_score_dw.cu).  Without, both gradients were 1.4 times as far from exact ones as their
-// own rounding to bf16 makes them.
+// rounding takes from that one, r_t, is not lost: dH's sums start at r_t W[v*_t], and dW's rows add r_t H_t, of
+// however many tokens, before they are rounded (fkl_score_dw.cu).  Without, both gradients were 1.4 times as far from
+// exact ones as their own rounding to bf16 makes them.
 //
 // The tensor pipe bounds both: 2 T V d operations forward, 6 T V d backward.  4096 x 201088 x 2880: 2.7 ms forward
 // (1730 TFLOP/s), 8.8 ms backward (1610), as the loss of the same shape.  Few tokens wait for the head's bytes: 64
 // tokens 200 us forward (5.8 TB/s) and 679 backward, of which reading the head twice and filling its gradient are 627.
+#include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/fkl_score.h"
 #include "fkl_gemm2.cuh"
@@ -315,8 +317,28 @@ __global__ void __launch_bounds__(kRowThreads)
 // rounding to bf16 takes from dS (2^-9), and the row is NaN.
 constexpr float kMaxLse = 32768.f;
 
+// The tokens of each vocabulary row: what the head's gradient adds back to it.  A row that more than kMaxTargets
+// tokens have is shared; one of more than kMostFew is long.
+constexpr int kMostFew = 64;
+struct TargetRows {
+  int* count;     // [V]: tokens of each row; then the counters below, zero at the start like it
+  int* token_of;  // [V][kMaxTargets]
+  int* slot_of;   // [V]: place among the shared rows
+  int* shared;    // [T / (kMaxTargets + 1)]: the shared rows
+  int* base_of;   // [T / (kMaxTargets + 1)]: where a shared row's tokens start in the list
+  int* longs;     // [T / (kMostFew + 1)]: slots of the long rows
+  int* row_of;    // [T]: the row of each token that takes part, or -1
+  int* order;     // [T]: how many of its row's tokens were counted before it
+  int* list;      // [T]: the shared rows' tokens
+  int V;
+  __device__ __forceinline__ int* counter(int i) const { return count + V + i; }
+};
+constexpr int kShared = 0, kLong = 1, kListed = 2, kBlocksDone = 3, kCounters = 4;
+
 // The factors of each token's dS, its entry at the token with what rounding takes from it, where its log q is counted
-// from, and the tokens of each vocabulary row that few have; a token outside the vocabulary is recorded.
+// from, and the tokens of each vocabulary row; a token outside the vocabulary is recorded.  Slots, places in the list and the
+// order within a row come from atomics, in any order: no sum depends on them (finish_few sorts, finish_long looks through
+// the tokens in order).
 __global__ void __launch_bounds__(kRowThreads)
     score_factors_kernel(TokenIds tokens, const uint8_t* __restrict__ mask, const float* __restrict__ logprob,
                          const float* __restrict__ entropy, const float* __restrict__ lse,
@@ -324,33 +346,56 @@ __global__ void __launch_bounds__(kRowThreads)
                          const float* __restrict__ grad_entropy, int64_t T, int V, float inv_tau,
                          uint32_t* __restrict__ status, float* __restrict__ c0, float* __restrict__ c1,
                          float* __restrict__ hit, float* __restrict__ rest, float2* __restrict__ ref,
-                         int* __restrict__ count, int* __restrict__ token_of) {
+                         const TargetRows rows) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (t >= T) return;
-  float a = 0.f, b = 0.f, h = 0.f, log2_q = 0.f;
-  int tok = -1;
-  if (mask == nullptr || mask[t] != 0) {
-    tok = tokens.get(t, V);
-    if (tok < 0) atomicOr(status, kStatusBadIdBit);
-    if (grad_logprob != nullptr) a = grad_logprob[t];
-    if (grad_entropy != nullptr) b = grad_entropy[t];
-    if (b != 0.f) h = entropy[t];
-    log2_q = fmaxf(logprob[t], -1000.f) * kLog2e;  // below that q is 0, and 0 * -inf would be none
+  if (t < T) {
+    float a = 0.f, b = 0.f, h = 0.f, log2_q = 0.f;
+    int tok = -1;
+    if (mask == nullptr || mask[t] != 0) {
+      tok = tokens.get(t, V);
+      if (tok < 0) atomicOr(status, kStatusBadIdBit);
+      if (grad_logprob != nullptr) a = grad_logprob[t];
+      if (grad_entropy != nullptr) b = grad_entropy[t];
+      if (b != 0.f) h = entropy[t];
+      log2_q = fmaxf(logprob[t], -1000.f) * kLog2e;  // below that q is 0, and 0 * -inf would be none
+    }
+    const float f0 = -fmaf(b, h, a) * inv_tau, f1 = -b * kLn2 * inv_tau;
+    const float entry = fmaf(exp2f(log2_q), fmaf(f1, log2_q, f0), a * inv_tau);
+    const float rounded = __uint_as_float(pack_bf16x2(entry, 0.f) << 16);
+    c0[t] = f0;
+    c1[t] = f1;
+    hit[t] = rounded;
+    rest[t] = entry - rounded;
+    if (stats != nullptr)
+      ref[t] = make_float2(stats[2 * t], stats[2 * t + 1] * kLog2e);
+    else
+      ref[t] = make_float2(0.f, fabsf(lse[t]) <= kMaxLse ? lse[t] * kLog2e : NAN);
+    const bool target = tok >= 0 && (f0 != 0.f || f1 != 0.f);
+    rows.row_of[t] = target ? tok : -1;
+    if (target) {
+      const int n = atomicAdd(&rows.count[tok], 1);
+      rows.order[t] = n;
+      if (n < kMaxTargets) rows.token_of[static_cast<size_t>(tok) * kMaxTargets + n] = static_cast<int>(t);
+      if (n == kMaxTargets) {
+        const int slot = atomicAdd(rows.counter(kShared), 1);
+        rows.shared[slot] = tok;
+        rows.slot_of[tok] = slot;
+      }
+    }
   }
-  const float f0 = -fmaf(b, h, a) * inv_tau, f1 = -b * kLn2 * inv_tau;
-  const float entry = fmaf(exp2f(log2_q), fmaf(f1, log2_q, f0), a * inv_tau);
-  const float rounded = __uint_as_float(pack_bf16x2(entry, 0.f) << 16);
-  c0[t] = f0;
-  c1[t] = f1;
-  hit[t] = rounded;
-  rest[t] = entry - rounded;
-  if (stats != nullptr)
-    ref[t] = make_float2(stats[2 * t], stats[2 * t + 1] * kLog2e);
-  else
-    ref[t] = make_float2(0.f, fabsf(lse[t]) <= kMaxLse ? lse[t] * kLog2e : NAN);
-  if (tok >= 0 && (f0 != 0.f || f1 != 0.f)) {
-    const int n = atomicAdd(&count[tok], 1);
-    if (n < kMaxTargets) token_of[static_cast<size_t>(tok) * kMaxTargets + n] = static_cast<int>(t);
+  // the last block to come here gives each shared row its part of the list
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(rows.counter(kBlocksDone), 1) == static_cast<int>(gridDim.x) - 1 ? 1 : 0;
+  __syncthreads();
+  if (last == 0) return;
+  __threadfence();
+  const int shared = __ldcg(rows.counter(kShared));
+  for (int i = static_cast<int>(threadIdx.x); i < shared; i += kRowThreads) {
+    const int n = __ldcg(&rows.count[__ldcg(&rows.shared[i])]);
+    rows.base_of[i] = atomicAdd(rows.counter(kListed), n);
+    if (n > kMostFew) rows.longs[atomicAdd(rows.counter(kLong), 1)] = i;
   }
 }
 
@@ -375,9 +420,18 @@ struct RowJobs {
   int64_t r0;
   const float* rest;     // of these rows
   int V, add;
+  TargetRows list;       // the list of the shared rows' tokens is filled in, where `listed` is not 0
+  int64_t listed;        // tokens of the batch
 };
 
 __global__ void __launch_bounds__(kRowThreads) row_jobs_kernel(const RowJobs p) {
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; t < p.listed;
+       t += static_cast<int64_t>(gridDim.x) * kRowThreads) {
+    const int row = p.list.row_of[t];
+    if (row >= 0 && p.list.count[row] > kMaxTargets)
+      p.list.list[p.list.base_of[p.list.slot_of[row]] + p.list.order[t]] = static_cast<int>(t);
+  }
+  if (p.few == nullptr && p.clean == nullptr && p.start == nullptr) return;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   const int64_t all = p.few != nullptr && p.rows < kLeastRows ? kLeastRows : p.rows;
   for (int64_t t = blockIdx.x; t < all; t += gridDim.x) {
@@ -411,10 +465,254 @@ __global__ void __launch_bounds__(kRowThreads) row_jobs_kernel(const RowJobs p) 
 }
 
 cudaError_t launch_row_jobs(const RowJobs& p, int sms, cudaStream_t st) {
-  if (p.few == nullptr && p.clean == nullptr && p.start == nullptr) return cudaSuccess;
+  if (p.few == nullptr && p.clean == nullptr && p.start == nullptr && p.listed == 0) return cudaSuccess;
   const int64_t rows = p.rows < kLeastRows ? kLeastRows : p.rows;
   row_jobs_kernel<<<static_cast<unsigned>(rows < 8 * sms ? rows : 8 * sms), kRowThreads, 0, st>>>(p);
   return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- behind the products
+struct FinishJobs {
+  const uint32_t* status;
+  void *dH, *dW;          // either may be NULL
+  int64_t nh, nw;         // their values
+  TargetRows targets;
+  const uint4* H;         // [T][per_row]
+  const float* rest;      // [T]
+  const float4* held;     // [shared row][per_row] fp32: such rows of a bf16 dW (DwParams)
+  int64_t T;
+  int per_row;
+};
+
+// What rounding took from the tokens of a shared row, sum_t rest_t H_t in the order of tokens, is added to dW by a CTA
+// (finish_few) or, for a long row, a cluster of them (finish_long).  A thread has up to two vectors of 8 columns; where a
+// row has fewer vectors than the CTA threads, groups of threads take equal parts of the list.  The groups' sums, then the
+// CTAs', are added in order, so that the bits are always the same.
+//
+// What bounds it is the latency of a few dependent reads for each row, and of a row's tokens one batch of 8 after another,
+// for which two CTAs of 128 registers are left to an SM.  With tokens drawn by 1 / rank: 16384 of a 50257 x 2880
+// head 67 us of 8.9 ms; 8192 of a 1000 x 2880 one, the longest row 1100 of them, 48 (a CTA to a row 99, a cluster to
+// every row 154).  No shared row: 3 us, as the check for errors takes alone.
+constexpr int kScan = 4 * kRowThreads;
+constexpr int kLongCluster = 8;
+
+struct FinishShared {
+  int list[kScan];
+  float taken[kScan];  // rest of the listed tokens
+  int raw[kMostFew];
+  int warp_found[kRowThreads / 32];
+  float4 part[2][kRowThreads][2];
+};
+
+// How a CTA's threads share a row's vectors.
+struct Columns {
+  int width, groups, group, c, span;  // vectors of a group; this thread's group and place in it; vectors at a time
+  __device__ __forceinline__ explicit Columns(int per_row) {
+    width = 32;
+    while (width < per_row && width < kRowThreads) width *= 2;
+    groups = kRowThreads / width;
+    group = static_cast<int>(threadIdx.x) / width;
+    c = static_cast<int>(threadIdx.x) - group * width;
+    span = groups == 1 ? 2 * kRowThreads : width;
+  }
+};
+
+__device__ __forceinline__ void add4(float4& s, const float4& v) {
+  s.x += v.x;
+  s.y += v.y;
+  s.z += v.z;
+  s.w += v.w;
+}
+
+// Adds the group's part of a list of n tokens: the columns of vector `at` and, where `two`, of at + kRowThreads.
+__device__ __forceinline__ void add_listed(const FinishJobs& p, const FinishShared& s, const Columns& col, int n, int at,
+                                           bool two, float4 (&v)[4]) {
+  const int to = n * (col.group + 1) / col.groups;
+#pragma unroll 8
+  for (int i = n * col.group / col.groups; i < to; ++i) {
+    const uint4* h = p.H + static_cast<int64_t>(s.list[i]) * p.per_row + at;
+    const float f = s.taken[i];
+    const uint4 x = h[0], y = two ? h[kRowThreads] : make_uint4(0u, 0u, 0u, 0u);
+    add_bf16x2(v[0].x, v[0].y, x.x, f);
+    add_bf16x2(v[0].z, v[0].w, x.y, f);
+    add_bf16x2(v[1].x, v[1].y, x.z, f);
+    add_bf16x2(v[1].z, v[1].w, x.w, f);
+    add_bf16x2(v[2].x, v[2].y, y.x, f);
+    add_bf16x2(v[2].z, v[2].w, y.y, f);
+    add_bf16x2(v[3].x, v[3].y, y.z, f);
+    add_bf16x2(v[3].z, v[3].w, y.w, f);
+  }
+}
+
+// The groups' sums in the first one's places of s.part (a single group's too); a barrier has to follow.
+__device__ __forceinline__ void join_groups(FinishShared& s, const Columns& col, float4 (&v)[4]) {
+  const int tid = static_cast<int>(threadIdx.x);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s.part[k / 2][tid][k % 2] = v[k];
+  if (col.groups == 1) return;
+  __syncthreads();
+  if (tid >= col.width) return;
+  for (int g = 1; g < col.groups; ++g) {
+    add4(v[0], s.part[0][g * col.width + tid][0]);
+    add4(v[1], s.part[0][g * col.width + tid][1]);
+  }
+  s.part[0][tid][0] = v[0];  // this thread alone has read it
+  s.part[0][tid][1] = v[1];
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void add_to_row(const FinishJobs& p, int slot, int row, int vec, float4 lo, float4 hi) {
+  const int64_t at = static_cast<int64_t>(row) * p.per_row + vec;
+  if constexpr (kBf16) {
+    const float4* from = p.held + (static_cast<int64_t>(slot) * p.per_row + vec) * 2;
+    add4(lo, from[0]);
+    add4(hi, from[1]);
+    static_cast<uint4*>(p.dW)[at] = make_uint4(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w), pack_bf16x2(hi.x, hi.y),
+                                               pack_bf16x2(hi.z, hi.w));
+  } else {
+    float4* o = static_cast<float4*>(p.dW) + 2 * at;
+    add4(lo, o[0]);
+    add4(hi, o[1]);
+    o[0] = lo;
+    o[1] = hi;
+  }
+}
+
+// The shared rows that are not long, one to a CTA: their part of the list, sorted.
+template <bool kBf16>
+__device__ __forceinline__ void finish_few(const FinishJobs& p, FinishShared& s) {
+  const Columns col(p.per_row);
+  const int tid = static_cast<int>(threadIdx.x), shared = *p.targets.counter(kShared);
+  for (int slot = static_cast<int>(blockIdx.x); slot < shared; slot += static_cast<int>(gridDim.x)) {
+    const int row = p.targets.shared[slot], n = p.targets.count[row];
+    if (n > kMostFew) continue;
+    const int token = tid < n ? p.targets.list[p.targets.base_of[slot] + tid] : INT_MAX;
+    const float rest = tid < n ? p.rest[token] : 0.f;
+    __syncthreads();  // the row before is done with the shared memory
+    if (tid < n) s.raw[tid] = token;
+    __syncthreads();
+    if (tid < n) {
+      int place = 0;
+      for (int j = 0; j < n; ++j) place += s.raw[j] < token ? 1 : 0;
+      s.list[place] = token;
+      s.taken[place] = rest;
+    }
+    __syncthreads();
+    for (int first = 0; first < p.per_row; first += col.span) {  // once, where there are several groups
+      const int at = first + col.c;
+      const bool two = col.groups == 1 && at + kRowThreads < p.per_row;
+      float4 v[4] = {};
+      if (at < p.per_row) add_listed(p, s, col, n, at, two, v);
+      if (col.groups > 1) join_groups(s, col, v);
+      if (col.group == 0 && at < p.per_row) add_to_row<kBf16>(p, slot, row, at, v[0], v[1]);
+      if (two) add_to_row<kBf16>(p, slot, row, at + kRowThreads, v[2], v[3]);
+    }
+  }
+}
+
+// The long rows, one to a cluster: each CTA looks through its share of all tokens, kScan at a time, and lists those of the
+// row in order.
+template <bool kBf16>
+__device__ __forceinline__ void finish_long(const FinishJobs& p, FinishShared& s) {
+  constexpr int kWarps = kRowThreads / 32;
+  const Columns col(p.per_row);
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int ranks = cluster_size(), rank = static_cast<int>(cluster_ctarank());
+  const int pieces = (p.per_row + col.span - 1) / col.span;
+  const int64_t items = static_cast<int64_t>(*p.targets.counter(kLong)) * pieces;
+  const int64_t share = (p.T + 4 * ranks - 1) / (4 * ranks) * 4, begin = rank * share;
+  const int64_t end = begin + share < p.T ? begin + share : p.T;
+  for (int64_t item = blockIdx.x / ranks; item < items; item += gridDim.x / ranks) {
+    const int slot = p.targets.longs[item / pieces], first = static_cast<int>(item % pieces) * col.span;
+    const int row = p.targets.shared[slot], at = first + col.c;
+    const bool two = col.groups == 1 && at + kRowThreads < p.per_row;
+    float4 v[4] = {};
+    for (int64_t t0 = begin; t0 < end; t0 += kScan) {
+      const int64_t t = t0 + tid * 4;
+      int4 r = make_int4(-1, -1, -1, -1);
+      if (t + 4 <= end) {
+        r = *reinterpret_cast<const int4*>(p.targets.row_of + t);
+      } else {
+        if (t < end) r.x = p.targets.row_of[t];
+        if (t + 1 < end) r.y = p.targets.row_of[t + 1];
+        if (t + 2 < end) r.z = p.targets.row_of[t + 2];
+      }
+      const uint32_t found = (r.x == row ? 1u : 0u) | (r.y == row ? 2u : 0u) | (r.z == row ? 4u : 0u) | (r.w == row ? 8u : 0u);
+      if (__syncthreads_count(found != 0) == 0) continue;  // also: the list before is read
+      int upto = __popc(found);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      if (lane == 31) s.warp_found[warp] = upto;
+      __syncthreads();
+      int place = upto - __popc(found), n = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) place += s.warp_found[w];
+        n += s.warp_found[w];
+      }
+      for (uint32_t left = found; left != 0; left &= left - 1, ++place) {
+        const int64_t token = t + (__ffs(left) - 1);
+        s.list[place] = static_cast<int>(token);
+        s.taken[place] = p.rest[token];
+      }
+      __syncthreads();
+      if (at < p.per_row) add_listed(p, s, col, n, at, two, v);
+    }
+    join_groups(s, col, v);
+    cluster_arrive();
+    cluster_wait();
+    const int q = tid * ranks + rank;  // every CTA adds up its share of the columns
+    if (q < col.span && first + q < p.per_row) {
+      const float4* mine = s.part[q / kRowThreads][q % kRowThreads];
+      float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+#pragma unroll 8
+      for (int k = 0; k < ranks; ++k) {
+        const float4* theirs = peer(mine, k);
+        add4(lo, theirs[0]);
+        add4(hi, theirs[1]);
+      }
+      add_to_row<kBf16>(p, slot, row, first + q, lo, hi);
+    }
+    cluster_arrive();  // the sums are read: their memory may be written, or the CTA end
+    cluster_wait();
+  }
+}
+
+// The last launch of the backward: NaN in both gradients where the device recorded an error, else the shared rows.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRowThreads, 2) finish_kernel(const FinishJobs p) {
+  if (*reinterpret_cast<const volatile uint32_t*>(p.status) != 0u) {
+    using T = std::conditional_t<kBf16, uint16_t, float>;
+    T nan;
+    if constexpr (kBf16) nan = 0x7FC0u; else nan = NAN;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRowThreads;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
+    for (int64_t i = at; i < p.nh; i += stride) static_cast<T*>(p.dH)[i] = nan;
+    for (int64_t i = at; i < p.nw; i += stride) static_cast<T*>(p.dW)[i] = nan;
+    return;
+  }
+  if (p.nw == 0) return;
+  __shared__ FinishShared s;
+  finish_long<kBf16>(p, s);
+  finish_few<kBf16>(p, s);
+}
+
+cudaError_t launch_finish(const FinishJobs& p, bool bf16, int sms, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * sms) / kLongCluster * kLongCluster);
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kLongCluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return bf16 ? cudaLaunchKernelEx(&cfg, finish_kernel<true>, p) : cudaLaunchKernelEx(&cfg, finish_kernel<false>, p);
 }
 
 unsigned row_blocks(int64_t T) { return static_cast<unsigned>((T + kRowThreads - 1) / kRowThreads); }
@@ -439,7 +737,8 @@ constexpr int kPieces = 160;
 struct Areas {
   size_t c0, c1, hit, rest;   // float [T]: the factors of dS, its entry at the token and what rounding takes from it
   size_t ref;                 // float2 [T]: reference logit and log2 of the sum
-  size_t count, token_of;     // int [V], int [V][kMaxTargets]: the tokens of each vocabulary row
+  size_t count, token_of, slot_of, shared, base_of, longs, row_of, order, list;  // int: TargetRows
+  size_t held;                // bf16 gradients: fp32 [T / (kMaxTargets + 1)][d], the shared rows of dW
   size_t few;                 // bf16 [kLeastRows][d]: see kLeastRows
   size_t clean;               // bf16 [Ct][d]: a block's hidden states without the rows that a mask leaves out
   size_t ds;                  // bf16 [Ct][Vmax]
@@ -456,13 +755,21 @@ Areas backward_areas(const Plan& p, bool bf16) {
   };
   const bool sums = bf16 && p.T > 0;
   Areas a;
-  a.count = take(p.V, 4);  // zeroed with the status before it
+  a.count = take(p.V + kCounters, 4);  // zeroed with the status before it
   a.c0 = take(p.T, 4);
   a.c1 = take(p.T, 4);
   a.hit = take(p.T, 4);
   a.rest = take(p.T, 4);
   a.ref = take(p.T, 8);
   a.token_of = take(p.V * kMaxTargets, 4);
+  a.slot_of = take(p.V, 4);
+  a.shared = take(p.T / (kMaxTargets + 1), 4);
+  a.base_of = take(p.T / (kMaxTargets + 1), 4);
+  a.longs = take(p.T / (kMostFew + 1), 4);
+  a.row_of = take(p.T, 4);
+  a.order = take(p.T, 4);
+  a.list = take(p.T, 4);
+  a.held = take(sums ? p.T / (kMaxTargets + 1) * p.d : 0, 4);
   a.few = take(p.T > 0 ? kLeastRows * p.d : 0, 2);
   a.clean = take(p.Ct * p.d, 2);
   a.ds = take(p.Ct * p.Vmax, 2);
@@ -587,6 +894,11 @@ struct Backward {
   Areas at;
   template <class P>
   P* area(size_t off) const { return reinterpret_cast<P*>(ws + off); }
+  TargetRows targets() const {
+    return TargetRows{area<int>(at.count),  area<int>(at.token_of), area<int>(at.slot_of),
+                      area<int>(at.shared), area<int>(at.base_of),  area<int>(at.longs),
+                      area<int>(at.row_of), area<int>(at.order),    area<int>(at.list), static_cast<int>(V)};
+  }
 };
 
 // One block: tokens [b Ct, ...) x vocabulary columns [j Vc, ...).
@@ -618,6 +930,8 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
   jobs.r0 = r0;
   jobs.rest = c.area<const float>(c.at.rest) + r0;
   jobs.V = static_cast<int>(c.V);
+  jobs.list = c.targets();
+  jobs.listed = c.dW != nullptr && b == 0 && j == 0 ? c.T : 0;  // the first block of either order
   jobs.add = !c.bf16 && (c.accumulate & FKL_ACCUMULATE_DH) != 0 ? 1 : 0;
   cudaError_t e = launch_row_jobs(jobs, c.sms, c.st);
   if (e != cudaSuccess) return fused_cuda(e);
@@ -670,6 +984,8 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
     // what rounding took is added with the last block's sums
     pw.count = b == pl.nt - 1 ? c.area<const int>(c.at.count) + v0 : nullptr;
     pw.token_of = c.area<const int>(c.at.token_of) + v0 * kMaxTargets;
+    pw.slot_of = c.area<const int>(c.at.slot_of) + v0;
+    pw.held = c.area<float>(c.at.held);
     if ((e = launch_score_dw(bn, ds_cols, h_cols, gw, pw, c.sms, c.st)) != cudaSuccess) return fused_cuda(e);
   }
   if (c.dH == nullptr) return FKL_OK;
@@ -822,7 +1138,7 @@ extern "C" fkl_status fkl_logprob_backward_ex(const uint16_t* H, const uint16_t*
                            {workspace, "workspace"}};
   if (const int e = check_device_memory(ptrs); e != FKL_OK) return static_cast<fkl_status>(e);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(c.ws);
-  cudaError_t e = cudaMemsetAsync(c.ws, 0, T > 0 ? c.at.count + static_cast<size_t>(V) * 4 : 256, c.st);
+  cudaError_t e = cudaMemsetAsync(c.ws, 0, T > 0 ? c.at.count + static_cast<size_t>(V + kCounters) * 4 : 256, c.st);
   if (e != cudaSuccess) return fused_cuda(e);
   if (T == 0) {
     if (dW != nullptr && !(accumulate & FKL_ACCUMULATE_DW) &&
@@ -834,15 +1150,25 @@ extern "C" fkl_status fkl_logprob_backward_ex(const uint16_t* H, const uint16_t*
   score_factors_kernel<<<row_blocks(T), kRowThreads, 0, c.st>>>(
       c.tokens, mask, logprob, entropy, lse, stats, grad_logprob, grad_entropy, T, static_cast<int>(V), 1.f / tau,
       &hdr->status, c.area<float>(c.at.c0), c.area<float>(c.at.c1), c.area<float>(c.at.hit), c.area<float>(c.at.rest),
-      c.area<float2>(c.at.ref), c.area<int>(c.at.count), c.area<int>(c.at.token_of));
+      c.area<float2>(c.at.ref), c.targets());
   if ((e = cudaGetLastError()) != cudaSuccess) return fused_cuda(e);
   const Plan& pl = c.pl;
   for (int64_t o = 0; o < (pl.slab_outer ? pl.nslabs : pl.nt); ++o)
     for (int64_t i = 0; i < (pl.slab_outer ? pl.nt : pl.nslabs); ++i)
       if ((s = score_block(c, pl.slab_outer ? i : o, pl.slab_outer ? o : i)) != FKL_OK) return s;
-  const int64_t nh = dH != nullptr ? T * d : 0, nw = dW != nullptr ? V * d : 0;
-  e = c.bf16 ? launch_poison16(static_cast<uint16_t*>(dH), nh, static_cast<uint16_t*>(dW), nw, &hdr->status, c.sms, c.st)
-             : launch_poison(static_cast<float*>(dH), nh, static_cast<float*>(dW), nw, &hdr->status, c.sms, c.st);
+  FinishJobs jobs{};
+  jobs.status = &hdr->status;
+  jobs.dH = dH;
+  jobs.dW = dW;
+  jobs.nh = dH != nullptr ? T * d : 0;
+  jobs.nw = dW != nullptr ? V * d : 0;
+  jobs.targets = c.targets();
+  jobs.H = reinterpret_cast<const uint4*>(H);
+  jobs.rest = c.area<const float>(c.at.rest);
+  jobs.held = c.area<const float4>(c.at.held);
+  jobs.T = T;
+  jobs.per_row = static_cast<int>(d / 8);
+  e = launch_finish(jobs, c.bf16, c.sms, c.st);
   if (e != cudaSuccess) return fused_cuda(e);
   return FKL_OK;
 }
