@@ -153,12 +153,14 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: Unio
     (float32 [B], differentiable in the logits) and the ``top_n`` (at most 128, and V) likeliest ids, int32 and
     float32 [B, top_n], likeliest first, ties by the lower id.
 
-    ``temperature`` is one number or a float32 tensor [B].  ``mask`` (uint8 or bool [B]) leaves rows out: log-probability,
+    ``temperature`` is one number or a float32 tensor [B], a constant: one that wants a gradient is refused.  ``mask`` (uint8 or bool [B]) leaves rows out: log-probability,
     entropy and gradient 0, ids -1.  -inf bans an id, NaN counts as -inf, +inf ids share all the
     probability.  A token outside [0, V) in another row gives NaN, in its log-probability and its row of
     the gradient; so does a row without any logit, and a temperature in a tensor that is not finite and above 0."""
     if not 0 <= top_n <= 128:
         raise ValueError("top_n must be between 0 and 128")
+    if isinstance(temperature, torch.Tensor) and temperature.requires_grad and torch.is_grad_enabled():
+        raise ValueError("temperature gets no gradient from the scores: pass temperature.detach()")
     if logits.requires_grad and torch.is_grad_enabled():
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, top_n, mask))
     return TokenLogprobs(*_score(logits, tokens, temperature, top_n, mask, False)[:4])

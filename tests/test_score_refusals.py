@@ -30,3 +30,14 @@ def test_the_backward_needs_lse_or_statistics(fkl):
     assert bwd() == INVALID and b"stats" in L.fkl_last_error()
     for f in (fwd, bwd):
         assert f(stats=18) == ALIGN and f(lse=18) == ALIGN and f(lse=16, stats=18) == ALIGN
+
+
+def test_a_temperature_that_wants_a_gradient(fkl):
+    """It would get none: the scores are differentiable in the logits alone."""
+    x, tok = torch.zeros(2, 5), torch.zeros(2, dtype=torch.int64)
+    T = torch.ones(2, requires_grad=True)
+    for logits in (x, x.clone().requires_grad_()):
+        with pytest.raises(ValueError, match="temperature.*gradient"):
+            fkl.token_logprobs(logits, tok, temperature=T)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # only the host tensor is wrong here
+        fkl.token_logprobs(x, tok, temperature=T)
