@@ -311,6 +311,7 @@ class _FusedLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, tokens, mask, tau, chunk):
         size, mask = _operands(H, W, tokens, mask)
+        _backward_bytes(H.shape[0], H.shape[1], W.shape[0], chunk, 1)  # refuses a chunk here, not in the backward
         stats = torch.empty((H.shape[0], 2), dtype=torch.float32, device=H.device)
         logprob, entropy = _launch_forward(H, W, tokens, size, mask, tau, None, None, stats)
         ctx.save_for_backward(H, W, tokens, mask, logprob, entropy, stats)

@@ -41,3 +41,13 @@ def test_a_temperature_that_wants_a_gradient(fkl):
             fkl.token_logprobs(logits, tok, temperature=T)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # only the host tensor is wrong here
         fkl.token_logprobs(x, tok, temperature=T)
+
+
+@pytest.mark.gpu
+def test_a_chunk_that_the_backward_would_refuse(fkl, cuda_device):
+    H = torch.randn(20, 64).bfloat16().cuda().requires_grad_()
+    W, tok = torch.randn(100, 64).bfloat16().cuda(), torch.zeros(20, dtype=torch.int64).cuda()
+    with pytest.raises(fkl.FklError):
+        fkl.fused_logprobs(H, W, tok, chunk=0)
+    with pytest.raises(fkl.FklError):
+        fkl.fused_logprobs(H, W, tok, chunk=-5)
