@@ -42,7 +42,8 @@ extern "C" {
  *   tokens   int32 or int64 [B] (token_bytes 4 or 8)
  *   mask     uint8 [B] or NULL
  *   temperature       T > 0 for all rows, or, where temperature_rows (float [B]) is not NULL, one per
- *                     row; a row whose T is not a finite number above 0 is NaN
+ *                     row; a row whose T is not a finite number above 0 is NaN.  From 4.25e-39 down log2(e) / T
+ *                     is no float: such a T is refused, or makes its row NaN
  *   top_n    0 <= top_n <= min(V, 128): the row's top_n largest logits, largest first, ties by the lower id
  *   logprob, entropy  float [B]
  *   stats    float [B][2] or NULL: the row's largest logit m and log sum_v exp((x_v - m) / T), for the
@@ -73,8 +74,8 @@ fkl_status fkl_token_logprobs_backward(const void* logits, int32_t type, int64_t
                                        void* dlogits, int64_t ldd, void* stream);
 
 /*
- * Scores tokens from hidden states: logits x = H W^T (bf16 inputs, fp32 accumulation) with temperature tau,
- * in one pass of the tensor-core product whose tiles are reduced where they are accumulated.
+ * Scores tokens from hidden states: logits x = H W^T (bf16 inputs, fp32 accumulation) with temperature tau
+ * (finite, and above 4.25e-39, from where log2(e) / tau is a float), in one pass of the tensor-core product whose tiles are reduced where they are accumulated.
  *   H  bf16 [T][d], W bf16 [V][d], 16-byte aligned, d a multiple of 8
  *   tokens  int32 or int64 [T] (token_bytes 4 or 8);  mask uint8 [T] or NULL
  *   logprob, entropy, lse   float [T]; lse (natural log of sum_v exp(x_v / tau)) is written for every row,

@@ -723,8 +723,8 @@ fkl_status check_rows(const void* logits, int32_t type, int64_t B, int64_t V, in
     return score_fail(FKL_ERR_INVALID_ARG, "need 0 <= B < 2^31, 1 <= V <= 2^22 and ld >= V");
   if (token_bytes != 4 && token_bytes != 8) return score_fail(FKL_ERR_INVALID_ARG, "token_bytes must be 4 or 8");
   if (B > 0 && (logits == nullptr || tokens == nullptr)) return score_fail(FKL_ERR_INVALID_ARG, "a required pointer is NULL");
-  if (temperature_rows == nullptr && !(temperature > 0.f && temperature < INFINITY))
-    return score_fail(FKL_ERR_INVALID_ARG, "temperature must be finite and > 0");
+  if (temperature_rows == nullptr && !(temperature > 0.f && temperature < INFINITY && kLog2e * (1.f / temperature) < INFINITY))
+    return score_fail(FKL_ERR_INVALID_ARG, "temperature must be finite and > 0, and its inverse too (4.25e-39 and more)");
   if (reinterpret_cast<uintptr_t>(logits) % type_bytes(type) != 0 ||
       reinterpret_cast<uintptr_t>(tokens) % token_bytes != 0 || reinterpret_cast<uintptr_t>(temperature_rows) % 4 != 0)
     return score_fail(FKL_ERR_ALIGNMENT, "logits and tokens must be aligned to their types, temperature_rows to 4 bytes");

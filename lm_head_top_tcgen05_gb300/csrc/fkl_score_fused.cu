@@ -1003,7 +1003,8 @@ fkl_status score_block(const Backward& c, int64_t b, int64_t j) {
 // What both directions check.
 fkl_status check_fused(const uint16_t* H, const uint16_t* W, const void* tokens, int32_t token_bytes, int64_t T,
                        float tau, const void* ws, size_t ws_bytes, size_t need) {
-  if (!(tau > 0.f) || !std::isfinite(tau)) return fused_fail(FKL_ERR_INVALID_ARG, "tau must be finite and > 0");
+  if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(kLog2e / tau))
+    return fused_fail(FKL_ERR_INVALID_ARG, "tau must be finite and > 0, and its inverse too (4.25e-39 and more)");
   if (token_bytes != 4 && token_bytes != 8) return fused_fail(FKL_ERR_INVALID_ARG, "token_bytes must be 4 or 8");
   if (W == nullptr || (T > 0 && (H == nullptr || tokens == nullptr)))
     return fused_fail(FKL_ERR_INVALID_ARG, "H, W and tokens must not be NULL");

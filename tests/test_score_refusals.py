@@ -51,3 +51,20 @@ def test_a_chunk_that_the_backward_would_refuse(fkl, cuda_device):
         fkl.fused_logprobs(H, W, tok, chunk=0)
     with pytest.raises(fkl.FklError):
         fkl.fused_logprobs(H, W, tok, chunk=-5)
+
+
+@pytest.mark.parametrize("T", [1e-39, 1e-45, 4e-39])
+def test_a_temperature_whose_inverse_is_infinite(fkl, T):
+    """log2(e) / T is what logits are multiplied by: from 4.25e-39 down it is no float."""
+    from lm_head_top_tcgen05_gb300._lib import lib
+
+    L = lib()
+
+    def refused(status):
+        return status == INVALID and b"inverse" in L.fkl_last_error()
+
+    assert refused(L.fkl_token_logprobs(16, 0, 4, 100, 100, 16, 8, None, T, None, 0, 16, 16, None, None, None, None))
+    assert refused(L.fkl_token_logprobs_backward(16, 0, 4, 100, 100, 16, 8, None, T, None, 16, 16, 16, None, 16, 100, None))
+    assert refused(L.fkl_logprob_forward(16, 16, 16, 4, None, 256, 256, 4096, T, 16, 16, 16, 256, 1 << 30, None))
+    assert refused(L.fkl_logprob_backward(16, 16, 16, 4, None, 16, 16, 16, 16, 16, 256, 256, 4096, T, 64, 0, 0, 16, 16, 256,
+                                          1 << 40, None))
