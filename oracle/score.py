@@ -67,11 +67,6 @@ def alternatives(row, n):
     return np.concatenate([ids, np.full(n - ids.size, -1, dtype=ids.dtype)])
 
 
-def fused_gradients(H, W, dS):
-    """(dH, dW) of the logits' gradient dS."""
-    return dS @ np.asarray(W, dtype=np.float64), dS.T @ np.asarray(H, dtype=np.float64)
-
-
 # ---------------------------------------------------------------- the cache's format, bit by bit
 def id_bits(V):
     return max(1, int(V).bit_length())
