@@ -21,6 +21,11 @@
  * Rows.  `mask` (uint8, 1 = valid; NULL = all valid) leaves rows out: their logprob and entropy
  * are 0, their gradient is 0, and neither their token nor what their logits or hidden states hold (NaN, say)
  * reaches anything else.  In the others a token outside [0, V) gives logprob NaN.
+ *
+ * NaN.  The two forms differ.  Over logits in memory it counts as -inf, as in the sampler whose tokens are scored: a row's
+ * score stays finite, and what a token outside [0, V) spoils is its own row of the gradient.  From hidden
+ * states, where a NaN is a fault of the product's operands, it makes its row's scores NaN, and a token outside [0, V) or
+ * a NaN row spoils the whole gradient of the head, into which all rows go (the former that of the hidden states too).
  */
 #ifndef FKL_SCORE_H_
 #define FKL_SCORE_H_
@@ -75,7 +80,8 @@ fkl_status fkl_token_logprobs_backward(const void* logits, int32_t type, int64_t
 
 /*
  * Scores tokens from hidden states: logits x = H W^T (bf16 inputs, fp32 accumulation) with temperature tau
- * (finite, and above 4.25e-39, from where log2(e) / tau is a float), in one pass of the tensor-core product whose tiles are reduced where they are accumulated.
+ * (finite, and above 4.25e-39, from where log2(e) / tau is a float), in one pass of the tensor-core product whose
+ * tiles are reduced where they are accumulated.
  *   H  bf16 [T][d], W bf16 [V][d], 16-byte aligned, d a multiple of 8
  *   tokens  int32 or int64 [T] (token_bytes 4 or 8);  mask uint8 [T] or NULL
  *   logprob, entropy, lse   float [T]; lse (natural log of sum_v exp(x_v / tau)) is written for every row,
@@ -101,8 +107,11 @@ fkl_status fkl_logprob_forward_ex(const uint16_t* H, const uint16_t* W, const vo
  * The gradient of sum_t (a_t logprob_t + b_t entropy_t): dH [T][d] and dW [V][d], as float or, with
  * grad_bf16 = 1, as bfloat16 bit patterns (fp32 sums rounded once), 16-byte aligned.  One of them may be NULL:
  * its product is left out (a frozen head, say).  The logits are recomputed block by block as in fkl_backward, and
- * `chunk` bounds the buffer of their gradient in the same way: at most chunk * V bfloat16 values (V rounded up to
- * whole tiles of 256).
+ * `chunk` bounds the buffer of their gradient: at most max(chunk * V, 256 * T) bfloat16 values, as a block is at least
+ * one tile of 256 columns wide and may take all tokens (where chunk >= T: T * V, V rounded up to whole tiles).
+ * Beside it the workspace holds 42 MB for partial tiles of dH, a bfloat16 copy of a block's hidden states, 24 bytes
+ * for each row of the head and, for bfloat16 gradients, fp32 sums of dH and of dW where several blocks add to them and
+ * of T / 5 rows of dW; it is sized for both gradients and a mask whether they are there or not.
  *   grad_logprob, grad_entropy   float [T]; NULL = 0
  *   logprob, entropy   the forward's
  *   lse, stats   the forward's; one of them may be NULL in fkl_logprob_backward_ex.  With `stats` q is right at any

@@ -18,10 +18,12 @@
 // Backward.  dx_v = ( q_v (c0 + c1 log2 q_v) + a 1[v = v*] ) / T with c0 = -(a + b entropy), c1 = -b ln 2,
 // q_v = 2^((x_v - M) log2(e) / T - log2 L), one pass that reads the logits and writes their gradient.
 //
-// What bounds it (GB300, on the device).  Many rows: HBM for fp32 (512 x 201088: 61 us, 6.7 TB/s), for 16 bits the 9
-// instructions of a logit beside it (2048 x 128256 bf16: 87 us, 6.0 TB/s; 512 x 151936: 31 us, 5.0 TB/s, as all
-// rows run at once and end together).  Few rows: latency (1 x 201088 fp32 4.4 us, with 20 alternatives 7.8).  The
-// gradient runs at the rate of a copy (2048 x 128256 bf16: 149 us, 7.1 TB/s).
+// What bounds it (GB300, on the device, logits in HBM).  Many rows: HBM for fp32 (512 x 201088: 61 us, 6.8 TB/s), for
+// 16 bits the 9 instructions of a logit beside it (2048 x 128256 bf16: 87 us, 6.0 TB/s; 512 x 151936: 31 us, 5.0 TB/s,
+// as all rows run at once and end together).  Few rows: latency (1 x 201088 fp32 5.5 us, with 20 alternatives 8.9; from
+// L2 4.4 and 7.8).  The gradient runs at the rate of a copy (2048 x 128256 bf16: 150 us, 7.0 TB/s), if its rows lie in
+// 16-byte vectors as the logits' do.  Where they do not (rows V + 1 apart in 16 bits) every element goes by itself: 804
+// us.  Rows that the mask leaves out are read and written too, on a path without loads in flight (half of those rows: 187 us).
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -704,9 +706,12 @@ cudaError_t launch_score(ScoreArgs& g, int64_t B, int sms, cudaStream_t st) {
 }
 
 // Blocks of 256 threads, four to an SM, spread many rows more evenly; 512 read a single row sooner, and a
-// thread's share of a row, which is read again for each alternative, is half as long.  Forward on the device:
-// 512 x 151936 bf16 31 us with 256 against 34 with 512, with 5 alternatives 39 against 42; 1 x 201088 fp32 with 20
-// alternatives 8.6 against 8.1, 64 of them 19 against 17; 203 x 50261 fp16 with 100 alternatives 20 against 16.
+// thread's share of a row, which is read again for each alternative, is half as long.  Forward on the device with
+// 0, 5, 8, 12, 20 and 100 alternatives, 256 threads and then 512, in us (behind a write of 256 MB, so above the figures at the
+// head of this file): 512 x 151936 bf16 33, 41, 43, 47, 52, 72 and 36, 45, 46, 47, 48, 67; 512 x 201088 fp32 70, 82, 89, 97,
+// 111, 158 and 70, 80, 83, 88, 97, 136; 1000 x 32000 bf16 18, 26, 26, 26, 27, 41 and 22, 34, 34, 34, 35, 41.  Few rows:
+// 1 x 201088 fp32 8.1, 11, 11, 11, 11, 15 and 6.4, 9.4, 9.4, 9.5, 9.6, 12; 203 x 50261 fp16 9.9, 15, 15, 15, 16, 21 and 10, 14,
+// 14, 14, 15, 17.
 constexpr int kFewTop = 8;
 template <class T>
 cudaError_t launch_score(ScoreArgs& g, int64_t B, int sms, cudaStream_t st) {

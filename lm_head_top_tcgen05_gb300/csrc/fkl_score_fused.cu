@@ -21,8 +21,8 @@
 // exact ones as their own rounding to bf16 makes them.
 //
 // The tensor pipe bounds both: 2 T V d operations forward, 6 T V d backward.  4096 x 201088 x 2880: 2.7 ms forward
-// (1730 TFLOP/s), 8.8 ms backward (1610), as the loss of the same shape.  Few tokens wait for the head's bytes: 64
-// tokens 200 us forward (5.8 TB/s) and 679 backward, of which reading the head twice and filling its gradient are 627.
+// (1750 TFLOP/s), 8.8 ms backward (1615), as the loss of the same shape.  Few tokens wait for the head's bytes: 64
+// tokens 202 us forward (5.7 TB/s) and 707 backward, of which reading the head twice and filling its gradient are 627.
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -782,8 +782,9 @@ Areas backward_areas(const Plan& p, bool bf16) {
 
 // Cuts dH's units along K.  Where there are more units than CTA pairs, the last wave's, as in the loss.  Else all of
 // them, into the number of pieces with the least time by this count: a wave's 64-deep steps at 645 cycles with 2500
-// for a tile's start and end, and a pass that adds the pieces up (1024 tokens: 48 units on 76 pairs, 851 us
-// whole and 585 in three pieces each).
+// for a tile's start and end, and a pass that adds the pieces up.  Whole and in pieces, on the device, with the
+// pass: 64 tokens of 201088 x 2880 836 and 191 us, 256 tokens 836 and 211, 1024 tokens (48 units on 76 pairs)
+// 867 and 720; 512 of 32000 x 512 145 and 33, 1024 of 50257 x 512 220 and 49.
 void plan_pieces(GemmShape* g, int pairs, float* pieces) {
   if (g->num_units >= pairs) {
     plan_ksplit(g, pairs, pieces, kKsplitSlots);

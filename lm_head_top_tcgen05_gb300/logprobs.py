@@ -153,10 +153,11 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: Unio
     (float32 [B], differentiable in the logits) and the ``top_n`` (at most 128, and V) likeliest ids, int32 and
     float32 [B, top_n], likeliest first, ties by the lower id.
 
-    ``temperature`` is one number or a float32 tensor [B], a constant: one that wants a gradient is refused.  ``mask`` (uint8 or bool [B]) leaves rows out: log-probability,
-    entropy and gradient 0, ids -1.  -inf bans an id, NaN counts as -inf, +inf ids share all the
-    probability.  A token outside [0, V) in another row gives NaN, in its log-probability and its row of
-    the gradient; so does a row without any logit, and a temperature in a tensor that is not finite and above 0."""
+    ``temperature`` is one number or a float32 tensor [B], a constant: one that wants a gradient is refused.  ``mask``
+    (uint8 or bool [B]) leaves rows out: log-probability, entropy and gradient 0, ids -1.  -inf bans an id, NaN counts as
+    -inf (in ``fused_logprobs`` it makes its row NaN), +inf ids share all the probability.  A token outside [0, V) in
+    another row gives NaN, in its log-probability and its row of the gradient; so does a row without any logit, and
+    a temperature in a tensor that is not finite and above 4.25e-39."""
     if not 0 <= top_n <= 128:
         raise ValueError("top_n must be between 0 and 128")
     if isinstance(temperature, torch.Tensor) and temperature.requires_grad and torch.is_grad_enabled():
@@ -264,9 +265,9 @@ def logprob_backward(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mas
 
     ``logprob``, ``entropy``, ``lse`` and ``stats`` are the forward's (with ``stats`` lse may be None).  Without ``stats``
     the probabilities come from lse, whose rounding is 2^-24 |lse| of them, and a row with |lse| above 32768 (low
-    temperatures: logits of 30 below tau = 1e-3) has NaN gradients.  ``chunk`` bounds the buffer of the logits' gradient as in
-    ``backward``.  ``out`` gives the tensors to write, one of them None if it is not wanted (a frozen head:
-    ``(dH, None)``); ``accumulate=True`` adds into them (float32)."""
+    temperatures: logits of 30 below tau = 1e-3) has NaN gradients.  ``chunk`` bounds the buffer of the logits' gradient:
+    at most max(chunk * V, 256 * T) bfloat16 values.  ``out`` gives the tensors to write, one of them None if it is not
+    wanted (a frozen head: ``(dH, None)``); ``accumulate=True`` adds into them (float32)."""
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("grad_dtype must be torch.float32 or torch.bfloat16")
     bf16 = grad_dtype == torch.bfloat16
@@ -329,8 +330,10 @@ def fused_logprobs(H: torch.Tensor, W: torch.Tensor, tokens: torch.Tensor, mask:
     """(logprob, entropy), float32 [T], of ``tokens`` [T] (int32 or int64) under softmax(H W^T / tau) for hidden
     states H [T, d] and LM head W [V, d] (bfloat16), without the [T, V] logits in memory; differentiable in H and W.
 
-    ``mask`` (uint8 or bool [T]) leaves tokens out: log-probability, entropy and gradient 0.  A token outside [0, V) in another row
-    gives NaN there, and NaN gradients; so does a NaN among a row's logits.  ``chunk`` bounds the backward's buffer as in ``fused_kl``."""
+    ``tau`` is any finite number above 4.25e-39.  ``mask`` (uint8 or bool [T]) leaves tokens out: log-probability, entropy
+    and gradient 0.  A token outside [0, V) in another row gives NaN there, and NaN gradients; so does a NaN among a
+    row's logits (in ``token_logprobs`` it counts as -inf), in the row's scores, its dH and dW.  ``chunk`` bounds the
+    backward's buffer of the logits' gradient: at most max(chunk * V, 256 * T) bfloat16 values."""
     if torch.is_grad_enabled() and (H.requires_grad or W.requires_grad):
         return _FusedLogprobs.apply(H, W, tokens, mask, tau, chunk)
     size, mask = _operands(H, W, tokens, mask)
