@@ -8,9 +8,8 @@ Tolerances.  Entries of other tokens in the row are bf16 (2^-8 of each).  A toke
 q off by log q's error.  Sums are made in the tensor cores, 16 products at a time: each product and the sum so far are cut off
 (towards zero) at 2^-25 of the largest one's binary order.  (1 + n products of 2^-26 comes to 1, with n products of
 2^-24 or 2^-25 to their sum; the results have fp32's 24 bits.)  A step so loses at most 16 * 2^-25 = 2^-21 and the cut of its
-result, 2^-23, of the terms' size; with equal signs it is half of the first on average, and a few percent of that were
-seen to pass the 2^-23 a step that an exact sum rounded once would lose (T = 3000: 1.05 of T / 16 * 2^-23).  What was
-taken adds one rounding a token, itself at most 2^-8 of the entry.
+result, 2^-23, of the terms' size.  (A step that rounded once would lose 2^-23 at most: T = 3000 tokens lost 1.05
+of T / 16 times that.)  What was taken adds one rounding a token, itself at most 2^-8 of the entry.
 """
 import numpy as np
 import pytest
@@ -110,3 +109,73 @@ def test_a_nan_in_a_shared_row_stays_there(fkl):
     lp, ent, lse = fkl.logprob_forward(H, W, tok, mask)
     got = fkl.logprob_backward(H, W, tok, mask, lp, ent, lse, a)
     assert torch.equal(want[1], got[1]) and torch.equal(want[0], got[0])
+
+
+def test_a_row_of_thousands_of_tokens(fkl):
+    """Longer than one look through the tokens of a CTA's share, beside rows of few and of tens of tokens."""
+    T, d, V = 12000, 24, 800
+    H, W, tok = make(T, d, V, 9000, seed=3)
+    tok[:70] = 9
+    a = torch.full((T,), 1 / 3001).cuda()
+    e = Exact(H, W, tok, None, 1.0)
+    lp, ent, lse = fkl.logprob_forward(H, W, tok)
+    got = fkl.logprob_backward(H, W, tok, None, lp, ent, lse, a)
+    check(e, got[1], a, False)
+    half = fkl.logprob_backward(H, W, tok, None, lp, ent, lse, a, grad_dtype=torch.bfloat16)
+    assert torch.equal(half[1], got[1].bfloat16())
+
+
+def test_shared_rows_in_a_graph(fkl):
+    """A captured step follows the tokens that it is replayed with: other rows are shared then, or none."""
+    T, d, V = 400, 64, 900
+    H, W, tok = make(T, d, V, 200)
+    a = torch.randn(T).cuda()
+    stats = torch.empty(T, 2, device="cuda")
+
+    def step():
+        lp, ent, lse = fkl.logprob_forward(H, W, tok, tau=0.01, stats=stats)
+        return (lp, ent) + fkl.logprob_backward(H, W, tok, None, lp, ent, None, a, tau=0.01, stats=stats,
+                                                grad_dtype=torch.bfloat16)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed, shared in ((1, 5), (2, 0), (3, 350)):
+        h, w, t = make(T, d, V, shared, seed)
+        H.copy_(h)
+        W.copy_(w)
+        tok.copy_(t)
+        graph.replay()
+        for x, y in zip(outs, step()):
+            assert torch.equal(x, y)
+
+
+def test_shared_rows_on_several_streams(fkl):
+    import threading
+
+    H, W, tok = make(700, 64, 900, 300, seed=4)
+    a = torch.randn(700).cuda()
+
+    def step():
+        Hl, Wl = H.clone().requires_grad_(), W.clone().requires_grad_()
+        lp, ent = fkl.fused_logprobs(Hl, Wl, tok, tau=0.05)
+        return torch.autograd.grad((lp, ent), (Hl, Wl), (a, a))
+
+    want = step()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(stream):
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = step()
+                stream.synchronize()
+                wrong.extend(1 for u, v in zip(got, want) if not torch.equal(u, v))
+
+    threads = [threading.Thread(target=work, args=(torch.cuda.Stream(),)) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
