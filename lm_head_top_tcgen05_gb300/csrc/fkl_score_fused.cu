@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(kRowThreads)
   entropy[t] = ent < 0.0 ? 0.f : static_cast<float>(ent);
 }
 
-// Without the rows' statistics log q is a logit less lse, off by 2^-24 lse.  Above this lse that passes what
-// rounding to bf16 takes from dS (2^-9), and the row is NaN.
+// Without the rows' statistics log q is a logit less lse, off by 2^-24 lse.  Above this lse that passes half a step of
+// dS's bf16 (2^-9 to 2^-8 of a value), and the row is NaN.
 constexpr float kMaxLse = 32768.f;
 
 // The tokens of each vocabulary row: what the head's gradient adds back to it.  A row that more than kMaxTargets
@@ -360,17 +360,17 @@ __global__ void __launch_bounds__(kRowThreads)
       log2_q = fmaxf(logprob[t], -1000.f) * kLog2e;  // below that q is 0, and 0 * -inf would be none
     }
     const float f0 = -fmaf(b, h, a) * inv_tau, f1 = -b * kLn2 * inv_tau;
-    const float entry = fmaf(exp2f(log2_q), fmaf(f1, log2_q, f0), a * inv_tau);
+    const float2 from = stats != nullptr ? make_float2(stats[2 * t], stats[2 * t + 1] * kLog2e)
+                                         : make_float2(0.f, fabsf(lse[t]) <= kMaxLse ? lse[t] * kLog2e : NAN);
+    const bool target = tok >= 0 && (f0 != 0.f || f1 != 0.f);
+    float entry = fmaf(exp2f(log2_q), fmaf(f1, log2_q, f0), a * inv_tau);
+    if (target && !(from.y == from.y)) entry = NAN;  // as the rest of its row
     const float rounded = __uint_as_float(pack_bf16x2(entry, 0.f) << 16);
     c0[t] = f0;
     c1[t] = f1;
     hit[t] = rounded;
     rest[t] = entry - rounded;
-    if (stats != nullptr)
-      ref[t] = make_float2(stats[2 * t], stats[2 * t + 1] * kLog2e);
-    else
-      ref[t] = make_float2(0.f, fabsf(lse[t]) <= kMaxLse ? lse[t] * kLog2e : NAN);
-    const bool target = tok >= 0 && (f0 != 0.f || f1 != 0.f);
+    ref[t] = from;
     rows.row_of[t] = target ? tok : -1;
     if (target) {
       const int n = atomicAdd(&rows.count[tok], 1);

@@ -168,3 +168,23 @@ def test_gradients_beside_logits_of_minus_infinity(fkl, T):
         lp, ent = fkl.fused_logprobs(Hl, W, tok)
         dH, = torch.autograd.grad(lp.sum() + b * ent.sum(), Hl)
         assert torch.isfinite(dH).all()
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_a_row_without_scores_has_no_gradient_either(fkl, T):
+    """A NaN in the head, or an lse that tells nothing: NaN in all of the head's gradient, the tokens' own rows too."""
+    H, W, tok, _ = make(T, 64, 900, seed=6)
+    tok[:] = 17
+    one = torch.ones(T, device="cuda")
+    lp, ent, lse = fkl.logprob_forward(H, W, tok, tau=1e-6)
+    for got in fkl.logprob_backward(H, W, tok, None, lp, ent, lse, one, one, tau=1e-6):
+        assert got.isnan().all()
+    W[5] = float("nan")
+    Wl = W.clone().requires_grad_()
+    lp, ent = fkl.fused_logprobs(H, Wl, tok)
+    assert lp.isnan().all() and ent.isnan().all()
+    assert torch.autograd.grad(lp.sum(), Wl)[0].isnan().all()
+    # rows that take no part in the sum stay out of it
+    lp, ent, lse = fkl.logprob_forward(H, W, tok)
+    none = fkl.logprob_backward(H, W, tok, None, lp, ent, lse, 0 * one, None, out=(None, torch.empty(900, 64, device="cuda")))
+    assert (none[1] == 0).all()
